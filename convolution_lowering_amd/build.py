@@ -35,7 +35,11 @@ def _units():
              ("lowering_kernels", "lowering_kernels.hip", []),
              ("direct_conv", "direct_conv.hip", []),
              ("patch_conv", "patch_conv.hip", []),
-             ("igemm_ablate", "igemm_ablate.hip", [])]
+             ("igemm_ablate", "igemm_ablate.hip", []),
+             ("mixer_api", "mixer_api.cpp", []),
+             ("conv1d_causal", "conv1d_causal.hip", []),
+             ("delta_tokens", "delta_tokens.hip", []),
+             ("branch_norm", "branch_norm.hip", [])]
     for dt, tag in ((1, "bf16"), (2, "f16"), (0, "f32")):  # IGEMM_DTYPE: 0 fp32, 1 bf16, 2 fp16
         for feed in range(10):  # the Feed values of conv_internal.h
             units.append((f"igemm_{tag}_feed{feed}", "igemm_inst.hip",

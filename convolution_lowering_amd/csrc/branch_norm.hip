@@ -1,0 +1,351 @@
+// The end of a block on rows of D values, and its gradients:
+//
+//   u = y rstd(y) w_post,  r = x + alpha act(gate) u,  h = r rstd(r) w_next
+//
+// A few operations for each value read: HBM bound.  A row is held in the
+// registers of TPR threads (V values of 16 bytes at a time, NV times), so each
+// tensor is read once and the two norms cost no second pass; a short row takes
+// part of a wavefront and a block holds several.  The backward pass gives a
+// block a run of rows, and each thread keeps the sums of its own columns for
+// the weights' gradients in registers until the run ends.
+#include <algorithm>
+
+#include "mixer_internal.h"
+
+namespace convlower {
+namespace {
+
+// Sum over the TPR threads of a row (a power of two: at most 64 lanes of one
+// wavefront, or the whole block); every thread gets it.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+#pragma unroll
+    for (int m = (TPR < 64 ? TPR : 64) / 2; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+    if constexpr (TPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) v += red[i];
+    }
+    return v;
+}
+
+__device__ __forceinline__ float act_of(float z, int act) {
+    return act == MIX_ACT_NONE ? z : act == MIX_ACT_SILU ? z * mix_sigmoid(z) : mix_sigmoid(z);
+}
+// Value and slope.
+__device__ __forceinline__ void act_grad(float z, int act, float *a, float *da) {
+    if (act == MIX_ACT_NONE) {
+        *a = z;
+        *da = 1.f;
+        return;
+    }
+    const float s = mix_sigmoid(z);
+    *a = act == MIX_ACT_SILU ? z * s : s;
+    *da = act == MIX_ACT_SILU ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
+}
+
+// The columns of a thread: V values from (i * TPR + lane) * V, i < NV.
+template <typename S, int V, int TPR, int NV>
+__device__ __forceinline__ void load_row(const S *p, int lane, int D, float (&f)[NV][V]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * V;
+        if (c < D) mix_load<S, V>(p + c, f[i]);
+        else
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[i][j] = 0.f;
+    }
+}
+template <typename S, int V, int TPR, int NV>
+__device__ __forceinline__ void store_row(S *p, int lane, int D, const float (&f)[NV][V]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * V;
+        if (c < D) mix_store<S, V>(p + c, f[i]);
+    }
+}
+
+template <typename S, int V, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void branch_norm_fwd_kernel(NormArgs A) {
+    constexpr int TB = TPR > 256 ? TPR : 256, ROWS = TB / TPR;
+    __shared__ float red[TB / 64];
+    const int lane = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    const bool live = row < A.R;  // a block of one row each is always live: the sums below meet all its threads
+    const int64_t at = (live ? row : 0) * A.D;
+    float r[NV][V], f[NV][V], w[NV][V];
+    load_row<S, V, TPR, NV>((const S *)A.y + at, lane, A.D, r);
+    if (A.gate) load_row<S, V, TPR, NV>((const S *)A.gate + (live ? row / A.rows_per_gate : 0) * A.D, lane, A.D, f);
+    load_row<S, V, TPR, NV>((const S *)A.w_post, lane, A.D, w);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+    const float rs = 1.f / sqrtf(row_sum<TPR>(ss, red) / A.D + A.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            r[i][j] *= rs * w[i][j];
+            if (A.gate) r[i][j] *= act_of(f[i][j], A.act);
+        }
+    if (A.x) {
+        load_row<S, V, TPR, NV>((const S *)A.x + at, lane, A.D, f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[i][j] = fmaf(A.alpha, r[i][j], f[i][j]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[i][j] *= A.alpha;
+    }
+    if (live) store_row<S, V, TPR, NV>((S *)A.r + at, lane, A.D, r);
+    if (A.stats && live && lane == 0) A.stats[row] = rs;
+    if (!A.w_next) return;
+    load_row<S, V, TPR, NV>((const S *)A.w_next, lane, A.D, w);
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if ((i * TPR + lane) * V < A.D) ss = fmaf(r[i][j], r[i][j], ss);
+    const float rn = 1.f / sqrtf(row_sum<TPR>(ss, red) / A.D + A.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) r[i][j] *= rn * w[i][j];
+    if (live) store_row<S, V, TPR, NV>((S *)A.h + at, lane, A.D, r);
+    if (A.stats && live && lane == 0) A.stats[A.R + row] = rn;
+}
+
+// The block's sum of each column over the rows it held side by side, to p[D].
+template <int V, int TPR, int NV>
+__device__ __forceinline__ void block_sums(float (&s)[NV][V], float *p, int lane, int D) {
+    if constexpr (TPR >= 256) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + lane) * V;
+            if (c < D) mix_store<float, V>(p + c, s[i]);
+        }
+    } else {
+        __shared__ float all[4][NV * TPR * V];  // one line a wavefront
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+#pragma unroll
+                for (int m = TPR; m < 64; m <<= 1) s[i][j] += __shfl_xor(s[i][j], m, 64);
+                if ((threadIdx.x & 63) < TPR) all[threadIdx.x >> 6][(i * TPR + lane) * V + j] = s[i][j];
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < D; c += 256) p[c] = (all[0][c] + all[1][c]) + (all[2][c] + all[3][c]);
+        __syncthreads();
+    }
+}
+
+// dr += rstd(r) (e - rn mean(e rn)), e = dh w_next;  dx = dr
+// du = alpha act(gate) dr;  dgate = alpha act'(gate) dr u
+// dy = rstd(y) (e - yn mean(e yn)), e = du w_post
+// r is built again from x and y: the rounded r would cost digits, and x is
+// the same number of bytes.
+template <typename S, int V, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void branch_norm_bwd_kernel(NormArgs A) {
+    constexpr int TB = TPR > 256 ? TPR : 256, ROWS = TB / TPR;
+    __shared__ float red[TB / 64];
+    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int64_t group = blockIdx.x / A.per_group;
+    const int part = blockIdx.x % A.per_group;
+    // gate rows of their own: the run of rows of one group is all rows
+    const int64_t span = A.G == A.R ? A.R : A.rows_per_gate, base = group * span;
+    const int64_t each = ((span + A.per_group - 1) / A.per_group + ROWS - 1) / ROWS * ROWS;
+    const int64_t first = part * each, last = first + each < span ? first + each : span;
+    const bool per_row = A.gate && A.G == A.R;
+    float sp[NV][V], sg[NV][V], sn[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sp[i][j] = sg[i][j] = sn[i][j] = 0.f;
+    for (int64_t o = first; o < last; o += ROWS) {
+        const bool live = o + sub < last;
+        const int64_t row = base + (live ? o + sub : o), at = row * A.D;
+        float y[NV][V], g[NV][V], d[NV][V], w[NV][V];
+        const float rs = A.stats[row];
+        load_row<S, V, TPR, NV>((const S *)A.y + at, lane, A.D, y);
+        load_row<S, V, TPR, NV>((const S *)A.w_post, lane, A.D, w);
+        if (A.gate) load_row<S, V, TPR, NV>((const S *)A.gate + (per_row ? row : group) * A.D, lane, A.D, g);
+        if (A.dr) load_row<S, V, TPR, NV>((const S *)A.dr + at, lane, A.D, d);
+        else
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) d[i][j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[i][j] *= rs;
+        if (A.w_next && A.dh) {
+            const float rn = A.stats[A.R + row];
+            float x[NV][V], e[NV][V], wn[NV][V];
+            if (A.x) load_row<S, V, TPR, NV>((const S *)A.x + at, lane, A.D, x);
+            load_row<S, V, TPR, NV>((const S *)A.dh + at, lane, A.D, e);
+            load_row<S, V, TPR, NV>((const S *)A.w_next, lane, A.D, wn);
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float u = y[i][j] * w[i][j];
+                    if (A.gate) u *= act_of(g[i][j], A.act);
+                    x[i][j] = (A.x ? fmaf(A.alpha, u, x[i][j]) : A.alpha * u) * rn;
+                    if (live) sn[i][j] = fmaf(e[i][j], x[i][j], sn[i][j]);
+                    e[i][j] *= wn[i][j];
+                    dot = fmaf(e[i][j], x[i][j], dot);
+                }
+            dot = row_sum<TPR>(dot, red) / A.D;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) d[i][j] = fmaf(rn, e[i][j] - x[i][j] * dot, d[i][j]);
+        }
+        if (A.dx && live) store_row<S, V, TPR, NV>((S *)A.dx + at, lane, A.D, d);
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float e = A.alpha * d[i][j];
+                if (A.gate) {
+                    float a, da;
+                    act_grad(g[i][j], A.act, &a, &da);
+                    g[i][j] = e * y[i][j] * w[i][j] * da;
+                    if (live) sg[i][j] += g[i][j];
+                    e *= a;
+                }
+                if (live) sp[i][j] = fmaf(e, y[i][j], sp[i][j]);
+                e *= w[i][j];
+                dot = fmaf(e, y[i][j], dot);
+                d[i][j] = e;
+            }
+        if (per_row && live) store_row<S, V, TPR, NV>((S *)A.dgate + at, lane, A.D, g);
+        dot = row_sum<TPR>(dot, red) / A.D;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[i][j] = rs * (d[i][j] - y[i][j] * dot);
+        if (live) store_row<S, V, TPR, NV>((S *)A.dy + at, lane, A.D, d);
+    }
+    block_sums<V, TPR, NV>(sp, A.part + (int64_t)blockIdx.x * A.D, lane, A.D);
+    const int64_t plane = (int64_t)gridDim.x * A.D;
+    if (A.w_next) block_sums<V, TPR, NV>(sn, A.part + plane + (int64_t)blockIdx.x * A.D, lane, A.D);
+    if (A.gate && !per_row) block_sums<V, TPR, NV>(sg, A.part + 2 * plane + (int64_t)blockIdx.x * A.D, lane, A.D);
+}
+
+// Sums of the blocks' partial sums for one output row of D columns: 64
+// columns a block, four runs of rows side by side, in a fixed order.
+// blockIdx.y: 0 w_post, 1 w_next, 2.. gate row y - 2.
+template <typename S>
+__global__ __launch_bounds__(256) void branch_norm_sum_kernel(NormArgs A) {
+    __shared__ float sum[4][64];
+    const int64_t plane = (int64_t)A.blocks * A.D;
+    const int what = blockIdx.y < 2 ? blockIdx.y : 2;
+    S *out = what == 0 ? (S *)A.dw_post : what == 1 ? (S *)A.dw_next : (S *)A.dgate;
+    if (!out || (what == 2 && A.G == A.R)) return;
+    const int64_t group = what == 2 ? blockIdx.y - 2 : 0;
+    const int n = what == 2 ? A.per_group : A.blocks;
+    const float *p = A.part + what * plane + group * A.per_group * A.D;
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < A.D)
+        for (int t = q; t < n; t += 4) s += p[(int64_t)t * A.D + c];
+    sum[q][lane] = s;
+    __syncthreads();
+    if (q || c >= A.D) return;
+    out[group * A.D + c] = mix_out<S>((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+}
+
+// Threads of a row: the fewest that hold it in at most four loads each.
+template <int V>
+int threads_of(int D) {
+    int t = 16;
+    while (t < 1024 && (int64_t)t * V * (V == 1 ? 4 : 2) < D) t *= 4;
+    return t;  // 16, 64, 256, 1024
+}
+int rows_of(int tpr) { return tpr >= 256 ? 1 : 256 / tpr; }
+
+template <typename S, int V, int TPR, int NV>
+hipError_t run_fwd(const NormArgs &a, hipStream_t st) {
+    const int rows = rows_of(TPR);
+    hipLaunchKernelGGL((branch_norm_fwd_kernel<S, V, TPR, NV>), dim3((unsigned)((a.R + rows - 1) / rows)),
+                       dim3(TPR > 256 ? TPR : 256), 0, st, a);
+    return hipGetLastError();
+}
+template <typename S, int V, int TPR, int NV>
+hipError_t run_bwd(const NormArgs &a, hipStream_t st) {
+    if (a.R) {
+        hipLaunchKernelGGL((branch_norm_bwd_kernel<S, V, TPR, NV>), dim3(a.blocks), dim3(TPR > 256 ? TPR : 256), 0, st,
+                           a);
+        if (const hipError_t e = hipGetLastError()) return e;
+    }
+    const unsigned gates = a.gate && a.G != a.R ? (unsigned)a.G : 0;
+    hipLaunchKernelGGL((branch_norm_sum_kernel<S>), dim3((a.D + 63) / 64, 2 + gates), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename S, int V, bool BWD>
+hipError_t norm_width(const NormArgs &a, hipStream_t st) {
+    constexpr int N4 = V == 1 ? 32 : 4;  // 1024 threads hold 32768 values
+#define MIX_NORM_RUN(TPR, NV) (BWD ? run_bwd<S, V, TPR, NV>(a, st) : run_fwd<S, V, TPR, NV>(a, st))
+    switch (threads_of<V>(a.D)) {
+        case 16: return MIX_NORM_RUN(16, (V == 1 ? 4 : 2));
+        case 64: return MIX_NORM_RUN(64, (V == 1 ? 4 : 2));
+        case 256: return MIX_NORM_RUN(256, (V == 1 ? 4 : 2));
+        default: return MIX_NORM_RUN(1024, (V == 4 ? 8 : N4));
+    }
+#undef MIX_NORM_RUN
+}
+
+template <typename S, bool BWD>
+hipError_t norm_typed(const NormArgs &a, hipStream_t st) {
+    constexpr int V = 16 / sizeof(S);
+    bool vec = a.D % V == 0;
+    for (const void *p : {a.x, a.y, a.w_post, a.gate, a.w_next, a.dr, a.dh, (const void *)a.r, (const void *)a.h,
+                          (const void *)a.dx, (const void *)a.dy, (const void *)a.dgate})
+        vec = vec && (uintptr_t)p % 16 == 0;
+    return vec ? norm_width<S, V, BWD>(a, st) : norm_width<S, 1, BWD>(a, st);
+}
+
+}  // namespace
+
+// Blocks of the backward pass: as many as the 256 CUs hold, each with rows of
+// one gate row only, and never more than rows.
+void branch_norm_bwd_plan(int64_t R, int D, int64_t G, int *per_group, int *blocks) {
+    const int64_t groups = G == R ? 1 : G;
+    const int64_t span = groups ? R / groups : 0;
+    int64_t per = (1024 + groups - 1) / (groups ? groups : 1);
+    const int64_t most = (span + 15) / 16 > 256 ? (span + 15) / 16 : span;  // at least 16 rows a block in long runs
+    per = per > most ? most : per;
+    *per_group = (int)(per < 1 ? 1 : per);
+    *blocks = (int)(*per_group * (groups ? groups : 1));
+}
+
+hipError_t launch_branch_norm_fwd(const NormArgs &a, int dtype, hipStream_t st) {
+    if (!a.R) return hipSuccess;
+    if (dtype == CONV_DTYPE_FP32) return norm_typed<float, false>(a, st);
+    if (dtype == CONV_DTYPE_FP16) return norm_typed<_Float16, false>(a, st);
+    return norm_typed<uint16_t, false>(a, st);
+}
+
+hipError_t launch_branch_norm_bwd(const NormArgs &a, int dtype, hipStream_t st) {
+    if (dtype == CONV_DTYPE_FP32) return norm_typed<float, true>(a, st);
+    if (dtype == CONV_DTYPE_FP16) return norm_typed<_Float16, true>(a, st);
+    return norm_typed<uint16_t, true>(a, st);
+}
+
+}  // namespace convlower

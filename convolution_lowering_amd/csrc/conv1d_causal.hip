@@ -1,0 +1,453 @@
+// Short depthwise causal convolution along packed sequences, its gradients
+// and its single-token form.
+//
+//   z[t,c] = bias[c] + sum_j w[c,j] x[t - (W-1) + j, c],   y = act(z)
+//
+// Two reads and writes per element against 2 W + 4 operations: HBM bound.  A
+// thread owns V channels (16 bytes) and walks along the tokens of one tile
+// with the last W-1 inputs in registers, so x is read once but for the W-1
+// tokens before a tile.  The token index is the same for a whole block, so
+// finding sequences costs scalar work only.
+#include <algorithm>
+
+#include "mixer_internal.h"
+
+namespace convlower {
+namespace {
+
+constexpr int kAhead = 4;  // tokens whose loads are issued together
+
+template <int WT>
+__device__ __forceinline__ int width_of(const Conv1dArgs &a) {
+    return WT < MIX_CONV1D_MAX_WIDTH ? WT : a.W;
+}
+
+// Weights of V channels as w[tap][channel], taps past the width zero.
+template <typename S, int V, int WT>
+__device__ __forceinline__ void load_taps(const S *w, int c0, int W, float (&wt)[WT][V]) {
+#pragma unroll
+    for (int j = 0; j < WT; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) wt[j][i] = j < W ? mix_f32(w[(int64_t)(c0 + i) * W + j]) : 0.f;
+}
+
+// hist[d-1] = the input d tokens before t in sequence [a, ..), from its state
+// or zero before a.
+template <typename S, int V, int WT>
+__device__ __forceinline__ void load_hist(const Conv1dArgs &A, int n, int64_t a, int64_t t, int c0, int W,
+                                          float (&hist)[WT][V]) {
+#pragma unroll
+    for (int d = 1; d < WT; ++d) {
+        const int64_t p = t - d;
+#pragma unroll
+        for (int i = 0; i < V; ++i) hist[d - 1][i] = 0.f;
+        if (d < W) {
+            if (p >= a) mix_load<S, V>((const S *)A.x + p * A.xs + c0, hist[d - 1]);
+            else if (A.state) {
+                const int64_t row = W - 1 + (p - a);  // negative only where cu_seqlens is out of order
+                mix_load<S, V>((const S *)A.state + ((int64_t)n * (W - 1) + (row < 0 ? 0 : row)) * A.D + c0, hist[d - 1]);
+            }
+        }
+    }
+}
+
+template <int V, int WT>
+__device__ __forceinline__ void push(float (&hist)[WT][V], const float (&x)[V]) {
+#pragma unroll
+    for (int d = WT - 1; d > 0; --d)
+#pragma unroll
+        for (int i = 0; i < V; ++i) hist[d][i] = hist[d - 1][i];
+#pragma unroll
+    for (int i = 0; i < V; ++i) hist[0][i] = x[i];
+}
+
+// z of one token: taps past the width are left out, not multiplied by zero.
+template <int V, int WT>
+__device__ __forceinline__ void taps(const float (&wt)[WT][V], const float (&b)[V], const float (&hist)[WT][V],
+                                     const float (&x)[V], int W, float (&z)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = b[i];
+#pragma unroll
+    for (int d = WT - 1; d >= 0; --d) {
+        if (d >= W) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            // weight of the input d tokens back
+            float w = wt[WT - 1 - d][i];
+            if (WT == MIX_CONV1D_MAX_WIDTH) {
+#pragma unroll
+                for (int j = 0; j < WT; ++j) w = j == W - 1 - d ? wt[j][i] : w;
+            }
+            z[i] = fmaf(w, d ? hist[d - 1][i] : x[i], z[i]);
+        }
+    }
+}
+
+template <typename S, int V, int WT>
+__global__ __launch_bounds__(256) void conv1d_fwd_kernel(Conv1dArgs A) {
+    const int W = width_of<WT>(A);
+    const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * V;
+    if (c >= A.D) return;
+    const int c0 = (int)c;
+    if ((int)blockIdx.x >= A.tiles) {  // the blocks past the tiles: one sequence's last inputs each
+        const int n = blockIdx.x - A.tiles;
+        int64_t a, e;
+        seq_range(A.s, n, &a, &e);
+        for (int j = 0; j < W - 1; ++j) {
+            const int64_t at = e - a - (W - 1) + j;
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = 0.f;
+            if (at >= 0) mix_load<S, V>((const S *)A.x + (a + at) * A.xs + c0, f);
+            else if (A.state) mix_load<S, V>((const S *)A.state + ((int64_t)n * (W - 1) + (W - 1 + at)) * A.D + c0, f);
+            mix_store<S, V>((S *)A.state_out + ((int64_t)n * (W - 1) + j) * A.D + c0, f);
+        }
+        return;
+    }
+    float wt[WT][V], b[V], hist[WT][V];
+    load_taps<S, V, WT>((const S *)A.w, c0, W, wt);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = A.bias ? mix_f32(((const S *)A.bias)[c0 + i]) : 0.f;
+    int64_t t = (int64_t)blockIdx.x * A.tile;
+    const int64_t t1 = t + A.tile < A.s.T ? t + A.tile : A.s.T;
+    int n = seq_of(A.s, t);
+    int64_t a, e;
+    seq_range(A.s, n, &a, &e);
+    load_hist<S, V, WT>(A, n, a, t, c0, W, hist);
+    for (; t < t1; t += kAhead) {
+        float x[kAhead][V];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (t + u < t1) mix_load<S, V>((const S *)A.x + (t + u) * A.xs + c0, x[u]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (t + u >= t1) break;
+            if (t + u >= e && n + 1 < A.s.N) {  // the next sequence that holds a token
+                n = seq_of(A.s, t + u);
+                seq_range(A.s, n, &a, &e);
+                load_hist<S, V, WT>(A, n, a, t + u, c0, W, hist);
+            }
+            float z[V];
+            taps<V, WT>(wt, b, hist, x[u], W, z);
+            if (A.act == MIX_ACT_SILU)
+#pragma unroll
+                for (int i = 0; i < V; ++i) z[i] *= mix_sigmoid(z[i]);
+            mix_store<S, V>((S *)A.y + (t + u) * A.D + c0, z);
+            push<V, WT>(hist, x[u]);
+        }
+    }
+}
+
+// dz of token t, whose inputs before it are in hist.
+template <typename S, int V, int WT>
+__device__ __forceinline__ void grad_z(const Conv1dArgs &A, const float (&wt)[WT][V], const float (&b)[V],
+                                       const float (&hist)[WT][V], const float (&x)[V], int64_t t, int c0, int W,
+                                       float (&dz)[V]) {
+    mix_load<S, V>((const S *)A.dy + t * A.dys + c0, dz);
+    if (A.act == MIX_ACT_SILU) {
+        float z[V];
+        taps<V, WT>(wt, b, hist, x, W, z);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float s = mix_sigmoid(z[i]);
+            dz[i] *= s * (1.f + z[i] * (1.f - s));
+        }
+    }
+}
+
+// dx[t] = sum_d w[W-1-d] dz[t+d]: a thread walks along its tile (and W-1
+// tokens past it), with the last inputs and the unfinished dx in registers.
+// dw and dbias of the tile go to `part`, summed over the tiles afterwards.
+template <typename S, int V, int WT>
+__global__ __launch_bounds__(256) void conv1d_bwd_kernel(Conv1dArgs A) {
+    const int W = width_of<WT>(A);
+    const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * V;
+    if (c >= A.D) return;
+    const int c0 = (int)c;
+    float wt[WT][V], b[V], hist[WT][V], x[V], dz[V];
+    load_taps<S, V, WT>((const S *)A.w, c0, W, wt);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = A.bias ? mix_f32(((const S *)A.bias)[c0 + i]) : 0.f;
+    if ((int)blockIdx.x >= A.tiles) {  // the blocks past the tiles: one sequence's state gradient each
+        const int n = blockIdx.x - A.tiles;
+        int64_t a, e;
+        seq_range(A.s, n, &a, &e);
+        float ds[WT][V];
+#pragma unroll
+        for (int j = 0; j < WT; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) ds[j][i] = 0.f;
+        load_hist<S, V, WT>(A, n, a, a, c0, W, hist);
+#pragma unroll
+        for (int p = 0; p < WT - 1; ++p) {  // token a + p reaches the state rows j >= p
+            if (p >= W - 1 || a + p >= e) continue;
+            mix_load<S, V>((const S *)A.x + (a + p) * A.xs + c0, x);
+            grad_z<S, V, WT>(A, wt, b, hist, x, a + p, c0, W, dz);
+            push<V, WT>(hist, x);
+#pragma unroll
+            for (int j = 0; j < WT - 1; ++j)
+                if (j >= p && j < W - 1)  // input a - (W-1) + j meets tap j - p
+#pragma unroll
+                    for (int i = 0; i < V; ++i) ds[j][i] = fmaf(wt[j - p < 0 ? 0 : j - p][i], dz[i], ds[j][i]);
+        }
+#pragma unroll
+        for (int j = 0; j < WT - 1; ++j) {
+            if (j >= W - 1) continue;
+            if (A.dstate_out && j >= e - a) {  // a short sequence hands part of its state on
+                float f[V];
+                mix_load<S, V>((const S *)A.dstate_out + ((int64_t)n * (W - 1) + j - (e - a)) * A.D + c0, f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) ds[j][i] += f[i];
+            }
+            mix_store<S, V>((S *)A.dstate + ((int64_t)n * (W - 1) + j) * A.D + c0, ds[j]);
+        }
+        return;
+    }
+    float dw[WT][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < WT; ++j) dw[j][i] = 0.f;
+    }
+    const int64_t t0 = (int64_t)blockIdx.x * A.tile;
+    const int64_t t1 = t0 + A.tile < A.s.T ? t0 + A.tile : A.s.T;
+    int n = seq_of(A.s, t0);
+    for (int64_t s0 = t0; s0 < t1;) {  // the part of the tile that lies in one sequence
+        int64_t a, e;
+        seq_range(A.s, n, &a, &e);
+        if (n + 1 == A.s.N && e < t1) e = t1;  // tokens past the last sequence's end belong to it
+        const int64_t s1 = e < t1 ? e : t1;
+        if (s1 > s0) {
+            load_hist<S, V, WT>(A, n, a, s0, c0, W, hist);
+            float acc[WT][V];  // acc[d]: dx of token t - d as far as it is summed
+#pragma unroll
+            for (int d = 0; d < WT; ++d)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[d][i] = 0.f;
+            for (int64_t t = s0; t < s1 + W - 1; ++t) {
+#pragma unroll
+                for (int d = WT - 1; d > 0; --d)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[d][i] = acc[d - 1][i];
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[0][i] = 0.f;
+                if (t < e) {
+                    mix_load<S, V>((const S *)A.x + t * A.xs + c0, x);
+                    grad_z<S, V, WT>(A, wt, b, hist, x, t, c0, W, dz);
+#pragma unroll
+                    for (int d = 0; d < WT; ++d) {
+                        if (d >= W) continue;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            float w = wt[WT - 1 - d][i];
+                            if (WT == MIX_CONV1D_MAX_WIDTH) {
+#pragma unroll
+                                for (int j = 0; j < WT; ++j) w = j == W - 1 - d ? wt[j][i] : w;
+                            }
+                            acc[d][i] = fmaf(w, dz[i], acc[d][i]);
+                        }
+                    }
+                    if (t < s1) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) db[i] += dz[i];
+#pragma unroll
+                        for (int d = 0; d < WT; ++d)  // dw[d]: the tap d tokens back
+#pragma unroll
+                            for (int i = 0; i < V; ++i)
+                                if (d < W) dw[d][i] = fmaf(dz[i], d ? hist[d - 1 < 0 ? 0 : d - 1][i] : x[i], dw[d][i]);
+                    }
+                    push<V, WT>(hist, x);
+                }
+                const int64_t o = t - (W - 1);
+                if (o >= s0) {
+                    float f[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        f[i] = acc[WT - 1][i];
+                        if (WT == MIX_CONV1D_MAX_WIDTH)
+#pragma unroll
+                            for (int d = 0; d < WT; ++d) f[i] = d == W - 1 ? acc[d][i] : f[i];
+                    }
+                    if (A.dstate_out && o >= e - (W - 1)) {
+                        float g[V];
+                        mix_load<S, V>((const S *)A.dstate_out + ((int64_t)n * (W - 1) + o - (e - (W - 1))) * A.D + c0,
+                                       g);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) f[i] += g[i];
+                    }
+                    mix_store<S, V>((S *)A.dx + o * A.D + c0, f);
+                }
+            }
+            s0 = s1;
+        }
+        if (++n >= A.s.N) break;
+    }
+    float *p = A.part + (int64_t)blockIdx.x * (W + 1) * A.D + c0;
+#pragma unroll
+    for (int d = 0; d < WT; ++d)
+        if (d < W)
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[(int64_t)d * A.D + i] = dw[d][i];
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[(int64_t)W * A.D + i] = db[i];
+}
+
+// Partial sums over the tiles in a fixed order: 64 columns of [W+1][D] a
+// block, four runs of tiles side by side.
+template <typename S>
+__global__ __launch_bounds__(256) void conv1d_bwd_sum_kernel(Conv1dArgs A) {
+    __shared__ float sum[4][64];
+    const int64_t cols = (int64_t)(A.W + 1) * A.D;
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (i < cols)
+        for (int t = q; t < A.tiles; t += 4) s += A.part[(int64_t)t * cols + i];
+    sum[q][lane] = s;
+    __syncthreads();
+    if (q || i >= cols) return;
+    s = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+    const int d = (int)(i / A.D);
+    const int64_t c = i - (int64_t)d * A.D;
+    if (d < A.W) ((S *)A.dw)[c * A.W + (A.W - 1 - d)] = mix_out<S>(s);
+    else if (A.dbias) ((S *)A.dbias)[c] = mix_out<S>(s);
+}
+
+template <typename S, int V>
+__global__ __launch_bounds__(64) void conv1d_step_kernel(const S *x, int64_t xs, const S *w, const S *bias, S *pool,
+                                                         const int32_t *slots, S *y, int P, int D, int W, int act) {
+    const int64_t c = ((int64_t)blockIdx.y * 64 + threadIdx.x) * V;
+    const int r = blockIdx.x;
+    if (c >= D) return;
+    const int c0 = (int)c;
+    const int slot = slots ? slots[r] : r;
+    float z[V], f[V];
+    if (slot < 0 || slot >= P) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = 0.f;
+        mix_store<S, V>(y + (int64_t)r * D + c0, z);
+        return;
+    }
+    S *st = pool + (int64_t)slot * (W - 1) * D + c0;
+    MixVec<S, V> line[MIX_CONV1D_MAX_WIDTH];
+#pragma unroll
+    for (int j = 0; j < MIX_CONV1D_MAX_WIDTH; ++j) {
+        if (j < W - 1) line[j] = *(const MixVec<S, V> *)(st + (int64_t)j * D);
+        else if (j == W - 1) line[j] = *(const MixVec<S, V> *)(x + r * xs + c0);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = bias ? mix_f32(bias[c0 + i]) : 0.f;
+#pragma unroll
+    for (int j = 0; j < MIX_CONV1D_MAX_WIDTH; ++j)
+        if (j < W)
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = fmaf(mix_f32(w[(int64_t)(c0 + i) * W + j]), mix_f32(line[j].v[i]), z[i]);
+#pragma unroll
+    for (int j = 1; j < MIX_CONV1D_MAX_WIDTH; ++j)
+        if (j < W) *(MixVec<S, V> *)(st + (int64_t)(j - 1) * D) = line[j];
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = act == MIX_ACT_SILU ? z[i] * mix_sigmoid(z[i]) : z[i];
+    mix_store<S, V>(y + (int64_t)r * D + c0, f);
+}
+
+bool aligned16(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if ((uintptr_t)p % 16) return false;
+    return true;
+}
+
+template <typename S, int V>
+hipError_t fwd_typed(const Conv1dArgs &a, hipStream_t st) {
+    const int cb = (a.D + 256 * V - 1) / (256 * V);
+    const dim3 grid(a.tiles + (a.state_out && a.W > 1 ? a.s.N : 0), cb);
+    if (!grid.x) return hipSuccess;
+    switch (a.W) {
+        case 2: hipLaunchKernelGGL((conv1d_fwd_kernel<S, V, 2>), grid, dim3(256), 0, st, a); break;
+        case 3: hipLaunchKernelGGL((conv1d_fwd_kernel<S, V, 3>), grid, dim3(256), 0, st, a); break;
+        case 4: hipLaunchKernelGGL((conv1d_fwd_kernel<S, V, 4>), grid, dim3(256), 0, st, a); break;
+        default: hipLaunchKernelGGL((conv1d_fwd_kernel<S, V, 8>), grid, dim3(256), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
+template <typename S, int V>
+hipError_t bwd_typed(const Conv1dArgs &a, hipStream_t st) {
+    const int cb = (a.D + 256 * V - 1) / (256 * V);
+    const dim3 grid(a.tiles + (a.dstate && a.W > 1 ? a.s.N : 0), cb);
+    if (grid.x) {
+        switch (a.W) {
+            case 2: hipLaunchKernelGGL((conv1d_bwd_kernel<S, V, 2>), grid, dim3(256), 0, st, a); break;
+            case 3: hipLaunchKernelGGL((conv1d_bwd_kernel<S, V, 3>), grid, dim3(256), 0, st, a); break;
+            case 4: hipLaunchKernelGGL((conv1d_bwd_kernel<S, V, 4>), grid, dim3(256), 0, st, a); break;
+            default: hipLaunchKernelGGL((conv1d_bwd_kernel<S, V, 8>), grid, dim3(256), 0, st, a);
+        }
+        if (const hipError_t e = hipGetLastError()) return e;
+    }
+    const int64_t cols = (int64_t)(a.W + 1) * a.D;
+    hipLaunchKernelGGL((conv1d_bwd_sum_kernel<S>), dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <typename S>
+hipError_t step_typed(const void *x, int64_t xs, const void *w, const void *bias, void *pool, const int32_t *slots,
+                      void *y, int R, int P, int D, int W, int act, hipStream_t st) {
+    constexpr int V = 16 / sizeof(S);
+    if (D % V == 0 && xs % V == 0 && aligned16({x, pool, y}))
+        hipLaunchKernelGGL((conv1d_step_kernel<S, V>), dim3(R, (D + 64 * V - 1) / (64 * V)), dim3(64), 0, st,
+                           (const S *)x, xs, (const S *)w, (const S *)bias, (S *)pool, slots, (S *)y, P, D, W, act);
+    else
+        hipLaunchKernelGGL((conv1d_step_kernel<S, 1>), dim3(R, (D + 63) / 64), dim3(64), 0, st, (const S *)x, xs,
+                           (const S *)w, (const S *)bias, (S *)pool, slots, (S *)y, P, D, W, act);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Tokens of a forward tile: the W-1 tokens before a tile are read again, so
+// long tiles, but enough blocks to fill the 256 CUs.
+static int fwd_tile(int64_t T, int D) {
+    const int64_t cb = (D + 2047) / 2048;
+    int tile = 64;
+    while (tile > 8 && (T + tile - 1) / tile * cb < 2048) tile /= 2;
+    return tile;
+}
+
+// Tokens of a backward tile: each leaves (W+1) D partial sums.
+int conv1d_bwd_tile(int64_t T, int D) {
+    const int64_t cb = (D + 2047) / 2048;
+    int tile = 128;
+    while (tile > 32 && (T + tile - 1) / tile * cb < 1024) tile /= 2;
+    return tile;
+}
+
+hipError_t launch_conv1d_fwd(Conv1dArgs a, int dtype, hipStream_t st) {
+    a.tile = fwd_tile(a.s.T, a.D);
+    a.tiles = (int)((a.s.T + a.tile - 1) / a.tile);
+    const int V = dtype == CONV_DTYPE_FP32 ? 4 : 8;
+    const bool vec = a.D % V == 0 && a.xs % V == 0 && aligned16({a.x, a.state, a.y, a.state_out});
+    if (dtype == CONV_DTYPE_FP32) return vec ? fwd_typed<float, 4>(a, st) : fwd_typed<float, 1>(a, st);
+    if (dtype == CONV_DTYPE_FP16) return vec ? fwd_typed<_Float16, 8>(a, st) : fwd_typed<_Float16, 1>(a, st);
+    return vec ? fwd_typed<uint16_t, 8>(a, st) : fwd_typed<uint16_t, 1>(a, st);
+}
+
+hipError_t launch_conv1d_bwd(Conv1dArgs a, int dtype, hipStream_t st) {
+    a.tile = conv1d_bwd_tile(a.s.T, a.D);
+    a.tiles = (int)((a.s.T + a.tile - 1) / a.tile);
+    const int V = dtype == CONV_DTYPE_FP32 ? 4 : 8;
+    const bool vec = a.D % V == 0 && a.xs % V == 0 && a.dys % V == 0 &&
+                     aligned16({a.x, a.state, a.dy, a.dstate_out, a.dx, a.dstate});
+    if (dtype == CONV_DTYPE_FP32) return vec ? bwd_typed<float, 4>(a, st) : bwd_typed<float, 1>(a, st);
+    if (dtype == CONV_DTYPE_FP16) return vec ? bwd_typed<_Float16, 8>(a, st) : bwd_typed<_Float16, 1>(a, st);
+    return vec ? bwd_typed<uint16_t, 8>(a, st) : bwd_typed<uint16_t, 1>(a, st);
+}
+
+hipError_t launch_conv1d_step(const void *x, int64_t xs, const void *w, const void *bias, void *pool,
+                              const int32_t *slots, void *y, int R, int P, int D, int W, int act, int dtype,
+                              hipStream_t st) {
+    if (dtype == CONV_DTYPE_FP32) return step_typed<float>(x, xs, w, bias, pool, slots, y, R, P, D, W, act, st);
+    if (dtype == CONV_DTYPE_FP16) return step_typed<_Float16>(x, xs, w, bias, pool, slots, y, R, P, D, W, act, st);
+    return step_typed<uint16_t>(x, xs, w, bias, pool, slots, y, R, P, D, W, act, st);
+}
+
+}  // namespace convlower
