@@ -39,6 +39,9 @@ def _units():
              ("mixer_api", "mixer_api.cpp", []),
              ("conv1d_causal", "conv1d_causal.hip", []),
              ("delta_tokens", "delta_tokens.hip", []),
+             ("delta_prep", "delta_prep.hip", []),
+             ("delta_scan", "delta_scan.hip", []),
+             ("delta_grad", "delta_grad.hip", []),
              ("branch_norm", "branch_norm.hip", [])]
     for dt, tag in ((1, "bf16"), (2, "f16"), (0, "f32")):  # IGEMM_DTYPE: 0 fp32, 1 bf16, 2 fp16
         for feed in range(10):  # the Feed values of conv_internal.h

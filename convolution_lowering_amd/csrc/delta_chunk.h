@@ -1,0 +1,169 @@
+// Shared by the kernels of the chunked gated delta rule.
+//
+// A chunk is C = 64 tokens of one sequence.  With gam the running sum of g
+// inside the chunk, G_ij = exp(gam_i - gam_j) and S the state before it:
+//
+//   L_ij = (k_i . k_j) G_ij, i > j        P_ij = (q_i . k_j) G_ij, i >= j
+//   Z = V - diag(e^gam) K S               what the state alone predicts wrongly
+//   Y = (1 + L diag(b))^-1 Z              v - S'k at each token's turn
+//   U = diag(b) Y
+//   O = diag(e^gam) Q S + P U
+//   S' = e^gam_C S + K' diag(e^(gam_C - gam)) U
+//
+// and backwards, with X the gradient of U as an output, G that of S':
+//
+//   X = P' dO + diag(e^(gam_C - gam)) K G
+//   E = (1 + L' diag(b))^-1 X             the gradient of U in full
+//   dZ = diag(b) E = dV,   db_i = Y_i . E_i
+//   dS = e^gam_C G + Q' diag(e^gam) dO - K' diag(e^gam) dZ
+//
+// (q holds the scale; q and k their norms where asked for.)
+//
+// Products run on the f16 matrix cores, with float32 results.  An operand
+// that is a bf16 or f16 input is exact there: each token's row is moved by a
+// power of two to the middle of f16's range.  Any other operand is split in
+// two, x = hi + lo, each 11 bits, after moving its column (or the whole
+// tile) by a power of two: 22 bits, so that the float32 state and the float32
+// gradients keep float32 accuracy; hi alone (or bf16) would leave three digits
+// in the state.  A product of two split operands leaves out lo * lo.  float32
+// inputs are split as well.
+//
+// The 16x16x32 product takes column (row) k of its left (right) operand from
+// lane group k / 8.  Results lie otherwise: row 4 g + r in group g.  So that
+// a result can be the next right operand without leaving its lanes, every
+// left operand's columns are stored in the order in which results lie:
+// place (g, j) of the 32-column step s holds column
+//   kappa(s, g, j) = 32 s + (j < 4 ? 4 g + j : 16 + 4 g + j - 4).
+#pragma once
+
+#include "mixer_internal.h"
+
+namespace convlower {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kC = 64;        // tokens of a chunk
+constexpr int kFrag = 512;    // f16 values of one operand fragment: 64 lanes x 8
+constexpr int kTri = 6;       // fragments of a triangular 64 x 64 operand: 16 rows x 32 columns each
+constexpr int kSlab = 64;     // value columns the gradient kernel takes at once
+
+// Fragment of a lower (upper) triangular left operand: rows 16 mt.., columns 32 s..
+__device__ __forceinline__ constexpr int tri_lower(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }
+__device__ __forceinline__ constexpr int tri_upper(int mt, int s) { return mt < 2 ? 2 * mt + s : mt + 2; }
+
+// Everything the kernels hand one another.  A "slot" is a chunk's place:
+// sequence n's chunk c is slot start(n) / 64 + n + c, which needs no sums over
+// the sequences' lengths (T / 64 + N slots hold any T tokens of N sequences).
+struct DeltaBuf {
+    int slots, dkp, dvp, ks;  // dk in 64 or 128 columns, dv in whole slabs, dkp / 32
+    int planes;               // 2: q and k in two halves (float32 inputs)
+    _Float16 *k, *kt, *q, *qt;  // [slots][Hk][planes][64 * dkp]: K, K', Q, Q' as left operands
+    _Float16 *t, *p;            // [slots][Hv][2][kTri * kFrag]: the inverse and P, hi and lo
+    float *rowk;                // [slots][Hk][4][64]: factor of k's row, k's norm, the same of q
+    float *rowf;                // [slots][Hv][4][64]: f1 = rho_k e^gam, f2 = rho_q e^gam, f3 = rho_k e^(gam_C - gam), b
+    float *scal;                // [slots][Hv][4]: e^gam_C, 1 / (the inverse's scale), 1 / (P's scale)
+    float *gam;                 // [slots][Hv][64] doubles: gam (gradients only)
+    float *S, *Y;               // saved: [slots][Hv][dkp][dvp], [slots][Hv][64][dvp]
+    float *G, *E;               // gradients: the same shapes
+};
+
+hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaBuf &b, bool grad, int dtype, hipStream_t st);
+hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaBuf &b, bool grad, int dtype, hipStream_t st);
+hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaBuf &b, int dtype, hipStream_t st);
+
+struct Chunk {
+    int n, c;       // sequence, chunk in it
+    int64_t t0;     // first token
+    int len;        // tokens, 0: the slot is not used
+};
+__device__ __forceinline__ int64_t slot_base(const Seqs &s, int n) {
+    return s.cu ? seq_start(s, n) / kC + n : (int64_t)n * ((s.each + kC - 1) / kC);
+}
+__device__ __forceinline__ Chunk chunk_of(const Seqs &s, int slot) {
+    int lo = 0, hi = s.N - 1;
+    if (!s.cu) {
+        const int64_t per = (s.each + kC - 1) / kC;
+        lo = per ? (int)(slot / per) : 0;
+        if (lo > hi) lo = hi;
+    } else {
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (slot_base(s, mid) <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+    }
+    Chunk r;
+    r.n = lo;
+    int64_t a, e;
+    seq_range(s, lo, &a, &e);
+    const int64_t c = slot - slot_base(s, lo);
+    r.c = (int)c;
+    r.t0 = a + c * kC;
+    const int64_t left = c < 0 ? 0 : e - r.t0;
+    r.len = left < 0 ? 0 : left > kC ? kC : (int)left;
+    return r;
+}
+
+// The power of two that brings m to [2^t, 2^(t+1)), and its inverse.
+__device__ __forceinline__ float pow2_to(float m, int t, float *inv) {
+    int e = 254 + t - (int)((__float_as_uint(m) >> 23) & 255);
+    e = e < 3 ? 3 : e > 251 ? 251 : e;
+    *inv = __uint_as_float((uint32_t)(254 - e) << 23);
+    return __uint_as_float((uint32_t)e << 23);
+}
+constexpr int kTop = 11;     // split operands: largest value in [2^11, 2^12)
+constexpr int kRowTop = 8;   // rows of q and k: products of 128 of them and a split operand stay far below f32's end
+
+struct Split {
+    f16x8 hi, lo;
+};
+__device__ __forceinline__ Split split8(f32x4 a, f32x4 b, float scale) {
+    Split r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float x = a[j] * scale, y = b[j] * scale;
+        r.hi[j] = (_Float16)x;
+        r.hi[j + 4] = (_Float16)y;
+        r.lo[j] = (_Float16)(x - (float)r.hi[j]);
+        r.lo[j + 4] = (_Float16)(y - (float)r.hi[j + 4]);
+    }
+    return r;
+}
+__device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma2(f16x8 a, const Split &b, f32x4 c) { return mma(a, b.hi, mma(a, b.lo, c)); }
+__device__ __forceinline__ f32x4 mma3(f16x8 ah, f16x8 al, const Split &b, f32x4 c) {
+    return mma(ah, b.hi, mma(ah, b.lo, mma(al, b.hi, c)));
+}
+// Left operand at p (its second half `half` values on where it has one).
+template <bool SPLIT>
+__device__ __forceinline__ f32x4 mma_in(const _Float16 *p, int half, const Split &b, f32x4 c) {
+    const f16x8 a = *(const f16x8 *)p;
+    if constexpr (SPLIT) return mma3(a, *(const f16x8 *)(p + half), b, c);
+    return mma2(a, b, c);
+}
+__device__ __forceinline__ float max4(f32x4 v, float m) {
+    return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), m);
+}
+// Largest over the four lane groups: of one column of a result.
+__device__ __forceinline__ float col_max(float m) {
+    m = fmaxf(m, __shfl_xor(m, 16, 64));
+    return fmaxf(m, __shfl_xor(m, 32, 64));
+}
+// Right operands of 32 rows each from a result of N tiles of 16 rows, moved
+// column by column; returns the inverse of the column's factor.
+template <int N>
+__device__ __forceinline__ float split_cols(const f32x4 (&v)[N], Split (&out)[N / 2]) {
+    float m = 0.f, inv;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = max4(v[i], m);
+    const float sc = pow2_to(col_max(m), kTop, &inv);
+#pragma unroll
+    for (int s = 0; s < N / 2; ++s) out[s] = split8(v[2 * s], v[2 * s + 1], sc);
+    return inv;
+}
+
+}  // namespace convlower

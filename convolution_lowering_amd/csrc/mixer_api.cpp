@@ -2,7 +2,7 @@
 // Every check is on the host, before the first launch.
 #include <initializer_list>
 
-#include "mixer_internal.h"
+#include "delta_chunk.h"
 
 namespace convlower {
 namespace {
@@ -50,6 +50,82 @@ conv_status_t norm_sizes(int64_t R, int D, int64_t G, bool gate, float eps, mix_
     if (act != MIX_ACT_NONE && act != MIX_ACT_SILU && act != MIX_ACT_SIGMOID) return CONV_ERR_INVALID_ARG;
     if (gate && (G < 1 || (R % G && R) || (G > R && R))) return CONV_ERR_INVALID_ARG;
     if (D > MIX_NORM_MAX_WIDTH || R > kMaxTokens || (gate && G != R && G > 60000)) return CONV_ERR_UNSUPPORTED;
+    return CONV_OK;
+}
+
+// Checks and fills in what delta_rule_fwd and _bwd share.
+conv_status_t delta_inputs(const void *q, int64_t qs, const void *k, int64_t ks, const void *v, int64_t vs,
+                           const float *g, const void *beta, const int32_t *cu, int64_t T, int N, int Hk, int Hv,
+                           int dk, int dv, float scale, int qk_norm, conv_dtype_t dtype, conv_dtype_t beta_dtype,
+                           DeltaArgs *a) {
+    conv_status_t st = delta_sizes(Hk, Hv, dk, dv, dtype, beta_dtype);
+    if (st != CONV_OK) return st;
+    if ((st = seqs_of(cu, T, N, &a->s)) != CONV_OK) return st;
+    if (T && (!q || !k || !v || !g || !beta)) return CONV_ERR_INVALID_ARG;
+    if (!pointers_ok({}, {q, k, v}, bytes_of(dtype)) || !pointers_ok({}, {beta}, bytes_of(beta_dtype)) ||
+        !pointers_ok({}, {g}, 4))
+        return CONV_ERR_INVALID_ARG;
+    if (qs < (int64_t)Hk * dk || ks < (int64_t)Hk * dk || vs < (int64_t)Hv * dv) return CONV_ERR_INVALID_ARG;
+    a->q = q, a->qs = qs, a->k = k, a->ks = ks, a->v = v, a->vs = vs, a->g = g, a->beta = beta;
+    a->Hk = Hk, a->Hv = Hv, a->dk = dk, a->dv = dv, a->qk_norm = qk_norm != 0, a->scale = scale;
+    a->beta_f32 = beta_dtype == CONV_DTYPE_FP32;
+    return CONV_OK;
+}
+
+// The buffers of the chunked form: PART_FWD and PART_BWD are workspaces,
+// PART_SAVED goes from the forward call to the backward one.
+enum Part { PART_FWD, PART_BWD, PART_SAVED };
+
+DeltaBuf delta_buf(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype) {
+    DeltaBuf b{};
+    b.slots = (int)(T / kC + N);
+    b.dkp = dk <= 64 ? 64 : 128;
+    b.ks = b.dkp / 32;
+    b.dvp = (dv + kSlab - 1) / kSlab * kSlab;
+    b.planes = dtype == CONV_DTYPE_FP32 ? 2 : 1;
+    return b;
+}
+// Gives b its part of the buffer at p; returns the bytes (p null: only that).
+size_t lay_out(DeltaBuf *b, int Hk, int Hv, Part part, void *p) {
+    size_t at = 0;
+    auto take = [&](size_t values, size_t each) {
+        void *r = p ? (char *)p + at : nullptr;
+        at += (values * each + 255) / 256 * 256;
+        return r;
+    };
+    const size_t kh = (size_t)b->slots * Hk, vh = (size_t)b->slots * Hv;
+    const size_t state = vh * b->dkp * b->dvp, tokens = vh * kC * b->dvp;
+    if (part == PART_SAVED) {
+        b->S = (float *)take(state, 4);
+        b->Y = (float *)take(tokens, 4);
+        return at;
+    }
+    const size_t rows = kh * b->planes * kC * b->dkp, tri = vh * 2 * kTri * kFrag;
+    b->k = (_Float16 *)take(rows, 2);
+    b->kt = (_Float16 *)take(rows, 2);
+    (part == PART_FWD ? b->q : b->qt) = (_Float16 *)take(rows, 2);
+    b->t = (_Float16 *)take(tri, 2);
+    b->p = (_Float16 *)take(tri, 2);
+    b->rowk = (float *)take(kh * 4 * kC, 4);
+    b->rowf = (float *)take(vh * 4 * kC, 4);
+    b->scal = (float *)take(vh * 4, 4);
+    if (part == PART_BWD) {
+        b->gam = (float *)take(vh * kC, 8);
+        b->G = (float *)take(state, 4);
+        b->E = (float *)take(tokens, 4);
+    }
+    return at;
+}
+conv_status_t delta_bytes(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype, Part part,
+                          size_t *bytes_out) {
+    if (!bytes_out || T < 0 || N < 1) return CONV_ERR_INVALID_ARG;
+    const conv_status_t st = delta_sizes(Hk, Hv, dk, dv, dtype, dtype);
+    if (st != CONV_OK) return st;
+    // blocks are counted in 32 bits
+    if (T > kMaxTokens || T / kC + N > kMaxTokens || (int64_t)N * Hv * (MIX_DELTA_MAX_DV / 16) > kMaxTokens)
+        return CONV_ERR_UNSUPPORTED;
+    DeltaBuf b = delta_buf(T, N, Hk, Hv, dk, dv, dtype);
+    *bytes_out = lay_out(&b, Hk, Hv, part, nullptr);
     return CONV_OK;
 }
 
@@ -147,11 +223,17 @@ conv_status_t delta_rule_step(const void *q, int64_t q_stride, const void *k, in
 
 conv_status_t delta_rule_fwd_workspace_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
                                             size_t *bytes_out) {
-    if (!bytes_out || T < 0 || N < 1) return CONV_ERR_INVALID_ARG;
-    const conv_status_t st = delta_sizes(Hk, Hv, dk, dv, dtype, dtype);
-    if (st != CONV_OK) return st;
-    *bytes_out = 0;
-    return CONV_OK;
+    return delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_FWD, bytes_out);
+}
+
+conv_status_t delta_rule_saved_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
+                                    size_t *bytes_out) {
+    return delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_SAVED, bytes_out);
+}
+
+conv_status_t delta_rule_bwd_workspace_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
+                                            size_t *bytes_out) {
+    return delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_BWD, bytes_out);
 }
 
 conv_status_t delta_rule_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -160,41 +242,55 @@ conv_status_t delta_rule_fwd(const void *q, int64_t q_stride, const void *k, int
                              int dk, int dv, float scale, int qk_norm, conv_dtype_t dtype, conv_dtype_t beta_dtype,
                              conv_stream_t stream, void *workspace, size_t workspace_bytes, void *saved,
                              size_t saved_bytes) {
-    conv_status_t st = delta_sizes(Hk, Hv, dk, dv, dtype, beta_dtype);
-    if (st != CONV_OK) return st;
     DeltaArgs a{};
-    if ((st = seqs_of(cu_seqlens, T, N, &a.s)) != CONV_OK) return st;
-    if ((int64_t)N * Hv > kMaxTokens) return CONV_ERR_UNSUPPORTED;
-    if (T && (!pointers_ok({q, k, v, o}, {}, bytes_of(dtype)) || !pointers_ok({beta}, {}, bytes_of(beta_dtype)) ||
-              !pointers_ok({g}, {}, 4)))
+    conv_status_t st = delta_inputs(q, q_stride, k, k_stride, v, v_stride, g, beta, cu_seqlens, T, N, Hk, Hv, dk, dv,
+                                    scale, qk_norm, dtype, beta_dtype, &a);
+    if (st != CONV_OK) return st;
+    if ((T && !o) || !pointers_ok({}, {o}, bytes_of(dtype)) || !pointers_ok({}, {state, state_out}, 4) ||
+        !pointers_ok({}, {workspace, saved}, 16))
         return CONV_ERR_INVALID_ARG;
-    if (!pointers_ok({}, {state, state_out}, 4)) return CONV_ERR_INVALID_ARG;
-    if (q_stride < (int64_t)Hk * dk || k_stride < (int64_t)Hk * dk || v_stride < (int64_t)Hv * dv)
+    size_t need = 0, keep = 0;
+    if ((st = delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_FWD, &need)) != CONV_OK) return st;
+    if ((st = delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_SAVED, &keep)) != CONV_OK) return st;
+    if (!workspace || workspace_bytes < need || (saved && saved_bytes < keep)) return CONV_ERR_WORKSPACE;
+    a.o = o, a.state = state, a.state_out = state_out;
+    DeltaBuf b = delta_buf(T, N, Hk, Hv, dk, dv, dtype);
+    lay_out(&b, Hk, Hv, PART_FWD, workspace);
+    if (saved) lay_out(&b, Hk, Hv, PART_SAVED, saved);
+    hipError_t e = launch_delta_prep(a, b, false, dtype, (hipStream_t)stream);
+    if (e == hipSuccess) e = launch_delta_scan(a, b, false, dtype, (hipStream_t)stream);
+    return hip_status(e);
+}
+
+conv_status_t delta_rule_bwd(const void *d_o, int64_t do_stride, const float *dstate_out, const void *q,
+                             int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                             const float *g, const void *beta, const int32_t *cu_seqlens, const void *saved,
+                             size_t saved_bytes, void *dq, void *dk_out, void *dv_out, float *dg, void *dbeta,
+                             float *dstate, int64_t T, int N, int Hk, int Hv, int dk, int dv, float scale,
+                             int qk_norm, conv_dtype_t dtype, conv_dtype_t beta_dtype, conv_stream_t stream,
+                             void *workspace, size_t workspace_bytes) {
+    DeltaArgs a{};
+    conv_status_t st = delta_inputs(q, q_stride, k, k_stride, v, v_stride, g, beta, cu_seqlens, T, N, Hk, Hv, dk, dv,
+                                    scale, qk_norm, dtype, beta_dtype, &a);
+    if (st != CONV_OK) return st;
+    if (T && (!d_o || !dq || !dk_out || !dv_out || !dg || !dbeta)) return CONV_ERR_INVALID_ARG;
+    if (do_stride < (int64_t)Hv * dv || !pointers_ok({}, {d_o, dq, dk_out, dv_out}, bytes_of(dtype)) ||
+        !pointers_ok({}, {dbeta}, bytes_of(beta_dtype)) || !pointers_ok({}, {dg, dstate, dstate_out}, 4) ||
+        !pointers_ok({}, {workspace, saved}, 16))
         return CONV_ERR_INVALID_ARG;
-    (void)workspace, (void)workspace_bytes, (void)saved, (void)saved_bytes;
-    a.q = q, a.qs = q_stride, a.k = k, a.ks = k_stride, a.v = v, a.vs = v_stride, a.g = g, a.beta = beta, a.o = o;
-    a.state = state, a.state_out = state_out;
-    a.Hk = Hk, a.Hv = Hv, a.dk = dk, a.dv = dv, a.qk_norm = qk_norm != 0, a.scale = scale;
-    a.beta_f32 = beta_dtype == CONV_DTYPE_FP32;
-    return hip_status(launch_delta_tokens(a, dtype, (hipStream_t)stream));
-}
-
-conv_status_t delta_rule_saved_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
-                                    size_t *bytes_out) {
-    return delta_rule_fwd_workspace_size(T, N, Hk, Hv, dk, dv, dtype, bytes_out);
-}
-
-conv_status_t delta_rule_bwd_workspace_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
-                                            size_t *bytes_out) {
-    return delta_rule_fwd_workspace_size(T, N, Hk, Hv, dk, dv, dtype, bytes_out);
-}
-
-// The chunked form is not here yet.
-conv_status_t delta_rule_bwd(const void *, int64_t, const float *, const void *, int64_t, const void *, int64_t,
-                             const void *, int64_t, const float *, const void *, const int32_t *, const void *, size_t,
-                             void *, void *, void *, float *, void *, float *, int64_t, int, int, int, int, int, float,
-                             int, conv_dtype_t, conv_dtype_t, conv_stream_t, void *, size_t) {
-    return CONV_ERR_UNSUPPORTED;
+    size_t need = 0, keep = 0;
+    if ((st = delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_BWD, &need)) != CONV_OK) return st;
+    if ((st = delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_SAVED, &keep)) != CONV_OK) return st;
+    if (!workspace || workspace_bytes < need || !saved || saved_bytes < keep) return CONV_ERR_WORKSPACE;
+    a.d_o = d_o, a.dos = do_stride, a.dstate_out = dstate_out;
+    a.dq = dq, a.dk_out = dk_out, a.dv_out = dv_out, a.dg = dg, a.dbeta = dbeta, a.dstate = dstate;
+    DeltaBuf b = delta_buf(T, N, Hk, Hv, dk, dv, dtype);
+    lay_out(&b, Hk, Hv, PART_BWD, workspace);
+    lay_out(&b, Hk, Hv, PART_SAVED, const_cast<void *>(saved));
+    hipError_t e = launch_delta_prep(a, b, true, dtype, (hipStream_t)stream);
+    if (e == hipSuccess) e = launch_delta_scan(a, b, true, dtype, (hipStream_t)stream);
+    if (e == hipSuccess) e = launch_delta_grad(a, b, dtype, (hipStream_t)stream);
+    return hip_status(e);
 }
 
 conv_status_t branch_norm_fwd(const void *x, const void *y, const void *w_post, const void *gate, const void *w_next,

@@ -237,6 +237,220 @@ def test_delta_rule_step_padding_requests():
     assert torch.equal(pool[0], before[0]) and not torch.equal(pool[1], before[1])
 
 
+def _delta_grads(case, seed=7, fast=1.0):
+    lens, Hk, Hv, dk, dv, dtype, has_state, packed, b32 = case
+    q, k, v, gate, beta, g = _delta_inputs(lens, Hk, Hv, dk, dv, dtype, packed=packed, beta32=b32, seed=seed, fast=fast)
+    cu = _cu(lens)
+    state = _randn(g, len(lens), Hv, dk, dv) * 0.3 if has_state else None
+    do = _randn(g, sum(lens), Hv, dv).to(q.dtype)
+    ds = _randn(g, len(lens), Hv, dk, dv) * 0.3 if has_state else None
+    return q, k, v, gate, beta, cu, state, do, ds
+
+
+@pytest.mark.parametrize("norm", [True, False], ids=["norm", "raw"])
+@pytest.mark.parametrize("case", DELTA, ids=[f"{c[5]}-{c[1]}x{c[2]}-{c[3]}x{c[4]}-{sum(c[0])}tok" for c in DELTA])
+def test_delta_rule_gradients(case, norm):
+    _say("delta bwd", case, norm)
+    q, k, v, gate, beta, cu, state, do, ds = _delta_grads(case)
+    if not norm:  # keys no longer than one, as the rule needs
+        k = (k.float() * 0.7 / k.float().norm(dim=-1).amax().clamp(min=1e-3)).to(k.dtype)
+    more = dict(cu_seqlens=cu, scale=0.3, qk_norm=norm)
+    o, s, saved = mixer.delta_rule_fwd(q, k, v, gate, beta, state=state, want_state=True, save=True, **more)
+    leaves = [z.double().requires_grad_(True) for z in (q, k, v, gate, beta)]
+    rstate = None if state is None else state.double().requires_grad_(True)
+    ro, rs = om.delta_rule(*leaves, cu.tolist(), rstate, 0.3, norm)
+    _near(o, ro.detach(), "o")
+    _near(s, rs.detach(), "state")
+    total = (ro * do.double()).sum()
+    if ds is not None:
+        total = total + (rs * ds.double()).sum()
+    ref = torch.autograd.grad(total, leaves + ([rstate] if rstate is not None else []))
+    got = mixer.delta_rule_bwd(do, q, k, v, gate, beta, saved, dstate_out=ds, want_dstate=state is not None, **more)
+    # one key of one value: with the norm, q and k are +-1 and their gradients the eps of the norm away from nothing
+    names = ("dq", "dk", "dv", "dg", "dbeta", "dstate")
+    for name, x, y in zip(names, got, ref):
+        if case[3] == 1 and norm and name in ("dq", "dk"):
+            assert torch.isfinite(x.float()).all()
+            continue
+        _near(x, y, name, 2e-5)  # forward and backward in series
+    if state is None:
+        assert got[5] is None
+
+
+def test_delta_rule_strong_and_cleared_decays():
+    """Decays from none to a cleared state (-inf) side by side."""
+    case = ([150, 64, 3], 2, 4, 128, 64, "fp32", True, True, True)
+    q, k, v, gate, beta, cu, state, do, ds = _delta_grads(case)
+    r = torch.rand(gate.shape, generator=_gen(3), device=DEV)
+    gate = torch.where(r < 0.1, -60.0, torch.where(r < 0.2, 0.0, torch.where(r < 0.25, -300.0, gate)))
+    soft = gate.clone()
+    gate = torch.where((r > 0.5) & (r < 0.53), -float("inf"), gate)
+    hard = torch.where((r > 0.5) & (r < 0.53), -5000.0, soft)  # e^-5000 is zero in 64 bits as well
+    more = dict(cu_seqlens=cu, scale=1.0, qk_norm=True)
+    o, s, saved = mixer.delta_rule_fwd(q, k, v, gate, beta, state=state, want_state=True, save=True, **more)
+    leaves = [z.double().requires_grad_(True) for z in (q, k, v, hard, beta, state)]
+    ro, rs = om.delta_rule(*leaves[:5], cu.tolist(), leaves[5], 1.0, True)
+    _near(o, ro.detach(), "o")
+    _near(s, rs.detach(), "state")
+    ref = torch.autograd.grad((ro * do.double()).sum() + (rs * ds.double()).sum(), leaves)
+    got = mixer.delta_rule_bwd(do, q, k, v, gate, beta, saved, dstate_out=ds, want_dstate=True, **more)
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta", "dstate"), got, ref):
+        _near(x, y, name, 2e-5)
+
+
+def test_delta_rule_repeated_keys():
+    """Every key of a chunk the same: the chunk's matrix is as far from 1 as
+    it gets, with beta = 1 and no decay."""
+    g = _gen(4)
+    k = _randn(g, 1, 1, 128).expand(100, 1, 128).contiguous()
+    q, v = _randn(g, 100, 1, 128), _randn(g, 100, 1, 128)
+    gate, beta = torch.zeros(100, 1, device=DEV), torch.ones(100, 1, device=DEV)
+    o, s, _ = mixer.delta_rule_fwd(q, k, v, gate, beta, qk_norm=True, want_state=True)
+    ro, rs = _delta_ref(q, k, v, gate, beta, None, None, 128 ** -0.5, True)
+    _near(o, ro, "o")
+    _near(s, rs, "state")
+
+
+@pytest.mark.parametrize("mag", [1e-6, 1.0, 3e4])
+def test_delta_rule_magnitudes(mag):
+    """Values, states and keys far from one: the powers of two that move
+    operands into f16's range."""
+    g = _gen(6)
+    q, k, v = (_randn(g, 90, 2, 64).bfloat16() for _ in range(3))
+    v, k = v * mag, k * mag
+    gate, beta = -torch.rand(90, 2, generator=g, device=DEV), torch.sigmoid(_randn(g, 90, 2)).bfloat16()
+    state = _randn(g, 1, 2, 64, 64) * mag
+    o, s, _ = mixer.delta_rule_fwd(q, k, v, gate, beta, state=state, qk_norm=True, want_state=True)
+    ro, rs = _delta_ref(q, k, v, gate, beta, None, state, 0.125, True)
+    _near(o, ro, "o")
+    _near(s, rs, "state")
+
+
+def test_delta_rule_sequences_cut_and_batched():
+    """[B, L] is the packed call; a sequence cut anywhere, its state handed
+    on, continues (in the token form too)."""
+    q, k, v, gate, beta, g = _delta_inputs([300], 2, 4, 128, 128, "bf16")
+    args = (q, k, v, gate, beta)
+    o, s, _ = mixer.delta_rule_fwd(*args, qk_norm=True, want_state=True)
+    ro, rs = _delta_ref(*args, None, None, 128 ** -0.5, True)
+    head = [z[:131].contiguous() for z in args]
+    o1, s1, _ = mixer.delta_rule_fwd(*head, qk_norm=True, want_state=True)
+    o2, s2, _ = mixer.delta_rule_fwd(*[z[131:] for z in args[:3]], gate[131:], beta[131:], state=s1, qk_norm=True,
+                                     want_state=True)
+    _near(torch.cat((o1, o2)), ro, "cut")
+    _near(s2, rs, "cut state")
+    pool = s1.clone()
+    one = [z[131:134].contiguous()[None] for z in args]
+    ot = mixer.delta_rule_step(*one, pool, qk_norm=True)
+    _near(ot[0], ro[131:134], "continued by tokens")
+    batched = [z.unflatten(0, (3, 100)) for z in args]
+    ob, sb, _ = mixer.delta_rule_fwd(*batched, qk_norm=True, want_state=True)
+    op, sp, _ = mixer.delta_rule_fwd(*args, cu_seqlens=_cu([100, 100, 100]), qk_norm=True, want_state=True)
+    assert torch.equal(ob.flatten(0, 1), op) and torch.equal(sb, sp)
+
+
+def test_delta_rule_without_tokens():
+    q = torch.zeros(0, 1, 64, device=DEV, dtype=torch.bfloat16)
+    g = torch.zeros(0, 1, device=DEV)
+    state = torch.randn(2, 1, 64, 64, device=DEV)
+    o, s, saved = mixer.delta_rule_fwd(q, q, q, g, g, cu_seqlens=_cu([0, 0]), state=state, want_state=True, save=True)
+    assert o.shape == (0, 1, 64) and torch.equal(s, state)
+    got = mixer.delta_rule_bwd(q, q, q, q, g, g, saved, cu_seqlens=_cu([0, 0]), dstate_out=state, want_dstate=True)
+    assert torch.equal(got[5], state)
+
+
+def test_delta_rule_twice_the_same_bits():
+    case = ([200, 31], 2, 4, 128, 128, "bf16", True, True, False)
+    q, k, v, gate, beta, cu, state, do, ds = _delta_grads(case)
+    runs = []
+    for _ in range(2):
+        o, s, saved = mixer.delta_rule_fwd(q, k, v, gate, beta, cu_seqlens=cu, state=state, qk_norm=True,
+                                           want_state=True, save=True)
+        runs.append((o, s, *mixer.delta_rule_bwd(do, q, k, v, gate, beta, saved, cu_seqlens=cu, qk_norm=True,
+                                                 dstate_out=ds, want_dstate=True)))
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+# ------------------------------------------------------------------ all together
+
+
+def _block(x, p, fn):
+    """conv -> delta rule -> gated head norm -> residual and next norm."""
+    T = x.shape[0]
+    m, _ = fn.conv1d_causal(x, p["w"], p["b"], cu_seqlens=p["cu"])
+    q, k, v = m.split((128, 128, 256), -1)
+    o, _ = fn.delta_rule(q.unflatten(1, (2, 64)), k.unflatten(1, (2, 64)), v.unflatten(1, (4, 64)), p["g"], p["beta"],
+                         cu_seqlens=p["cu"], qk_norm=True)
+    u, _ = fn.branch_norm(None, o.reshape(T * 4, 64), p["wn"], p["z"], act="silu")
+    return fn.branch_norm(p["x0"], u.reshape(T, 256), p["wp"], p["gate"], p["w2"], alpha=0.5)
+
+
+def _block_params(T, t, g):
+    r = lambda *s: _randn(g, *s).to(t)
+    return dict(w=r(512, 4), b=r(512), cu=_cu([T - 40, 40]), g=-torch.rand(T, 4, generator=g, device=DEV),
+                beta=torch.sigmoid(_randn(g, T, 4)).to(t), wn=r(64), z=r(T * 4, 64), x0=r(T, 256), wp=r(256),
+                gate=r(1, 256), w2=r(256))
+
+
+def test_autograd_through_the_operators_together():
+    """Gradients of a whole mixer by autograd against those of the 64-bit
+    definitions: float32, whose five steps in series stay within 1e-4."""
+    g = _gen(9)
+    p = _block_params(150, torch.float32, g)
+    x = _randn(g, 150, 512)
+    names = ["w", "b", "g", "beta", "wn", "z", "x0", "wp", "gate", "w2"]
+    leaves = [x.requires_grad_(True)] + [p[n].requires_grad_(True) for n in names]
+    r, h = _block(x, p, mixer)
+    dr, dh = _randn(g, 150, 256), _randn(g, 150, 256)
+    got = torch.autograd.grad((r, h), leaves, (dr, dh))
+
+    class Ref:
+        conv1d_causal = staticmethod(lambda x, w, b, cu_seqlens: om.conv1d_causal(x, w, b, cu_seqlens, None, "silu"))
+        delta_rule = staticmethod(lambda q, k, v, g, b, cu_seqlens, qk_norm:
+                                  om.delta_rule(q, k, v, g, b, cu_seqlens, None, 64 ** -0.5, True))
+        branch_norm = staticmethod(lambda x, y, wp, gate, wn=None, alpha=1.0, act="none":
+                                   om.branch_norm(x, y, wp, gate, wn, alpha, 1e-6, act))
+
+    pd = {n: z.detach().double().requires_grad_(n in names) if z.is_floating_point() else z.tolist() for n, z in p.items()}
+    xd = x.detach().double().requires_grad_(True)
+    rr, rh = _block(xd, pd, Ref)
+    ref = torch.autograd.grad((rr, rh), [xd] + [pd[n] for n in names], (dr.double(), dh.double()))
+    _near(r.detach(), rr.detach(), "r", 1e-4)
+    _near(h.detach(), rh.detach(), "h", 1e-4)
+    for n, a, b in zip(["x"] + names, got, ref):
+        _near(a, b, n, 1e-4)
+
+
+def test_operators_on_another_stream_and_in_a_graph():
+    """The same bits on a side stream, and from a captured graph replayed with
+    other inputs between eager work."""
+    g = _gen(10)
+    p = _block_params(200, torch.bfloat16, g)
+    x = _randn(g, 200, 512).bfloat16()
+    xs = [_randn(g, 200, 512).bfloat16() for _ in range(3)]
+    with torch.no_grad():
+        ref = [tuple(z.clone() for z in _block(y, p, mixer)) for y in xs]
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            r, h = _block(xs[0], p, mixer)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(r, ref[0][0]) and torch.equal(h, ref[0][1])
+        y, _ = mixer.conv1d_causal_fwd(x, p["w"], p["b"], cu_seqlens=p["cu"], stream=side)
+        side.synchronize()
+        assert torch.equal(y, mixer.conv1d_causal_fwd(x, p["w"], p["b"], cu_seqlens=p["cu"])[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            r, h = _block(x, p, mixer)
+        for i, y in enumerate(xs):
+            x.copy_(y)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(r, ref[i][0]) and torch.equal(h, ref[i][1])
+            _block(xs[0], p, mixer)
+
+
 # ------------------------------------------------------------------- branch norm
 
 NORM = [  # rows, D, gate rows, act, x, w_next, dtype
