@@ -36,6 +36,7 @@
 //   kappa(s, g, j) = 32 s + (j < 4 ? 4 g + j : 16 + 4 g + j - 4).
 #pragma once
 
+#include "igemm_impl.h"
 #include "mixer_internal.h"
 
 namespace convlower {
@@ -49,31 +50,38 @@ constexpr int kFrag = 512;    // f16 values of one operand fragment: 64 lanes x 
 constexpr int kTri = 6;       // fragments of a triangular 64 x 64 operand: 16 rows x 32 columns each
 constexpr int kSlab = 64;     // value columns the gradient kernel takes at once
 
-// Fragment of a lower (upper) triangular left operand: rows 16 mt.., columns 32 s..
+// Fragment of a lower triangular left operand: rows 16 mt.., columns 32 s..
 __device__ __forceinline__ constexpr int tri_lower(int mt, int s) { return mt < 2 ? mt : 2 * mt - 2 + s; }
-__device__ __forceinline__ constexpr int tri_upper(int mt, int s) { return mt < 2 ? 2 * mt + s : mt + 2; }
 
 // Everything the kernels hand one another.  A "slot" is a chunk's place:
 // sequence n's chunk c is slot start(n) / 64 + n + c, which needs no sums over
 // the sequences' lengths (T / 64 + N slots hold any T tokens of N sequences).
+// Matrices in "result order" lie as the lanes hold them: [tile of 16 columns]
+// [tile of 16 rows][lane][4 rows].
 struct DeltaBuf {
-    int slots, dkp, dvp, ks;  // dk in 64 or 128 columns, dv in whole slabs, dkp / 32
-    int planes;               // 2: q and k in two halves (float32 inputs)
-    _Float16 *k, *kt, *q, *qt;  // [slots][Hk][planes][64 * dkp]: K, K', Q, Q' as left operands
-    _Float16 *t, *p;            // [slots][Hv][2][kTri * kFrag]: the inverse and P, hi and lo
-    float *rowk;                // [slots][Hk][4][64]: factor of k's row, k's norm, the same of q
-    float *rowf;                // [slots][Hv][4][64]: f1 = rho_k e^gam, f2 = rho_q e^gam, f3 = rho_k e^(gam_C - gam), b
-    float *scal;                // [slots][Hv][4]: e^gam_C, 1 / (the inverse's scale), 1 / (P's scale)
-    float *gam;                 // [slots][Hv][64] doubles: gam (gradients only)
-    float *S, *Y;               // saved: [slots][Hv][dkp][dvp], [slots][Hv][64][dvp]
-    float *G, *E;               // gradients: the same shapes
+    int slots, dkp, dvp;  // dk in 64 or 128 columns, dv in whole slabs
+    int planes;           // 2: q and k in two halves (float32 inputs)
+    _Float16 *kq;  // [slots][Hk][K, Q][planes][64 * dkp] as left operands
+    char *tp;      // [slots][Hv] of kTpBytes: the inverse, P, and the rows' factors
+    char *tpg;     // the same for the way back (saved): the other inverse, P, factors
+    float *rowk;   // saved: [slots][Hk][4][64]: factor of k's row, k's norm, the same of q
+    double *gam;   // saved: [slots][Hv][64]
+    float *S, *Y;  // saved: [slots][Hv], [dkp][dvp] and [64][dvp] in result order
+    float *Smax;   // saved: [slots][Hv][dvp / 16]: largest |S| of the tile
+    float *G, *E, *Gmax;  // gradients: the same of G and E
 };
+// One chunk of one value head: 6 + 6 fragments of each triangular operand (hi,
+// lo), then four rows of 64 factors, f1 = rho_k e^gam, f2 = rho_q e^gam,
+// f3 = rho_k e^(gam_C - gam), b, and e^gam_C, 1 / (the inverse's scale),
+// 1 / (P's scale).
+constexpr int kTpRows = 4 * kTri * kFrag * 2;  // bytes before the factors
+constexpr int kTpBytes = kTpRows + 2048;
 
 hipError_t launch_delta_prep(const DeltaArgs &a, const DeltaBuf &b, bool grad, int dtype, hipStream_t st);
 hipError_t launch_delta_scan(const DeltaArgs &a, const DeltaBuf &b, bool grad, int dtype, hipStream_t st);
 hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaBuf &b, int dtype, hipStream_t st);
 
-struct Chunk {
+struct DeltaChunk {
     int n, c;       // sequence, chunk in it
     int64_t t0;     // first token
     int len;        // tokens, 0: the slot is not used
@@ -81,7 +89,7 @@ struct Chunk {
 __device__ __forceinline__ int64_t slot_base(const Seqs &s, int n) {
     return s.cu ? seq_start(s, n) / kC + n : (int64_t)n * ((s.each + kC - 1) / kC);
 }
-__device__ __forceinline__ Chunk chunk_of(const Seqs &s, int slot) {
+__device__ __forceinline__ DeltaChunk chunk_of(const Seqs &s, int slot) {
     int lo = 0, hi = s.N - 1;
     if (!s.cu) {
         const int64_t per = (s.each + kC - 1) / kC;
@@ -94,7 +102,7 @@ __device__ __forceinline__ Chunk chunk_of(const Seqs &s, int slot) {
             else hi = mid - 1;
         }
     }
-    Chunk r;
+    DeltaChunk r;
     r.n = lo;
     int64_t a, e;
     seq_range(s, lo, &a, &e);
@@ -123,11 +131,11 @@ __device__ __forceinline__ Split split8(f32x4 a, f32x4 b, float scale) {
     Split r;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float x = a[j] * scale, y = b[j] * scale;
-        r.hi[j] = (_Float16)x;
-        r.hi[j + 4] = (_Float16)y;
-        r.lo[j] = (_Float16)(x - (float)r.hi[j]);
-        r.lo[j + 4] = (_Float16)(y - (float)r.hi[j + 4]);
+        // written as fused multiply-adds, which the mixed-precision instructions do in one step each
+        r.hi[j] = (_Float16)fmaf(a[j], scale, 0.f);
+        r.hi[j + 4] = (_Float16)fmaf(b[j], scale, 0.f);
+        r.lo[j] = (_Float16)fmaf(a[j], scale, -(float)r.hi[j]);
+        r.lo[j + 4] = (_Float16)fmaf(b[j], scale, -(float)r.hi[j + 4]);
     }
     return r;
 }
@@ -153,6 +161,11 @@ __device__ __forceinline__ float col_max(float m) {
     m = fmaxf(m, __shfl_xor(m, 16, 64));
     return fmaxf(m, __shfl_xor(m, 32, 64));
 }
+__device__ __forceinline__ float tile_max(float m) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    return m;
+}
 // Right operands of 32 rows each from a result of N tiles of 16 rows, moved
 // column by column; returns the inverse of the column's factor.
 template <int N>
@@ -164,6 +177,44 @@ __device__ __forceinline__ float split_cols(const f32x4 (&v)[N], Split (&out)[N 
 #pragma unroll
     for (int s = 0; s < N / 2; ++s) out[s] = split8(v[2 * s], v[2 * s + 1], sc);
     return inv;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
+typedef __attribute__((address_space(3))) char *lds_bytes;
+
+// A left operand's fragment in LDS.
+__device__ __forceinline__ f16x8 frag_at(const char *p) { return *(const f16x8 *)(p + (threadIdx.x & 63) * 16); }
+// Where this lane reads in a fragment for its transpose: lane t of a group of
+// 16 reads columns 4 (t % 4) .. + 3 of row 4 g + t / 4 and gets column t of
+// the group's four rows.
+__device__ __forceinline__ int trans_lane() {
+    const int lane = threadIdx.x & 63, g = lane >> 4, t = lane & 15;
+    return (4 * g + (t >> 2) + 16 * (t & 3)) * 16;
+}
+// Fragment (mt, s) of the transpose: a and b hold rows 32 s.. and 32 s + 16..,
+// both their fragment of columns 32 (mt / 2)...
+__device__ __forceinline__ f16x8 trans_at(const char *a, const char *b, int mt, int tl) {
+    const int o = tl + (mt & 1) * 8;
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)((lds_bytes)(lds_ptr_t)a + o));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)((lds_bytes)(lds_ptr_t)b + o));
+    return __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// 16-byte copies into LDS, 1 KB an instruction, `units` of them shared by the
+// block's wavefronts.
+template <int NW>
+__device__ __forceinline__ void copy_in(const void *src, int units, char *dst) {
+    // the same for the whole wavefront, whatever it was computed from
+    const uint64_t p = (uint64_t)src;
+    const uint64_t u0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)p);
+    const uint64_t u1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32));
+    const __amdgpu_buffer_rsrc_t r = make_rsrc((const void *)(u0 | u1 << 32), units * 1024);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)dst, v = (threadIdx.x & 63) * 16;
+#pragma unroll
+    for (int u = 0; u < units; u += NW)
+        if (u + w < units) lds_dma16(r, v + (u + w) * 1024, d + (u + w) * 1024);
 }
 
 }  // namespace convlower

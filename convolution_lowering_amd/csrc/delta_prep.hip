@@ -2,7 +2,8 @@
 // not need the state.  A block takes one chunk of one query/key head: it puts
 // q and k in the order of the matrix cores' left operands, multiplies K K' and
 // Q K' once, and for each value head of the group forms the decays, P and the
-// inverse of the chunk's unit lower triangular matrix.
+// inverse of the chunk's unit lower triangular matrix: (1 + L diag(b))^-1 for
+// the way forward and, where gradients are wanted, (1 + diag(b) L)^-1 too.
 //
 // The inverse is built from 16 x 16 diagonal blocks (substitution, one
 // wavefront each) and joined twice: [A 0; B C]^-1 = [A' 0; -C' B A', C'].
@@ -18,7 +19,7 @@ constexpr int kLd = 68;  // floats from row to row of the 64 x 64 matrices in LD
 // Loads 16-byte pieces of row `row` (a quarter of it a thread), finds its
 // largest value and its sum of squares, and leaves it in LDS as f16.
 template <typename S, int DKP, bool SPLIT>
-__device__ __forceinline__ void load_rows(const S *src, int64_t stride, const Chunk &ch, int dk, bool vec, int norm,
+__device__ __forceinline__ void load_rows(const S *src, int64_t stride, const DeltaChunk &ch, int dk, bool vec, int norm,
                                           float scale, _Float16 *dst, float *rho, float *rnorm) {
     constexpr int Q = DKP / 4, V = 16 / sizeof(S), LD = DKP + 8;
     const int row = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * Q;
@@ -76,20 +77,6 @@ __device__ __forceinline__ f16x8 row_frag(const _Float16 *x, int mt, int s) {
     const f16x4 a = *(const f16x4 *)p, b = *(const f16x4 *)(p + 16);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// The same of the transpose: rows 16 mt.. are columns of x.
-template <int LD>
-__device__ __forceinline__ f16x8 col_frag(const _Float16 *x, int mt, int s) {
-    const int lane = threadIdx.x & 63;
-    const _Float16 *p = x + (32 * s + 4 * (lane >> 4)) * LD + 16 * mt + (lane & 15);
-    f16x8 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        r[j] = p[j * LD];
-        r[j + 4] = p[(16 + j) * LD];
-    }
-    return r;
-}
-
 // Largest |x| of a 64 x 64 matrix in LDS, to every thread (256).
 __device__ __forceinline__ float block_max(float m, float *red) {
 #pragma unroll
@@ -158,27 +145,21 @@ __device__ __forceinline__ void invert(const float *m, float *x, float *tmp) {
     __syncthreads();
 }
 
-// The triangular matrix in LDS as six left operands in two halves, or its
-// transpose.  Six wavefront-sized pieces over four wavefronts.
-template <bool TRANS>
-__device__ __forceinline__ void store_tri(const float *x, float scale, _Float16 *out) {
+// The triangular matrix in LDS as six left operands in two halves, to one or
+// two places.  Six wavefront-sized pieces over four wavefronts.
+__device__ __forceinline__ void store_tri(const float *x, float scale, char *out, char *out2) {
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     for (int f = threadIdx.x >> 6; f < kTri; f += 4) {
-        int mt, s;
-        if (TRANS) mt = f < 4 ? f / 2 : f - 2, s = f < 4 ? f % 2 : 1;
-        else mt = f < 2 ? f : f / 2 + 1, s = f < 2 ? 0 : f % 2;
-        f32x4 a, b;
-        if (TRANS) {
-            const float *p = x + (32 * s + 4 * g) * kLd + 16 * mt + r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[j] = p[j * kLd], b[j] = p[(16 + j) * kLd];
-        } else {
-            const float *p = x + (16 * mt + r) * kLd + 32 * s + 4 * g;
-            a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 16);
+        const int mt = f < 2 ? f : f / 2 + 1, s = f < 2 ? 0 : f % 2;
+        const float *p = x + (16 * mt + r) * kLd + 32 * s + 4 * g;
+        const Split v = split8(*(const f32x4 *)p, *(const f32x4 *)(p + 16), scale);
+        const int at = (f * kFrag + lane * 8) * 2;
+        *(f16x8 *)(out + at) = v.hi;
+        *(f16x8 *)(out + at + kTri * kFrag * 2) = v.lo;
+        if (out2) {
+            *(f16x8 *)(out2 + at) = v.hi;
+            *(f16x8 *)(out2 + at + kTri * kFrag * 2) = v.lo;
         }
-        const Split v = split8(a, b, scale);
-        *(f16x8 *)(out + f * kFrag + lane * 8) = v.hi;
-        *(f16x8 *)(out + (kTri + f) * kFrag + lane * 8) = v.lo;
     }
 }
 
@@ -195,14 +176,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
     __shared__ float rk[kC], nk[kC], rq[kC], nq[kC], sb[kC], red[4];
     __shared__ double sg[kC];
     const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const Chunk ch = chunk_of(A.s, slot);
+    const DeltaChunk ch = chunk_of(A.s, slot);
     if (ch.len == 0) return;
     load_rows<S, DKP, SPLIT>((const S *)A.k + (int64_t)hk * A.dk, A.ks, ch, A.dk, vec, A.qk_norm, 1.f, sk, rk, nk);
     load_rows<S, DKP, SPLIT>((const S *)A.q + (int64_t)hk * A.dk, A.qs, ch, A.dk, vec, A.qk_norm, A.scale, sq, rq, nq);
     __syncthreads();
     const int64_t head = (int64_t)slot * A.Hk + hk;
-    const int64_t at = head * PL * kC * DKP;
-    if (tid < kC) {
+    const int64_t at = head * 2 * PL * kC * DKP;
+    if (GRAD && tid < kC) {
         float *o = B.rowk + head * 4 * kC + tid;
         o[0] = rk[tid], o[kC] = nk[tid], o[2 * kC] = rq[tid], o[3 * kC] = nq[tid];
     }
@@ -212,12 +193,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
         const int64_t o = at + (int64_t)pl * kC * DKP + lane * 8;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            *(f16x8 *)(B.k + o + (w * KS + s) * kFrag) = row_frag<LD>(k, w, s);
-            if (!GRAD) *(f16x8 *)(B.q + o + (w * KS + s) * kFrag) = row_frag<LD>(q, w, s);
-        }
-        for (int f = w; f < DKP / 8; f += 4) {  // [dkp / 16][2]
-            *(f16x8 *)(B.kt + o + f * kFrag) = col_frag<LD>(k, f >> 1, f & 1);
-            if (GRAD) *(f16x8 *)(B.qt + o + f * kFrag) = col_frag<LD>(q, f >> 1, f & 1);
+            *(f16x8 *)(B.kq + o + (w * KS + s) * kFrag) = row_frag<LD>(k, w, s);
+            *(f16x8 *)(B.kq + o + PL * kC * DKP + (w * KS + s) * kFrag) = row_frag<LD>(q, w, s);
         }
     }
     {  // K K' and Q K': rows 16 w.., lower triangle
@@ -257,6 +234,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
     for (int v = 0; v < rep; ++v) {
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
+        char *tp = B.tp + vh * kTpBytes, *tpg = GRAD ? B.tpg + vh * kTpBytes : nullptr;
         if (w == 0) {
             float g = 0.f, b = 0.f;
             if (lane < ch.len) {
@@ -275,13 +253,18 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             sg[lane] = s;
             sb[lane] = b;
             const float rise = expf((float)s);
-            float *f = B.rowf + vh * 4 * kC + lane;
-            f[0] = rk[lane] * rise;
-            f[kC] = rq[lane] * rise;
-            f[2 * kC] = rk[lane] * expf((float)(all - s));
-            f[3 * kC] = b;
-            if (GRAD) ((double *)B.gam)[vh * kC + lane] = s;
-            if (lane == 0) B.scal[vh * 4] = expf((float)all);
+            const float f1 = rk[lane] * rise, f2 = rq[lane] * rise, f3 = rk[lane] * expf((float)(all - s));
+            const float last = expf((float)all);
+            auto put = [&](char *tp) {
+                float *f = (float *)(tp + kTpRows) + lane;
+                f[0] = f1, f[kC] = f2, f[2 * kC] = f3, f[3 * kC] = b;
+                if (lane == 0) f[4 * kC] = last;
+            };
+            put(tp);
+            if (GRAD) {
+                put(tpg);
+                B.gam[vh * kC + lane] = s;
+            }
         }
         __syncthreads();
         // the matrix to invert into lm, P into xi
@@ -292,7 +275,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             if (j <= i) {
                 const float d = expf((float)(sg[i] - sg[j]));
                 p = qk[i * kLd + j] * d;
-                if (j < i) l = kk[i * kLd + j] * d * (GRAD ? sb[i] : sb[j]);
+                if (j < i) l = kk[i * kLd + j] * d * sb[j];
             }
             lm[i * kLd + j] = l;
             xi[i * kLd + j] = p;
@@ -300,15 +283,27 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
         }
         float inv;
         float sc = pow2_to(block_max(mp, red), kTop, &inv);
-        store_tri<GRAD>(xi, sc, B.p + vh * 2 * kTri * kFrag);
-        if (tid == 0) B.scal[vh * 4 + 2] = inv;
-        __syncthreads();
-        invert(lm, xi, tmp);
-        mp = 0.f;
-        for (int e = tid; e < kC * kC; e += 256) mp = fmaxf(mp, fabsf(xi[(e >> 6) * kLd + (e & 63)]));
-        sc = pow2_to(block_max(mp, red), kTop, &inv);
-        store_tri<GRAD>(xi, sc, B.t + vh * 2 * kTri * kFrag);
-        if (tid == 0) B.scal[vh * 4 + 1] = inv;
+        store_tri(xi, sc, tp + kTpRows / 2, GRAD ? tpg + kTpRows / 2 : nullptr);
+        if (tid == 0) {
+            ((float *)(tp + kTpRows))[4 * kC + 2] = inv;
+            if (GRAD) ((float *)(tpg + kTpRows))[4 * kC + 2] = inv;
+        }
+        for (int way = 0; way < (GRAD ? 2 : 1); ++way) {
+            __syncthreads();
+            if (way) {  // b beside the row instead of the column
+                for (int e = tid; e < kC * kC; e += 256) {
+                    const int i = e >> 6, j = e & 63;
+                    lm[i * kLd + j] = j < i ? kk[i * kLd + j] * expf((float)(sg[i] - sg[j])) * sb[i] : 0.f;
+                }
+                __syncthreads();
+            }
+            invert(lm, xi, tmp);
+            mp = 0.f;
+            for (int e = tid; e < kC * kC; e += 256) mp = fmaxf(mp, fabsf(xi[(e >> 6) * kLd + (e & 63)]));
+            sc = pow2_to(block_max(mp, red), kTop, &inv);
+            store_tri(xi, sc, way ? tpg : tp, nullptr);
+            if (tid == 0) ((float *)((way ? tpg : tp) + kTpRows))[4 * kC + 1] = inv;
+        }
         __syncthreads();
     }
 }

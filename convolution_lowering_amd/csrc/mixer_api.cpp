@@ -72,15 +72,15 @@ conv_status_t delta_inputs(const void *q, int64_t qs, const void *k, int64_t ks,
     return CONV_OK;
 }
 
-// The buffers of the chunked form: PART_FWD and PART_BWD are workspaces,
-// PART_SAVED goes from the forward call to the backward one.
-enum Part { PART_FWD, PART_BWD, PART_SAVED };
+// The buffers of the chunked form: PART_FWD and PART_BWD are workspaces (that
+// of a forward call which saves is a part of PART_FWD), PART_SAVED goes from
+// the forward call to the backward one.
+enum Part { PART_FWD, PART_FWD_SAVING, PART_BWD, PART_SAVED };
 
 DeltaBuf delta_buf(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype) {
     DeltaBuf b{};
     b.slots = (int)(T / kC + N);
     b.dkp = dk <= 64 ? 64 : 128;
-    b.ks = b.dkp / 32;
     b.dvp = (dv + kSlab - 1) / kSlab * kSlab;
     b.planes = dtype == CONV_DTYPE_FP32 ? 2 : 1;
     return b;
@@ -94,25 +94,23 @@ size_t lay_out(DeltaBuf *b, int Hk, int Hv, Part part, void *p) {
         return r;
     };
     const size_t kh = (size_t)b->slots * Hk, vh = (size_t)b->slots * Hv;
-    const size_t state = vh * b->dkp * b->dvp, tokens = vh * kC * b->dvp;
-    if (part == PART_SAVED) {
-        b->S = (float *)take(state, 4);
-        b->Y = (float *)take(tokens, 4);
-        return at;
-    }
-    const size_t rows = kh * b->planes * kC * b->dkp, tri = vh * 2 * kTri * kFrag;
-    b->k = (_Float16 *)take(rows, 2);
-    b->kt = (_Float16 *)take(rows, 2);
-    (part == PART_FWD ? b->q : b->qt) = (_Float16 *)take(rows, 2);
-    b->t = (_Float16 *)take(tri, 2);
-    b->p = (_Float16 *)take(tri, 2);
-    b->rowk = (float *)take(kh * 4 * kC, 4);
-    b->rowf = (float *)take(vh * 4 * kC, 4);
-    b->scal = (float *)take(vh * 4, 4);
+    const size_t state = vh * b->dkp * b->dvp, tokens = vh * kC * b->dvp, tiles = vh * (b->dvp / 16);
+    const size_t kq = kh * 2 * b->planes * kC * b->dkp;
     if (part == PART_BWD) {
-        b->gam = (float *)take(vh * kC, 8);
         b->G = (float *)take(state, 4);
         b->E = (float *)take(tokens, 4);
+        b->Gmax = (float *)take(tiles, 4);
+        return at;
+    }
+    if (part == PART_FWD || part == PART_FWD_SAVING) b->tp = (char *)take(vh, kTpBytes);
+    if (part == PART_FWD || part == PART_SAVED) b->kq = (_Float16 *)take(kq, 2);
+    if (part == PART_SAVED) {
+        b->tpg = (char *)take(vh, kTpBytes);
+        b->rowk = (float *)take(kh * 4 * kC, 4);
+        b->gam = (double *)take(vh * kC, 8);
+        b->S = (float *)take(state, 4);
+        b->Y = (float *)take(tokens, 4);
+        b->Smax = (float *)take(tiles, 4);
     }
     return at;
 }
@@ -255,9 +253,9 @@ conv_status_t delta_rule_fwd(const void *q, int64_t q_stride, const void *k, int
     if (!workspace || workspace_bytes < need || (saved && saved_bytes < keep)) return CONV_ERR_WORKSPACE;
     a.o = o, a.state = state, a.state_out = state_out;
     DeltaBuf b = delta_buf(T, N, Hk, Hv, dk, dv, dtype);
-    lay_out(&b, Hk, Hv, PART_FWD, workspace);
+    lay_out(&b, Hk, Hv, saved ? PART_FWD_SAVING : PART_FWD, workspace);
     if (saved) lay_out(&b, Hk, Hv, PART_SAVED, saved);
-    hipError_t e = launch_delta_prep(a, b, false, dtype, (hipStream_t)stream);
+    hipError_t e = launch_delta_prep(a, b, saved != nullptr, dtype, (hipStream_t)stream);
     if (e == hipSuccess) e = launch_delta_scan(a, b, false, dtype, (hipStream_t)stream);
     return hip_status(e);
 }
@@ -287,8 +285,7 @@ conv_status_t delta_rule_bwd(const void *d_o, int64_t do_stride, const float *ds
     DeltaBuf b = delta_buf(T, N, Hk, Hv, dk, dv, dtype);
     lay_out(&b, Hk, Hv, PART_BWD, workspace);
     lay_out(&b, Hk, Hv, PART_SAVED, const_cast<void *>(saved));
-    hipError_t e = launch_delta_prep(a, b, true, dtype, (hipStream_t)stream);
-    if (e == hipSuccess) e = launch_delta_scan(a, b, true, dtype, (hipStream_t)stream);
+    hipError_t e = launch_delta_scan(a, b, true, dtype, (hipStream_t)stream);
     if (e == hipSuccess) e = launch_delta_grad(a, b, dtype, (hipStream_t)stream);
     return hip_status(e);
 }
