@@ -158,13 +158,24 @@ __device__ __forceinline__ float max4(f32x4 v, float m) {
 }
 // Largest over the four lane groups: of one column of a result.
 __device__ __forceinline__ float col_max(float m) {
-    m = fmaxf(m, __shfl_xor(m, 16, 64));
-    return fmaxf(m, __shfl_xor(m, 32, 64));
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const uint32_t a = __float_as_uint(m);
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, a, false, false));
+    const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
+    const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+    return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+// Largest over a wavefront.
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float m) {
+    const int x = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), CTRL, 0xf, 0xf, true);
+    return fmaxf(m, __builtin_bit_cast(float, x));
 }
 __device__ __forceinline__ float tile_max(float m) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-    return m;
+    m = dpp_max<0x121>(m);  // row_ror 1, 2, 4, 8: the 16 lanes of a group
+    m = dpp_max<0x122>(m);
+    m = dpp_max<0x124>(m);
+    return col_max(dpp_max<0x128>(m));
 }
 // Right operands of 32 rows each from a result of N tiles of 16 rows, moved
 // column by column; returns the inverse of the column's factor.
@@ -201,20 +212,20 @@ __device__ __forceinline__ f16x8 trans_at(const char *a, const char *b, int mt, 
     return __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// 16-byte copies into LDS, 1 KB an instruction, `units` of them shared by the
-// block's wavefronts.
-template <int NW>
-__device__ __forceinline__ void copy_in(const void *src, int units, char *dst) {
+// 16-byte copies into LDS, 1 KB an instruction, shared by the block's NW
+// wavefronts.
+template <int NW, int UNITS>
+__device__ __forceinline__ void copy_in(const void *src, char *dst) {
     // the same for the whole wavefront, whatever it was computed from
     const uint64_t p = (uint64_t)src;
     const uint64_t u0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)p);
     const uint64_t u1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32));
-    const __amdgpu_buffer_rsrc_t r = make_rsrc((const void *)(u0 | u1 << 32), units * 1024);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc((const void *)(u0 | u1 << 32), UNITS * 1024);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)dst, v = (threadIdx.x & 63) * 16;
+    const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)dst + w * 1024, v = (threadIdx.x & 63) * 16 + w * 1024;
 #pragma unroll
-    for (int u = 0; u < units; u += NW)
-        if (u + w < units) lds_dma16(r, v + (u + w) * 1024, d + (u + w) * 1024);
+    for (int u = 0; u < UNITS; u += NW)
+        if (u + NW <= UNITS || u + w < UNITS) lds_dma16(r, v + u * 1024, d + u * 1024);
 }
 
 }  // namespace convlower

@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
 #pragma unroll
             for (int i = 0; i < 4; ++i) *(f32x4 *)&dbs[w][16 * i + 4 * g] = dbp[i];
         __syncthreads();
-        copy_in<4>((const char *)B.kq + head * IN, IN / 1024, second);
+        copy_in<4, IN / 1024>((const char *)B.kq + head * IN, second);
         if (tid < ch.len) {
             const float db = (dbs[0][tid] + dbs[1][tid]) + (dbs[2][tid] + dbs[3][tid]);
             const int64_t th = (ch.t0 + tid) * A.Hv + h;

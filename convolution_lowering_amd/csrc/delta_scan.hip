@@ -73,49 +73,48 @@ struct Scan {
     }
     __device__ __forceinline__ void issue(const DeltaArgs &A, const DeltaBuf &B, int64_t c, const char *tp, char *lds) const {
         const int64_t slot = base + c;
-        copy_in<NW>((const char *)B.kq + (slot * A.Hk + hk) * kIn, kIn / 1024, lds);
-        copy_in<NW>(tp + (slot * A.Hv + h) * kTpBytes, kTpBytes / 1024, lds + kIn);
+        copy_in<NW, kIn / 1024>((const char *)B.kq + (slot * A.Hk + hk) * kIn, lds);
+        copy_in<NW, kTpBytes / 1024>(tp + (slot * A.Hv + h) * kTpBytes, lds + kIn);
     }
-    // Columns of a [64][..] tensor of the caller's in result order, as they
-    // lie.  Lanes past the last column keep the zeros they start with; rows
-    // past the chunk's end repeat its last one: their b, K and Q are zero.
+    // Columns of a [64][..] tensor of the caller's in result order, by buffer
+    // accesses: rows past the chunk's end and columns past the last read as
+    // zeros and are not written, being past the buffer's end.
     __device__ __forceinline__ void load(const S *p, int64_t stride, int len, uint32_t (&v)[NT][16]) const {
-        typedef typename Bits<sizeof(S)>::type U;
+        const __amdgpu_buffer_rsrc_t r = rows_of(p);
+        const int st = (int)stride * (int)sizeof(S);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            if (!live[t]) continue;
-            const U *q = (const U *)p + (tile + t) * 16 + m;
-            if (len == kC) {
-                q += (int64_t)(4 * g) * stride;
+            const int at = live[t] ? 4 * g * st + ((tile + t) * 16 + m) * (int)sizeof(S) : (int)kOutOfRange;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[t][i] = q[(16 * (i / 4) + i % 4) * stride];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int row = 16 * (i / 4) + 4 * g + i % 4;
-                    v[t][i] = q[(row < len ? row : len - 1) * stride];
-                }
+            for (int i = 0; i < 16; ++i) {
+                const int row = 16 * (i / 4) + i % 4;  // and 4 g
+                const int o = len == kC || row + 4 * g < len ? at : (int)kOutOfRange;
+                if constexpr (sizeof(S) == 2) v[t][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, row * st, 0);
+                else v[t][i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, o, row * st, 0);
             }
         }
     }
     __device__ __forceinline__ void store(S *p, int64_t stride, int len, const f32x4 (&v)[NT][4]) const {
+        const __amdgpu_buffer_rsrc_t r = rows_of(p);
+        const int st = (int)stride * (int)sizeof(S);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            S *q = p + (tile + t) * 16 + m + (int64_t)(4 * g) * stride;
-            if (len == kC) {
-                if (live[t])
+            const int at = live[t] ? 4 * g * st + ((tile + t) * 16 + m) * (int)sizeof(S) : (int)kOutOfRange;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) q[(16 * i + r) * stride] = mix_out<S>(v[t][i][r]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (live[t] && 16 * i + 4 * g + r < len) q[(16 * i + r) * stride] = mix_out<S>(v[t][i][r]);
+            for (int i = 0; i < 16; ++i) {
+                const int row = 16 * (i / 4) + i % 4;
+                const int o = len == kC || row + 4 * g < len ? at : (int)kOutOfRange;
+                const S x = mix_out<S>(v[t][i / 4][i % 4]);
+                if constexpr (sizeof(S) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, x), r, o, row * st, 0);
+                else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, x), r, o, row * st, 0);
             }
         }
+    }
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_of(const void *p) {
+        const uint64_t a = (uint64_t)p;
+        const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
+        const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32));
+        return make_rsrc((const void *)(lo | hi << 32), 0x7fffffff);
     }
     template <int N>
     __device__ __forceinline__ void store_result(float *p, int tiles, const f32x4 (&v)[NT][N]) const {
@@ -152,21 +151,28 @@ struct Scan {
                 }
     }
 
-    // Products with what lies in LDS.
-    __device__ __forceinline__ void by_rows(const char *x, const Split (&b)[NT][KS], f32x4 (&c)[NT][4]) const {
+    // Products with what lies in LDS.  Consecutive products go to different
+    // results, so that none waits for the one before it.
+    __device__ __forceinline__ void by_rows(const char *x, int s, const Split (&b)[NT][KS], f32x4 (&c)[NT][4]) const {
+        f16x8 f[4];
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int mt = 0; mt < 4; ++mt) f[mt] = frag_at(x + (mt * KS + s) * 1024);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                const f16x8 f = frag_at(x + (mt * KS + s) * 1024);
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) c[t][mt] = mma2(f, b[t][s], c[t][mt]);
-                if constexpr (SPLIT) {
-                    const f16x8 l = frag_at(x + kMat + (mt * KS + s) * 1024);
+            for (int mt = 0; mt < 4; ++mt) c[t][mt] = mma(f[mt], b[t][s].lo, c[t][mt]);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) c[t][mt] = mma(l, b[t][s].hi, c[t][mt]);
-                }
-            }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) c[t][mt] = mma(f[mt], b[t][s].hi, c[t][mt]);
+        if constexpr (SPLIT) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) f[mt] = frag_at(x + kMat + (mt * KS + s) * 1024);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) c[t][mt] = mma(f[mt], b[t][s].hi, c[t][mt]);
+        }
     }
     // c[t] = (rows 16 mt.. of the transpose) b[t]
     __device__ __forceinline__ void by_cols(const char *x, int mt, const Split (&b)[NT][2], f32x4 (&c)[NT]) const {
@@ -242,6 +248,11 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_kernel(DeltaArgs A, DeltaB
     auto values = [&](int64_t c) {
         w.load((const S *)A.v + (w.a + c * kC) * A.vs + (int64_t)w.h * A.dv, A.vs, w.len_of(c), next);
     };
+    // stored after the next chunk has begun: a chunk begins by waiting for all memory accesses before it
+    f32x4 o[NT][4];
+    auto results = [&](int64_t c) {
+        w.store((S *)A.o + ((w.a + c * kC) * A.Hv + w.h) * A.dv, (int64_t)A.Hv * A.dv, w.len_of(c), o);
+    };
     if (w.chunks > 0) {
         if (W::STAGES == 2) w.issue(A, B, 0, B.tp, lds);
         values(0);
@@ -255,6 +266,7 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_kernel(DeltaArgs A, DeltaB
         f32x4 z[NT][4];
         chunk_ready<S>(next, z);
         const int64_t vh = (w.base + c) * A.Hv + w.h;
+        if (c > 0) results(c - 1);
         if (c + 1 < w.chunks) {
             if (W::STAGES == 2) w.issue(A, B, c + 1, B.tp, lds + (c & 1 ? 0 : W::kStage));
             values(c + 1);
@@ -277,11 +289,13 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_kernel(DeltaArgs A, DeltaB
                 if ((threadIdx.x & 63) == 0 && w.tile + t < B.dvp / 16) B.Smax[vh * (B.dvp / 16) + w.tile + t] = mx;
             }
         }
-        f32x4 y[NT][4], o[NT][4];
+        f32x4 y[NT][4];
         zero(y);
-        w.by_rows(x, sb, y);
         zero(o);
-        w.by_rows(x + W::kIn / 2, sb, o);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) w.by_rows(x, s, sb, y);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) w.by_rows(x + W::kIn / 2, s, sb, o);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -320,8 +334,8 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_kernel(DeltaArgs A, DeltaB
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[t][i] = o[t][i] * (*(const f32x4 *)(f + kC + 16 * i) * is[t]) + y[t][i] * inv[t];
-        w.store((S *)A.o + ((w.a + c * kC) * A.Hv + w.h) * A.dv, (int64_t)A.Hv * A.dv, w.len_of(c), o);
     }
+    if (w.chunks > 0) results(w.chunks - 1);
     w.store_state(A, A.state_out, st);
 }
 
@@ -339,6 +353,11 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_grad_kernel(DeltaArgs A, D
     auto values = [&](int64_t c) {
         w.load((const S *)A.d_o + (w.a + c * kC) * A.dos + (int64_t)w.h * A.dv, A.dos, w.len_of(c), next);
     };
+    f32x4 e[NT][4], dz[NT][4];  // stored after the next chunk has begun
+    auto results = [&](int64_t c) {
+        w.store_result(B.E + ((w.base + c) * A.Hv + w.h) * kC * B.dvp, B.dvp / 16, e);
+        w.store((S *)A.dv_out + ((w.a + c * kC) * A.Hv + w.h) * A.dv, (int64_t)A.Hv * A.dv, w.len_of(c), dz);
+    };
     if (w.chunks > 0) {
         if (W::STAGES == 2) w.issue(A, B, w.chunks - 1, B.tpg, lds);
         values(w.chunks - 1);
@@ -355,6 +374,7 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_grad_kernel(DeltaArgs A, D
         f32x4 d[NT][4];
         chunk_ready<S>(next, d);
         const int64_t vh = (w.base + c) * A.Hv + w.h;
+        if (c + 1 < w.chunks) results(c + 1);
         if (c > 0) {
             if (W::STAGES == 2) w.issue(A, B, c - 1, B.tpg, lds + half * W::kStage);
             values(c - 1);
@@ -375,10 +395,11 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_grad_kernel(DeltaArgs A, D
             if ((threadIdx.x & 63) == 0 && w.tile + t < B.dvp / 16) B.Gmax[vh * (B.dvp / 16) + w.tile + t] = mx;
             inv[t] = split_cols<4>(d[t], xb[t]) * ip;
         }
-        f32x4 y[NT][4], e[NT][4];
+        f32x4 y[NT][4];
         w.template by_tri<true>(x + W::kP, xb, y);
         zero(e);
-        w.by_rows(x, gb, e);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) w.by_rows(x, s, gb, e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -391,22 +412,16 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_grad_kernel(DeltaArgs A, D
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[t][i] *= inv[t];
-        w.store_result(B.E + vh * kC * B.dvp, B.dvp / 16, e);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[t][i] *= *(const f32x4 *)(f + 3 * kC + 16 * i);  // dZ
-        w.store((S *)A.dv_out + ((w.a + c * kC) * A.Hv + w.h) * A.dv, (int64_t)A.Hv * A.dv, w.len_of(c), e);
+            for (int i = 0; i < 4; ++i) {
+                e[t][i] *= inv[t];
+                dz[t][i] = e[t][i] * *(const f32x4 *)(f + 3 * kC + 16 * i);
+                d[t][i] *= *(const f32x4 *)(f + kC + 16 * i);
+                y[t][i] = dz[t][i] * *(const f32x4 *)(f + 16 * i);
+            }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d[t][i] *= *(const f32x4 *)(f + kC + 16 * i);
-                e[t][i] *= *(const f32x4 *)(f + 16 * i);
-            }
             id[t] = split_cols<4>(d[t], db[t]);
-            iy[t] = split_cols<4>(e[t], xb[t]);
+            iy[t] = split_cols<4>(y[t], xb[t]);
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -417,6 +432,7 @@ __global__ __launch_bounds__(64 * NW) void delta_scan_grad_kernel(DeltaArgs A, D
             for (int t = 0; t < NT; ++t) G[t][mt] = G[t][mt] * last + p[t] * id[t] - q[t] * iy[t];
         }
     }
+    if (w.chunks > 0) results(0);
     w.store_state(A, A.dstate, G);
 }
 

@@ -66,6 +66,8 @@ conv_status_t delta_inputs(const void *q, int64_t qs, const void *k, int64_t ks,
         !pointers_ok({}, {g}, 4))
         return CONV_ERR_INVALID_ARG;
     if (qs < (int64_t)Hk * dk || ks < (int64_t)Hk * dk || vs < (int64_t)Hv * dv) return CONV_ERR_INVALID_ARG;
+    // a chunk's 64 tokens are addressed by 32-bit byte offsets
+    if (vs > MIX_DELTA_MAX_STRIDE || (int64_t)Hv * dv > MIX_DELTA_MAX_STRIDE) return CONV_ERR_UNSUPPORTED;
     a->q = q, a->qs = qs, a->k = k, a->ks = ks, a->v = v, a->vs = vs, a->g = g, a->beta = beta;
     a->Hk = Hk, a->Hv = Hv, a->dk = dk, a->dv = dv, a->qk_norm = qk_norm != 0, a->scale = scale;
     a->beta_f32 = beta_dtype == CONV_DTYPE_FP32;
@@ -276,6 +278,7 @@ conv_status_t delta_rule_bwd(const void *d_o, int64_t do_stride, const float *ds
         !pointers_ok({}, {dbeta}, bytes_of(beta_dtype)) || !pointers_ok({}, {dg, dstate, dstate_out}, 4) ||
         !pointers_ok({}, {workspace, saved}, 16))
         return CONV_ERR_INVALID_ARG;
+    if (do_stride > MIX_DELTA_MAX_STRIDE) return CONV_ERR_UNSUPPORTED;
     size_t need = 0, keep = 0;
     if ((st = delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_BWD, &need)) != CONV_OK) return st;
     if ((st = delta_bytes(T, N, Hk, Hv, dk, dv, dtype, PART_SAVED, &keep)) != CONV_OK) return st;

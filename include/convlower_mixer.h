@@ -42,6 +42,7 @@ typedef enum { MIX_ACT_NONE = 0, MIX_ACT_SILU = 1, MIX_ACT_SIGMOID = 2 } mix_act
 #define MIX_CONV1D_MAX_WIDTH 8   /* taps of conv1d_causal_* */
 #define MIX_DELTA_MAX_DK 128     /* key head size of delta_rule_* */
 #define MIX_DELTA_MAX_DV 256     /* value head size of delta_rule_* */
+#define MIX_DELTA_MAX_STRIDE (1 << 22) /* token stride of v, o and d_o of delta_rule_fwd and _bwd, in elements */
 #define MIX_NORM_MAX_WIDTH 32768 /* row length of branch_norm_* */
 
 /* ---- causal convolution --------------------------------------------------
