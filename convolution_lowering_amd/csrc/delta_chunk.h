@@ -71,9 +71,28 @@ struct DeltaBuf {
     float *G, *E, *Gmax;  // gradients: the same of G and E
 };
 // One chunk of one value head: 6 + 6 fragments of each triangular operand (hi,
-// lo), then four rows of 64 factors, f1 = rho_k e^gam, f2 = rho_q e^gam,
-// f3 = rho_k e^(gam_C - gam), b, and e^gam_C, 1 / (the inverse's scale),
-// 1 / (P's scale).
+// lo), then rows of 64 factors and, in the last row, scalars.
+enum TpRow {
+    ROW_F1 = 0,   // rho_k e^gam
+    ROW_F2 = 1,   // rho_q e^gam
+    ROW_F3 = 2,   // rho_k e^(gam_C - gam)
+    ROW_B = 3,    // b
+    ROW_F3B = 4,  // f3 b
+    ROW_F1B = 5,  // f1 b
+    ROW_SCALARS = 7,
+};
+// The scalars.  The largest values bound what a product's result can be, and
+// so give the next operand's power of two without looking at it: f16's range
+// leaves 17 bits of room above the 22 that are wanted.
+enum TpScalar {
+    SC_LAST = 0,  // e^gam_C
+    SC_IT = 1,    // 1 / (the inverse's factor)
+    SC_IP = 2,    // 1 / (P's factor)
+    SC_TB = 3,    // 64 max |inverse| max |b|
+    SC_TF3 = 4,   // 64 max |inverse| max |f3 b|
+    SC_TF1 = 5,   // 64 max |inverse| max |f1 b|
+    SC_F2 = 6,    // max |f2|
+};
 constexpr int kTpRows = 4 * kTri * kFrag * 2;  // bytes before the factors
 constexpr int kTpBytes = kTpRows + 2048;
 
@@ -122,6 +141,7 @@ __device__ __forceinline__ float pow2_to(float m, int t, float *inv) {
     return __uint_as_float((uint32_t)e << 23);
 }
 constexpr int kTop = 11;     // split operands: largest value in [2^11, 2^12)
+constexpr int kBound = 14;   // those with a bound: the bound in [2^14, 2^15)
 constexpr int kRowTop = 8;   // rows of q and k: products of 128 of them and a split operand stay far below f32's end
 
 struct Split {
@@ -177,17 +197,18 @@ __device__ __forceinline__ float tile_max(float m) {
     m = dpp_max<0x124>(m);
     return col_max(dpp_max<0x128>(m));
 }
-// Right operands of 32 rows each from a result of N tiles of 16 rows, moved
-// column by column; returns the inverse of the column's factor.
+// Right operands of 32 rows each from a result of N tiles of 16 rows.
 template <int N>
-__device__ __forceinline__ float split_cols(const f32x4 (&v)[N], Split (&out)[N / 2]) {
-    float m = 0.f, inv;
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = max4(v[i], m);
-    const float sc = pow2_to(col_max(m), kTop, &inv);
+__device__ __forceinline__ void split_by(const f32x4 (&v)[N], float sc, Split (&out)[N / 2]) {
 #pragma unroll
     for (int s = 0; s < N / 2; ++s) out[s] = split8(v[2 * s], v[2 * s + 1], sc);
-    return inv;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const f32x4 (&v)[N]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = max4(v[i], m);
+    return m;
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -213,7 +234,7 @@ __device__ __forceinline__ f16x8 trans_at(const char *a, const char *b, int mt, 
 }
 
 // 16-byte copies into LDS, 1 KB an instruction, shared by the block's NW
-// wavefronts.
+// wavefronts (NW = 1: done by the one that calls).
 template <int NW, int UNITS>
 __device__ __forceinline__ void copy_in(const void *src, char *dst) {
     // the same for the whole wavefront, whatever it was computed from
@@ -221,7 +242,7 @@ __device__ __forceinline__ void copy_in(const void *src, char *dst) {
     const uint64_t u0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)p);
     const uint64_t u1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32));
     const __amdgpu_buffer_rsrc_t r = make_rsrc((const void *)(u0 | u1 << 32), UNITS * 1024);
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int w = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)dst + w * 1024, v = (threadIdx.x & 63) * 16 + w * 1024;
 #pragma unroll
     for (int u = 0; u < UNITS; u += NW)

@@ -134,9 +134,9 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
             sg[tid] = x;
             rise[tid] = expf((float)x);
             fall[tid] = expf((float)(all - x));
-            sb[tid] = fac[3 * kC + tid];
+            sb[tid] = fac[ROW_B * kC + tid];
         }
-        const float last = fac[4 * kC];
+        const float last = fac[ROW_SCALARS * kC + SC_LAST];
         f32x4 dp[4], dl[4], dbp[4];
 #pragma unroll
         for (int i = 0; i < MT; ++i) dq[i] = dk[i] = gu[i] = f32x4{0.f, 0.f, 0.f, 0.f};

@@ -77,10 +77,10 @@ __device__ __forceinline__ f16x8 row_frag(const _Float16 *x, int mt, int s) {
     const f16x4 a = *(const f16x4 *)p, b = *(const f16x4 *)(p + 16);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// Largest |x| of a 64 x 64 matrix in LDS, to every thread (256).
+__device__ __forceinline__ float wave_max(float m) { return tile_max(m); }
+// Largest of all 256 threads' values, to every thread.
 __device__ __forceinline__ float block_max(float m, float *red) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    m = wave_max(m);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
     __syncthreads();
@@ -231,6 +231,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             }
     }
     const int rep = A.Hv / A.Hk;
+    float mf[4] = {};
     for (int v = 0; v < rep; ++v) {
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
@@ -255,10 +256,13 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             const float rise = expf((float)s);
             const float f1 = rk[lane] * rise, f2 = rq[lane] * rise, f3 = rk[lane] * expf((float)(all - s));
             const float last = expf((float)all);
+            mf[0] = wave_max(fabsf(b)), mf[1] = wave_max(fabsf(f3 * b));
+            mf[2] = wave_max(fabsf(f1 * b)), mf[3] = wave_max(fabsf(f2));
             auto put = [&](char *tp) {
                 float *f = (float *)(tp + kTpRows) + lane;
-                f[0] = f1, f[kC] = f2, f[2 * kC] = f3, f[3 * kC] = b;
-                if (lane == 0) f[4 * kC] = last;
+                f[ROW_F1 * kC] = f1, f[ROW_F2 * kC] = f2, f[ROW_F3 * kC] = f3, f[ROW_B * kC] = b;
+                f[ROW_F3B * kC] = f3 * b, f[ROW_F1B * kC] = f1 * b;
+                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last, f[ROW_SCALARS * kC + SC_F2] = mf[3];
             };
             put(tp);
             if (GRAD) {
@@ -285,8 +289,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
         float sc = pow2_to(block_max(mp, red), kTop, &inv);
         store_tri(xi, sc, tp + kTpRows / 2, GRAD ? tpg + kTpRows / 2 : nullptr);
         if (tid == 0) {
-            ((float *)(tp + kTpRows))[4 * kC + 2] = inv;
-            if (GRAD) ((float *)(tpg + kTpRows))[4 * kC + 2] = inv;
+            ((float *)(tp + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
+            if (GRAD) ((float *)(tpg + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
         }
         for (int way = 0; way < (GRAD ? 2 : 1); ++way) {
             __syncthreads();
@@ -300,9 +304,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             invert(lm, xi, tmp);
             mp = 0.f;
             for (int e = tid; e < kC * kC; e += 256) mp = fmaxf(mp, fabsf(xi[(e >> 6) * kLd + (e & 63)]));
-            sc = pow2_to(block_max(mp, red), kTop, &inv);
+            mp = block_max(mp, red);
+            sc = pow2_to(mp, kTop, &inv);
             store_tri(xi, sc, way ? tpg : tp, nullptr);
-            if (tid == 0) ((float *)((way ? tpg : tp) + kTpRows))[4 * kC + 1] = inv;
+            if (tid == 0) {
+                float *o = (float *)((way ? tpg : tp) + kTpRows) + ROW_SCALARS * kC;
+                o[SC_IT] = inv;
+                o[SC_TB] = kC * mp * mf[0], o[SC_TF3] = kC * mp * mf[1], o[SC_TF1] = kC * mp * mf[2];
+            }
         }
         __syncthreads();
     }

@@ -1,13 +1,16 @@
 // The part of the chunked gated delta rule that runs along the sequence, and
 // its mirror image for the gradients.
 //
-// Columns of the state never meet, so a wavefront takes 16 NT columns of one
-// value head and holds them, [dk][16 NT] in float32, in registers from the
-// first chunk to the last.  A chunk is five products whose right operands come
-// out of registers.  The left operands (K, Q, the inverse and P, 58 KB for a
-// 16-bit dk = 128) are the same for all columns: the block's wavefronts copy
-// the next chunk's into the other half of LDS while they work on this one's,
-// with one barrier a chunk.  K', Q', and on the way back the transposes of the
+// Columns of the state never meet, so a wavefront takes 16 columns of one
+// value head and holds them, [dk][16] in float32, in registers from the first
+// chunk to the last.  A chunk is five products whose right operands come out
+// of registers, each from the result before it, so what counts is how long
+// that chain is.  The left operands (K, Q, the inverse and P, 58 KB for a
+// 16-bit dk = 128) and the rows of V are the same for all columns or lie
+// across them: one more wavefront of the block copies the next chunk's into the other half of LDS and
+// takes the last chunk's results from there to memory (issuing those accesses
+// took a fifth of a chunk's time from the wavefronts that compute).  One
+// barrier a chunk.  K', Q', and on the way back the transposes of the
 // triangular operands, are read from the same bytes by the transposing LDS
 // read.
 #include "delta_chunk.h"
@@ -15,37 +18,27 @@
 namespace convlower {
 namespace {
 
-template <int BYTES>
-struct Bits {
-    typedef uint16_t type;
-};
-template <>
-struct Bits<4> {
-    typedef uint32_t type;
-};
-
-template <int N, int NT>
-__device__ __forceinline__ void zero(f32x4 (&v)[NT][N]) {
+template <int N>
+__device__ __forceinline__ void zero(f32x4 (&v)[N]) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < N; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// What a wavefront works on, and where things lie.
-template <typename S, int DKP, int NT, int NW>
+// What a block works on, and where things lie.
+template <typename S, int DKP, int NW>
 struct Scan {
     static constexpr bool SPLIT = sizeof(S) == 4;
-    static constexpr int KS = DKP / 32, MT = DKP / 16, PL = SPLIT ? 2 : 1;
+    static constexpr int KS = DKP / 32, MT = DKP / 16, PL = SPLIT ? 2 : 1, COLS = 16 * NW, ES = sizeof(S);
     static constexpr int kMat = kC * DKP * 2;                  // bytes of one half of K or Q
     static constexpr int kIn = 2 * PL * kMat;                  // K and Q
     static constexpr int kStage = kIn + kTpBytes;
-    static constexpr int STAGES = 2 * kStage <= 160 * 1024 ? 2 : 1;
+    static constexpr int kRow = COLS * ES, kTile = kC * kRow;  // a row and all rows of V, dO, O or dV
+    static constexpr int STAGES = 2 * kStage + 4 * kTile <= 160 * 1024 ? 2 : 1;
     static constexpr int kTi = kIn, kP = kIn + kTpRows / 2, kRows = kIn + kTpRows;
+    static constexpr int kVals = STAGES * kStage, kOuts = kVals + 2 * kTile, kLds = kOuts + 2 * kTile;
 
-    int n, h, hk, tile, g, m, tl;
+    int n, h, hk, c0, w, g, m, tl;  // c0: the block's first column; w: the wavefront
     int64_t a, e, base, chunks;
-    bool live[NT];
 
     // Blocks of one query/key head go to one XCD (every eighth block), whose
     // L2 then serves K and Q to all of them.
@@ -58,10 +51,10 @@ struct Scan {
         n = (int)(unit / A.Hk);
         hk = (int)(unit % A.Hk);
         h = hk * rep + in / groups;
-        tile = ((in % groups) * NW + (threadIdx.x >> 6)) * NT;
+        c0 = (in % groups) * COLS;
+        w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int lane = threadIdx.x & 63;
         g = lane >> 4, m = lane & 15, tl = trans_lane();
-        for (int t = 0; t < NT; ++t) live[t] = (tile + t) * 16 + m < A.dv;
         seq_range(A.s, n, &a, &e);
         base = slot_base(A.s, n);
         chunks = (e - a + kC - 1) / kC;
@@ -71,390 +64,412 @@ struct Scan {
         const int64_t left = e - a - c * kC;
         return left < kC ? (int)left : kC;
     }
-    __device__ __forceinline__ void issue(const DeltaArgs &A, const DeltaBuf &B, int64_t c, const char *tp, char *lds) const {
-        const int64_t slot = base + c;
-        copy_in<NW, kIn / 1024>((const char *)B.kq + (slot * A.Hk + hk) * kIn, lds);
-        copy_in<NW, kTpBytes / 1024>(tp + (slot * A.Hv + h) * kTpBytes, lds + kIn);
-    }
-    // Columns of a [64][..] tensor of the caller's in result order, by buffer
-    // accesses: rows past the chunk's end and columns past the last read as
-    // zeros and are not written, being past the buffer's end.
-    __device__ __forceinline__ void load(const S *p, int64_t stride, int len, uint32_t (&v)[NT][16]) const {
-        const __amdgpu_buffer_rsrc_t r = rows_of(p);
-        const int st = (int)stride * (int)sizeof(S);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int at = live[t] ? 4 * g * st + ((tile + t) * 16 + m) * (int)sizeof(S) : (int)kOutOfRange;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 16 * (i / 4) + i % 4;  // and 4 g
-                const int o = len == kC || row + 4 * g < len ? at : (int)kOutOfRange;
-                if constexpr (sizeof(S) == 2) v[t][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, o, row * st, 0);
-                else v[t][i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, o, row * st, 0);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(S *p, int64_t stride, int len, const f32x4 (&v)[NT][4]) const {
-        const __amdgpu_buffer_rsrc_t r = rows_of(p);
-        const int st = (int)stride * (int)sizeof(S);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int at = live[t] ? 4 * g * st + ((tile + t) * 16 + m) * (int)sizeof(S) : (int)kOutOfRange;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 16 * (i / 4) + i % 4;
-                const int o = len == kC || row + 4 * g < len ? at : (int)kOutOfRange;
-                const S x = mix_out<S>(v[t][i / 4][i % 4]);
-                if constexpr (sizeof(S) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, x), r, o, row * st, 0);
-                else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, x), r, o, row * st, 0);
-            }
-        }
-    }
+
+    // ---- the copying wavefront
     __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_of(const void *p) {
         const uint64_t a = (uint64_t)p;
         const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
         const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32));
         return make_rsrc((const void *)(lo | hi << 32), 0x7fffffff);
     }
+    // Rows of the block's columns, [64][..] of the caller's, to LDS: 16 bytes a
+    // lane, or one value at a time where the rows do not lie that way.  What is
+    // past the chunk's end or the last column reads as zero.
+    __device__ __forceinline__ void rows_in(const S *p, int64_t stride, int len, int dv, bool vec, char *lds) const {
+        const __amdgpu_buffer_rsrc_t r = rows_of(p + c0);
+        const int lane = threadIdx.x & 63, st = (int)stride * ES;
+        if (vec) {
+            constexpr int L = kRow / 16;  // lanes of a row
+            const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
+            const int col = lane % L * 16;
+#pragma unroll
+            for (int u = 0; u < kTile / 1024; ++u) {
+                const int row = u * (64 / L) + lane / L;
+                lds_dma16(r, row < len && c0 + col / ES < dv ? (uint32_t)(row * st + col) : kOutOfRange, d + u * 1024);
+            }
+        } else {
+            for (int u = lane; u < kC * COLS; u += 64) {
+                const int row = u / COLS, col = u % COLS;
+                const int o = row < len && c0 + col < dv ? row * st + col * ES : (int)kOutOfRange;
+                if constexpr (ES == 2) ((uint16_t *)lds)[u] = __builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0);
+                else ((uint32_t *)lds)[u] = __builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void rows_out(S *p, int64_t stride, int len, int dv, bool vec, const char *lds) const {
+        const __amdgpu_buffer_rsrc_t r = rows_of(p + c0);
+        const int lane = threadIdx.x & 63, st = (int)stride * ES;
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        if (vec) {
+            constexpr int L = kRow / 16;
+            const int col = lane % L * 16;
+            i32x4 v[kTile / 1024];
+#pragma unroll
+            for (int u = 0; u < kTile / 1024; ++u) v[u] = *(const i32x4 *)(lds + u * 1024 + lane * 16);
+#pragma unroll
+            for (int u = 0; u < kTile / 1024; ++u) {
+                const int row = u * (64 / L) + lane / L;
+                const int o = row < len && c0 + col / ES < dv ? row * st + col : (int)kOutOfRange;
+                __builtin_amdgcn_raw_buffer_store_b128(v[u], r, o, 0, 0);
+            }
+        } else {
+            for (int u = lane; u < kC * COLS; u += 64) {
+                const int row = u / COLS, col = u % COLS;
+                const int o = row < len && c0 + col < dv ? row * st + col * ES : (int)kOutOfRange;
+                if constexpr (ES == 2) __builtin_amdgcn_raw_buffer_store_b16(((const short *)lds)[u], r, o, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b32(((const int *)lds)[u], r, o, 0, 0);
+            }
+        }
+    }
+    // The copying wavefront's whole life: chunks first, first + step, ..
+    template <bool BACK>
+    __device__ __forceinline__ void copy(const DeltaArgs &A, const DeltaBuf &B, bool vec, char *lds) const {
+        const char *tp = BACK ? B.tpg : B.tp;
+        const S *in = BACK ? (const S *)A.d_o : (const S *)A.v;
+        S *out = BACK ? (S *)A.dv_out : (S *)A.o;
+        const int64_t is = BACK ? A.dos : A.vs, os = (int64_t)A.Hv * A.dv;
+        auto chunk = [&](int64_t i) { return BACK ? chunks - 1 - i : i; };
+        auto issue = [&](int64_t i) {
+            const int64_t c = chunk(i), slot = base + c;
+            char *d = lds + (STAGES == 2 ? i & 1 : 0) * kStage;
+            rows_in(in + (a + c * kC) * is + (int64_t)h * A.dv, is, len_of(c), A.dv, vec, lds + kVals + (i & 1) * kTile);
+            copy_in<1, kIn / 1024>((const char *)B.kq + (slot * A.Hk + hk) * kIn, d);
+            copy_in<1, kTpBytes / 1024>(tp + (slot * A.Hv + h) * kTpBytes, d + kIn);
+        };
+        auto results = [&](int64_t i) {
+            const int64_t c = chunk(i);
+            rows_out(out + (a + c * kC) * os + (int64_t)h * A.dv, os, len_of(c), A.dv, vec, lds + kOuts + (i & 1) * kTile);
+        };
+        if (STAGES == 2 && chunks > 0) issue(0);
+        for (int64_t i = 0; i < chunks; ++i) {
+            if (STAGES == 1) {
+                block_barrier();  // nobody reads the chunk before any more
+                issue(i);
+                if (i > 0) results(i - 1);
+            }
+            CONVLOWER_WAIT_VMCNT_LDS(0);
+            block_barrier();  // the chunk is in LDS, the results of the one before too
+            if (STAGES == 2) {
+                if (i > 0) results(i - 1);
+                if (i + 1 < chunks) issue(i + 1);
+            }
+        }
+        block_barrier();
+        if (chunks > 0) results(chunks - 1);
+    }
+    // The other wavefronts' side of it.
+    __device__ __forceinline__ static void next_chunk() {
+        CONVLOWER_WAIT_LDS();
+        if (STAGES == 1) block_barrier();
+        block_barrier();
+    }
+
+    // ---- the computing wavefronts
+    __device__ __forceinline__ void values(const char *lds, f32x4 (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (ES == 2) {
+                const char *p = lds + (16 * i + 4 * g + (m >> 2)) * kRow + (16 * w + 4 * (m & 3)) * 2;
+                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)((lds_bytes)(lds_ptr_t)p));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[i][r] = mix_f32(__builtin_bit_cast(S, (short)x[r]));
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[i][r] = *(const float *)(lds + (16 * i + 4 * g + r) * kRow + (16 * w + m) * 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void results(char *lds, const f32x4 (&v)[4]) const {
+        S *p = (S *)(lds + 4 * g * kRow) + 16 * w + m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[(16 * i + r) * COLS] = mix_out<S>(v[i][r]);
+    }
+    // Result order, for the gradient kernel; tile: of 16 columns.
     template <int N>
-    __device__ __forceinline__ void store_result(float *p, int tiles, const f32x4 (&v)[NT][N]) const {
+    __device__ __forceinline__ void keep(float *p, int tile, const f32x4 (&v)[N]) const {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (tile + t < tiles) *(f32x4 *)(p + (((tile + t) * N + i) * 64 + (threadIdx.x & 63)) * 4) = v[t][i];
+        for (int i = 0; i < N; ++i) *(f32x4 *)(p + ((tile * N + i) * 64 + (threadIdx.x & 63)) * 4) = v[i];
     }
     // [dk][dv] float32 of the caller's.
-    __device__ __forceinline__ void load_state(const DeltaArgs &A, const float *p, f32x4 (&v)[NT][MT]) const {
-        const int64_t at = ((int64_t)n * A.Hv + h) * A.dk * A.dv;
+    __device__ __forceinline__ void load_state(const DeltaArgs &A, const float *p, f32x4 (&v)[MT]) const {
+        const int col = c0 + 16 * w + m;
+        const int64_t at = ((int64_t)n * A.Hv + h) * A.dk * A.dv + col;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * i + 4 * g + r;
-                    v[t][i][r] = p && live[t] && row < A.dk ? p[at + (int64_t)row * A.dv + (tile + t) * 16 + m] : 0.f;
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * g + r;
+                v[i][r] = p && col < A.dv && row < A.dk ? p[at + (int64_t)row * A.dv] : 0.f;
+            }
     }
-    __device__ __forceinline__ void store_state(const DeltaArgs &A, float *p, const f32x4 (&v)[NT][MT]) const {
-        if (!p) return;
-        const int64_t at = ((int64_t)n * A.Hv + h) * A.dk * A.dv;
+    __device__ __forceinline__ void store_state(const DeltaArgs &A, float *p, const f32x4 (&v)[MT]) const {
+        const int col = c0 + 16 * w + m;
+        const int64_t at = ((int64_t)n * A.Hv + h) * A.dk * A.dv + col;
+        if (!p || col >= A.dv) return;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * i + 4 * g + r;
-                    if (live[t] && row < A.dk) p[at + (int64_t)row * A.dv + (tile + t) * 16 + m] = v[t][i][r];
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * g + r;
+                if (row < A.dk) p[at + (int64_t)row * A.dv] = v[i][r];
+            }
     }
 
     // Products with what lies in LDS.  Consecutive products go to different
     // results, so that none waits for the one before it.
-    __device__ __forceinline__ void by_rows(const char *x, int s, const Split (&b)[NT][KS], f32x4 (&c)[NT][4]) const {
+    __device__ __forceinline__ static void by_rows(const char *x, int s, const Split &b, f32x4 (&c)[4]) {
         f16x8 f[4];
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) f[mt] = frag_at(x + (mt * KS + s) * 1024);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f[mt], b.lo, c[mt]);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) c[t][mt] = mma(f[mt], b[t][s].lo, c[t][mt]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) c[t][mt] = mma(f[mt], b[t][s].hi, c[t][mt]);
+        for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f[mt], b.hi, c[mt]);
         if constexpr (SPLIT) {
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) f[mt] = frag_at(x + kMat + (mt * KS + s) * 1024);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int mt = 0; mt < 4; ++mt) c[t][mt] = mma(f[mt], b[t][s].hi, c[t][mt]);
+            for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f[mt], b.hi, c[mt]);
         }
     }
-    // c[t] = (rows 16 mt.. of the transpose) b[t]
-    __device__ __forceinline__ void by_cols(const char *x, int mt, const Split (&b)[NT][2], f32x4 (&c)[NT]) const {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) c[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const char *p = x + (2 * s * KS + mt / 2) * 1024;
-            const f16x8 f = trans_at(p, p + KS * 1024, mt, tl);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) c[t] = mma2(f, b[t][s], c[t]);
-            if constexpr (SPLIT) {
-                const f16x8 l = trans_at(p + kMat, p + kMat + KS * 1024, mt, tl);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) c[t] = mma(l, b[t][s].hi, c[t]);
-            }
-        }
-    }
-    template <bool TRANS>
-    __device__ __forceinline__ void by_tri(const char *x, const Split (&b)[NT][2], f32x4 (&c)[NT][4]) const {
+    // Rows 16 mt.. of the transpose, four tiles of them from mt.
+    __device__ __forceinline__ void by_cols(const char *x, int mt, const Split (&b)[2], f32x4 (&c)[4]) const {
         zero(c);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
+        for (int s = 0; s < 2; ++s) {
+            f16x8 f[4];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int i = 0; i < 4; ++i) {
+                const char *p = x + (2 * s * KS + (mt + i) / 2) * 1024;
+                f[i] = trans_at(p, p + KS * 1024, mt + i, tl);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = mma(f[i], b[s].lo, c[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = mma(f[i], b[s].hi, c[i]);
+            if constexpr (SPLIT) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const char *p = x + kMat + (2 * s * KS + (mt + i) / 2) * 1024;
+                    c[i] = mma(trans_at(p, p + KS * 1024, mt + i, tl), b[s].hi, c[i]);
+                }
+            }
+        }
+    }
+    // A triangular operand, or its transpose; ONE: the right operand has no
+    // second half.
+    template <bool TRANS, bool ONE>
+    __device__ __forceinline__ void by_tri(const char *x, const Split (&b)[2], f32x4 (&c)[4]) const {
+        f16x8 hi[4][2], lo[4][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
                 if (TRANS ? s < mt / 2 : s > mt / 2) continue;
-                f16x8 hi, lo;
                 if constexpr (TRANS) {
                     const char *p = x + tri_lower(2 * s, mt / 2) * 1024, *q = x + tri_lower(2 * s + 1, mt / 2) * 1024;
-                    hi = trans_at(p, q, mt, tl), lo = trans_at(p + kTri * 1024, q + kTri * 1024, mt, tl);
+                    hi[mt][s] = trans_at(p, q, mt, tl), lo[mt][s] = trans_at(p + kTri * 1024, q + kTri * 1024, mt, tl);
                 } else {
                     const char *p = x + tri_lower(mt, s) * 1024;
-                    hi = frag_at(p), lo = frag_at(p + kTri * 1024);
+                    hi[mt][s] = frag_at(p), lo[mt][s] = frag_at(p + kTri * 1024);
                 }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) c[t][mt] = mma3(hi, lo, b[t][s], c[t][mt]);
             }
+        zero(c);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    if ((TRANS ? s < mt / 2 : s > mt / 2) || (ONE && k == 1)) continue;
+                    c[mt] = mma(k == 0 ? lo[mt][s] : hi[mt][s], k == 1 ? b[s].lo : b[s].hi, c[mt]);
+                }
     }
 };
 
-// Starts a chunk: its operands are in LDS, its own rows in registers, and
-// nobody reads the other half of LDS any more.  Waiting for this wavefront's
-// copies before the barrier makes everybody's visible after it.  The rows are
-// taken over before new loads are issued, which the compiler counts without
-// the copies to LDS.
-template <typename S, int NT>
-__device__ __forceinline__ void chunk_ready(uint32_t (&rows)[NT][16], f32x4 (&v)[NT][4]) {
-    CONVLOWER_WAIT_VMCNT_LDS(0);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            asm volatile("" : "+v"(rows[t][i]));
-            v[t][i / 4][i % 4] = mix_f32(__builtin_bit_cast(S, (typename Bits<sizeof(S)>::type)rows[t][i]));
-        }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(v[t][i]));
-    block_barrier();
-}
+// Power of two for a column whose largest value is in m (four lane groups).
+__device__ __forceinline__ float col_scale(float m, float *inv) { return pow2_to(col_max(m), kTop, inv); }
 
-template <typename S, int DKP, int NT, int NW, bool SAVE>
-__global__ __launch_bounds__(64 * NW) void delta_scan_kernel(DeltaArgs A, DeltaBuf B, int groups) {
-    typedef Scan<S, DKP, NT, NW> W;
+template <typename S, int DKP, int NW, bool SAVE>
+__global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
+    typedef Scan<S, DKP, NW> W;
     constexpr int MT = W::MT, KS = W::KS;
-    __shared__ __align__(16) char lds[W::STAGES * W::kStage];
+    __shared__ __align__(16) char lds[W::kLds];
     W w;
     if (!w.place(A, groups)) return;
-    f32x4 st[NT][MT];
+    if (w.w == NW) return w.template copy<false>(A, B, vec, lds);
+    const int tile = w.c0 / 16 + w.w;
+    const bool kept = SAVE && tile < B.dvp / 16;
+    f32x4 st[MT];
     w.load_state(A, A.state, st);
-    uint32_t next[NT][16] = {};
-    auto values = [&](int64_t c) {
-        w.load((const S *)A.v + (w.a + c * kC) * A.vs + (int64_t)w.h * A.dv, A.vs, w.len_of(c), next);
-    };
-    // stored after the next chunk has begun: a chunk begins by waiting for all memory accesses before it
-    f32x4 o[NT][4];
-    auto results = [&](int64_t c) {
-        w.store((S *)A.o + ((w.a + c * kC) * A.Hv + w.h) * A.dv, (int64_t)A.Hv * A.dv, w.len_of(c), o);
-    };
-    if (w.chunks > 0) {
-        if (W::STAGES == 2) w.issue(A, B, 0, B.tp, lds);
-        values(0);
-    }
+    float smax = max_of(st);
     for (int64_t c = 0; c < w.chunks; ++c) {
-        const char *x = lds + (W::STAGES == 2 && (c & 1) ? W::kStage : 0);
-        if (W::STAGES == 1) {
-            block_barrier();
-            w.issue(A, B, c, B.tp, lds);
-        }
-        f32x4 z[NT][4];
-        chunk_ready<S>(next, z);
-        const int64_t vh = (w.base + c) * A.Hv + w.h;
-        if (c > 0) results(c - 1);
-        if (c + 1 < w.chunks) {
-            if (W::STAGES == 2) w.issue(A, B, c + 1, B.tp, lds + (c & 1 ? 0 : W::kStage));
-            values(c + 1);
-        }
+        W::next_chunk();
+        const char *x = lds + (W::STAGES == 2 ? c & 1 : 0) * W::kStage;
         const float *f = (const float *)(x + W::kRows) + 4 * w.g;
-        const float *sc = (const float *)(x + W::kRows) + 4 * kC;
-        const float last = sc[0], it = sc[1], ip = sc[2];
-        Split sb[NT][KS], xb[NT][2];
-        float is[NT], inv[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) is[t] = split_cols<MT>(st[t], sb[t]);
+        const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
+        auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
+        const int64_t vh = (w.base + c) * A.Hv + w.h;
+        f32x4 z[4], y[4], o[4];
+        w.values(lds + W::kVals + (c & 1) * W::kTile, z);
+        float is, iz, iu, iw;
+        smax = col_max(smax);
+        const float ss = pow2_to(smax, kTop, &is);
         if constexpr (SAVE) {
-            w.store_result(B.S + vh * DKP * B.dvp, B.dvp / 16, st);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float mx = 0.f;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) mx = max4(st[t][i], mx);
-                mx = tile_max(mx);
-                if ((threadIdx.x & 63) == 0 && w.tile + t < B.dvp / 16) B.Smax[vh * (B.dvp / 16) + w.tile + t] = mx;
+            if (kept) {
+                w.keep(B.S + vh * DKP * B.dvp, tile, st);
+                const float mx = tile_max(smax);
+                if ((threadIdx.x & 63) == 0) B.Smax[vh * (B.dvp / 16) + tile] = mx;
             }
         }
-        f32x4 y[NT][4];
+        Split sb[KS], zb[2], ub[2], wb[2];
+        split_by(st, ss, sb);
         zero(y);
         zero(o);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) w.by_rows(x, s, sb, y);
+        for (int s = 0; s < KS; ++s) W::by_rows(x, s, sb[s], y);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) w.by_rows(x + W::kIn / 2, s, sb, o);
+        for (int s = 0; s < KS; ++s) W::by_rows(x + W::kIn / 2, s, sb[s], o);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int i = 0; i < 4; ++i) z[i] -= y[i] * (row(ROW_F1, i) * is);
+        const float zmax = col_max(max_of(z));
+        split_by(z, pow2_to(zmax, kTop, &iz), zb);
+        w.template by_tri<false, false>(x + W::kTi, zb, y);
+        iz *= sc[SC_IT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[t][i] -= y[t][i] * (*(const f32x4 *)(f + 16 * i) * is[t]);
-            inv[t] = split_cols<4>(z[t], xb[t]) * it;
-        }
-        w.template by_tri<false>(x + W::kTi, xb, y);
-        if constexpr (SAVE) {
+        for (int i = 0; i < 4; ++i) y[i] *= iz;
+        if (kept) w.keep(B.Y + vh * kC * B.dvp, tile, y);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < 4; ++i) z[i] = y[i] * row(ROW_F3B, i);
+        split_by(z, pow2_to(zmax * sc[SC_TF3], kBound, &iw), wb);
+        const float last = sc[SC_LAST];
+        smax = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[t][i] = y[t][i] * inv[t];
-            w.store_result(B.Y + vh * kC * B.dvp, B.dvp / 16, z);
-        }
-        Split ub[NT][2];
-        float iu[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int mt = 0; mt < MT; mt += 4) {
+            f32x4 d[4];
+            w.by_cols(x, mt, wb, d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                y[t][i] *= *(const f32x4 *)(f + 3 * kC + 16 * i) * inv[t];  // U
-                z[t][i] = y[t][i] * *(const f32x4 *)(f + 2 * kC + 16 * i);
+                st[mt + i] = st[mt + i] * last + d[i] * iw;
+                smax = max4(st[mt + i], smax);
             }
-            iu[t] = split_cols<4>(z[t], ub[t]);
-            inv[t] = split_cols<4>(y[t], xb[t]) * ip;
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            f32x4 d[NT];
-            w.by_cols(x, mt, ub, d);
+        for (int i = 0; i < 4; ++i) y[i] *= row(ROW_B, i);
+        split_by(y, pow2_to(zmax * sc[SC_TB], kBound, &iu), ub);
+        w.template by_tri<false, false>(x + W::kP, ub, y);
+        iu *= sc[SC_IP];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) st[t][mt] = st[t][mt] * last + d[t] * iu[t];
-        }
-        w.template by_tri<false>(x + W::kP, xb, y);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[t][i] = o[t][i] * (*(const f32x4 *)(f + kC + 16 * i) * is[t]) + y[t][i] * inv[t];
+        for (int i = 0; i < 4; ++i) o[i] = o[i] * (row(ROW_F2, i) * is) + y[i] * iu;
+        w.results(lds + W::kOuts + (c & 1) * W::kTile, o);
     }
-    if (w.chunks > 0) results(w.chunks - 1);
+    CONVLOWER_WAIT_LDS();
+    block_barrier();
     w.store_state(A, A.state_out, st);
 }
 
 // From the last chunk to the first, with G, the gradient of the state.
-template <typename S, int DKP, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_scan_grad_kernel(DeltaArgs A, DeltaBuf B, int groups) {
-    typedef Scan<S, DKP, NT, NW> W;
+template <typename S, int DKP, int NW>
+__global__ __launch_bounds__(64 * NW + 64) void delta_scan_grad_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
+    typedef Scan<S, DKP, NW> W;
     constexpr int MT = W::MT, KS = W::KS;
-    __shared__ __align__(16) char lds[W::STAGES * W::kStage];
+    __shared__ __align__(16) char lds[W::kLds];
     W w;
     if (!w.place(A, groups)) return;
-    f32x4 G[NT][MT];
+    if (w.w == NW) return w.template copy<true>(A, B, vec, lds);
+    const int tile = w.c0 / 16 + w.w;
+    const bool kept = tile < B.dvp / 16;
+    f32x4 G[MT];
     w.load_state(A, A.dstate_out, G);
-    uint32_t next[NT][16] = {};
-    auto values = [&](int64_t c) {
-        w.load((const S *)A.d_o + (w.a + c * kC) * A.dos + (int64_t)w.h * A.dv, A.dos, w.len_of(c), next);
-    };
-    f32x4 e[NT][4], dz[NT][4];  // stored after the next chunk has begun
-    auto results = [&](int64_t c) {
-        w.store_result(B.E + ((w.base + c) * A.Hv + w.h) * kC * B.dvp, B.dvp / 16, e);
-        w.store((S *)A.dv_out + ((w.a + c * kC) * A.Hv + w.h) * A.dv, (int64_t)A.Hv * A.dv, w.len_of(c), dz);
-    };
-    if (w.chunks > 0) {
-        if (W::STAGES == 2) w.issue(A, B, w.chunks - 1, B.tpg, lds);
-        values(w.chunks - 1);
-    }
-    int half = 0;
-    for (int64_t c = w.chunks - 1; c >= 0; --c) {
-        const char *x = lds + half * W::kStage;
-        if (W::STAGES == 1) {
-            block_barrier();
-            w.issue(A, B, c, B.tpg, lds);
-        } else {
-            half ^= 1;
-        }
-        f32x4 d[NT][4];
-        chunk_ready<S>(next, d);
-        const int64_t vh = (w.base + c) * A.Hv + w.h;
-        if (c + 1 < w.chunks) results(c + 1);
-        if (c > 0) {
-            if (W::STAGES == 2) w.issue(A, B, c - 1, B.tpg, lds + half * W::kStage);
-            values(c - 1);
-        }
+    float gmax = max_of(G);
+    for (int64_t j = 0; j < w.chunks; ++j) {
+        W::next_chunk();
+        const char *x = lds + (W::STAGES == 2 ? j & 1 : 0) * W::kStage;
         const float *f = (const float *)(x + W::kRows) + 4 * w.g;
-        const float *sc = (const float *)(x + W::kRows) + 4 * kC;
-        const float last = sc[0], it = sc[1], ip = sc[2];
-        Split gb[NT][KS], xb[NT][2];
-        float ig[NT], inv[NT];
-        w.store_result(B.G + vh * DKP * B.dvp, B.dvp / 16, G);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            ig[t] = split_cols<MT>(G[t], gb[t]);
-            float mx = 0.f;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) mx = max4(G[t][i], mx);
-            mx = tile_max(mx);
-            if ((threadIdx.x & 63) == 0 && w.tile + t < B.dvp / 16) B.Gmax[vh * (B.dvp / 16) + w.tile + t] = mx;
-            inv[t] = split_cols<4>(d[t], xb[t]) * ip;
+        const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
+        auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
+        const int64_t vh = (w.base + w.chunks - 1 - j) * A.Hv + w.h;
+        f32x4 d[4], y[4], e[4];
+        w.values(lds + W::kVals + (j & 1) * W::kTile, d);
+        float ig, id, ie, iy;
+        gmax = col_max(gmax);
+        const float gs = pow2_to(gmax, kTop, &ig);
+        if (kept) {
+            w.keep(B.G + vh * DKP * B.dvp, tile, G);
+            const float mx = tile_max(gmax);
+            if ((threadIdx.x & 63) == 0) B.Gmax[vh * (B.dvp / 16) + tile] = mx;
         }
-        f32x4 y[NT][4];
-        w.template by_tri<true>(x + W::kP, xb, y);
+        Split gb[KS], db[2], eb[2], yb[2];
+        split_by(G, gs, gb);
         zero(e);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) w.by_rows(x, s, gb, e);
+        for (int s = 0; s < KS; ++s) W::by_rows(x, s, gb[s], e);
+        // 16-bit dO is exact in one half
+        const float dmax = col_max(max_of(d));
+        split_by(d, pow2_to(dmax, kTop, &id), db);
+        w.template by_tri<true, !W::SPLIT>(x + W::kP, db, y);
+        id *= sc[SC_IP];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int i = 0; i < 4; ++i) e[i] = e[i] * (row(ROW_F3, i) * ig) + y[i] * id;
+        const float emax = col_max(max_of(e));
+        split_by(e, pow2_to(emax, kTop, &ie), eb);
+        w.template by_tri<true, false>(x + W::kTi, eb, e);
+        ie *= sc[SC_IT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[t][i] = e[t][i] * (*(const f32x4 *)(f + 2 * kC + 16 * i) * ig[t]) + y[t][i] * inv[t];
-            inv[t] = split_cols<4>(e[t], xb[t]) * it;
+        for (int i = 0; i < 4; ++i) {
+            e[i] *= ie;
+            y[i] = e[i] * row(ROW_F1B, i);
+            d[i] *= row(ROW_F2, i);
         }
-        w.template by_tri<true>(x + W::kTi, xb, e);
-        Split db[NT][2];
-        float id[NT], iy[NT];
+        split_by(y, pow2_to(emax * sc[SC_TF1], kBound, &iy), yb);
+        split_by(d, pow2_to(dmax * sc[SC_F2], kBound, &id), db);
+        const float last = sc[SC_LAST];
+        gmax = 0.f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int mt = 0; mt < MT; mt += 4) {
+            f32x4 p[4], q[4];
+            w.by_cols(x, mt, yb, q);
+            w.by_cols(x + W::kIn / 2, mt, db, p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                e[t][i] *= inv[t];
-                dz[t][i] = e[t][i] * *(const f32x4 *)(f + 3 * kC + 16 * i);
-                d[t][i] *= *(const f32x4 *)(f + kC + 16 * i);
-                y[t][i] = dz[t][i] * *(const f32x4 *)(f + 16 * i);
+                G[mt + i] = G[mt + i] * last + p[i] * id - q[i] * iy;
+                gmax = max4(G[mt + i], gmax);
             }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            id[t] = split_cols<4>(d[t], db[t]);
-            iy[t] = split_cols<4>(y[t], xb[t]);
         }
+        if (kept) w.keep(B.E + vh * kC * B.dvp, tile, e);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            f32x4 p[NT], q[NT];
-            w.by_cols(x + W::kIn / 2, mt, db, p);
-            w.by_cols(x, mt, xb, q);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) G[t][mt] = G[t][mt] * last + p[t] * id[t] - q[t] * iy[t];
-        }
+        for (int i = 0; i < 4; ++i) e[i] *= row(ROW_B, i);  // dZ
+        w.results(lds + W::kOuts + (j & 1) * W::kTile, e);
     }
-    if (w.chunks > 0) results(0);
+    CONVLOWER_WAIT_LDS();
+    block_barrier();
     w.store_state(A, A.dstate, G);
 }
 
-template <typename S, int DKP, int NT, int NW>
+template <typename S, int DKP, int NW>
 hipError_t scan_run(const DeltaArgs &a, const DeltaBuf &b, bool grad, hipStream_t st) {
     // saved matrices are written in whole slabs of columns
     const int cols = grad || b.S ? b.dvp : a.dv;
-    const int groups = (cols + 16 * NT * NW - 1) / (16 * NT * NW);
+    const int groups = (cols + 16 * NW - 1) / (16 * NW);
     const int64_t units = ((int64_t)a.s.N * a.Hk + 7) / 8 * 8;
     const dim3 grid((unsigned)(units * groups * (a.Hv / a.Hk)));
+    const int64_t is = (grad ? a.dos : a.vs) * sizeof(S);
+    const uintptr_t in = (uintptr_t)(grad ? a.d_o : a.v), out = (uintptr_t)(grad ? a.dv_out : a.o);
+    const bool vec = a.dv * sizeof(S) % 16 == 0 && is % 16 == 0 && in % 16 == 0 && out % 16 == 0;
     auto run = [&](auto kern) {
-        hipLaunchKernelGGL(kern, grid, dim3(64 * NW), 0, st, a, b, groups);
+        hipLaunchKernelGGL(kern, grid, dim3(64 * NW + 64), 0, st, a, b, groups, vec);
         return hipGetLastError();
     };
-    if (grad) return run(delta_scan_grad_kernel<S, DKP, NT, NW>);
-    if (b.S) return run(delta_scan_kernel<S, DKP, NT, NW, true>);
-    return run(delta_scan_kernel<S, DKP, NT, NW, false>);
+    if (grad) return run(delta_scan_grad_kernel<S, DKP, NW>);
+    if (b.S) return run(delta_scan_kernel<S, DKP, NW, true>);
+    return run(delta_scan_kernel<S, DKP, NW, false>);
 }
 
 template <typename S, int DKP>
 hipError_t scan_typed(const DeltaArgs &a, const DeltaBuf &b, bool grad, hipStream_t st) {
-    return scan_run<S, DKP, 1, 2>(a, b, grad, st);
+    return scan_run<S, DKP, 2>(a, b, grad, st);
 }
 
 }  // namespace
