@@ -121,8 +121,9 @@ struct Scan {
             }
         }
     }
-    // The copying wavefront's whole life: chunks first, first + step, ..
-    template <bool BACK>
+    // The copying wavefront's whole life.  LAG: after how many barriers a
+    // chunk's results are in LDS.
+    template <bool BACK, int LAG>
     __device__ __forceinline__ void copy(const DeltaArgs &A, const DeltaBuf &B, bool vec, char *lds) const {
         const char *tp = BACK ? B.tpg : B.tp;
         const S *in = BACK ? (const S *)A.d_o : (const S *)A.v;
@@ -145,17 +146,17 @@ struct Scan {
             if (STAGES == 1) {
                 block_barrier();  // nobody reads the chunk before any more
                 issue(i);
-                if (i > 0) results(i - 1);
+                if (i >= LAG) results(i - LAG);
             }
             CONVLOWER_WAIT_VMCNT_LDS(0);
             block_barrier();  // the chunk is in LDS, the results of the one before too
             if (STAGES == 2) {
-                if (i > 0) results(i - 1);
+                if (i >= LAG) results(i - LAG);
                 if (i + 1 < chunks) issue(i + 1);
             }
         }
         block_barrier();
-        if (chunks > 0) results(chunks - 1);
+        for (int64_t i = chunks > LAG ? chunks - LAG : 0; i < chunks; ++i) results(i);
     }
     // The other wavefronts' side of it.
     __device__ __forceinline__ static void next_chunk() {
@@ -258,11 +259,13 @@ struct Scan {
             }
         }
     }
-    // A triangular operand, or its transpose; ONE: the right operand has no
-    // second half.
-    template <bool TRANS, bool ONE>
-    __device__ __forceinline__ void by_tri(const char *x, const Split (&b)[2], f32x4 (&c)[4]) const {
+    // A triangular operand's fragments, or its transpose's, and its product;
+    // ONE: the right operand has no second half.
+    struct Tri {
         f16x8 hi[4][2], lo[4][2];
+    };
+    template <bool TRANS>
+    __device__ __forceinline__ void tri_load(const char *x, Tri &f) const {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -270,12 +273,15 @@ struct Scan {
                 if (TRANS ? s < mt / 2 : s > mt / 2) continue;
                 if constexpr (TRANS) {
                     const char *p = x + tri_lower(2 * s, mt / 2) * 1024, *q = x + tri_lower(2 * s + 1, mt / 2) * 1024;
-                    hi[mt][s] = trans_at(p, q, mt, tl), lo[mt][s] = trans_at(p + kTri * 1024, q + kTri * 1024, mt, tl);
+                    f.hi[mt][s] = trans_at(p, q, mt, tl), f.lo[mt][s] = trans_at(p + kTri * 1024, q + kTri * 1024, mt, tl);
                 } else {
                     const char *p = x + tri_lower(mt, s) * 1024;
-                    hi[mt][s] = frag_at(p), lo[mt][s] = frag_at(p + kTri * 1024);
+                    f.hi[mt][s] = frag_at(p), f.lo[mt][s] = frag_at(p + kTri * 1024);
                 }
             }
+    }
+    template <bool TRANS, bool ONE>
+    __device__ __forceinline__ static void tri_mul(const Tri &f, const Split (&b)[2], f32x4 (&c)[4]) {
         zero(c);
 #pragma unroll
         for (int k = 0; k < 3; ++k)
@@ -284,8 +290,14 @@ struct Scan {
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     if ((TRANS ? s < mt / 2 : s > mt / 2) || (ONE && k == 1)) continue;
-                    c[mt] = mma(k == 0 ? lo[mt][s] : hi[mt][s], k == 1 ? b[s].lo : b[s].hi, c[mt]);
+                    c[mt] = mma(k == 0 ? f.lo[mt][s] : f.hi[mt][s], k == 1 ? b[s].lo : b[s].hi, c[mt]);
                 }
+    }
+    template <bool TRANS, bool ONE>
+    __device__ __forceinline__ void by_tri(const char *x, const Split (&b)[2], f32x4 (&c)[4]) const {
+        Tri f;
+        tri_load<TRANS>(x, f);
+        tri_mul<TRANS, ONE>(f, b, c);
     }
 };
 
@@ -299,33 +311,48 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, D
     __shared__ __align__(16) char lds[W::kLds];
     W w;
     if (!w.place(A, groups)) return;
-    if (w.w == NW) return w.template copy<false>(A, B, vec, lds);
+    if (w.w == NW) return w.template copy<false, 2>(A, B, vec, lds);
     const int tile = w.c0 / 16 + w.w;
     const bool kept = SAVE && tile < B.dvp / 16;
     f32x4 st[MT];
     w.load_state(A, A.state, st);
     float smax = max_of(st);
+    // The last product of a chunk, P U, waits for the next chunk, whose own
+    // first product has to wait for the state to be split.
+    typename W::Tri pf = {};
+    Split ub[2] = {};
+    f32x4 o[4];
+    float iu = 0.f;
+    zero(o);
+    auto finish = [&](int64_t c) {
+        f32x4 y[4];
+        W::template tri_mul<false, false>(pf, ub, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += y[i] * iu;
+        w.results(lds + W::kOuts + (c & 1) * W::kTile, o);
+    };
     for (int64_t c = 0; c < w.chunks; ++c) {
         W::next_chunk();
         const char *x = lds + (W::STAGES == 2 ? c & 1 : 0) * W::kStage;
         const float *f = (const float *)(x + W::kRows) + 4 * w.g;
         const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
         auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
-        const int64_t vh = (w.base + c) * A.Hv + w.h;
-        f32x4 z[4], y[4], o[4];
+        f32x4 z[4], y[4];
         w.values(lds + W::kVals + (c & 1) * W::kTile, z);
-        float is, iz, iu, iw;
+        float is, iz, iw;
         smax = col_max(smax);
         const float ss = pow2_to(smax, kTop, &is);
         if constexpr (SAVE) {
             if (kept) {
+                const int64_t vh = (w.base + c) * A.Hv + w.h;
                 w.keep(B.S + vh * DKP * B.dvp, tile, st);
                 const float mx = tile_max(smax);
                 if ((threadIdx.x & 63) == 0) B.Smax[vh * (B.dvp / 16) + tile] = mx;
             }
         }
-        Split sb[KS], zb[2], ub[2], wb[2];
+        Split sb[KS], zb[2], wb[2];
         split_by(st, ss, sb);
+        finish(c - 1);  // (before the first chunk: zeros, which nobody takes)
         zero(y);
         zero(o);
 #pragma unroll
@@ -340,7 +367,8 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, D
         iz *= sc[SC_IT];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] *= iz;
-        if (kept) w.keep(B.Y + vh * kC * B.dvp, tile, y);
+        if constexpr (SAVE)
+            if (kept) w.keep(B.Y + ((w.base + c) * A.Hv + w.h) * kC * B.dvp, tile, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = y[i] * row(ROW_F3B, i);
         split_by(z, pow2_to(zmax * sc[SC_TF3], kBound, &iw), wb);
@@ -357,14 +385,15 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, D
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] *= row(ROW_B, i);
+        for (int i = 0; i < 4; ++i) {
+            y[i] *= row(ROW_B, i);
+            o[i] *= row(ROW_F2, i) * is;
+        }
         split_by(y, pow2_to(zmax * sc[SC_TB], kBound, &iu), ub);
-        w.template by_tri<false, false>(x + W::kP, ub, y);
         iu *= sc[SC_IP];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * (row(ROW_F2, i) * is) + y[i] * iu;
-        w.results(lds + W::kOuts + (c & 1) * W::kTile, o);
+        w.template tri_load<false>(x + W::kP, pf);
     }
+    finish(w.chunks - 1);
     CONVLOWER_WAIT_LDS();
     block_barrier();
     w.store_state(A, A.state_out, st);
@@ -378,7 +407,7 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_grad_kernel(DeltaArgs
     __shared__ __align__(16) char lds[W::kLds];
     W w;
     if (!w.place(A, groups)) return;
-    if (w.w == NW) return w.template copy<true>(A, B, vec, lds);
+    if (w.w == NW) return w.template copy<true, 1>(A, B, vec, lds);
     const int tile = w.c0 / 16 + w.w;
     const bool kept = tile < B.dvp / 16;
     f32x4 G[MT];
