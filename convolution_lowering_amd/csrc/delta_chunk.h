@@ -88,11 +88,12 @@ enum TpScalar {
     SC_LAST = 0,  // e^gam_C
     SC_IT = 1,    // 1 / (the inverse's factor)
     SC_IP = 2,    // 1 / (P's factor)
-    SC_TB = 3,    // 64 max |inverse| max |b|
+    SC_T = 3,     // 64 max |inverse|
     SC_TF3 = 4,   // 64 max |inverse| max |f3 b|
     SC_TF1 = 5,   // 64 max |inverse| max |f1 b|
     SC_F2 = 6,    // max |f2|
 };
+// P stands with its columns times b on the way forward (P U = (P b) Y).
 constexpr int kTpRows = 4 * kTri * kFrag * 2;  // bytes before the factors
 constexpr int kTpBytes = kTpRows + 2048;
 
@@ -142,11 +143,26 @@ __device__ __forceinline__ float pow2_to(float m, int t, float *inv) {
 }
 constexpr int kTop = 11;     // split operands: largest value in [2^11, 2^12)
 constexpr int kBound = 14;   // those with a bound: the bound in [2^14, 2^15)
-constexpr int kRowTop = 8;   // rows of q and k: products of 128 of them and a split operand stay far below f32's end
+// Rows of q and k: largest value in [1, 2).  What f16 then loses of a bf16 or
+// f16 row is below 2^-25 of its largest value.
+constexpr int kRowTop = 0;
+constexpr float kRowSum = 2.f * kC;  // so |K' u| <= kRowSum max |u|
 
 struct Split {
     f16x8 hi, lo;
 };
+// Two pieces of four rows that are in f16's range already.
+__device__ __forceinline__ Split split8(f32x4 a, f32x4 b) {
+    typedef float f32x8 __attribute__((ext_vector_type(8)));
+    const f32x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    float one = 1.f;
+    asm("" : "+v"(one));  // or the multiply-add is taken apart again
+    Split r;
+    r.hi = __builtin_convertvector(v, f16x8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.lo[j] = (_Float16)fmaf(v[j], one, -(float)r.hi[j]);
+    return r;
+}
 __device__ __forceinline__ Split split8(f32x4 a, f32x4 b, float scale) {
     Split r;
 #pragma unroll
@@ -173,23 +189,25 @@ __device__ __forceinline__ f32x4 mma_in(const _Float16 *p, int half, const Split
     if constexpr (SPLIT) return mma3(a, *(const f16x8 *)(p + half), b, c);
     return mma2(a, b, c);
 }
+// (NaN if there is one: two values an instruction, without quieting them first)
+__device__ __forceinline__ float max2(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float max4(f32x4 v, float m) {
-    return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))), m);
+    return max2(max2(fabsf(v[2]), fabsf(v[3])), max2(max2(fabsf(v[0]), fabsf(v[1])), m));
 }
 // Largest over the four lane groups: of one column of a result.
 __device__ __forceinline__ float col_max(float m) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     const uint32_t a = __float_as_uint(m);
     const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(a, a, false, false));
-    const uint32_t b = __float_as_uint(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])));
+    const uint32_t b = __float_as_uint(max2(__uint_as_float(x[0]), __uint_as_float(x[1])));
     const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(b, b, false, false));
-    return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+    return max2(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 // Largest over a wavefront.
 template <int CTRL>
 __device__ __forceinline__ float dpp_max(float m) {
     const int x = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), CTRL, 0xf, 0xf, true);
-    return fmaxf(m, __builtin_bit_cast(float, x));
+    return max2(m, __builtin_bit_cast(float, x));
 }
 __device__ __forceinline__ float tile_max(float m) {
     m = dpp_max<0x121>(m);  // row_ror 1, 2, 4, 8: the 16 lanes of a group

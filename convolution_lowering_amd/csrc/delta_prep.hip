@@ -145,9 +145,9 @@ __device__ __forceinline__ void invert(const float *m, float *x, float *tmp) {
     __syncthreads();
 }
 
-// The triangular matrix in LDS as six left operands in two halves, to one or
-// two places.  Six wavefront-sized pieces over four wavefronts.
-__device__ __forceinline__ void store_tri(const float *x, float scale, char *out, char *out2) {
+// The triangular matrix in LDS as six left operands in two halves.  Six
+// wavefront-sized pieces over four wavefronts.
+__device__ __forceinline__ void store_tri(const float *x, float scale, char *out) {
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     for (int f = threadIdx.x >> 6; f < kTri; f += 4) {
         const int mt = f < 2 ? f : f / 2 + 1, s = f < 2 ? 0 : f % 2;
@@ -156,10 +156,6 @@ __device__ __forceinline__ void store_tri(const float *x, float scale, char *out
         const int at = (f * kFrag + lane * 8) * 2;
         *(f16x8 *)(out + at) = v.hi;
         *(f16x8 *)(out + at + kTri * kFrag * 2) = v.lo;
-        if (out2) {
-            *(f16x8 *)(out2 + at) = v.hi;
-            *(f16x8 *)(out2 + at + kTri * kFrag * 2) = v.lo;
-        }
     }
 }
 
@@ -256,13 +252,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             const float rise = expf((float)s);
             const float f1 = rk[lane] * rise, f2 = rq[lane] * rise, f3 = rk[lane] * expf((float)(all - s));
             const float last = expf((float)all);
-            mf[0] = wave_max(fabsf(b)), mf[1] = wave_max(fabsf(f3 * b));
-            mf[2] = wave_max(fabsf(f1 * b)), mf[3] = wave_max(fabsf(f2));
+            mf[0] = wave_max(fabsf(f3 * b)), mf[1] = wave_max(fabsf(f1 * b)), mf[2] = wave_max(fabsf(f2));
             auto put = [&](char *tp) {
                 float *f = (float *)(tp + kTpRows) + lane;
                 f[ROW_F1 * kC] = f1, f[ROW_F2 * kC] = f2, f[ROW_F3 * kC] = f3, f[ROW_B * kC] = b;
                 f[ROW_F3B * kC] = f3 * b, f[ROW_F1B * kC] = f1 * b;
-                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last, f[ROW_SCALARS * kC + SC_F2] = mf[3];
+                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last, f[ROW_SCALARS * kC + SC_F2] = mf[2];
             };
             put(tp);
             if (GRAD) {
@@ -278,20 +273,28 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             float l = 0.f, p = 0.f;
             if (j <= i) {
                 const float d = expf((float)(sg[i] - sg[j]));
-                p = qk[i * kLd + j] * d;
+                p = qk[i * kLd + j] * d * (GRAD ? 1.f : sb[j]);
                 if (j < i) l = kk[i * kLd + j] * d * sb[j];
             }
             lm[i * kLd + j] = l;
             xi[i * kLd + j] = p;
             mp = fmaxf(mp, fabsf(p));
         }
-        float inv;
-        float sc = pow2_to(block_max(mp, red), kTop, &inv);
-        store_tri(xi, sc, tp + kTpRows / 2, GRAD ? tpg + kTpRows / 2 : nullptr);
-        if (tid == 0) {
-            ((float *)(tp + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
-            if (GRAD) ((float *)(tpg + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
+        float inv, sc;
+        if (GRAD) {
+            sc = pow2_to(block_max(mp, red), kTop, &inv);
+            store_tri(xi, sc, tpg + kTpRows / 2);
+            if (tid == 0) ((float *)(tpg + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
+            __syncthreads();
+            mp = 0.f;
+            for (int e = tid; e < kC * kC; e += 256) {
+                const float p = xi[(e >> 6) * kLd + (e & 63)] *= sb[e & 63];
+                mp = fmaxf(mp, fabsf(p));
+            }
         }
+        sc = pow2_to(block_max(mp, red), kTop, &inv);
+        store_tri(xi, sc, tp + kTpRows / 2);
+        if (tid == 0) ((float *)(tp + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
         for (int way = 0; way < (GRAD ? 2 : 1); ++way) {
             __syncthreads();
             if (way) {  // b beside the row instead of the column
@@ -306,11 +309,11 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             for (int e = tid; e < kC * kC; e += 256) mp = fmaxf(mp, fabsf(xi[(e >> 6) * kLd + (e & 63)]));
             mp = block_max(mp, red);
             sc = pow2_to(mp, kTop, &inv);
-            store_tri(xi, sc, way ? tpg : tp, nullptr);
+            store_tri(xi, sc, way ? tpg : tp);
             if (tid == 0) {
                 float *o = (float *)((way ? tpg : tp) + kTpRows) + ROW_SCALARS * kC;
                 o[SC_IT] = inv;
-                o[SC_TB] = kC * mp * mf[0], o[SC_TF3] = kC * mp * mf[1], o[SC_TF1] = kC * mp * mf[2];
+                o[SC_T] = kC * mp, o[SC_TF3] = kC * mp * mf[0], o[SC_TF1] = kC * mp * mf[1];
             }
         }
         __syncthreads();

@@ -24,6 +24,11 @@ __device__ __forceinline__ void zero(f32x4 (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
+// A block has fewer threads; but with room for 512 in a kernel's bounds the
+// compiler keeps to 256 registers and leaves products' results among the
+// ordinary ones (otherwise 160 moves a chunk from the others).
+constexpr int kScanBounds = 512;
+
 // What a block works on, and where things lie.
 template <typename S, int DKP, int NW>
 struct Scan {
@@ -220,41 +225,54 @@ struct Scan {
 
     // Products with what lies in LDS.  Consecutive products go to different
     // results, so that none waits for the one before it.
-    __device__ __forceinline__ static void by_rows(const char *x, int s, const Split &b, f32x4 (&c)[4]) {
-        f16x8 f[4];
+    struct Rows {
+        f16x8 f[KS][4];
+    };
+    __device__ __forceinline__ static void rows_load(const char *x, int s0, int s1, Rows &f) {
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) f[mt] = frag_at(x + (mt * KS + s) * 1024);
+        for (int s = s0; s < s1; ++s)
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f[mt], b.lo, c[mt]);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f[mt], b.hi, c[mt]);
-        if constexpr (SPLIT) {
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) f[mt] = frag_at(x + kMat + (mt * KS + s) * 1024);
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f[mt], b.hi, c[mt]);
-        }
+            for (int mt = 0; mt < 4; ++mt) f.f[s][mt] = frag_at(x + (mt * KS + s) * 1024);
     }
-    // Rows 16 mt.. of the transpose, four tiles of them from mt.
-    __device__ __forceinline__ void by_cols(const char *x, int mt, const Split (&b)[2], f32x4 (&c)[4]) const {
+    __device__ __forceinline__ static void rows_mul(const char *x, const Rows &f, const Split (&b)[KS], f32x4 (&c)[4]) {
         zero(c);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            f16x8 f[4];
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f.f[s][mt], b[s].lo, c[mt]);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) c[mt] = mma(f.f[s][mt], b[s].hi, c[mt]);
+            if constexpr (SPLIT) {
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) c[mt] = mma(frag_at(x + kMat + (mt * KS + s) * 1024), b[s].hi, c[mt]);
+            }
+        }
+    }
+    // Rows 16 mt.. of the transpose (four tiles of them) times b, added to c.
+    struct Cols {
+        f16x8 f[2][4];
+    };
+    __device__ __forceinline__ void cols_load(const char *x, int mt, Cols &f) const {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const char *p = x + (2 * s * KS + (mt + i) / 2) * 1024;
-                f[i] = trans_at(p, p + KS * 1024, mt + i, tl);
+                f.f[s][i] = trans_at(p, p + KS * 1024, mt + i, tl);
             }
+    }
+    __device__ __forceinline__ void cols_mul(const char *x, int mt, const Cols &f, const Split (&b)[2], f32x4 (&c)[MT]) const {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = mma(f[i], b[s].lo, c[i]);
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[i] = mma(f[i], b[s].hi, c[i]);
+            for (int i = 0; i < 4; ++i) c[mt + i] = mma(f.f[s][i], b[s].lo, c[mt + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[mt + i] = mma(f.f[s][i], b[s].hi, c[mt + i]);
             if constexpr (SPLIT) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const char *p = x + kMat + (2 * s * KS + (mt + i) / 2) * 1024;
-                    c[i] = mma(trans_at(p, p + KS * 1024, mt + i, tl), b[s].hi, c[i]);
+                    c[mt + i] = mma(trans_at(p, p + KS * 1024, mt + i, tl), b[s].hi, c[mt + i]);
                 }
             }
         }
@@ -264,20 +282,17 @@ struct Scan {
     struct Tri {
         f16x8 hi[4][2], lo[4][2];
     };
+    static constexpr int kLo = kTri * 1024;  // from a triangular operand's first half to its second
     template <bool TRANS>
-    __device__ __forceinline__ void tri_load(const char *x, Tri &f) const {
+    __device__ __forceinline__ void tri_load(const char *x, f16x8 (&f)[4][2]) const {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
                 if (TRANS ? s < mt / 2 : s > mt / 2) continue;
-                if constexpr (TRANS) {
-                    const char *p = x + tri_lower(2 * s, mt / 2) * 1024, *q = x + tri_lower(2 * s + 1, mt / 2) * 1024;
-                    f.hi[mt][s] = trans_at(p, q, mt, tl), f.lo[mt][s] = trans_at(p + kTri * 1024, q + kTri * 1024, mt, tl);
-                } else {
-                    const char *p = x + tri_lower(mt, s) * 1024;
-                    f.hi[mt][s] = frag_at(p), f.lo[mt][s] = frag_at(p + kTri * 1024);
-                }
+                if constexpr (TRANS)
+                    f[mt][s] = trans_at(x + tri_lower(2 * s, mt / 2) * 1024, x + tri_lower(2 * s + 1, mt / 2) * 1024, mt, tl);
+                else f[mt][s] = frag_at(x + tri_lower(mt, s) * 1024);
             }
     }
     template <bool TRANS, bool ONE>
@@ -290,22 +305,17 @@ struct Scan {
 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     if ((TRANS ? s < mt / 2 : s > mt / 2) || (ONE && k == 1)) continue;
-                    c[mt] = mma(k == 0 ? f.lo[mt][s] : f.hi[mt][s], k == 1 ? b[s].lo : b[s].hi, c[mt]);
+                    c[mt] = mma(k == 2 ? f.lo[mt][s] : f.hi[mt][s], k == 1 ? b[s].lo : b[s].hi, c[mt]);
                 }
-    }
-    template <bool TRANS, bool ONE>
-    __device__ __forceinline__ void by_tri(const char *x, const Split (&b)[2], f32x4 (&c)[4]) const {
-        Tri f;
-        tri_load<TRANS>(x, f);
-        tri_mul<TRANS, ONE>(f, b, c);
     }
 };
 
-// Power of two for a column whose largest value is in m (four lane groups).
-__device__ __forceinline__ float col_scale(float m, float *inv) { return pow2_to(col_max(m), kTop, inv); }
+// A phase of a chunk ends here: its accesses to LDS, which serve the next
+// one, are not moved into that.
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
 template <typename S, int DKP, int NW, bool SAVE>
-__global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
+__global__ __launch_bounds__(kScanBounds) void delta_scan_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
     typedef Scan<S, DKP, NW> W;
     constexpr int MT = W::MT, KS = W::KS;
     __shared__ __align__(16) char lds[W::kLds];
@@ -314,21 +324,30 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, D
     if (w.w == NW) return w.template copy<false, 2>(A, B, vec, lds);
     const int tile = w.c0 / 16 + w.w;
     const bool kept = SAVE && tile < B.dvp / 16;
+    // The state, each column times a power of two that keeps it in f16's
+    // range; is: the inverse.  What a chunk adds is bounded before it is
+    // known, and comes in the same measure.
     f32x4 st[MT];
     w.load_state(A, A.state, st);
-    float smax = max_of(st);
-    // The last product of a chunk, P U, waits for the next chunk, whose own
-    // first product has to wait for the state to be split.
+    float is, smax = col_max(max_of(st));
+    {
+        const float s = pow2_to(smax, kTop, &is);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) st[i] *= s;
+        smax *= s;
+    }
+    // The last product of a chunk, (P b) Y, waits for the next chunk, whose
+    // own first product has to wait for the state to be split.
     typename W::Tri pf = {};
-    Split ub[2] = {};
+    Split yb[2] = {};
     f32x4 o[4];
-    float iu = 0.f;
+    float iy = 0.f;
     zero(o);
     auto finish = [&](int64_t c) {
         f32x4 y[4];
-        W::template tri_mul<false, false>(pf, ub, y);
+        W::template tri_mul<false, false>(pf, yb, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += y[i] * iu;
+        for (int i = 0; i < 4; ++i) o[i] += y[i] * iy;
         w.results(lds + W::kOuts + (c & 1) * W::kTile, o);
     };
     for (int64_t c = 0; c < w.chunks; ++c) {
@@ -337,71 +356,97 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_kernel(DeltaArgs A, D
         const float *f = (const float *)(x + W::kRows) + 4 * w.g;
         const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
         auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
-        f32x4 z[4], y[4];
-        w.values(lds + W::kVals + (c & 1) * W::kTile, z);
-        float is, iz, iw;
-        smax = col_max(smax);
-        const float ss = pow2_to(smax, kTop, &is);
+        // the state in two halves; the chunk before is finished meanwhile
+        f32x4 z[4], y[4], f1[4], f2[4];
+        typename W::Rows kf, qf;
+        W::rows_load(x, 0, KS / 2, kf);
         if constexpr (SAVE) {
             if (kept) {
                 const int64_t vh = (w.base + c) * A.Hv + w.h;
-                w.keep(B.S + vh * DKP * B.dvp, tile, st);
-                const float mx = tile_max(smax);
+                f32x4 s[MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) s[i] = st[i] * is;
+                w.keep(B.S + vh * DKP * B.dvp, tile, s);
+                const float mx = tile_max(smax * is);
                 if ((threadIdx.x & 63) == 0) B.Smax[vh * (B.dvp / 16) + tile] = mx;
             }
         }
         Split sb[KS], zb[2], wb[2];
-        split_by(st, ss, sb);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) sb[s] = split8(st[2 * s], st[2 * s + 1]);
         finish(c - 1);  // (before the first chunk: zeros, which nobody takes)
-        zero(y);
-        zero(o);
+        phase();
+        // K S
+        W::rows_load(x, KS / 2, KS, kf);
+        w.values(lds + W::kVals + (c & 1) * W::kTile, z);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) W::by_rows(x, s, sb[s], y);
+        for (int i = 0; i < 4; ++i) f1[i] = row(ROW_F1, i);
+        W::rows_load(x + W::kIn / 2, 0, KS / 2, qf);
+        W::rows_mul(x, kf, sb, y);
+        phase();
+        // Q S; Z
+        typename W::Tri tf;
+        W::rows_load(x + W::kIn / 2, KS / 2, KS, qf);
+        w.template tri_load<false>(x + W::kTi, tf.hi);
+        const float last = sc[SC_LAST], it = sc[SC_IT], ip = sc[SC_IP], bt = sc[SC_T], bw = sc[SC_TF3];
+        W::rows_mul(x + W::kIn / 2, qf, sb, o);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) W::by_rows(x + W::kIn / 2, s, sb[s], o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] -= y[i] * (row(ROW_F1, i) * is);
+        for (int i = 0; i < 4; ++i) z[i] -= y[i] * (f1[i] * is);
+        float iz;
         const float zmax = col_max(max_of(z));
         split_by(z, pow2_to(zmax, kTop, &iz), zb);
-        w.template by_tri<false, false>(x + W::kTi, zb, y);
-        iz *= sc[SC_IT];
+        iz *= it;
+        phase();
+        // Y
+        typename W::Cols kc[MT / 4];
+        w.template tri_load<false>(x + W::kTi + W::kLo, tf.lo);
+        f32x4 f3b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] *= iz;
-        if constexpr (SAVE)
-            if (kept) w.keep(B.Y + ((w.base + c) * A.Hv + w.h) * kC * B.dvp, tile, y);
+        for (int i = 0; i < 4; ++i) f3b[i] = row(ROW_F3B, i), f2[i] = row(ROW_F2, i);
+        w.cols_load(x, 0, kc[0]);
+        W::template tri_mul<false, false>(tf, zb, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = y[i] * row(ROW_F3B, i);
-        split_by(z, pow2_to(zmax * sc[SC_TF3], kBound, &iw), wb);
-        const float last = sc[SC_LAST];
-        smax = 0.f;
+        for (int i = 0; i < 4; ++i) o[i] *= f2[i] * is;
+        // the next power of two, and the state in it
+        const float ss = pow2_to(smax * is * last + kRowSum * (zmax * bw), kBound, &iy);
+        const float step = last * (ss * is);
+        is = iy;
 #pragma unroll
-        for (int mt = 0; mt < MT; mt += 4) {
-            f32x4 d[4];
-            w.by_cols(x, mt, wb, d);
+        for (int i = 0; i < MT; ++i) st[i] *= step;
+        phase();
+        // W, and K' W into the state
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                st[mt + i] = st[mt + i] * last + d[i] * iw;
-                smax = max4(st[mt + i], smax);
+        for (int i = 0; i < 4; ++i) z[i] = y[i] * f3b[i];
+        split_by(z, iz * ss, wb);
+        if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
+        phase();
+        w.template tri_load<false>(x + W::kP, pf.hi);
+        w.template tri_load<false>(x + W::kP + W::kLo, pf.lo);
+#pragma unroll
+        for (int i = 0; i < MT / 4; ++i) w.cols_mul(x, 4 * i, kc[i], wb, st);
+        if constexpr (SAVE) {
+            if (kept) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = y[i] * iz;
+                w.keep(B.Y + ((w.base + c) * A.Hv + w.h) * kC * B.dvp, tile, z);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[i] *= row(ROW_B, i);
-            o[i] *= row(ROW_F2, i) * is;
-        }
-        split_by(y, pow2_to(zmax * sc[SC_TB], kBound, &iu), ub);
-        iu *= sc[SC_IP];
-        w.template tri_load<false>(x + W::kP, pf);
+        split_by(y, iz * pow2_to(zmax * bt, kBound, &iy), yb);
+        iy *= ip;
+        phase();
+        smax = col_max(max_of(st));
     }
     finish(w.chunks - 1);
     CONVLOWER_WAIT_LDS();
     block_barrier();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) st[i] *= is;
     w.store_state(A, A.state_out, st);
 }
 
 // From the last chunk to the first, with G, the gradient of the state.
 template <typename S, int DKP, int NW>
-__global__ __launch_bounds__(64 * NW + 64) void delta_scan_grad_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
+__global__ __launch_bounds__(kScanBounds) void delta_scan_grad_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
     typedef Scan<S, DKP, NW> W;
     constexpr int MT = W::MT, KS = W::KS;
     __shared__ __align__(16) char lds[W::kLds];
@@ -412,7 +457,13 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_grad_kernel(DeltaArgs
     const bool kept = tile < B.dvp / 16;
     f32x4 G[MT];
     w.load_state(A, A.dstate_out, G);
-    float gmax = max_of(G);
+    float is, gmax = col_max(max_of(G));
+    {
+        const float s = pow2_to(gmax, kTop, &is);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) G[i] *= s;
+        gmax *= s;
+    }
     for (int64_t j = 0; j < w.chunks; ++j) {
         W::next_chunk();
         const char *x = lds + (W::STAGES == 2 ? j & 1 : 0) * W::kStage;
@@ -420,60 +471,91 @@ __global__ __launch_bounds__(64 * NW + 64) void delta_scan_grad_kernel(DeltaArgs
         const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
         auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
         const int64_t vh = (w.base + w.chunks - 1 - j) * A.Hv + w.h;
-        f32x4 d[4], y[4], e[4];
+        f32x4 d[4], y[4], e[4], f3[4], f1b[4], f2[4], b[4];
+        typename W::Rows kf;
+        typename W::Tri pf, tf;
+        W::rows_load(x, 0, KS / 2, kf);
         w.values(lds + W::kVals + (j & 1) * W::kTile, d);
-        float ig, id, ie, iy;
-        gmax = col_max(gmax);
-        const float gs = pow2_to(gmax, kTop, &ig);
+        w.template tri_load<true>(x + W::kP, pf.hi);
+        w.template tri_load<true>(x + W::kP + W::kLo, pf.lo);
         if (kept) {
-            w.keep(B.G + vh * DKP * B.dvp, tile, G);
-            const float mx = tile_max(gmax);
+            f32x4 s[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) s[i] = G[i] * is;
+            w.keep(B.G + vh * DKP * B.dvp, tile, s);
+            const float mx = tile_max(gmax * is);
             if ((threadIdx.x & 63) == 0) B.Gmax[vh * (B.dvp / 16) + tile] = mx;
         }
+        float id, ie;
         Split gb[KS], db[2], eb[2], yb[2];
-        split_by(G, gs, gb);
-        zero(e);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) W::by_rows(x, s, gb[s], e);
-        // 16-bit dO is exact in one half
+        for (int s = 0; s < KS; ++s) gb[s] = split8(G[2 * s], G[2 * s + 1]);
+        phase();
+        // K G, P' dO (16-bit dO is exact in one half)
+        W::rows_load(x, KS / 2, KS, kf);
+        w.template tri_load<true>(x + W::kTi, tf.hi);
+        w.template tri_load<true>(x + W::kTi + W::kLo, tf.lo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f3[i] = row(ROW_F3, i), f2[i] = row(ROW_F2, i);
+        const float last = sc[SC_LAST], it = sc[SC_IT], ip = sc[SC_IP], bf1 = sc[SC_TF1], bf2 = sc[SC_F2];
+        W::rows_mul(x, kf, gb, e);
         const float dmax = col_max(max_of(d));
         split_by(d, pow2_to(dmax, kTop, &id), db);
-        w.template by_tri<true, !W::SPLIT>(x + W::kP, db, y);
-        id *= sc[SC_IP];
+        W::template tri_mul<true, !W::SPLIT>(pf, db, y);
+        id *= ip;
+        phase();
+        // X, E
+        typename W::Cols kc, qc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = e[i] * (row(ROW_F3, i) * ig) + y[i] * id;
+        for (int i = 0; i < 4; ++i) e[i] = e[i] * (f3[i] * is) + y[i] * id;
         const float emax = col_max(max_of(e));
         split_by(e, pow2_to(emax, kTop, &ie), eb);
-        w.template by_tri<true, false>(x + W::kTi, eb, e);
-        ie *= sc[SC_IT];
+        ie *= it;
+        w.cols_load(x, 0, kc);
+        phase();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f1b[i] = row(ROW_F1B, i), b[i] = row(ROW_B, i);
+        W::template tri_mul<true, false>(tf, eb, e);
+        float ig;
+        const float ss = pow2_to(gmax * is * last + kRowSum * (emax * bf1 + dmax * bf2), kBound, &ig);
+        const float step = last * (ss * is);
+        is = ig;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) G[i] *= step;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] *= f2[i];
+        split_by(d, ss, db);
+        w.cols_load(x + W::kIn / 2, 0, qc);
+        phase();
+        // dS = .. + Q' (f2 dO) - K' (f1 b E)
+        w.cols_mul(x + W::kIn / 2, 0, qc, db, G);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             e[i] *= ie;
-            y[i] = e[i] * row(ROW_F1B, i);
-            d[i] *= row(ROW_F2, i);
+            y[i] = e[i] * f1b[i];
         }
-        split_by(y, pow2_to(emax * sc[SC_TF1], kBound, &iy), yb);
-        split_by(d, pow2_to(dmax * sc[SC_F2], kBound, &id), db);
-        const float last = sc[SC_LAST];
-        gmax = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < MT; mt += 4) {
-            f32x4 p[4], q[4];
-            w.by_cols(x, mt, yb, q);
-            w.by_cols(x + W::kIn / 2, mt, db, p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                G[mt + i] = G[mt + i] * last + p[i] * id - q[i] * iy;
-                gmax = max4(G[mt + i], gmax);
-            }
+        split_by(y, -ss, yb);
+        phase();
+        w.cols_mul(x, 0, kc, yb, G);
+        if (MT > 4) {
+            w.cols_load(x, 4, kc);
+            w.cols_load(x + W::kIn / 2, 4, qc);
         }
         if (kept) w.keep(B.E + vh * kC * B.dvp, tile, e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] *= row(ROW_B, i);  // dZ
+        for (int i = 0; i < 4; ++i) e[i] *= b[i];  // dZ
         w.results(lds + W::kOuts + (j & 1) * W::kTile, e);
+        phase();
+        if (MT > 4) {
+            w.cols_mul(x + W::kIn / 2, 4, qc, db, G);
+            w.cols_mul(x, 4, kc, yb, G);
+        }
+        gmax = col_max(max_of(G));
     }
     CONVLOWER_WAIT_LDS();
     block_barrier();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) G[i] *= is;
     w.store_state(A, A.dstate, G);
 }
 
