@@ -64,7 +64,7 @@ struct DeltaBuf {
     _Float16 *kq;  // [slots][Hk][K, Q][planes][64 * dkp] as left operands
     char *tp;      // [slots][Hv] of kTpBytes: the inverse, P, and the rows' factors
     char *tpg;     // the same for the way back (saved): the other inverse, P, factors
-    float *rowk;   // saved: [slots][Hk][4][64]: factor of k's row, k's norm, the same of q
+    float *rowk;   // saved: [slots][Hk][4][64]: factor of k's row, 1 / k's norm, the same of q
     double *gam;   // saved: [slots][Hv][64]
     float *S, *Y;  // saved: [slots][Hv], [dkp][dvp] and [64][dvp] in result order
     float *Smax;   // saved: [slots][Hv][dvp / 16]: largest |S| of the tile
@@ -214,6 +214,14 @@ __device__ __forceinline__ float tile_max(float m) {
     m = dpp_max<0x122>(m);
     m = dpp_max<0x124>(m);
     return col_max(dpp_max<0x128>(m));
+}
+// Sum over the 16 lanes of a group, to all of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    return dpp_add<0x121>(dpp_add<0x122>(dpp_add<0x124>(dpp_add<0x128>(v))));
 }
 // Right operands of 32 rows each from a result of N tiles of 16 rows.
 template <int N>

@@ -11,7 +11,8 @@
 //
 // since e^gam_i stands beside q_i and k_i as a row, e^-gam_i beside k_i as a
 // column.  A block takes one chunk of one query/key head and adds up the value
-// heads that share it; its four wavefronts take 16 tokens each.
+// heads that share it; each of its eight wavefronts takes 16 tokens and half
+// of the key columns.
 //
 // S, G, Y and E come in result order, one column and four rows a lane.  They
 // are put into LDS as [column][row], split in two, and read as operands by the
@@ -77,10 +78,12 @@ __device__ __forceinline__ Split slab_split(const _Float16 *hi, const _Float16 *
     return r;
 }
 
-template <typename S, int DKP, bool GROUP>
-__global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBuf B, bool vec) {
+// The sums of several value heads are kept in one place; what one head adds to
+// a dot product is the difference of two.
+template <typename S, int DKP>
+__global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B, bool vec, bool vec_out) {
     constexpr bool SPLIT = sizeof(S) == 4;
-    constexpr int KS = DKP / 32, MT = DKP / 16, PL = SPLIT ? 2 : 1, MAT = kC * DKP * 2, IN = 2 * PL * MAT;
+    constexpr int KS = DKP / 32, MT = DKP / 16, MH = MT / 2, PL = SPLIT ? 2 : 1, MAT = kC * DKP * 2, IN = 2 * PL * MAT;
     constexpr int SLD = DKP + 8;
     constexpr int kState = 2 * kSlab * SLD * 2, kDF = 2 * kC * kLd * 4, kTok = 4 * kSlab * kTokLd * 2;
     // a slab of S or G, then D and F
@@ -91,37 +94,45 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
     float *dm = (float *)first, *fm = dm + kC * kLd;
     _Float16 *uh = (_Float16 *)second, *ul = uh + kSlab * kTokLd, *eh = ul + kSlab * kTokLd, *el = eh + kSlab * kTokLd;
     const char *kq = second;
-    __shared__ __align__(16) float sb[kC], rise[kC], fall[kC], rk[kC], nk[kC], rq[kC], nq[kC], dgam[kC];
-    __shared__ __align__(16) float dbs[4][kC], red[4], mx[2][4];
+    __shared__ __align__(16) float sb[kC], rise[kC], fall[kC], rk[kC], nk[kC], uq[kC], rq[kC], nq[kC], dgam[2][kC];
+    __shared__ __align__(16) float dbs[4][kC], red[8], mx[2][8], sums[2][2][kC];
     __shared__ double sg[kC];
-    const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int w = tid >> 6 & 3, hf = __builtin_amdgcn_readfirstlane(tid >> 8);  // rows 16 w.., columns 16 MH hf..
     const int g = lane >> 4, m = lane & 15, tl = trans_lane(), so = trans_off<SLD>(), to = trans_off<kTokLd>();
     const DeltaChunk ch = chunk_of(A.s, slot);
     if (ch.len == 0) return;
     const int64_t head = (int64_t)slot * A.Hk + hk;
     if (tid < kC) {
         const float *o = B.rowk + head * 4 * kC + tid;
-        rk[tid] = o[0], nk[tid] = o[kC], rq[tid] = o[2 * kC], nq[tid] = o[3 * kC];
+        rk[tid] = o[0], nk[tid] = o[kC], uq[tid] = o[2 * kC], nq[tid] = o[3 * kC];
+        rq[tid] = uq[tid] * A.scale;
     }
     const int row = 16 * w + m;  // this lane's row of left operands
     const bool in = row < ch.len;
-    // k or q with its norm (q with the scale too), four rows of column 16 nt + m as results lie
-    auto unit = [&](const char *x, const float *rho, int nt) {
-        const char *p = x + (w * KS + nt / 2) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + ((nt & 1) * 4 + (m & 3)) * 2;
-        f32x4 v;
+    // x . (k or q with its norm; q with the scale too) of four rows, over this wavefront's columns
+    auto dot = [&](const char *x, const float *rho, const f32x4 (&v)[MH]) {
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            v[r] = (float)*(const _Float16 *)(p + r * 16);
-            if (SPLIT) v[r] += (float)*(const _Float16 *)(p + MAT + r * 16);
+        for (int i = 0; i < MH; ++i) {
+            const int nt = MH * hf + i;
+            const char *p = x + (w * KS + nt / 2) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + ((nt & 1) * 4 + (m & 3)) * 2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float u = (float)*(const _Float16 *)(p + r * 16);
+                if (SPLIT) u += (float)*(const _Float16 *)(p + MAT + r * 16);
+                sum[r] = fmaf(u, v[i][r], sum[r]);
+            }
         }
-        return v * *(const f32x4 *)(rho + 16 * w + 4 * g);
-    };
-    f32x4 dqt[GROUP ? MT : 1], dkt[GROUP ? MT : 1], dotq = {0.f, 0.f, 0.f, 0.f}, dotk = dotq;
-    f32x4 dq[MT], dk[MT], gu[MT];
-    if constexpr (GROUP)
+        sum *= *(const f32x4 *)(rho + 16 * w + 4 * g);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) dqt[i] = dkt[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int rep = GROUP ? A.Hv / A.Hk : 1;
+        for (int r = 0; r < 4; ++r) sum[r] = group_sum(sum[r]);
+        return sum;
+    };
+    f32x4 dq[MH], dk[MH], gu[MH], dotq = {0.f, 0.f, 0.f, 0.f}, dotr = dotq, dotc = dotq;
+#pragma unroll
+    for (int i = 0; i < MH; ++i) dq[i] = dk[i] = gu[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int rep = A.Hv / A.Hk;
     for (int v = 0; v < rep; ++v) {
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
@@ -136,23 +147,23 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
             fall[tid] = expf((float)(all - x));
             sb[tid] = fac[ROW_B * kC + tid];
         }
+        if (hf == 0) dbs[w][lane] = 0.f;
         const float last = fac[ROW_SCALARS * kC + SC_LAST];
-        f32x4 dp[4], dl[4], dbp[4];
+        f32x4 dp[2], dl[2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) dq[i] = dk[i] = gu[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dp[i] = dl[i] = dbp[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 2; ++i) dp[i] = dl[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         float sgsum = 0.f;
         __syncthreads();
+        const f32x4 up = *(const f32x4 *)(rise + 16 * w + 4 * g), down = *(const f32x4 *)(fall + 16 * w + 4 * g);
         for (int c0 = 0; c0 < B.dvp; c0 += kSlab) {
-            const int tile = c0 / 16 + w;  // this wavefront's columns of the slab: 16 w..
-            f32x4 s4[MT], y4[4], e4[4];
+            const int tile = c0 / 16 + w;  // this wavefront's columns of the slab: 16 w.., and half their rows
+            f32x4 s4[MH], y4[2], e4[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y4[i] = *(const f32x4 *)(gY + (tile * 4 + i) * 256);
+            for (int i = 0; i < 2; ++i) y4[i] = *(const f32x4 *)(gY + (tile * 4 + 2 * hf + i) * 256);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e4[i] = *(const f32x4 *)(gE + (tile * 4 + i) * 256);
+            for (int i = 0; i < 2; ++i) e4[i] = *(const f32x4 *)(gE + (tile * 4 + 2 * hf + i) * 256);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) s4[i] = *(const f32x4 *)(gS + (tile * MT + i) * 256);
+            for (int i = 0; i < MH; ++i) s4[i] = *(const f32x4 *)(gS + (tile * MT + MH * hf + i) * 256);
             float xo[2][8];
             const S *po = (const S *)A.d_o + (ch.t0 + (in ? row : 0)) * A.dos + (int64_t)h * A.dv + c0 + 8 * g;
 #pragma unroll
@@ -171,58 +182,50 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
             float smax = 0.f, gmax = 0.f, is, ig, iu, ie;
 #pragma unroll
             for (int i = 0; i < kSlab / 16; ++i) {
-                smax = fmaxf(smax, B.Smax[vh * (B.dvp / 16) + c0 / 16 + i]);
-                gmax = fmaxf(gmax, B.Gmax[vh * (B.dvp / 16) + c0 / 16 + i]);
+                smax = max2(smax, B.Smax[vh * (B.dvp / 16) + c0 / 16 + i]);
+                gmax = max2(gmax, B.Gmax[vh * (B.dvp / 16) + c0 / 16 + i]);
             }
             const float ss = pow2_to(smax, kTop, &is), sgs = pow2_to(gmax, kTop, &ig);
             float um = 0.f, em = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 b = *(const f32x4 *)(sb + 16 * i + 4 * g);
-                dbp[i] += y4[i] * e4[i];
+            for (int i = 0; i < 2; ++i) {
+                const int t = 16 * (2 * hf + i) + 4 * g;
+                const f32x4 b = *(const f32x4 *)(sb + t);
+                f32x4 p = y4[i] * e4[i];  // b's gradient
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[r] = group_sum(p[r]);
+                if (m == 0) *(f32x4 *)&dbs[w][t] += p;
                 y4[i] *= b;    // U
                 e4[i] *= -b;   // -dZ
                 um = max4(y4[i], um);
                 em = max4(e4[i], em);
             }
             um = tile_max(um), em = tile_max(em);
-            if (lane == 0) mx[0][w] = um, mx[1][w] = em;
+            if (lane == 0) mx[0][tid >> 6] = um, mx[1][tid >> 6] = em;
             __syncthreads();  // mx; and the slab before is done with
-            const float us = pow2_to(fmaxf(fmaxf(mx[0][0], mx[0][1]), fmaxf(mx[0][2], mx[0][3])), kTop, &iu);
-            const float es = pow2_to(fmaxf(fmaxf(mx[1][0], mx[1][1]), fmaxf(mx[1][2], mx[1][3])), kTop, &ie);
+            const float us = pow2_to(max4(*(const f32x4 *)mx[0], max4(*(const f32x4 *)(mx[0] + 4), 0.f)), kTop, &iu);
+            const float es = pow2_to(max4(*(const f32x4 *)mx[1], max4(*(const f32x4 *)(mx[1] + 4), 0.f)), kTop, &ie);
             const int col = 16 * w + m;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int o = col * kTokLd + 16 * i + 4 * g;
+            for (int i = 0; i < 2; ++i) {
+                const int o = col * kTokLd + 16 * (2 * hf + i) + 4 * g;
                 put4(y4[i], us, uh + o, ul + o);
                 put4(e4[i], es, eh + o, el + o);
             }
 #pragma unroll
-            for (int i = 0; i < MT; ++i) put4(s4[i], ss, sh + col * SLD + 16 * i + 4 * g, sl + col * SLD + 16 * i + 4 * g);
-            // G of the same place, on its way while S is worked with
-            f32x4 g4[MT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i) g4[i] = *(const f32x4 *)(gG + (tile * MT + i) * 256);
+            for (int i = 0; i < MH; ++i) {
+                const int o = col * SLD + 16 * (MH * hf + i) + 4 * g;
+                put4(s4[i], ss, sh + o, sl + o);
+            }
             Split fo[2];
-            const f32x4 io = split_rows(xo, fo);
+            f32x4 io = split_rows(xo, fo);
             __syncthreads();
             Split fe[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) fe[s] = slab_split<kTokLd>(eh, el, w, s, to);
 #pragma unroll
-            for (int nt = 0; nt < MT; ++nt) {
-                f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const Split x = slab_split<SLD>(sh, sl, nt, s, so);
-                    a = SPLIT ? mma_split(fo[s], x, a) : mma2(fo[s].hi, x, a);
-                    b = mma_split(fe[s], x, b);
-                }
-                dq[nt] += a * (io * is);
-                dk[nt] += b * (ie * is);
-            }
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
+            for (int i = 0; i < 2; ++i) {
+                const int nt = 2 * hf + i;
                 if (nt > w) continue;
                 f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
@@ -231,40 +234,52 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
                     a = SPLIT ? mma_split(fo[s], x, a) : mma2(fo[s].hi, x, a);
                     b = mma_split(fe[s], x, b);
                 }
-                dp[nt] += a * (io * iu);
-                dl[nt] += b * (ie * iu);
+                dp[i] += a * (io * iu);
+                dl[i] += b * (ie * iu);
             }
+            io *= up * is;
+            const f32x4 je = up * (ie * is);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int i = 0; i < MH; ++i) {
+                f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sgsum = fmaf(s4[i][r], g4[i][r], sgsum);
+                for (int s = 0; s < 2; ++s) {
+                    const Split x = slab_split<SLD>(sh, sl, MH * hf + i, s, so);
+                    a = SPLIT ? mma_split(fo[s], x, a) : mma2(fo[s].hi, x, a);
+                    b = mma_split(fe[s], x, b);
+                }
+                dq[i] += a * io;
+                dk[i] += b * je;
+            }
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < MT; ++i) put4(g4[i], sgs, sh + col * SLD + 16 * i + 4 * g, sl + col * SLD + 16 * i + 4 * g);
+            for (int i = 0; i < MH; ++i) s4[i] = *(const f32x4 *)(gG + (tile * MT + MH * hf + i) * 256);
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < MH; ++i) {  // in the place of this lane's S
+                const int o = col * SLD + 16 * (MH * hf + i) + 4 * g;
+                _Float16 *h = sh + o, *l = sl + o;
+                const f16x4 a = *(const f16x4 *)h, b = *(const f16x4 *)l;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) part = fmaf(s4[i][r], (float)a[r] + (float)b[r], part);
+                put4(s4[i], sgs, h, l);
+            }
+            sgsum = fmaf(part, is, sgsum);
             __syncthreads();
             Split fu[2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) fu[s] = slab_split<kTokLd>(uh, ul, w, s, to);
+            const f32x4 ju = down * (iu * ig);
 #pragma unroll
-            for (int nt = 0; nt < MT; ++nt) {
+            for (int i = 0; i < MH; ++i) {
                 f32x4 a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) a = mma_split(fu[s], slab_split<SLD>(sh, sl, nt, s, so), a);
-                gu[nt] += a * (iu * ig);
+                for (int s = 0; s < 2; ++s) a = mma_split(fu[s], slab_split<SLD>(sh, sl, MH * hf + i, s, so), a);
+                gu[i] += a * ju;
             }
         }
-        // db over the columns: 16 lanes, then the wavefronts
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) dbp[i][r] += __shfl_xor(dbp[i][r], d, 64);
-        if (m == 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *(f32x4 *)&dbs[w][16 * i + 4 * g] = dbp[i];
         __syncthreads();
-        copy_in<4, IN / 1024>((const char *)B.kq + head * IN, second);
+        copy_in<8, IN / 1024>((const char *)B.kq + head * IN, second);
         if (tid < ch.len) {
             const float db = (dbs[0][tid] + dbs[1][tid]) + (dbs[2][tid] + dbs[3][tid]);
             const int64_t th = (ch.t0 + tid) * A.Hv + h;
@@ -273,30 +288,24 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
         }
         // D and F, the decays in place
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = 16 * w + 4 * g + r, j = 16 * nt + m;
+                const int i = 16 * w + 4 * g + r, j = 16 * (2 * hf + t) + m;
                 const float d = j <= i ? expf((float)(sg[i] - sg[j])) : 0.f;
-                dm[i * kLd + j] = j <= i ? dp[nt][r] * d : 0.f;
-                fm[i * kLd + j] = j < i ? dl[nt][r] * d : 0.f;
+                dm[i * kLd + j] = j <= i ? dp[t][r] * d : 0.f;
+                fm[i * kLd + j] = j < i ? dl[t][r] * d : 0.f;
             }
         CONVLOWER_WAIT_VMCNT_LDS(0);  // the copies
         __syncthreads();
-        const f32x4 up = *(const f32x4 *)(rise + 16 * w + 4 * g), down = *(const f32x4 *)(fall + 16 * w + 4 * g);
-        f32x4 dot = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int nt = 0; nt < MT; ++nt) {
-            dq[nt] *= up;
-            dk[nt] *= up;
-            gu[nt] *= down;
-            dot += gu[nt] * unit(kq, rk, nt);
-        }
         // <S', G> = e^gam_C <S, G> + sum_j k_j . (its column part from the state)
-        float end = last * sgsum + dot[0] + dot[1] + dot[2] + dot[3];
+        {
+            const f32x4 x = dot(kq, rk, gu) - dotc;
+            float end = last * sgsum + (m == 0 ? x[0] + x[1] + x[2] + x[3] : 0.f);
 #pragma unroll
-        for (int d = 32; d > 0; d >>= 1) end += __shfl_xor(end, d, 64);
-        if (lane == 0) red[w] = end;
+            for (int d = 32; d > 0; d >>= 1) end += __shfl_xor(end, d, 64);
+            if (lane == 0) red[tid >> 6] = end;
+        }
         // products inside the chunk: D and F by K, their transposes by Q and K
         Split fa[2], fb[2];
         float xa[2][8], xb[2][8];
@@ -309,9 +318,9 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
                 xb[s][j] = fm[row * kLd + c] * rk[c];
             }
         f32x4 ia = split_rows(xa, fa), ib = split_rows(xb, fb);
-        f32x4 dg = {0.f, 0.f, 0.f, 0.f}, dr = dg, dc = dg;
 #pragma unroll
-        for (int nt = 0; nt < MT; ++nt) {
+        for (int i = 0; i < MH; ++i) {
+            const int nt = MH * hf + i;
             f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -325,10 +334,8 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
                     b = mma(fb[s].hi, y, b);
                 }
             }
-            dq[nt] += a * ia;
-            dk[nt] += b * ib;
-            dg += dq[nt] * unit(kq + IN / 2, rq, nt);
-            dr += dk[nt] * unit(kq, rk, nt);
+            dq[i] += a * ia;
+            dk[i] += b * ib;
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -341,7 +348,8 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
         ia = split_rows(xa, fa);
         ib = split_rows(xb, fb);
 #pragma unroll
-        for (int nt = 0; nt < MT; ++nt) {
+        for (int i = 0; i < MH; ++i) {
+            const int nt = MH * hf + i;
             f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -354,28 +362,18 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
                     b = mma(fb[s].hi, trans_at(p + MAT, p + MAT + KS * 1024, nt, tl), b);
                 }
             }
-            gu[nt] += a * ia + b * ib;
-            dc += gu[nt] * unit(kq, rk, nt);
-            dk[nt] += gu[nt];
+            gu[i] += a * ia + b * ib;
         }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                dg[r] += __shfl_xor(dg[r], d, 64);
-                dr[r] += __shfl_xor(dr[r], d, 64);
-                dc[r] += __shfl_xor(dc[r], d, 64);
-            }
-        dotq += dg;
-        dotk += dr + dc;
-        if constexpr (GROUP)
-#pragma unroll
-            for (int nt = 0; nt < MT; ++nt) dqt[nt] += dq[nt], dkt[nt] += dk[nt];
-        if (m == 0) *(f32x4 *)(dgam + 16 * w + 4 * g) = dg + dr - dc;
+        const f32x4 oq = dotq, orr = dotr, oc = dotc;
+        dotq = dot(kq + IN / 2, rq, dq);
+        dotr = dot(kq, rk, dk);
+        dotc = dot(kq, rk, gu);
+        if (m == 0) *(f32x4 *)(dgam[hf] + 16 * w + 4 * g) = (dotq - oq) + (dotr - orr) - (dotc - oc);
         __syncthreads();
-        if (w == 0) {  // sums from each token to the chunk's end
-            double x = dgam[lane];
-            if (lane == 63) x += (double)red[0] + red[1] + red[2] + red[3];
+        if (tid < 64) {  // sums from each token to the chunk's end
+            double x = (double)dgam[0][lane] + dgam[1][lane];
+            if (lane == 63)
+                for (int i = 0; i < 8; ++i) x += red[i];
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double o = __shfl_down(x, d, 64);
@@ -384,36 +382,61 @@ __global__ __launch_bounds__(256, 1) void delta_grad_kernel(DeltaArgs A, DeltaBu
             if (lane < ch.len) A.dg[(ch.t0 + lane) * A.Hv + h] = (float)x;
         }
     }
-    // back through the scale and the norms: x / |x| of a unit row is the row's value over the scale
-    const f32x4 vq = *(const f32x4 *)(nq + 16 * w + 4 * g), vk = *(const f32x4 *)(nk + 16 * w + 4 * g);
+    // Back through the norms: a unit row is K's or Q's with its factor.  The
+    // rows leave by way of LDS, 16 bytes a lane.
+    constexpr int OLD = DKP + 16 / sizeof(S);
+    S *rows = (S *)first;
+    auto leave = [&](const char *x, const float *rho, const float *norm, const f32x4 (&v)[MH], f32x4 dots, float scale, S *out) {
+        const f32x4 rh = *(const f32x4 *)(rho + 16 * w + 4 * g), nv = *(const f32x4 *)(norm + 16 * w + 4 * g);
 #pragma unroll
-    for (int nt = 0; nt < MT; ++nt) {
-        f32x4 x = (GROUP ? dqt[GROUP ? nt : 0] : dq[nt]), y = (GROUP ? dkt[GROUP ? nt : 0] : dk[nt]);
-        x *= A.scale;
-        const int c = 16 * nt + m;
+        for (int i = 0; i < MH; ++i) {
+            const int nt = MH * hf + i;
+            const char *p = x + (w * KS + nt / 2) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + ((nt & 1) * 4 + (m & 3)) * 2;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 16 * w + 4 * g + r;
-            if (t >= ch.len || c >= A.dk) continue;
-            float a = x[r], b = y[r];
-            if (A.qk_norm) {
-                const int64_t qo = (ch.t0 + t) * A.qs + (int64_t)hk * A.dk + c, ko = (ch.t0 + t) * A.ks + (int64_t)hk * A.dk + c;
-                a = vq[r] * (a - mix_f32(((const S *)A.q)[qo]) * vq[r] * dotq[r]);
-                b = vk[r] * (b - mix_f32(((const S *)A.k)[ko]) * vk[r] * dotk[r]);
+            for (int r = 0; r < 4; ++r) {
+                float o = v[i][r] * scale;
+                if (A.qk_norm) {
+                    float u = (float)*(const _Float16 *)(p + r * 16);
+                    if (SPLIT) u += (float)*(const _Float16 *)(p + MAT + r * 16);
+                    o = nv[r] * (o - u * rh[r] * dots[r]);
+                }
+                rows[(16 * w + 4 * g + r) * OLD + 16 * nt + m] = mix_out<S>(o);
             }
-            const int64_t o = ((ch.t0 + t) * A.Hk + hk) * A.dk + c;
-            ((S *)A.dq)[o] = mix_out<S>(a);
-            ((S *)A.dk_out)[o] = mix_out<S>(b);
         }
-    }
+        __syncthreads();
+        S *to = out + (ch.t0 * A.Hk + hk) * A.dk;
+        constexpr int V = 16 / sizeof(S);
+        if (vec_out) {
+            for (int i = tid; i < kC * DKP / V; i += 512) {
+                const int t = i / (DKP / V), c = i % (DKP / V) * V;
+                if (t < ch.len && c < A.dk)
+                    *(MixVec<S, V> *)(to + (int64_t)t * A.Hk * A.dk + c) = *(const MixVec<S, V> *)(rows + t * OLD + c);
+            }
+        } else {
+            for (int i = tid; i < kC * DKP; i += 512) {
+                const int t = i / DKP, c = i % DKP;
+                if (t < ch.len && c < A.dk) to[(int64_t)t * A.Hk * A.dk + c] = rows[t * OLD + c];
+            }
+        }
+        __syncthreads();
+    };
+    const int at = 16 * w + 4 * g;
+    if (m == 0) *(f32x4 *)(sums[0][hf] + at) = dotq, *(f32x4 *)(sums[1][hf] + at) = dotr + dotc;
+    __syncthreads();
+    const f32x4 sq = *(const f32x4 *)(sums[0][0] + at) + *(const f32x4 *)(sums[0][1] + at);
+    const f32x4 sk = *(const f32x4 *)(sums[1][0] + at) + *(const f32x4 *)(sums[1][1] + at);
+    leave(kq + IN / 2, uq, nq, dq, sq, A.scale, (S *)A.dq);
+#pragma unroll
+    for (int i = 0; i < MH; ++i) gu[i] += dk[i];
+    leave(kq, rk, nk, gu, sk, 1.f, (S *)A.dk_out);
 }
 
 template <typename S, int DKP>
 hipError_t grad_run(const DeltaArgs &a, const DeltaBuf &b, hipStream_t st) {
     const dim3 grid(b.slots, a.Hk);
     const bool vec = a.dv % 8 == 0 && a.dos % 8 == 0 && (uintptr_t)a.d_o % (8 * sizeof(S)) == 0;
-    if (a.Hv > a.Hk) hipLaunchKernelGGL((delta_grad_kernel<S, DKP, true>), grid, dim3(256), 0, st, a, b, vec);
-    else hipLaunchKernelGGL((delta_grad_kernel<S, DKP, false>), grid, dim3(256), 0, st, a, b, vec);
+    const bool vec_out = a.dk * sizeof(S) % 16 == 0 && (uintptr_t)a.dq % 16 == 0 && (uintptr_t)a.dk_out % 16 == 0;
+    hipLaunchKernelGGL((delta_grad_kernel<S, DKP>), grid, dim3(512), 0, st, a, b, vec, vec_out);
     return hipGetLastError();
 }
 

@@ -20,7 +20,7 @@ constexpr int kLd = 68;  // floats from row to row of the 64 x 64 matrices in LD
 // largest value and its sum of squares, and leaves it in LDS as f16.
 template <typename S, int DKP, bool SPLIT>
 __device__ __forceinline__ void load_rows(const S *src, int64_t stride, const DeltaChunk &ch, int dk, bool vec, int norm,
-                                          float scale, _Float16 *dst, float *rho, float *rnorm) {
+                                          _Float16 *dst, float *rho, float *rnorm) {
     constexpr int Q = DKP / 4, V = 16 / sizeof(S), LD = DKP + 8;
     const int row = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * Q;
     float f[Q];
@@ -65,7 +65,7 @@ __device__ __forceinline__ void load_rows(const S *src, int64_t stride, const De
     if ((threadIdx.x & 3) == 0) {
         const float r = norm ? 1.f / sqrtf(ss + kDeltaEps) : 1.f;
         rnorm[row] = r;
-        rho[row] = inv * r * scale;
+        rho[row] = inv * r;
     }
 }
 
@@ -169,19 +169,21 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
     _Float16 *sk = (_Float16 *)both, *sq = sk + PL * kC * LD;
     float *lm = (float *)both, *xi = lm + kC * kLd, *tmp = xi + kC * kLd;
     __shared__ __align__(16) float kk[kC * kLd], qk[kC * kLd];
-    __shared__ float rk[kC], nk[kC], rq[kC], nq[kC], sb[kC], red[4];
+    __shared__ float rk[kC], nk[kC], uq[kC], rq[kC], nq[kC], sb[kC], red[4];
     __shared__ double sg[kC];
     const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const DeltaChunk ch = chunk_of(A.s, slot);
     if (ch.len == 0) return;
-    load_rows<S, DKP, SPLIT>((const S *)A.k + (int64_t)hk * A.dk, A.ks, ch, A.dk, vec, A.qk_norm, 1.f, sk, rk, nk);
-    load_rows<S, DKP, SPLIT>((const S *)A.q + (int64_t)hk * A.dk, A.qs, ch, A.dk, vec, A.qk_norm, A.scale, sq, rq, nq);
+    load_rows<S, DKP, SPLIT>((const S *)A.k + (int64_t)hk * A.dk, A.ks, ch, A.dk, vec, A.qk_norm, sk, rk, nk);
+    load_rows<S, DKP, SPLIT>((const S *)A.q + (int64_t)hk * A.dk, A.qs, ch, A.dk, vec, A.qk_norm, sq, uq, nq);
+    __syncthreads();
+    if (tid < kC) rq[tid] = uq[tid] * A.scale;
     __syncthreads();
     const int64_t head = (int64_t)slot * A.Hk + hk;
     const int64_t at = head * 2 * PL * kC * DKP;
     if (GRAD && tid < kC) {
         float *o = B.rowk + head * 4 * kC + tid;
-        o[0] = rk[tid], o[kC] = nk[tid], o[2 * kC] = rq[tid], o[3 * kC] = nq[tid];
+        o[0] = rk[tid], o[kC] = nk[tid], o[2 * kC] = uq[tid], o[3 * kC] = nq[tid];
     }
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl) {
