@@ -98,8 +98,11 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
     __shared__ __align__(16) float dbs[4][kC], red[8], mx[2][8], sums[2][2][kC];
     __shared__ double sg[kC];
     const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
-    const int w = tid >> 6 & 3, hf = __builtin_amdgcn_readfirstlane(tid >> 8);  // rows 16 w.., columns 16 MH hf..
-    const int g = lane >> 4, m = lane & 15, tl = trans_lane(), so = trans_off<SLD>(), to = trans_off<kTokLd>();
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6 & 3), hf = __builtin_amdgcn_readfirstlane(tid >> 8);  // rows 16 w.., columns 16 MH hf..
+    // Lane numbers, renewed in each part of the loops: or the compiler keeps some
+    // hundred LDS addresses made of them in registers throughout, and spills.
+    int g = lane >> 4, m = lane & 15, tl = trans_lane(), so = trans_off<SLD>(), to = trans_off<kTokLd>();
+    auto renew = [&] { asm volatile("" : "+v"(g), "+v"(m), "+v"(tl), "+v"(so), "+v"(to)); };
     const DeltaChunk ch = chunk_of(A.s, slot);
     if (ch.len == 0) return;
     const int64_t head = (int64_t)slot * A.Hk + hk;
@@ -108,15 +111,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         rk[tid] = o[0], nk[tid] = o[kC], uq[tid] = o[2 * kC], nq[tid] = o[3 * kC];
         rq[tid] = uq[tid] * A.scale;
     }
-    const int row = 16 * w + m;  // this lane's row of left operands
-    const bool in = row < ch.len;
+    // this wavefront's columns: where they begin in K' (fragments), in K (this lane's element) and in a slab of S
+    const int fo0 = hf * (MH / 2) * 1024;
+    const _Float16 *shh = sh + 16 * MH * hf, *slh = sl + 16 * MH * hf;
     // x . (k or q with its norm; q with the scale too) of four rows, over this wavefront's columns
     auto dot = [&](const char *x, const float *rho, const f32x4 (&v)[MH]) {
         f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < MH; ++i) {
-            const int nt = MH * hf + i;
-            const char *p = x + (w * KS + nt / 2) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + ((nt & 1) * 4 + (m & 3)) * 2;
+            const char *p = x + (w * KS + hf * (MH / 2)) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + (m & 3) * 2 + (i / 2) * 1024 + (i & 1) * 8;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float u = (float)*(const _Float16 *)(p + r * 16);
@@ -132,12 +135,58 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
     f32x4 dq[MH], dk[MH], gu[MH], dotq = {0.f, 0.f, 0.f, 0.f}, dotr = dotq, dotc = dotq;
 #pragma unroll
     for (int i = 0; i < MH; ++i) dq[i] = dk[i] = gu[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int rep = A.Hv / A.Hk;
+    const int rep = A.Hv / A.Hk, slabs = B.dvp / kSlab;
+    // What a slab begins with, fetched while the one before it is worked with.
+    // Buffer loads: the base in scalar registers, one offset for all of them.
+    // (Any spill in here would wait for these loads.)
+    const int l16 = lane * 16;
+    auto load4 = [&](__amdgpu_buffer_rsrc_t r, int at) {
+        return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, l16, at, 0));
+    };
+    const int do_at = 16 * w + m < ch.len ? (16 * w + m) * (int)A.dos * (int)sizeof(S) + 8 * g * (int)sizeof(S) : (int)kOutOfRange;
+    f32x4 s4[MH], y4[2], e4[2];
+    typedef MixVec<S, 8> Do8;
+    Do8 do8[2];
+    auto fetch = [&](int v, int slab) {
+        const int64_t vh = (int64_t)slot * A.Hv + hk * rep + v;
+        const int tile = slab * (kSlab / 16) + w;  // this wavefront's columns of the slab: 16 w.., and half their rows
+        const __amdgpu_buffer_rsrc_t ry = make_rsrc(B.Y + vh * kC * B.dvp, 0x7fffffff);
+        const __amdgpu_buffer_rsrc_t re = make_rsrc(B.E + vh * kC * B.dvp, 0x7fffffff);
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(B.S + vh * DKP * B.dvp, 0x7fffffff);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y4[i] = load4(ry, (tile * 4 + 2 * hf + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) e4[i] = load4(re, (tile * 4 + 2 * hf + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < MH; ++i) s4[i] = load4(rs, (tile * MT + MH * hf + i) * 1024);
+        const __amdgpu_buffer_rsrc_t rd = make_rsrc((const S *)A.d_o + ch.t0 * A.dos + (int64_t)(hk * rep + v) * A.dv, 0x7fffffff);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int c = slab * kSlab + 32 * s;  // and 8 g
+            if (vec) {
+                const int at = c + 8 * g < A.dv ? do_at : (int)kOutOfRange;
+                if constexpr (sizeof(S) == 2) {
+                    do8[s] = __builtin_bit_cast(Do8, __builtin_amdgcn_raw_buffer_load_b128(rd, at, c * 2, 0));
+                } else {
+                    ((uint4 *)&do8[s])[0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rd, at, c * 4, 0));
+                    ((uint4 *)&do8[s])[1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rd, at, c * 4 + 16, 0));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int at = c + 8 * g + j < A.dv ? do_at : (int)kOutOfRange;
+                    if constexpr (sizeof(S) == 2)
+                        do8[s].v[j] = __builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b16(rd, at, (c + j) * 2, 0));
+                    else do8[s].v[j] = __builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b32(rd, at, (c + j) * 4, 0));
+                }
+            }
+        }
+    };
+    fetch(0, 0);
     for (int v = 0; v < rep; ++v) {
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
-        const float *gS = B.S + vh * DKP * B.dvp + lane * 4, *gG = B.G + vh * DKP * B.dvp + lane * 4;
-        const float *gY = B.Y + vh * kC * B.dvp + lane * 4, *gE = B.E + vh * kC * B.dvp + lane * 4;
+        const __amdgpu_buffer_rsrc_t rg = make_rsrc(B.G + vh * DKP * B.dvp, 0x7fffffff);
         const float *fac = (const float *)(B.tpg + vh * kTpBytes + kTpRows);
         __syncthreads();
         if (tid < kC) {
@@ -155,30 +204,17 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         float sgsum = 0.f;
         __syncthreads();
         const f32x4 up = *(const f32x4 *)(rise + 16 * w + 4 * g), down = *(const f32x4 *)(fall + 16 * w + 4 * g);
-        for (int c0 = 0; c0 < B.dvp; c0 += kSlab) {
-            const int tile = c0 / 16 + w;  // this wavefront's columns of the slab: 16 w.., and half their rows
-            f32x4 s4[MH], y4[2], e4[2];
+        for (int slab = 0; slab < slabs; ++slab) {
+            renew();
+            const int c0 = slab * kSlab;
+            f32x4 g4[MH];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) y4[i] = *(const f32x4 *)(gY + (tile * 4 + 2 * hf + i) * 256);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) e4[i] = *(const f32x4 *)(gE + (tile * 4 + 2 * hf + i) * 256);
-#pragma unroll
-            for (int i = 0; i < MH; ++i) s4[i] = *(const f32x4 *)(gS + (tile * MT + MH * hf + i) * 256);
+            for (int i = 0; i < MH; ++i) g4[i] = load4(rg, ((c0 / 16 + w) * MT + MH * hf + i) * 1024);
             float xo[2][8];
-            const S *po = (const S *)A.d_o + (ch.t0 + (in ? row : 0)) * A.dos + (int64_t)h * A.dv + c0 + 8 * g;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (vec) {
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) xo[s][j] = 0.f;
-                    if (c0 + 32 * s + 8 * g < A.dv) mix_load<S, 8>(po + 32 * s, xo[s]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) xo[s][j] = c0 + 32 * s + 8 * g + j < A.dv ? mix_f32(po[32 * s + j]) : 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) xo[s][j] = in ? xo[s][j] : 0.f;
-            }
+                for (int j = 0; j < 8; ++j) xo[s][j] = mix_f32(do8[s].v[j]);
             float smax = 0.f, gmax = 0.f, is, ig, iu, ie;
 #pragma unroll
             for (int i = 0; i < kSlab / 16; ++i) {
@@ -219,6 +255,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             }
             Split fo[2];
             f32x4 io = split_rows(xo, fo);
+            if (slab + 1 < slabs) fetch(v, slab + 1);
+            else if (v + 1 < rep) fetch(v + 1, 0);
             __syncthreads();
             Split fe[2];
 #pragma unroll
@@ -244,7 +282,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                 f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const Split x = slab_split<SLD>(sh, sl, MH * hf + i, s, so);
+                    const Split x = slab_split<SLD>(shh, slh, i, s, so);
                     a = SPLIT ? mma_split(fo[s], x, a) : mma2(fo[s].hi, x, a);
                     b = mma_split(fe[s], x, b);
                 }
@@ -252,8 +290,6 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                 dk[i] += b * je;
             }
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < MH; ++i) s4[i] = *(const f32x4 *)(gG + (tile * MT + MH * hf + i) * 256);
             float part = 0.f;
 #pragma unroll
             for (int i = 0; i < MH; ++i) {  // in the place of this lane's S
@@ -261,8 +297,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                 _Float16 *h = sh + o, *l = sl + o;
                 const f16x4 a = *(const f16x4 *)h, b = *(const f16x4 *)l;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) part = fmaf(s4[i][r], (float)a[r] + (float)b[r], part);
-                put4(s4[i], sgs, h, l);
+                for (int r = 0; r < 4; ++r) part = fmaf(g4[i][r], (float)a[r] + (float)b[r], part);
+                put4(g4[i], sgs, h, l);
             }
             sgsum = fmaf(part, is, sgsum);
             __syncthreads();
@@ -274,11 +310,13 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             for (int i = 0; i < MH; ++i) {
                 f32x4 a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) a = mma_split(fu[s], slab_split<SLD>(sh, sl, MH * hf + i, s, so), a);
+                for (int s = 0; s < 2; ++s) a = mma_split(fu[s], slab_split<SLD>(shh, slh, i, s, so), a);
                 gu[i] += a * ju;
             }
         }
         __syncthreads();
+        renew();
+        const int row = 16 * w + m;  // this lane's row of left operands
         copy_in<8, IN / 1024>((const char *)B.kq + head * IN, second);
         if (tid < ch.len) {
             const float db = (dbs[0][tid] + dbs[1][tid]) + (dbs[2][tid] + dbs[3][tid]);
@@ -320,16 +358,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         f32x4 ia = split_rows(xa, fa), ib = split_rows(xb, fb);
 #pragma unroll
         for (int i = 0; i < MH; ++i) {
-            const int nt = MH * hf + i;
             f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const char *p = kq + (2 * s * KS + nt / 2) * 1024;
-                const f16x8 x = trans_at(p, p + KS * 1024, nt, tl);
+                const char *p = kq + fo0 + (2 * s * KS + i / 2) * 1024;
+                const f16x8 x = trans_at(p, p + KS * 1024, i, tl);
                 a = mma(fa[s].hi, x, mma(fa[s].lo, x, a));
                 b = mma(fb[s].hi, x, mma(fb[s].lo, x, b));
                 if constexpr (SPLIT) {
-                    const f16x8 y = trans_at(p + MAT, p + MAT + KS * 1024, nt, tl);
+                    const f16x8 y = trans_at(p + MAT, p + MAT + KS * 1024, i, tl);
                     a = mma(fa[s].hi, y, a);
                     b = mma(fb[s].hi, y, b);
                 }
@@ -349,21 +386,21 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         ib = split_rows(xb, fb);
 #pragma unroll
         for (int i = 0; i < MH; ++i) {
-            const int nt = MH * hf + i;
             f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const char *p = kq + (2 * s * KS + nt / 2) * 1024, *q = p + IN / 2;
-                const f16x8 x = trans_at(q, q + KS * 1024, nt, tl), y = trans_at(p, p + KS * 1024, nt, tl);
+                const char *p = kq + fo0 + (2 * s * KS + i / 2) * 1024, *q = p + IN / 2;
+                const f16x8 x = trans_at(q, q + KS * 1024, i, tl), y = trans_at(p, p + KS * 1024, i, tl);
                 a = mma(fa[s].hi, x, mma(fa[s].lo, x, a));
                 b = mma(fb[s].hi, y, mma(fb[s].lo, y, b));
                 if constexpr (SPLIT) {
-                    a = mma(fa[s].hi, trans_at(q + MAT, q + MAT + KS * 1024, nt, tl), a);
-                    b = mma(fb[s].hi, trans_at(p + MAT, p + MAT + KS * 1024, nt, tl), b);
+                    a = mma(fa[s].hi, trans_at(q + MAT, q + MAT + KS * 1024, i, tl), a);
+                    b = mma(fb[s].hi, trans_at(p + MAT, p + MAT + KS * 1024, i, tl), b);
                 }
             }
             gu[i] += a * ia + b * ib;
         }
+        renew();
         const f32x4 oq = dotq, orr = dotr, oc = dotc;
         dotq = dot(kq + IN / 2, rq, dq);
         dotr = dot(kq, rk, dk);
@@ -390,8 +427,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         const f32x4 rh = *(const f32x4 *)(rho + 16 * w + 4 * g), nv = *(const f32x4 *)(norm + 16 * w + 4 * g);
 #pragma unroll
         for (int i = 0; i < MH; ++i) {
-            const int nt = MH * hf + i;
-            const char *p = x + (w * KS + nt / 2) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + ((nt & 1) * 4 + (m & 3)) * 2;
+            const char *p = x + (w * KS + hf * (MH / 2)) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + (m & 3) * 2 + (i / 2) * 1024 + (i & 1) * 8;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float o = v[i][r] * scale;
@@ -400,7 +436,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                     if (SPLIT) u += (float)*(const _Float16 *)(p + MAT + r * 16);
                     o = nv[r] * (o - u * rh[r] * dots[r]);
                 }
-                rows[(16 * w + 4 * g + r) * OLD + 16 * nt + m] = mix_out<S>(o);
+                rows[(16 * w + 4 * g + r) * OLD + 16 * (MH * hf + i) + m] = mix_out<S>(o);
             }
         }
         __syncthreads();
