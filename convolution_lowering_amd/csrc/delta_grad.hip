@@ -144,7 +144,9 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, l16, at, 0));
     };
     const int do_at = 16 * w + m < ch.len ? (16 * w + m) * (int)A.dos * (int)sizeof(S) + 8 * g * (int)sizeof(S) : (int)kOutOfRange;
-    f32x4 s4[MH], y4[2], e4[2];
+    f32x4 s4[MH], y4[2], e4[2], smax4, gmax4;
+    double gam_t = 0., gam_end = 0.;  // of a head's first slab: this thread's token and the last
+    float b_t = 0.f, last = 0.f;
     typedef MixVec<S, 8> Do8;
     Do8 do8[2];
     auto fetch = [&](int v, int slab) {
@@ -153,6 +155,13 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         const __amdgpu_buffer_rsrc_t ry = make_rsrc(B.Y + vh * kC * B.dvp, 0x7fffffff);
         const __amdgpu_buffer_rsrc_t re = make_rsrc(B.E + vh * kC * B.dvp, 0x7fffffff);
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(B.S + vh * DKP * B.dvp, 0x7fffffff);
+        if (slab == 0) {
+            const float *fac = (const float *)(B.tpg + vh * kTpBytes + kTpRows);
+            gam_t = B.gam[vh * kC + lane], gam_end = B.gam[vh * kC + kC - 1];
+            b_t = fac[ROW_B * kC + lane], last = fac[ROW_SCALARS * kC + SC_LAST];
+        }
+        smax4 = *(const f32x4 *)(B.Smax + vh * (B.dvp / 16) + slab * 4);
+        gmax4 = *(const f32x4 *)(B.Gmax + vh * (B.dvp / 16) + slab * 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) y4[i] = load4(ry, (tile * 4 + 2 * hf + i) * 1024);
 #pragma unroll
@@ -187,17 +196,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
         const __amdgpu_buffer_rsrc_t rg = make_rsrc(B.G + vh * DKP * B.dvp, 0x7fffffff);
-        const float *fac = (const float *)(B.tpg + vh * kTpBytes + kTpRows);
         __syncthreads();
         if (tid < kC) {
-            const double x = B.gam[vh * kC + tid], all = B.gam[vh * kC + kC - 1];
-            sg[tid] = x;
-            rise[tid] = expf((float)x);
-            fall[tid] = expf((float)(all - x));
-            sb[tid] = fac[ROW_B * kC + tid];
+            sg[tid] = gam_t;
+            rise[tid] = expf((float)gam_t);
+            fall[tid] = expf((float)(gam_end - gam_t));
+            sb[tid] = b_t;
         }
         if (hf == 0) dbs[w][lane] = 0.f;
-        const float last = fac[ROW_SCALARS * kC + SC_LAST];
+        const float last_v = last;
         f32x4 dp[2], dl[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) dp[i] = dl[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -215,13 +222,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) xo[s][j] = mix_f32(do8[s].v[j]);
-            float smax = 0.f, gmax = 0.f, is, ig, iu, ie;
-#pragma unroll
-            for (int i = 0; i < kSlab / 16; ++i) {
-                smax = max2(smax, B.Smax[vh * (B.dvp / 16) + c0 / 16 + i]);
-                gmax = max2(gmax, B.Gmax[vh * (B.dvp / 16) + c0 / 16 + i]);
-            }
-            const float ss = pow2_to(smax, kTop, &is), sgs = pow2_to(gmax, kTop, &ig);
+            float is, ig, iu, ie;
+            const float ss = pow2_to(max4(smax4, 0.f), kTop, &is), sgs = pow2_to(max4(gmax4, 0.f), kTop, &ig);
             float um = 0.f, em = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -339,7 +341,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         // <S', G> = e^gam_C <S, G> + sum_j k_j . (its column part from the state)
         {
             const f32x4 x = dot(kq, rk, gu) - dotc;
-            float end = last * sgsum + (m == 0 ? x[0] + x[1] + x[2] + x[3] : 0.f);
+            float end = last_v * sgsum + (m == 0 ? x[0] + x[1] + x[2] + x[3] : 0.f);
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) end += __shfl_xor(end, d, 64);
             if (lane == 0) red[tid >> 6] = end;
