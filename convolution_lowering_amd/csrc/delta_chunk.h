@@ -109,24 +109,32 @@ struct DeltaChunk {
 __device__ __forceinline__ int64_t slot_base(const Seqs &s, int n) {
     return s.cu ? seq_start(s, n) / kC + n : (int64_t)n * ((s.each + kC - 1) / kC);
 }
+// All 64 lanes take part: they look at 64 sequences at once.
 __device__ __forceinline__ DeltaChunk chunk_of(const Seqs &s, int slot) {
-    int lo = 0, hi = s.N - 1;
+    int lo = 0;
     if (!s.cu) {
         const int64_t per = (s.each + kC - 1) / kC;
         lo = per ? (int)(slot / per) : 0;
-        if (lo > hi) lo = hi;
+        if (lo > s.N - 1) lo = s.N - 1;
     } else {
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (slot_base(s, mid) <= slot) lo = mid;
-            else hi = mid - 1;
+        // the last sequence whose first slot is not past this one
+        for (int span = s.N; span > 1;) {
+            const int step = (span + 63) / 64;
+            const int n = lo + (int)(threadIdx.x & 63) * step;
+            const uint64_t before = __ballot(n < lo + span && slot_base(s, n) <= slot);
+            const int k = before ? 63 - __builtin_clzll(before) : 0;
+            const int left = lo + span - (lo + k * step);
+            lo += k * step;
+            span = left < step ? left : step;
         }
+        lo = __builtin_amdgcn_readfirstlane(lo);
     }
     DeltaChunk r;
     r.n = lo;
     int64_t a, e;
     seq_range(s, lo, &a, &e);
-    const int64_t c = slot - slot_base(s, lo);
+    const int64_t base = s.cu ? a / kC + lo : slot_base(s, lo);
+    const int64_t c = slot - base;
     r.c = (int)c;
     r.t0 = a + c * kC;
     const int64_t left = c < 0 ? 0 : e - r.t0;

@@ -5,8 +5,9 @@
 // inverse of the chunk's unit lower triangular matrix: (1 + L diag(b))^-1 for
 // the way forward and, where gradients are wanted, (1 + diag(b) L)^-1 too.
 //
-// The inverse is built from 16 x 16 diagonal blocks (substitution, one
-// wavefront each) and joined twice: [A 0; B C]^-1 = [A' 0; -C' B A', C'].
+// The inverse is built from 16 x 16 diagonal blocks (substitution, a lane a
+// column) and joined twice, [A 0; B C]^-1 = [A' 0; -C' B A', C'], on the
+// float32 matrix cores.
 // Sums of g are held in float64: gam_i - gam_j loses too many digits in 32
 // bits where a chunk holds strong decays beside weak ones.
 #include "delta_chunk.h"
@@ -16,36 +17,39 @@ namespace {
 
 constexpr int kLd = 68;  // floats from row to row of the 64 x 64 matrices in LDS
 
-// Loads 16-byte pieces of row `row` (a quarter of it a thread), finds its
-// largest value and its sum of squares, and leaves it in LDS as f16.
-template <typename S, int DKP, bool SPLIT>
-__device__ __forceinline__ void load_rows(const S *src, int64_t stride, const DeltaChunk &ch, int dk, bool vec, int norm,
-                                          _Float16 *dst, float *rho, float *rnorm) {
-    constexpr int Q = DKP / 4, V = 16 / sizeof(S), LD = DKP + 8;
+// A quarter of row `row` a thread, as it lies.
+template <typename S, int DKP>
+__device__ __forceinline__ void fetch_rows(const S *src, int64_t stride, const DeltaChunk &ch, int dk, bool vec,
+                                           S (&f)[DKP / 4]) {
+    constexpr int Q = DKP / 4, V = 16 / sizeof(S);
     const int row = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * Q;
-    float f[Q];
 #pragma unroll
-    for (int i = 0; i < Q; ++i) f[i] = 0.f;
-    if (row < ch.len) {
-        const S *p = src + (ch.t0 + row) * stride + c0;
-        if (vec) {
+    for (int i = 0; i < Q; ++i) f[i] = S(0);
+    if (row >= ch.len) return;
+    const S *p = src + (ch.t0 + row) * stride + c0;
+    if (vec) {
 #pragma unroll
-            for (int i = 0; i < Q; i += V)
-                if (c0 + i < dk) mix_load<S, V>(p + i, *(float(*)[V]) & f[i]);
-        } else {
+        for (int i = 0; i < Q; i += V)
+            if (c0 + i < dk) *(MixVec<S, V> *)&f[i] = *(const MixVec<S, V> *)(p + i);
+    } else {
 #pragma unroll
-            for (int i = 0; i < Q; ++i)
-                if (c0 + i < dk) f[i] = mix_f32(p[i]);
-        }
+        for (int i = 0; i < Q; ++i)
+            if (c0 + i < dk) f[i] = p[i];
     }
+}
+// Its largest value and sum of squares; the row goes to LDS as f16.
+template <typename S, int DKP, bool SPLIT>
+__device__ __forceinline__ void put_rows(const S (&f)[DKP / 4], int norm, _Float16 *dst, float *rho, float *rnorm) {
+    constexpr int Q = DKP / 4, LD = DKP + 8;
+    const int row = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * Q;
     float m = 0.f, ss = 0.f;
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
-        m = fmaxf(m, fabsf(f[i]));
-        ss = fmaf(f[i], f[i], ss);
+        m = max2(m, fabsf(mix_f32(f[i])));
+        ss = fmaf(mix_f32(f[i]), mix_f32(f[i]), ss);
     }
-    m = fmaxf(m, __shfl_xor(m, 1, 64));
-    m = fmaxf(m, __shfl_xor(m, 2, 64));
+    m = max2(m, __shfl_xor(m, 1, 64));
+    m = max2(m, __shfl_xor(m, 2, 64));
     ss += __shfl_xor(ss, 1, 64);
     ss += __shfl_xor(ss, 2, 64);
     float inv;
@@ -55,7 +59,7 @@ __device__ __forceinline__ void load_rows(const S *src, int64_t stride, const De
         f16x8 h, l;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float x = f[i + j] * sc;
+            const float x = mix_f32(f[i + j]) * sc;
             h[j] = (_Float16)x;
             l[j] = (_Float16)(x - (float)h[j]);
         }
@@ -77,82 +81,102 @@ __device__ __forceinline__ f16x8 row_frag(const _Float16 *x, int mt, int s) {
     const f16x4 a = *(const f16x4 *)p, b = *(const f16x4 *)(p + 16);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-__device__ __forceinline__ float wave_max(float m) { return tile_max(m); }
-// Largest of all 256 threads' values, to every thread.
-__device__ __forceinline__ float block_max(float m, float *red) {
-    m = wave_max(m);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-    __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+__device__ __forceinline__ f32x4 mma32(float a, float b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// X = M^-1 for the unit lower triangular M = 1 + (strict part in m), both
-// [64][kLd] in LDS.  256 threads; X's upper part is left zero.
-__device__ __forceinline__ void invert(const float *m, float *x, float *tmp) {
-    const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63;
-    for (int i = tid; i < kC * kLd; i += 256) x[i] = 0.f;
-    __syncthreads();
-    if (lane < 16) {  // column `lane` of diagonal block w
-        const float *b = m + 16 * w * (kLd + 1);
-        float col[16];
+// Both inverses of a chunk, from the strictly lower L ([64][kLd] in LDS) and
+// b: X[0] = (1 + L diag(b))^-1 and, WAYS = 2, X[1] = (1 + diag(b) L)^-1.
+// 256 threads, three barriers inside, none after.  m[way]: the largest value
+// this thread wrote.
+//
+// A float32 product's left operand has row m, step s column 4 s + g in lane
+// (g, m).  The second product of a join takes the columns in the order
+// 4 g + r instead: then the first one's result is its right operand as it is.
+template <int WAYS>
+__device__ __forceinline__ void invert(const float *L, const float *b, float *X, float (&mx)[2]) {
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, m = lane & 15;
+    constexpr int kX = kC * kLd;
+    mx[0] = mx[1] = 0.f;
+    if (g < WAYS) {  // column m of diagonal block w
+        const float *l = L + 16 * w * (kLd + 1);
+        float v[16], big = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float s = i == lane ? 1.f : 0.f;
+            float s = 0.f;
 #pragma unroll
-            for (int j = 0; j < i; ++j) s = fmaf(-b[i * kLd + j], col[j], s);
-            col[i] = s;
+            for (int j = 0; j < i; j += 4) {
+                const f32x4 r = *(const f32x4 *)(l + i * kLd + j);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (j + k < i) s = fmaf(r[k], v[j + k], s);
+            }
+            const float bi = b[16 * w + i];
+            const float x = (i == m ? 1.f : 0.f) - (g ? bi * s : s);
+            v[i] = g ? x : bi * x;
+            X[g * kX + (16 * w + i) * kLd + 16 * w + m] = x;
+            big = max2(big, fabsf(x));
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[(16 * w + i) * kLd + 16 * w + lane] = col[i];
+        mx[0] = g ? 0.f : big, mx[1] = g ? big : 0.f;
     }
     __syncthreads();
-    {  // two 32 x 32 blocks: tmp = B A', then -C' tmp; 128 threads each
-        const int h = tid >> 7, r = (tid >> 3) & 15, c = (tid & 7) * 2, o = 32 * h;
-        float s0 = 0.f, s1 = 0.f;
+    if ((w >> 1) < WAYS) {  // rows 16.., columns 0.. of each half: a pair and a way a wavefront
+        const int o = 32 * (w & 1), way = w >> 1;
+        float *x = X + way * kX;
+        f32x4 t = {0.f, 0.f, 0.f, 0.f}, c = t;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float b = m[(o + 16 + r) * kLd + o + j];
-            s0 = fmaf(b, x[(o + j) * kLd + o + c], s0);
-            s1 = fmaf(b, x[(o + j) * kLd + o + c + 1], s1);
-        }
-        tmp[(16 * h + r) * kLd + c] = s0;
-        tmp[(16 * h + r) * kLd + c + 1] = s1;
-        __syncthreads();
-        s0 = s1 = 0.f;
+        for (int s = 0; s < 4; ++s)
+            t = mma32(L[(o + 16 + m) * kLd + o + 4 * s + g] * b[way ? o + 16 + m : o + 4 * s + g], x[(o + 4 * s + g) * kLd + o + m], t);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float b = x[(o + 16 + r) * kLd + o + 16 + j];
-            s0 = fmaf(-b, tmp[(16 * h + j) * kLd + c], s0);
-            s1 = fmaf(-b, tmp[(16 * h + j) * kLd + c + 1], s1);
-        }
-        x[(o + 16 + r) * kLd + o + c] = s0;
-        x[(o + 16 + r) * kLd + o + c + 1] = s1;
+        for (int r = 0; r < 4; ++r) c = mma32(x[(o + 16 + m) * kLd + o + 16 + 4 * g + r], t[r], c);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[(o + 16 + 4 * g + r) * kLd + o + m] = -c[r];
+        mx[way] = max4(c, mx[way]);
     }
     __syncthreads();
-    {  // the lower left 32 x 32 block
-        const int r = tid >> 3, c = (tid & 7) * 4;
-        f32x4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int j = 0; j < 32; ++j) s += m[(32 + r) * kLd + j] * *(const f32x4 *)(x + j * kLd + c);
-        *(f32x4 *)(tmp + r * kLd + c) = s;
-        __syncthreads();
-        s = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int j = 0; j < 32; ++j) s -= x[(32 + r) * kLd + 32 + j] * *(const f32x4 *)(tmp + j * kLd + c);
-        *(f32x4 *)(x + (32 + r) * kLd + c) = s;
+    {  // rows 32.., columns 0..31: a tile of columns a wavefront; two ways, or two tiles of rows
+        const int tj = w & 1, way = WAYS == 2 ? w >> 1 : 0;
+        float *x = X + way * kX;
+        f32x4 t[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            t[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                if (l < tj) continue;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int row = 32 + 16 * k + m, col = 16 * l + 4 * s + g;
+                    t[k] = mma32(L[row * kLd + col] * b[way ? row : col], x[col * kLd + 16 * tj + m], t[k]);
+                }
+            }
+        }
+#pragma unroll
+        for (int ti = 0; ti < 2; ++ti) {
+            if (WAYS == 1 && ti != w >> 1) continue;
+            f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k <= ti; ++k)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) c = mma32(x[(32 + 16 * ti + m) * kLd + 32 + 16 * k + 4 * g + r], t[k][r], c);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[(32 + 16 * ti + 4 * g + r) * kLd + 16 * tj + m] = -c[r];
+            mx[way] = max4(c, mx[way]);
+        }
     }
-    __syncthreads();
 }
 
-// The triangular matrix in LDS as six left operands in two halves.  Six
-// wavefront-sized pieces over four wavefronts.
-__device__ __forceinline__ void store_tri(const float *x, float scale, char *out) {
+// The triangular matrix in LDS, its columns times `by` where that is given,
+// as six left operands in two halves.  Six wavefront-sized pieces over four
+// wavefronts.
+__device__ __forceinline__ void store_tri(const float *x, const float *by, float scale, char *out) {
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     for (int f = threadIdx.x >> 6; f < kTri; f += 4) {
         const int mt = f < 2 ? f : f / 2 + 1, s = f < 2 ? 0 : f % 2;
         const float *p = x + (16 * mt + r) * kLd + 32 * s + 4 * g;
-        const Split v = split8(*(const f32x4 *)p, *(const f32x4 *)(p + 16), scale);
+        f32x4 a = *(const f32x4 *)p, c = *(const f32x4 *)(p + 16);
+        if (by) a *= *(const f32x4 *)(by + 32 * s + 4 * g), c *= *(const f32x4 *)(by + 32 * s + 4 * g + 16);
+        const Split v = split8(a, c, scale);
         const int at = (f * kFrag + lane * 8) * 2;
         *(f16x8 *)(out + at) = v.hi;
         *(f16x8 *)(out + at + kTri * kFrag * 2) = v.lo;
@@ -160,24 +184,39 @@ __device__ __forceinline__ void store_tri(const float *x, float scale, char *out
 }
 
 template <typename S, int DKP, bool GRAD>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B, bool vec) {
+__global__ __launch_bounds__(256, GRAD ? 2 : 3) void delta_prep_kernel(DeltaArgs A, DeltaBuf B, bool vec) {
     constexpr bool SPLIT = sizeof(S) == 4;
-    constexpr int LD = DKP + 8, KS = DKP / 32, PL = SPLIT ? 2 : 1;
-    // q and k first, the value heads' matrices afterwards, in one place: 78 KB in all, two blocks a CU
-    constexpr int kIn = PL * 2 * kC * LD * 2, kMat = (2 * kC + 32) * kLd * 4;
+    constexpr int LD = DKP + 8, KS = DKP / 32, PL = SPLIT ? 2 : 1, WAYS = GRAD ? 2 : 1;
+    // q and k first, then a value head's L and inverses (P before those)
+    constexpr int kIn = PL * 2 * kC * LD * 2, kMat = (1 + WAYS) * kC * kLd * 4;
     __shared__ __align__(16) char both[kIn > kMat ? kIn : kMat];
     _Float16 *sk = (_Float16 *)both, *sq = sk + PL * kC * LD;
-    float *lm = (float *)both, *xi = lm + kC * kLd, *tmp = xi + kC * kLd;
-    __shared__ __align__(16) float kk[kC * kLd], qk[kC * kLd];
-    __shared__ float rk[kC], nk[kC], uq[kC], rq[kC], nq[kC], sb[kC], red[4];
-    __shared__ double sg[kC];
-    const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    float *lm = (float *)both, *xi = lm + kC * kLd;
+    __shared__ __align__(16) float rk[kC], nk[kC], uq[kC], nq[kC], sb[4][kC], red[4][4], mfs[4][4];
+    __shared__ __align__(16) double sg[4][kC];
+    const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const DeltaChunk ch = chunk_of(A.s, slot);
     if (ch.len == 0) return;
-    load_rows<S, DKP, SPLIT>((const S *)A.k + (int64_t)hk * A.dk, A.ks, ch, A.dk, vec, A.qk_norm, sk, rk, nk);
-    load_rows<S, DKP, SPLIT>((const S *)A.q + (int64_t)hk * A.dk, A.qs, ch, A.dk, vec, A.qk_norm, sq, uq, nq);
-    __syncthreads();
-    if (tid < kC) rq[tid] = uq[tid] * A.scale;
+    const int rep = A.Hv / A.Hk;
+    // g and b of one value head a wavefront, four heads at a time
+    float gt, bt;
+    auto fetch_gates = [&](int v) {
+        gt = bt = 0.f;
+        if (v < rep && lane < ch.len) {
+            const int64_t th = (ch.t0 + lane) * A.Hv + hk * rep + v;
+            gt = A.g[th];
+            bt = A.beta_f32 ? ((const float *)A.beta)[th] : mix_f32(((const S *)A.beta)[th]);
+        }
+    };
+    {
+        S fk[DKP / 4], fq[DKP / 4];
+        fetch_rows<S, DKP>((const S *)A.k + (int64_t)hk * A.dk, A.ks, ch, A.dk, vec, fk);
+        fetch_rows<S, DKP>((const S *)A.q + (int64_t)hk * A.dk, A.qs, ch, A.dk, vec, fq);
+        fetch_gates(w);
+        put_rows<S, DKP, SPLIT>(fk, A.qk_norm, sk, rk, nk);
+        put_rows<S, DKP, SPLIT>(fq, A.qk_norm, sq, uq, nq);
+    }
     __syncthreads();
     const int64_t head = (int64_t)slot * A.Hk + hk;
     const int64_t at = head * 2 * PL * kC * DKP;
@@ -195,130 +234,129 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs A, DeltaBuf B
             *(f16x8 *)(B.kq + o + PL * kC * DKP + (w * KS + s) * kFrag) = row_frag<LD>(q, w, s);
         }
     }
-    {  // K K' and Q K': rows 16 w.., lower triangle
-        f32x4 a[4], b[4];
+    // K K' and Q K', rows 16 w.. of the lower triangle: they stay in registers
+    f32x4 kk[4], qk[4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) a[nt] = b[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int nt = 0; nt < 4; ++nt) kk[nt] = qk[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const f16x8 kh = row_frag<LD>(sk, w, s), qh = row_frag<LD>(sq, w, s);
-            f16x8 kl, ql;
-            if (SPLIT) kl = row_frag<LD>(sk + kC * LD, w, s), ql = row_frag<LD>(sq + kC * LD, w, s);
+    for (int s = 0; s < KS; ++s) {
+        const f16x8 kh = row_frag<LD>(sk, w, s), qh = row_frag<LD>(sq, w, s);
+        f16x8 kl, ql;
+        if (SPLIT) kl = row_frag<LD>(sk + kC * LD, w, s), ql = row_frag<LD>(sq + kC * LD, w, s);
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                if (nt > w) continue;
-                const f16x8 rh = row_frag<LD>(sk, nt, s);
-                if (SPLIT) {
-                    const f16x8 rl = row_frag<LD>(sk + kC * LD, nt, s);
-                    a[nt] = mma(kl, rh, mma(kh, rl, a[nt]));
-                    b[nt] = mma(ql, rh, mma(qh, rl, b[nt]));
-                }
-                a[nt] = mma(kh, rh, a[nt]);
-                b[nt] = mma(qh, rh, b[nt]);
+        for (int nt = 0; nt < 4; ++nt) {
+            if (nt > w) continue;
+            const f16x8 rh = row_frag<LD>(sk, nt, s);
+            if (SPLIT) {
+                const f16x8 rl = row_frag<LD>(sk + kC * LD, nt, s);
+                kk[nt] = mma(kl, rh, mma(kh, rl, kk[nt]));
+                qk[nt] = mma(ql, rh, mma(qh, rl, qk[nt]));
             }
+            kk[nt] = mma(kh, rh, kk[nt]);
+            qk[nt] = mma(qh, rh, qk[nt]);
         }
-        const int g = lane >> 4;
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * w + 4 * g + r, j = 16 * nt + (lane & 15);
-                const float rj = rk[j];
-                kk[i * kLd + j] = a[nt][r] * rk[i] * rj;
-                qk[i * kLd + j] = b[nt][r] * rq[i] * rj;
-            }
     }
-    const int rep = A.Hv / A.Hk;
-    float mf[4] = {};
-    for (int v = 0; v < rep; ++v) {
-        const int h = hk * rep + v;
-        const int64_t vh = (int64_t)slot * A.Hv + h;
-        char *tp = B.tp + vh * kTpBytes, *tpg = GRAD ? B.tpg + vh * kTpBytes : nullptr;
-        if (w == 0) {
-            float g = 0.f, b = 0.f;
-            if (lane < ch.len) {
-                const int64_t th = (ch.t0 + lane) * A.Hv + h;
-                g = A.g[th];
-                g = g < -1e4f ? -1e4f : g;  // -inf too: e^-1e4 is zero, and differences stay numbers
-                b = A.beta_f32 ? ((const float *)A.beta)[th] : mix_f32(((const S *)A.beta)[th]);
-            }
-            double s = g;
+    const int row = 16 * w + 4 * g;  // of this lane's four
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+        const float rj = rk[16 * nt + m];
+        kk[nt] *= *(const f32x4 *)(rk + row) * rj;
+        qk[nt] *= *(const f32x4 *)(uq + row) * (A.scale * rj);
+    }
+    for (int v0 = 0; v0 < rep; v0 += 4) {
+        __syncthreads();  // q and k, or the heads before, are done with
+        if (v0 + w < rep) {
+            const int64_t vh = (int64_t)slot * A.Hv + hk * rep + v0 + w;
+            char *tp = B.tp + vh * kTpBytes;
+            const float ga = gt < -1e4f ? -1e4f : gt;  // -inf too: e^-1e4 is zero, and differences stay numbers
+            double s = ga;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double o = __shfl_up(s, d, 64);
                 if (lane >= d) s += o;
             }
             const double all = __shfl(s, 63, 64);
-            sg[lane] = s;
-            sb[lane] = b;
-            const float rise = expf((float)s);
-            const float f1 = rk[lane] * rise, f2 = rq[lane] * rise, f3 = rk[lane] * expf((float)(all - s));
-            const float last = expf((float)all);
-            mf[0] = wave_max(fabsf(f3 * b)), mf[1] = wave_max(fabsf(f1 * b)), mf[2] = wave_max(fabsf(f2));
-            auto put = [&](char *tp) {
-                float *f = (float *)(tp + kTpRows) + lane;
-                f[ROW_F1 * kC] = f1, f[ROW_F2 * kC] = f2, f[ROW_F3 * kC] = f3, f[ROW_B * kC] = b;
-                f[ROW_F3B * kC] = f3 * b, f[ROW_F1B * kC] = f1 * b;
-                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last, f[ROW_SCALARS * kC + SC_F2] = mf[2];
+            sg[w][lane] = s;
+            sb[w][lane] = bt;
+            const float rise = expf((float)s), last = expf((float)all);
+            const float f1 = rk[lane] * rise, f2 = uq[lane] * A.scale * rise, f3 = rk[lane] * expf((float)(all - s));
+            const float m0 = tile_max(fabsf(f3 * bt)), m1 = tile_max(fabsf(f1 * bt)), m2 = tile_max(fabsf(f2));
+            if (lane == 0) mfs[w][0] = m0, mfs[w][1] = m1;
+            auto put = [&](char *p) {
+                float *f = (float *)(p + kTpRows) + lane;
+                f[ROW_F1 * kC] = f1, f[ROW_F2 * kC] = f2, f[ROW_F3 * kC] = f3, f[ROW_B * kC] = bt;
+                f[ROW_F3B * kC] = f3 * bt, f[ROW_F1B * kC] = f1 * bt;
+                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last, f[ROW_SCALARS * kC + SC_F2] = m2;
             };
             put(tp);
             if (GRAD) {
-                put(tpg);
+                put(B.tpg + vh * kTpBytes);
                 B.gam[vh * kC + lane] = s;
             }
         }
-        __syncthreads();
-        // the matrix to invert into lm, P into xi
-        float mp = 0.f;
-        for (int e = tid; e < kC * kC; e += 256) {
-            const int i = e >> 6, j = e & 63;
-            float l = 0.f, p = 0.f;
-            if (j <= i) {
-                const float d = expf((float)(sg[i] - sg[j]));
-                p = qk[i * kLd + j] * d * (GRAD ? 1.f : sb[j]);
-                if (j < i) l = kk[i * kLd + j] * d * sb[j];
-            }
-            lm[i * kLd + j] = l;
-            xi[i * kLd + j] = p;
-            mp = fmaxf(mp, fabsf(p));
+        fetch_gates(v0 + 4 + w);
+        // tiles right of the diagonal that the operands of 32 columns reach into: (0, 1) and (2, 3)
+        for (int i = tid; i < WAYS * 512; i += 256) {
+            const int x = i >> 9, t = i >> 8 & 1, e = i & 255;
+            xi[x * kC * kLd + (32 * t + (e >> 4)) * kLd + 32 * t + 16 + (e & 15)] = 0.f;
         }
-        float inv, sc;
-        if (GRAD) {
-            sc = pow2_to(block_max(mp, red), kTop, &inv);
-            store_tri(xi, sc, tpg + kTpRows / 2);
-            if (tid == 0) ((float *)(tpg + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
+        const int heads = rep - v0 < 4 ? rep - v0 : 4;
+        for (int v = 0; v < heads; ++v) {
+            const int64_t vh = (int64_t)slot * A.Hv + hk * rep + v0 + v;
+            char *tp = B.tp + vh * kTpBytes, *tpg = GRAD ? B.tpg + vh * kTpBytes : nullptr;
             __syncthreads();
-            mp = 0.f;
-            for (int e = tid; e < kC * kC; e += 256) {
-                const float p = xi[(e >> 6) * kLd + (e & 63)] *= sb[e & 63];
-                mp = fmaxf(mp, fabsf(p));
-            }
-        }
-        sc = pow2_to(block_max(mp, red), kTop, &inv);
-        store_tri(xi, sc, tp + kTpRows / 2);
-        if (tid == 0) ((float *)(tp + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
-        for (int way = 0; way < (GRAD ? 2 : 1); ++way) {
-            __syncthreads();
-            if (way) {  // b beside the row instead of the column
-                for (int e = tid; e < kC * kC; e += 256) {
-                    const int i = e >> 6, j = e & 63;
-                    lm[i * kLd + j] = j < i ? kk[i * kLd + j] * expf((float)(sg[i] - sg[j])) * sb[i] : 0.f;
+            // L into lm, P into xi
+            float mp = 0.f, mpb = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                if (nt > w) continue;
+                const int j = 16 * nt + m;
+                const double gj = sg[v][j];
+                const float bj = sb[v][j];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = row + r;
+                    const float d = j <= i ? expf((float)(sg[v][i] - gj)) : 0.f;
+                    const float p = j <= i ? qk[nt][r] * d : 0.f;
+                    lm[i * kLd + j] = j < i ? kk[nt][r] * d : 0.f;
+                    xi[i * kLd + j] = p;
+                    mp = max2(mp, fabsf(p));
+                    mpb = max2(mpb, fabsf(p * bj));
                 }
-                __syncthreads();
             }
-            invert(lm, xi, tmp);
-            mp = 0.f;
-            for (int e = tid; e < kC * kC; e += 256) mp = fmaxf(mp, fabsf(xi[(e >> 6) * kLd + (e & 63)]));
-            mp = block_max(mp, red);
-            sc = pow2_to(mp, kTop, &inv);
-            store_tri(xi, sc, way ? tpg : tp);
-            if (tid == 0) {
-                float *o = (float *)((way ? tpg : tp) + kTpRows) + ROW_SCALARS * kC;
-                o[SC_IT] = inv;
-                o[SC_T] = kC * mp, o[SC_TF3] = kC * mp * mf[0], o[SC_TF1] = kC * mp * mf[1];
+            mp = tile_max(mp), mpb = tile_max(mpb);
+            if (lane == 0) red[0][w] = mp, red[1][w] = mpb;
+            __syncthreads();
+            float inv;
+            float sc = pow2_to(max4(*(const f32x4 *)red[1], 0.f), kTop, &inv);
+            store_tri(xi, sb[v], sc, tp + kTpRows / 2);
+            if (tid == 0) ((float *)(tp + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
+            if (GRAD) {
+                sc = pow2_to(max4(*(const f32x4 *)red[0], 0.f), kTop, &inv);
+                store_tri(xi, nullptr, sc, tpg + kTpRows / 2);
+                if (tid == 0) ((float *)(tpg + kTpRows))[ROW_SCALARS * kC + SC_IP] = inv;
+            }
+            __syncthreads();
+            float mx[2];
+            invert<WAYS>(lm, sb[v], xi, mx);
+#pragma unroll
+            for (int way = 0; way < WAYS; ++way) {
+                const float x = tile_max(mx[way]);
+                if (lane == 0) red[2 + way][w] = x;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int way = 0; way < WAYS; ++way) {
+                const float big = max4(*(const f32x4 *)red[2 + way], 0.f);
+                sc = pow2_to(big, kTop, &inv);
+                store_tri(xi + way * kC * kLd, nullptr, sc, way ? tpg : tp);
+                if (tid == 0) {
+                    float *o = (float *)((way ? tpg : tp) + kTpRows) + ROW_SCALARS * kC;
+                    o[SC_IT] = inv;
+                    o[SC_T] = kC * big, o[SC_TF3] = kC * big * mfs[v][0], o[SC_TF1] = kC * big * mfs[v][1];
+                }
             }
         }
-        __syncthreads();
     }
 }
 
