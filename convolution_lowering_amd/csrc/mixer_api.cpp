@@ -158,8 +158,8 @@ conv_status_t conv1d_causal_bwd_workspace_size(int64_t T, int N, int D, int W, s
     const conv_status_t st = conv1d_sizes(D, W, MIX_ACT_NONE, CONV_DTYPE_FP32);
     if (st != CONV_OK) return st;
     if (T > kMaxTokens) return CONV_ERR_UNSUPPORTED;
-    const int tile = conv1d_bwd_tile(T, D);
-    *bytes_out = (size_t)((T + tile - 1) / tile) * (W + 1) * D * sizeof(float);
+    const int64_t tokens = (int64_t)conv1d_bwd_tile(T, D) * kConvRuns;
+    *bytes_out = (size_t)((T + tokens - 1) / tokens) * (W + 1) * D * sizeof(float);
     return CONV_OK;
 }
 

@@ -46,7 +46,9 @@ __device__ __forceinline__ void mix_store(S *p, const float (&f)[V]) {
     *(MixVec<S, V> *)p = t;
 }
 
-__device__ __forceinline__ float mix_sigmoid(float z) { return 1.f / (1.f + __expf(-z)); }
+// The reciprocal instruction is good to one unit in the last place; an exact
+// division costs ten instructions, which these kernels have no time for.
+__device__ __forceinline__ float mix_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // ---- packed sequences.  cu null: every sequence holds T / N tokens.  Values
 // outside [0, T] are clamped, so that a bad array reads and writes nothing
@@ -83,12 +85,13 @@ __device__ __forceinline__ int seq_of(const Seqs &s, int64_t t) {
 struct Conv1dArgs {
     const void *x, *w, *bias, *state, *dy, *dstate_out;
     void *y, *state_out, *dx, *dw, *dbias, *dstate;
-    float *part;  // bwd: [tiles][W + 1][D] partial sums
+    float *part;  // bwd: [blocks][W + 1][D] partial sums
     int64_t xs, dys;
     Seqs s;
     int D, W, act, tiles, tile;
 };
-int conv1d_bwd_tile(int64_t T, int D);  // tokens of one partial sum
+constexpr int kConvRuns = 4;  // runs of tokens whose sums a backward block adds up
+int conv1d_bwd_tile(int64_t T, int D);  // tokens of one run
 hipError_t launch_conv1d_fwd(Conv1dArgs a, int dtype, hipStream_t st);
 hipError_t launch_conv1d_bwd(Conv1dArgs a, int dtype, hipStream_t st);
 hipError_t launch_conv1d_step(const void *x, int64_t xs, const void *w, const void *bias, void *pool,
