@@ -18,6 +18,7 @@ tensor); everything inside a token is dense.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -120,12 +121,20 @@ def _packing(lead, cu_seqlens, device):
     return lead[0], cu_seqlens.numel() - 1, _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, device)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream, device):
-    return torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+    """Where outputs and workspaces are allocated: torch's current stream as
+    it is (entering it again costs a one-token call a third of its time), or
+    the caller's."""
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _raw(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _act(act, allowed=("none", "silu")):
@@ -221,11 +230,8 @@ def conv1d_causal_step(x, w, bias, pool, slots=None, *, act="silu", out=None, st
     P = pool.shape[0]
     args = (xp, xs, _dense(w, "w", w.shape, dt, dev), _dense(bias, "bias", (D,), dt, dev),
             _dense(pool, "pool", (P, W - 1, D), dt, dev), _dense(slots, "slots", (R,), torch.int32, dev))
-    if stream is None:
+    with _on(stream, dev):
         y = torch.empty((R, D), dtype=dt, device=dev) if out is None else out
-    else:
-        with _on(stream, dev):
-            y = torch.empty((R, D), dtype=dt, device=dev) if out is None else out
     _check("conv1d_causal_step",
            _mixer_lib().conv1d_causal_step(*args, _dense(y, "out", (R, D), dt, dev), R, P, D, W, _act(act), code,
                                            _raw(stream, dev)))
@@ -331,11 +337,8 @@ def delta_rule_step(q, k, v, g, beta, pool, slots=None, *, scale=None, qk_norm=F
     P = pool.shape[0]
     pp = _dense(pool, "pool", (P, Hv, dk, dv), torch.float32, dev)
     sp = _dense(slots, "slots", (R,), torch.int32, dev)
-    if stream is None:
+    with _on(stream, dev):
         o = torch.empty(v.shape, dtype=q.dtype, device=dev) if out is None else out
-    else:
-        with _on(stream, dev):
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev) if out is None else out
     _check("delta_rule_step",
            _mixer_lib().delta_rule_step(*ptrs, pp, sp, _dense(o, "out", v.shape, q.dtype, dev), R, L, P, *sizes,
                                         dk ** -0.5 if scale is None else scale, qk_norm, code, bcode,
