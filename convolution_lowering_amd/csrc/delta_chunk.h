@@ -267,15 +267,23 @@ __device__ __forceinline__ f16x8 trans_at(const char *a, const char *b, int mt, 
     return __builtin_bit_cast(f16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// The bytes at p as a buffer.  p is the same for the whole wavefront, whatever
+// it was computed from.  A buffer access may read scalars that a vector
+// instruction wrote only five cycles later; the compiler does not see into the
+// copies below, so the wait is here.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void *p, uint32_t bytes) {
+    const uint64_t a = (uint64_t)p;
+    uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
+    uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32));
+    asm volatile("s_nop 4" : "+s"(lo), "+s"(hi));
+    return make_rsrc((const void *)(lo | (uint64_t)hi << 32), bytes);
+}
+
 // 16-byte copies into LDS, 1 KB an instruction, shared by the block's NW
 // wavefronts (NW = 1: done by the one that calls).
 template <int NW, int UNITS>
 __device__ __forceinline__ void copy_in(const void *src, char *dst) {
-    // the same for the whole wavefront, whatever it was computed from
-    const uint64_t p = (uint64_t)src;
-    const uint64_t u0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)p);
-    const uint64_t u1 = (uint32_t)__builtin_amdgcn_readfirstlane((int)(p >> 32));
-    const __amdgpu_buffer_rsrc_t r = make_rsrc((const void *)(u0 | u1 << 32), UNITS * 1024);
+    const __amdgpu_buffer_rsrc_t r = uniform_rsrc(src, UNITS * 1024);
     const int w = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)dst + w * 1024, v = (threadIdx.x & 63) * 16 + w * 1024;
 #pragma unroll

@@ -71,12 +71,7 @@ struct Scan {
     }
 
     // ---- the copying wavefront
-    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_of(const void *p) {
-        const uint64_t a = (uint64_t)p;
-        const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
-        const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32));
-        return make_rsrc((const void *)(lo | hi << 32), 0x7fffffff);
-    }
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows_of(const void *p) { return uniform_rsrc(p, 0x7fffffff); }
     // Rows of the block's columns, [64][..] of the caller's, to LDS: 16 bytes a
     // lane, or one value at a time where the rows do not lie that way.  What is
     // past the chunk's end or the last column reads as zero.

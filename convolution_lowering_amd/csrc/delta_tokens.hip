@@ -21,11 +21,9 @@ __device__ __forceinline__ float rows_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
-// One head's 32 columns over the tokens [t0, t1), S in and out at st (null
-// in: zero; null out: not kept).
+// One head's 32 columns over the tokens [t0, t1), S in and out at st.
 template <typename S, int NR, bool VEC>
-__device__ __forceinline__ void run_tokens(const DeltaArgs &A, const float *in, float *out, int h, int c0, int64_t t0,
-                                           int64_t t1) {
+__device__ __forceinline__ void run_tokens(const DeltaArgs &A, float *st, int h, int c0, int64_t t0, int64_t t1) {
     const int lane = threadIdx.x, rg = lane >> 3, c = c0 + (lane & 7) * 4;
     const int hk = h / (A.Hv / A.Hk);
     float s[NR][4];
@@ -34,8 +32,8 @@ __device__ __forceinline__ void run_tokens(const DeltaArgs &A, const float *in, 
         const int row = i * 8 + rg;
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-        if (in && row < A.dk) {
-            const float *p = in + (int64_t)row * A.dv + c;
+        if (row < A.dk) {
+            const float *p = st + (int64_t)row * A.dv + c;
             if (VEC) {
                 if (c < A.dv) mix_load<float, 4>(p, s[i]);
             } else {
@@ -98,12 +96,11 @@ __device__ __forceinline__ void run_tokens(const DeltaArgs &A, const float *in, 
                 if (c + j < A.dv) op[j] = mix_out<S>(o[j]);
         }
     }
-    if (!out) return;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int row = i * 8 + rg;
         if (row >= A.dk) continue;
-        float *p = out + (int64_t)row * A.dv + c;
+        float *p = st + (int64_t)row * A.dv + c;
         if (VEC) {
             if (c < A.dv) mix_store<float, 4>(p, s[i]);
         } else {
@@ -114,37 +111,26 @@ __device__ __forceinline__ void run_tokens(const DeltaArgs &A, const float *in, 
     }
 }
 
-// blockIdx.x: (request or sequence) * Hv + head; blockIdx.y: 32 columns.
+// blockIdx.x: request * Hv + head; blockIdx.y: 32 columns.
 template <typename S, int NR, bool VEC>
 __global__ __launch_bounds__(64) void delta_tokens_kernel(DeltaArgs A) {
     const int n = blockIdx.x / A.Hv, h = blockIdx.x % A.Hv, c0 = blockIdx.y * kStepCols;
-    const int64_t one = (int64_t)A.dk * A.dv;
-    if (A.pool) {
-        const int slot = A.slots ? A.slots[n] : n;
-        const int64_t t0 = (int64_t)n * A.L;
-        if (slot < 0 || slot >= A.P) {  // a padding request: zeros, and no state
-            for (int64_t t = t0; t < t0 + A.L; ++t)
-                for (int c = threadIdx.x; c < kStepCols; c += 64)
-                    if (c0 + c < A.dv) ((S *)A.o)[(t * A.Hv + h) * A.dv + c0 + c] = mix_out<S>(0.f);
-            return;
-        }
-        float *st = A.pool + ((int64_t)slot * A.Hv + h) * one;
-        run_tokens<S, NR, VEC>(A, st, st, h, c0, t0, t0 + A.L);
+    const int slot = A.slots ? A.slots[n] : n;
+    const int64_t t0 = (int64_t)n * A.L;
+    if (slot < 0 || slot >= A.P) {  // a padding request: zeros, and no state
+        for (int64_t t = t0; t < t0 + A.L; ++t)
+            for (int c = threadIdx.x; c < kStepCols; c += 64)
+                if (c0 + c < A.dv) ((S *)A.o)[(t * A.Hv + h) * A.dv + c0 + c] = mix_out<S>(0.f);
         return;
     }
-    int64_t a, e;
-    seq_range(A.s, n, &a, &e);
-    const int64_t at = ((int64_t)n * A.Hv + h) * one;
-    run_tokens<S, NR, VEC>(A, A.state ? A.state + at : nullptr, A.state_out ? A.state_out + at : nullptr, h, c0, a, e);
+    run_tokens<S, NR, VEC>(A, A.pool + ((int64_t)slot * A.Hv + h) * A.dk * A.dv, h, c0, t0, t0 + A.L);
 }
 
 template <typename S>
 hipError_t tokens_typed(const DeltaArgs &a, hipStream_t st) {
-    const int n = a.pool ? a.R : a.s.N;
-    if (!n) return hipSuccess;
-    const dim3 grid((unsigned)((int64_t)n * a.Hv), (a.dv + kStepCols - 1) / kStepCols);
-    bool vec = a.dv % 4 == 0;
-    for (const float *p : {(const float *)a.pool, a.state, (const float *)a.state_out}) vec = vec && (uintptr_t)p % 16 == 0;
+    if (!a.R) return hipSuccess;
+    const dim3 grid((unsigned)((int64_t)a.R * a.Hv), (a.dv + kStepCols - 1) / kStepCols);
+    const bool vec = a.dv % 4 == 0 && (uintptr_t)a.pool % 16 == 0;
     if (a.dk <= 64) {
         if (vec) hipLaunchKernelGGL((delta_tokens_kernel<S, 8, true>), grid, dim3(64), 0, st, a);
         else hipLaunchKernelGGL((delta_tokens_kernel<S, 8, false>), grid, dim3(64), 0, st, a);

@@ -49,11 +49,11 @@ typedef __attribute__((address_space(3))) void *lds_ptr_t;
 // everything" where control flow merges, which would drain the pipeline.
 // All waits for them are the explicit vmcnt waits in the main loop.  M0 is
 // used by nothing else in these kernels (LDS instructions on gfx9 and later
-// do not read it).
+// do not read it); one cycle has to pass between its write and the load.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :
                  : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(lds_base))
                  : "memory", "m0");
