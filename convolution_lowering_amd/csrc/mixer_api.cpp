@@ -206,7 +206,10 @@ conv_status_t delta_rule_step(const void *q, int64_t q_stride, const void *k, in
     const conv_status_t st = delta_sizes(Hk, Hv, dk, dv, dtype, beta_dtype);
     if (st != CONV_OK) return st;
     if (R < 0 || L < 0 || P < 0 || (!slots && R > P)) return CONV_ERR_INVALID_ARG;
-    if ((int64_t)R * L > kMaxTokens || (int64_t)R * Hv > kMaxTokens) return CONV_ERR_UNSUPPORTED;
+    // one wavefront for 32 columns, threads counted in 32 bits
+    if ((int64_t)R * L > kMaxTokens || (int64_t)R * Hv > kMaxTokens ||
+        (int64_t)R * Hv * ((dv + 31) / 32) > kMaxTokens / 64)
+        return CONV_ERR_UNSUPPORTED;
     if (!R || !L) return CONV_OK;
     if (!pointers_ok({q, k, v, o}, {}, bytes_of(dtype)) || !pointers_ok({beta}, {}, bytes_of(beta_dtype)) ||
         !pointers_ok({g, pool}, {slots}, 4))
