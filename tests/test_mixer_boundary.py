@@ -86,9 +86,30 @@ def delta_fwd(q=P, qs=256, k=P, ks=256, v=P, vs=512, g=P, beta=P, state=None, cu
     (dict(qs=255), INVALID), (dict(vs=511), INVALID), (dict(Hv=3), INVALID), (dict(Hk=0), INVALID),
     (dict(dk=0), INVALID), (dict(dt=3), INVALID), (dict(bdt=2), INVALID), (dict(T=9, N=2), INVALID),
     (dict(dk=129, qs=400, ks=400), UNSUPPORTED), (dict(dv=257, vs=2000), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED),
+    (dict(vs=(1 << 22) + 1), UNSUPPORTED), (dict(Hv=40000, vs=40000 * 128), UNSUPPORTED), (dict(Hv=65536), UNSUPPORTED),
+    (dict(ws=None), WORKSPACE), (dict(nbytes=8), WORKSPACE), (dict(saved=P, saved_bytes=8), WORKSPACE),
+    (dict(ws=ODD), INVALID), (dict(saved=ODD, saved_bytes=1 << 40), INVALID),
 ])
 def test_delta_fwd_refusals(bad, want):
     assert delta_fwd(**bad) == want
+
+
+def delta_bwd(d_o=P, dos=512, q=P, qs=256, k=P, ks=256, v=P, vs=512, g=P, beta=P, cu=None, dst=None, dq=P, dk_=P, dv_=P,
+              dg=P, dbeta=P, ds=None, T=8, N=1, Hk=2, Hv=4, dk=128, dv=128, dt=1, bdt=1, ws=P, nbytes=1 << 40, saved=P,
+              saved_bytes=1 << 40):
+    return L().delta_rule_bwd(d_o, dos, dst, q, qs, k, ks, v, vs, g, beta, cu, saved, saved_bytes, dq, dk_, dv_, dg,
+                              dbeta, ds, T, N, Hk, Hv, dk, dv, 1.0, 0, dt, bdt, None, ws, nbytes)
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(d_o=None), INVALID), (dict(d_o=ODD), INVALID), (dict(dos=511), INVALID), (dict(q=None), INVALID),
+    (dict(dq=None), INVALID), (dict(dk_=None), INVALID), (dict(dv_=None), INVALID), (dict(dg=None), INVALID),
+    (dict(dbeta=None), INVALID), (dict(dst=ODD), INVALID), (dict(ds=ODD), INVALID), (dict(ks=255), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(nbytes=8), WORKSPACE), (dict(saved=None), WORKSPACE), (dict(saved_bytes=8), WORKSPACE),
+    (dict(dos=(1 << 22) + 1), UNSUPPORTED), (dict(dk=129, qs=400, ks=400), UNSUPPORTED),
+])
+def test_delta_bwd_refusals(bad, want):
+    assert delta_bwd(**bad) == want
 
 
 def delta_step(q=P, qs=256, v=P, vs=512, g=P, beta=P, pool=P, slots=P, o=P, R=2, Ln=1, Pn=4, Hk=2, Hv=4, dk=128, dv=128):
@@ -99,6 +120,7 @@ def delta_step(q=P, qs=256, v=P, vs=512, g=P, beta=P, pool=P, slots=P, o=P, R=2,
     (dict(q=None), INVALID), (dict(pool=None), INVALID), (dict(pool=ODD), INVALID), (dict(slots=ODD), INVALID),
     (dict(R=-1), INVALID), (dict(Ln=-1), INVALID), (dict(slots=None, R=5), INVALID), (dict(qs=4), INVALID),
     (dict(Hv=5), INVALID), (dict(R=0), OK), (dict(Ln=0), OK), (dict(dk=130, qs=400), UNSUPPORTED),
+    (dict(R=1 << 23, Hv=4), UNSUPPORTED),  # more wavefronts than a launch has
 ])
 def test_delta_step_refusals(bad, want):
     assert delta_step(**bad) == want
