@@ -5,14 +5,29 @@
 // value head and holds them, [dk][16] in float32, in registers from the first
 // chunk to the last.  A chunk is five products whose right operands come out
 // of registers, each from the result before it, so what counts is how long
-// that chain is.  The left operands (K, Q, the inverse and P, 58 KB for a
-// 16-bit dk = 128) and the rows of V are the same for all columns or lie
-// across them: one more wavefront of the block copies the next chunk's into the other half of LDS and
-// takes the last chunk's results from there to memory (issuing those accesses
-// took a fifth of a chunk's time from the wavefronts that compute).  One
-// barrier a chunk.  K', Q', and on the way back the transposes of the
-// triangular operands, are read from the same bytes by the transposing LDS
-// read.
+// that chain is, and what is not in it is taken elsewhere:
+//
+//   - A second wavefront does what the chain does not wait for: the outputs
+//     Q S and P U and the copies kept for the gradients; on the way back P' dO
+//     and Q' (f2 dO), which need no state, before the chain asks for them, and
+//     dV.  The two hand over operands and results through LDS, lane by lane.
+//   - The left operands (K, Q, the inverse and P, 58 KB for a 16-bit dk = 128)
+//     and the rows of V are the same for all columns or lie across them: a
+//     third kind of wavefront, one for the block, copies the next chunk's into
+//     the other half of LDS and takes the last chunk's results to memory.  It
+//     also brings the chunk after that into L2, each block of a query/key head
+//     an equal part of the lines: otherwise all of them wait for memory at once.
+//
+// One barrier a chunk, and one or two inside it for the pair.  K', Q', and on
+// the way back the transposes of the triangular operands, are read from the
+// same bytes by the transposing LDS read.
+//
+// 16384 tokens in 6 sequences, the longest of 129 chunks, 32 heads of 128 x 128:
+// 300 us, 4400 cycles a chunk of which the chain's products are 1312 (82 of
+// 16x16x32); one wavefront doing all of it 338 us, without the lines brought to
+// L2 322 us.  32 chunks x 64 heads, with what is kept for the gradients (200 MB)
+// 92 us, was 111; back 106 us, was 113.  Two more pairs of columns in a block do
+// not fit LDS, and a wavefront's columns cannot be fewer than a product's 16.
 #include "delta_chunk.h"
 
 namespace convlower {
@@ -38,26 +53,35 @@ struct Scan {
     static constexpr int kIn = 2 * PL * kMat;                  // K and Q
     static constexpr int kStage = kIn + kTpBytes;
     static constexpr int kRow = COLS * ES, kTile = kC * kRow;  // a row and all rows of V, dO, O or dV
-    static constexpr int STAGES = 2 * kStage + 4 * kTile <= 160 * 1024 ? 2 : 1;
+    // what a pair of wavefronts hand each other: a state's operands, a result of four tiles, scalars
+    static constexpr int kPairTiles = 2 * KS * 1024, kPairRows = kPairTiles + 4096, kPair = kPairRows + 1024;
+    static constexpr int STAGES = 2 * kStage + 4 * kTile + NW * kPair + 1024 <= 160 * 1024 ? 2 : 1;
     static constexpr int kTi = kIn, kP = kIn + kTpRows / 2, kRows = kIn + kTpRows;
-    static constexpr int kVals = STAGES * kStage, kOuts = kVals + 2 * kTile, kLds = kOuts + 2 * kTile;
+    static constexpr int kVals = STAGES * kStage, kOuts = kVals + 2 * kTile, kPairs = kOuts + 2 * kTile;
+    static constexpr int kTouch = kPairs + NW * kPair, kLds = kTouch + 1024;  // (and 1 KB that nobody reads)
+    static constexpr int kTouches = 5;
 
-    int n, h, hk, c0, w, g, m, tl;  // c0: the block's first column; w: the wavefront
+    int n, h, hk, c0, w, role, g, m, tl;  // c0: the block's first column; w: which 16 of its columns
+    int inner, share, groups;             // blocks of a query/key head, this one's number, those of a value head
     int64_t a, e, base, chunks;
 
     // Blocks of one query/key head go to one XCD (every eighth block), whose
     // L2 then serves K and Q to all of them.
-    __device__ __forceinline__ bool place(const DeltaArgs &A, int groups) {
-        const int rep = A.Hv / A.Hk, inner = groups * rep;
+    __device__ __forceinline__ bool place(const DeltaArgs &A, int groups_) {
+        groups = groups_;
+        const int rep = A.Hv / A.Hk;
+        inner = groups * rep;
         const int64_t b = blockIdx.x;
         const int64_t unit = b / (8 * inner) * 8 + b % 8;
         const int in = (int)(b / 8 % inner);
+        share = in;
         if (unit >= (int64_t)A.s.N * A.Hk) return false;
         n = (int)(unit / A.Hk);
         hk = (int)(unit % A.Hk);
         h = hk * rep + in / groups;
         c0 = (in % groups) * COLS;
-        w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        w = wave % NW, role = wave / NW;
         const int lane = threadIdx.x & 63;
         g = lane >> 4, m = lane & 15, tl = trans_lane();
         seq_range(A.s, n, &a, &e);
@@ -121,51 +145,119 @@ struct Scan {
             }
         }
     }
-    // The copying wavefront's whole life.  LAG: after how many barriers a
-    // chunk's results are in LDS.
-    template <bool BACK, int LAG>
+    // The copying wavefront's whole life.  A chunk's results are in LDS at the
+    // next chunk's barrier.
+    template <bool BACK>
     __device__ __forceinline__ void copy(const DeltaArgs &A, const DeltaBuf &B, bool vec, char *lds) const {
         const char *tp = BACK ? B.tpg : B.tp;
         const S *in = BACK ? (const S *)A.d_o : (const S *)A.v;
         S *out = BACK ? (S *)A.dv_out : (S *)A.o;
         const int64_t is = BACK ? A.dos : A.vs, os = (int64_t)A.Hv * A.dv;
         auto chunk = [&](int64_t i) { return BACK ? chunks - 1 - i : i; };
-        auto issue = [&](int64_t i) {
+        auto issue = [&](int64_t i, int part) {
             const int64_t c = chunk(i), slot = base + c;
             char *d = lds + (STAGES == 2 ? i & 1 : 0) * kStage;
-            rows_in(in + (a + c * kC) * is + (int64_t)h * A.dv, is, len_of(c), A.dv, vec, lds + kVals + (i & 1) * kTile);
-            copy_in<1, kIn / 1024>((const char *)B.kq + (slot * A.Hk + hk) * kIn, d);
-            copy_in<1, kTpBytes / 1024>(tp + (slot * A.Hv + h) * kTpBytes, d + kIn);
+            if (part != 1) {
+                rows_in(in + (a + c * kC) * is + (int64_t)h * A.dv, is, len_of(c), A.dv, vec, lds + kVals + (i & 1) * kTile);
+                copy_in<1, kIn / 1024>((const char *)B.kq + (slot * A.Hk + hk) * kIn, d);
+            }
+            if (part != 0) copy_in<1, kTpBytes / 1024>(tp + (slot * A.Hv + h) * kTpBytes, d + kIn);
+        };
+        // One access a line brings a later chunk's bytes as far as L2 (what it
+        // copies is not looked at): this block's share of q's, k's and the
+        // triangular operands', and its columns' of V.  Always kTouches of them.
+        auto touch = [&](int64_t i) {
+            const int64_t c = chunk(i < chunks ? i : chunks - 1), slot = base + c;
+            const int lane = threadIdx.x & 63;
+            const uint32_t d = (uint32_t)(uintptr_t)(lds_ptr_t)(lds + kTouch);
+            const __amdgpu_buffer_rsrc_t rk = uniform_rsrc((const char *)B.kq + (slot * A.Hk + hk) * kIn, kIn);
+            const __amdgpu_buffer_rsrc_t rt = uniform_rsrc(tp + (slot * A.Hv + h) * kTpBytes, kTpBytes);
+            const __amdgpu_buffer_rsrc_t rv = rows_of(in + (a + c * kC) * is + (int64_t)h * A.dv + c0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                lds_dma16(rk, (uint32_t)((lane + 64 * u) * inner + share) * 128, d);
+                lds_dma16(rt, (uint32_t)((lane + 64 * u) * groups + c0 / COLS) * 128, d);
+            }
+            lds_dma16(rv, vec && c0 < A.dv && lane < len_of(c) ? (uint32_t)(lane * (int)is * ES) : kOutOfRange, d);
         };
         auto results = [&](int64_t i) {
             const int64_t c = chunk(i);
             rows_out(out + (a + c * kC) * os + (int64_t)h * A.dv, os, len_of(c), A.dv, vec, lds + kOuts + (i & 1) * kTile);
         };
-        if (STAGES == 2 && chunks > 0) issue(0);
+        if (STAGES == 2 && chunks > 0) issue(0, 2), touch(1);
         for (int64_t i = 0; i < chunks; ++i) {
             if (STAGES == 1) {
                 block_barrier();  // nobody reads the chunk before any more
-                issue(i);
-                if (i >= LAG) results(i - LAG);
+                issue(i, 2);
+                if (i > 0) results(i - 1);
             }
-            CONVLOWER_WAIT_VMCNT_LDS(0);
+            CONVLOWER_WAIT_VMCNT_LDS(STAGES == 2 ? kTouches : 0);
             block_barrier();  // the chunk is in LDS, the results of the one before too
-            if (STAGES == 2) {
-                if (i >= LAG) results(i - LAG);
-                if (i + 1 < chunks) issue(i + 1);
-            }
+            const bool more = STAGES == 2 && i + 1 < chunks;
+            // The way back's first barrier comes soon, and issuing the copies
+            // takes a third of a chunk's time.
+            if (!BACK && more) issue(i + 1, 2);
+            block_barrier();
+            if (BACK && more) issue(i + 1, 0);
+            if (BACK) block_barrier();
+            if (BACK && more) issue(i + 1, 1);
+            if (STAGES == 2 && i > 0) results(i - 1);
+            touch(i + STAGES);
         }
         block_barrier();
-        for (int64_t i = chunks > LAG ? chunks - LAG : 0; i < chunks; ++i) results(i);
+        if (chunks > 0) results(chunks - 1);
+        CONVLOWER_WAIT_VMCNT(0);  // nothing is on its way into LDS when the block ends
     }
     // The other wavefronts' side of it.
     __device__ __forceinline__ static void next_chunk() {
+        asm volatile("" ::: "memory");
         CONVLOWER_WAIT_LDS();
         if (STAGES == 1) block_barrier();
         block_barrier();
     }
 
+    // Inside a chunk: what this wavefront wrote is there for its partner.
+    __device__ __forceinline__ static void hand_over() {
+        asm volatile("" ::: "memory");
+        CONVLOWER_WAIT_LDS();
+        block_barrier();
+    }
+
     // ---- the computing wavefronts
+    template <int N>
+    __device__ __forceinline__ static void put(char *p, const f32x4 (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *(f32x4 *)(p + i * 1024 + (threadIdx.x & 63) * 16) = v[i];
+    }
+    template <int N>
+    __device__ __forceinline__ static void get(const char *p, f32x4 (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = *(const f32x4 *)(p + i * 1024 + (threadIdx.x & 63) * 16);
+    }
+    __device__ __forceinline__ static void put(char *p, const Split (&v)[KS]) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            *(f16x8 *)(p + 2 * s * 1024 + (threadIdx.x & 63) * 16) = v[s].hi;
+            *(f16x8 *)(p + (2 * s + 1) * 1024 + (threadIdx.x & 63) * 16) = v[s].lo;
+        }
+    }
+    __device__ __forceinline__ static void get(const char *p, Split (&v)[KS]) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) v[s].hi = frag_at(p + 2 * s * 1024), v[s].lo = frag_at(p + (2 * s + 1) * 1024);
+    }
+    // A float a lane; which: 0 the state's measure, 1 and 2 of the chunk.
+    __device__ __forceinline__ static float &scalar(char *pair, int which) {
+        return ((float *)(pair + kPairRows) + which * 64)[threadIdx.x & 63];
+    }
+    // The state that a pair's operands stand for, 16 rows by 16 (22 bits: what
+    // the gradients' products take of it).
+    __device__ __forceinline__ static void unsplit(const Split (&b)[KS], float is, f32x4 (&v)[MT]) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[i][r] = ((float)b[i / 2].hi[4 * (i & 1) + r] + (float)b[i / 2].lo[4 * (i & 1) + r]) * is;
+    }
     __device__ __forceinline__ void values(const char *lds, f32x4 (&v)[4]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -272,6 +364,20 @@ struct Scan {
             }
         }
     }
+    // One half of that product: rows 32 s.. of b.
+    __device__ __forceinline__ void cols_step(const char *x, int mt, int s, const Cols &f, const Split &b, f32x4 (&c)[MT]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[mt + i] = mma(f.f[s][i], b.lo, c[mt + i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[mt + i] = mma(f.f[s][i], b.hi, c[mt + i]);
+        if constexpr (SPLIT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const char *p = x + kMat + (2 * s * KS + (mt + i) / 2) * 1024;
+                c[mt + i] = mma(trans_at(p, p + KS * 1024, mt + i, tl), b.hi, c[mt + i]);
+            }
+        }
+    }
     // A triangular operand's fragments, or its transpose's, and its product;
     // ONE: the right operand has no second half.
     struct Tri {
@@ -309,82 +415,56 @@ struct Scan {
 // one, are not moved into that.
 __device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
-template <typename S, int DKP, int NW, bool SAVE>
-__global__ __launch_bounds__(kScanBounds) void delta_scan_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
-    typedef Scan<S, DKP, NW> W;
+// The wavefront that keeps the state: from it the rows that the chunk's tokens
+// miss, and the next state.
+template <typename W, typename S>
+__device__ __forceinline__ void scan_state(const W &w, const DeltaArgs &A, char *lds) {
     constexpr int MT = W::MT, KS = W::KS;
-    __shared__ __align__(16) char lds[W::kLds];
-    W w;
-    if (!w.place(A, groups)) return;
-    if (w.w == NW) return w.template copy<false, 2>(A, B, vec, lds);
-    const int tile = w.c0 / 16 + w.w;
-    const bool kept = SAVE && tile < B.dvp / 16;
+    char *pair = lds + W::kPairs + w.w * W::kPair;
     // The state, each column times a power of two that keeps it in f16's
     // range; is: the inverse.  What a chunk adds is bounded before it is
     // known, and comes in the same measure.
     f32x4 st[MT];
+    Split sb[KS];
     w.load_state(A, A.state, st);
-    float is, smax = col_max(max_of(st));
+    float is;
     {
-        const float s = pow2_to(smax, kTop, &is);
+        const float s = pow2_to(col_max(max_of(st)), kTop, &is);
 #pragma unroll
         for (int i = 0; i < MT; ++i) st[i] *= s;
-        smax *= s;
     }
-    // The last product of a chunk, (P b) Y, waits for the next chunk, whose
-    // own first product has to wait for the state to be split.
-    typename W::Tri pf = {};
-    Split yb[2] = {};
-    f32x4 o[4];
-    float iy = 0.f;
-    zero(o);
-    auto finish = [&](int64_t c) {
-        f32x4 y[4];
-        W::template tri_mul<false, false>(pf, yb, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += y[i] * iy;
-        w.results(lds + W::kOuts + (c & 1) * W::kTile, o);
-    };
+    for (int s = 0; s < 2; ++s) sb[s] = split8(st[2 * s], st[2 * s + 1]);
     for (int64_t c = 0; c < w.chunks; ++c) {
+#pragma unroll
+        for (int s = 2; s < KS; ++s) sb[s] = split8(st[2 * s], st[2 * s + 1]);
+        W::put(pair, sb);
+        W::scalar(pair, 0) = is;
         W::next_chunk();
         const char *x = lds + (W::STAGES == 2 ? c & 1 : 0) * W::kStage;
         const float *f = (const float *)(x + W::kRows) + 4 * w.g;
         const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
         auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
-        // the state in two halves; the chunk before is finished meanwhile
-        f32x4 z[4], y[4], f1[4], f2[4];
-        typename W::Rows kf, qf;
-        W::rows_load(x, 0, KS / 2, kf);
-        if constexpr (SAVE) {
-            if (kept) {
-                const int64_t vh = (w.base + c) * A.Hv + w.h;
-                f32x4 s[MT];
-#pragma unroll
-                for (int i = 0; i < MT; ++i) s[i] = st[i] * is;
-                w.keep(B.S + vh * DKP * B.dvp, tile, s);
-                const float mx = tile_max(smax * is);
-                if ((threadIdx.x & 63) == 0) B.Smax[vh * (B.dvp / 16) + tile] = mx;
-            }
-        }
-        Split sb[KS], zb[2], wb[2];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) sb[s] = split8(st[2 * s], st[2 * s + 1]);
-        finish(c - 1);  // (before the first chunk: zeros, which nobody takes)
-        phase();
+        f32x4 z[4], y[4], f1[4], f3b[4];
+        Split zb[2], wb[2];
         // K S
-        W::rows_load(x, KS / 2, KS, kf);
+        typename W::Rows kf;
+        typename W::Tri tf;
+        W::rows_load(x, 0, KS, kf);
         w.values(lds + W::kVals + (c & 1) * W::kTile, z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f1[i] = row(ROW_F1, i);
-        W::rows_load(x + W::kIn / 2, 0, KS / 2, qf);
-        W::rows_mul(x, kf, sb, y);
-        phase();
-        // Q S; Z
-        typename W::Tri tf;
-        W::rows_load(x + W::kIn / 2, KS / 2, KS, qf);
+        const float last = sc[SC_LAST], it = sc[SC_IT], bw = sc[SC_TF3];
         w.template tri_load<false>(x + W::kTi, tf.hi);
-        const float last = sc[SC_LAST], it = sc[SC_IT], ip = sc[SC_IP], bt = sc[SC_T], bw = sc[SC_TF3];
-        W::rows_mul(x + W::kIn / 2, qf, sb, o);
+        W::rows_mul(x, kf, sb, y);
+        const float smax = col_max(max_of(st));
+        phase();
+        // Z
+        typename W::Cols kc[MT / 4];
+        w.template tri_load<false>(x + W::kTi + W::kLo, tf.lo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f3b[i] = row(ROW_F3B, i);
+        w.cols_load(x, 0, kc[0]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] -= y[i] * (f1[i] * is);
         float iz;
@@ -393,123 +473,170 @@ __global__ __launch_bounds__(kScanBounds) void delta_scan_kernel(DeltaArgs A, De
         iz *= it;
         phase();
         // Y
-        typename W::Cols kc[MT / 4];
-        w.template tri_load<false>(x + W::kTi + W::kLo, tf.lo);
-        f32x4 f3b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f3b[i] = row(ROW_F3B, i), f2[i] = row(ROW_F2, i);
-        w.cols_load(x, 0, kc[0]);
         W::template tri_mul<false, false>(tf, zb, y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] *= f2[i] * is;
         // the next power of two, and the state in it
-        const float ss = pow2_to(smax * is * last + kRowSum * (zmax * bw), kBound, &iy);
+        float in;
+        const float ss = pow2_to(smax * is * last + kRowSum * (zmax * bw), kBound, &in);
         const float step = last * (ss * is);
-        is = iy;
+        is = in;
 #pragma unroll
         for (int i = 0; i < MT; ++i) st[i] *= step;
+        W::scalar(pair, 1) = iz;
+        W::scalar(pair, 2) = zmax;
         phase();
         // W, and K' W into the state
+        W::put(pair + W::kPairTiles, y);
+        if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = y[i] * f3b[i];
-        split_by(z, iz * ss, wb);
-        if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
+        wb[0] = split8(z[0], z[1], iz * ss);
+        W::hand_over();
         phase();
-        w.template tri_load<false>(x + W::kP, pf.hi);
-        w.template tri_load<false>(x + W::kP + W::kLo, pf.lo);
 #pragma unroll
-        for (int i = 0; i < MT / 4; ++i) w.cols_mul(x, 4 * i, kc[i], wb, st);
-        if constexpr (SAVE) {
-            if (kept) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = y[i] * iz;
-                w.keep(B.Y + ((w.base + c) * A.Hv + w.h) * kC * B.dvp, tile, z);
-            }
-        }
-        split_by(y, iz * pow2_to(zmax * bt, kBound, &iy), yb);
-        iy *= ip;
+        for (int i = 0; i < MT / 4; ++i) w.cols_step(x, 4 * i, 0, kc[i], wb[0], st);
+        wb[1] = split8(z[2], z[3], iz * ss);
         phase();
-        smax = col_max(max_of(st));
+        w.cols_step(x, 0, 1, kc[0], wb[1], st);
+        phase();
+        // (the state's first rows are split while its last ones are still to come)
+        if (MT > 4) w.cols_step(x, MT - 4, 1, kc[MT / 4 - 1], wb[1], st);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) sb[s] = split8(st[2 * s], st[2 * s + 1]);
+        phase();
     }
-    finish(w.chunks - 1);
-    CONVLOWER_WAIT_LDS();
-    block_barrier();
+    W::hand_over();
 #pragma unroll
     for (int i = 0; i < MT; ++i) st[i] *= is;
     w.store_state(A, A.state_out, st);
 }
 
-// From the last chunk to the first, with G, the gradient of the state.
-template <typename S, int DKP, int NW>
-__global__ __launch_bounds__(kScanBounds) void delta_scan_grad_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
+// Its partner: the outputs, and what is kept for the gradients.
+template <typename W, typename S, bool SAVE>
+__device__ __forceinline__ void scan_outputs(const W &w, const DeltaArgs &A, const DeltaBuf &B, char *lds) {
+    constexpr int MT = W::MT, KS = W::KS, DKP = 16 * MT;
+    char *pair = lds + W::kPairs + w.w * W::kPair;
+    const int tile = w.c0 / 16 + w.w;
+    const bool kept = SAVE && tile < B.dvp / 16;
+    for (int64_t c = 0; c < w.chunks; ++c) {
+        W::next_chunk();
+        const char *x = lds + (W::STAGES == 2 ? c & 1 : 0) * W::kStage;
+        const float *f = (const float *)(x + W::kRows) + 4 * w.g;
+        const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
+        const int64_t vh = (w.base + c) * A.Hv + w.h;
+        f32x4 o[4], y[4], f2[4];
+        Split sb[KS], yb[2];
+        typename W::Rows qf;
+        typename W::Tri pf;
+        // Q S
+        W::get(pair, sb);
+        const float is = W::scalar(pair, 0);
+        W::rows_load(x + W::kIn / 2, 0, KS, qf);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2[i] = *(const f32x4 *)(f + ROW_F2 * kC + 16 * i);
+        const float ip = sc[SC_IP], bt = sc[SC_T];
+        W::rows_mul(x + W::kIn / 2, qf, sb, o);
+        phase();
+        w.template tri_load<false>(x + W::kP, pf.hi);
+        w.template tri_load<false>(x + W::kP + W::kLo, pf.lo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= f2[i] * is;
+        if constexpr (SAVE) {
+            if (kept) {
+                f32x4 s[MT];
+                W::unsplit(sb, is, s);
+                w.keep(B.S + vh * DKP * B.dvp, tile, s);
+                const float mx = tile_max(max_of(s));
+                if ((threadIdx.x & 63) == 0) B.Smax[vh * (B.dvp / 16) + tile] = mx;
+            }
+        }
+        W::hand_over();
+        phase();
+        // P Y
+        W::get(pair + W::kPairTiles, y);
+        const float iz = W::scalar(pair, 1), zmax = W::scalar(pair, 2);
+        float iy;
+        split_by(y, iz * pow2_to(zmax * bt, kBound, &iy), yb);
+        iy *= ip;
+        if constexpr (SAVE) {
+            if (kept) {
+                f32x4 z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] = y[i] * iz;
+                w.keep(B.Y + vh * kC * B.dvp, tile, z);
+            }
+        }
+        W::template tri_mul<false, false>(pf, yb, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += y[i] * iy;
+        w.results(lds + W::kOuts + (c & 1) * W::kTile, o);
+    }
+    W::hand_over();
+}
+
+template <typename S, int DKP, int NW, bool SAVE>
+__global__ __launch_bounds__(kScanBounds) void delta_scan_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
     typedef Scan<S, DKP, NW> W;
-    constexpr int MT = W::MT, KS = W::KS;
     __shared__ __align__(16) char lds[W::kLds];
     W w;
     if (!w.place(A, groups)) return;
-    if (w.w == NW) return w.template copy<true, 1>(A, B, vec, lds);
-    const int tile = w.c0 / 16 + w.w;
-    const bool kept = tile < B.dvp / 16;
+    if (w.role == 0) scan_outputs<W, S, SAVE>(w, A, B, lds);
+    else if (w.role == 1) scan_state<W, S>(w, A, lds);
+    else w.template copy<false>(A, B, vec, lds);
+}
+
+// From the last chunk to the first, with G, the gradient of the state.
+template <typename W, typename S>
+__device__ __forceinline__ void scan_grad_state(const W &w, const DeltaArgs &A, char *lds) {
+    constexpr int MT = W::MT, KS = W::KS;
+    char *pair = lds + W::kPairs + w.w * W::kPair;
     f32x4 G[MT];
     w.load_state(A, A.dstate_out, G);
-    float is, gmax = col_max(max_of(G));
+    float is;
     {
-        const float s = pow2_to(gmax, kTop, &is);
+        const float s = pow2_to(col_max(max_of(G)), kTop, &is);
 #pragma unroll
         for (int i = 0; i < MT; ++i) G[i] *= s;
-        gmax *= s;
     }
     for (int64_t j = 0; j < w.chunks; ++j) {
+        Split gb[KS], eb[2], yb[2];
         W::next_chunk();
         const char *x = lds + (W::STAGES == 2 ? j & 1 : 0) * W::kStage;
         const float *f = (const float *)(x + W::kRows) + 4 * w.g;
         const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
         auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
-        const int64_t vh = (w.base + w.chunks - 1 - j) * A.Hv + w.h;
-        f32x4 d[4], y[4], e[4], f3[4], f1b[4], f2[4], b[4];
+        f32x4 e[4], y[4], f3[4], f1b[4], q[MT];
+        // K G
         typename W::Rows kf;
-        typename W::Tri pf, tf;
-        W::rows_load(x, 0, KS / 2, kf);
-        w.values(lds + W::kVals + (j & 1) * W::kTile, d);
-        w.template tri_load<true>(x + W::kP, pf.hi);
-        w.template tri_load<true>(x + W::kP + W::kLo, pf.lo);
-        if (kept) {
-            f32x4 s[MT];
+        typename W::Tri tf;
+        W::rows_load(x, 0, KS, kf);
+        w.template tri_load<true>(x + W::kTi, tf.hi);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) s[i] = G[i] * is;
-            w.keep(B.G + vh * DKP * B.dvp, tile, s);
-            const float mx = tile_max(gmax * is);
-            if ((threadIdx.x & 63) == 0) B.Gmax[vh * (B.dvp / 16) + tile] = mx;
-        }
-        float id, ie;
-        Split gb[KS], db[2], eb[2], yb[2];
+        for (int i = 0; i < 4; ++i) f3[i] = row(ROW_F3, i);
+        const float last = sc[SC_LAST], it = sc[SC_IT], bf1 = sc[SC_TF1], bf2 = sc[SC_F2];
 #pragma unroll
         for (int s = 0; s < KS; ++s) gb[s] = split8(G[2 * s], G[2 * s + 1]);
+        W::put(pair, gb);
+        W::scalar(pair, 0) = is;
+        W::hand_over();
         phase();
-        // K G, P' dO (16-bit dO is exact in one half)
-        W::rows_load(x, KS / 2, KS, kf);
-        w.template tri_load<true>(x + W::kTi, tf.hi);
+        W::get(pair + W::kPairTiles, y);
+        const float dmax = W::scalar(pair, 1);
         w.template tri_load<true>(x + W::kTi + W::kLo, tf.lo);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f3[i] = row(ROW_F3, i), f2[i] = row(ROW_F2, i);
-        const float last = sc[SC_LAST], it = sc[SC_IT], ip = sc[SC_IP], bf1 = sc[SC_TF1], bf2 = sc[SC_F2];
         W::rows_mul(x, kf, gb, e);
-        const float dmax = col_max(max_of(d));
-        split_by(d, pow2_to(dmax, kTop, &id), db);
-        W::template tri_mul<true, !W::SPLIT>(pf, db, y);
-        id *= ip;
+        const float gmax = col_max(max_of(G));
         phase();
-        // X, E
-        typename W::Cols kc, qc;
+        // X = .. + P' dO, E
+        typename W::Cols kc[MT / 4];
+        w.cols_load(x, 0, kc[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = e[i] * (f3[i] * is) + y[i] * id;
+        for (int i = 0; i < 4; ++i) f1b[i] = row(ROW_F1B, i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = e[i] * (f3[i] * is) + y[i];
+        float ie;
         const float emax = col_max(max_of(e));
         split_by(e, pow2_to(emax, kTop, &ie), eb);
         ie *= it;
-        w.cols_load(x, 0, kc);
         phase();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f1b[i] = row(ROW_F1B, i), b[i] = row(ROW_B, i);
         W::template tri_mul<true, false>(tf, eb, e);
         float ig;
         const float ss = pow2_to(gmax * is * last + kRowSum * (emax * bf1 + dmax * bf2), kBound, &ig);
@@ -517,41 +644,110 @@ __global__ __launch_bounds__(kScanBounds) void delta_scan_grad_kernel(DeltaArgs 
         is = ig;
 #pragma unroll
         for (int i = 0; i < MT; ++i) G[i] *= step;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] *= f2[i];
-        split_by(d, ss, db);
-        w.cols_load(x + W::kIn / 2, 0, qc);
         phase();
         // dS = .. + Q' (f2 dO) - K' (f1 b E)
-        w.cols_mul(x + W::kIn / 2, 0, qc, db, G);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            e[i] *= ie;
-            y[i] = e[i] * f1b[i];
-        }
+        for (int i = 0; i < 4; ++i) e[i] *= ie;
+        W::put(pair + W::kPairTiles, e);
+        if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
+        W::hand_over();
+        W::get(pair, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = e[i] * f1b[i];
         split_by(y, -ss, yb);
-        phase();
-        w.cols_mul(x, 0, kc, yb, G);
-        if (MT > 4) {
-            w.cols_load(x, 4, kc);
-            w.cols_load(x + W::kIn / 2, 4, qc);
-        }
-        if (kept) w.keep(B.E + vh * kC * B.dvp, tile, e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] *= b[i];  // dZ
-        w.results(lds + W::kOuts + (j & 1) * W::kTile, e);
+        for (int i = 0; i < MT; ++i) G[i] += q[i] * ss;
         phase();
-        if (MT > 4) {
-            w.cols_mul(x + W::kIn / 2, 4, qc, db, G);
-            w.cols_mul(x, 4, kc, yb, G);
-        }
-        gmax = col_max(max_of(G));
+#pragma unroll
+        for (int i = 0; i < MT / 4; ++i) w.cols_mul(x, 4 * i, kc[i], yb, G);
+        phase();
     }
-    CONVLOWER_WAIT_LDS();
-    block_barrier();
+    W::hand_over();
 #pragma unroll
     for (int i = 0; i < MT; ++i) G[i] *= is;
     w.store_state(A, A.dstate, G);
+}
+
+// Its partner: what needs dO alone, P' dO and Q' (f2 dO); dV, and what is kept.
+template <typename W, typename S>
+__device__ __forceinline__ void scan_grad_outputs(const W &w, const DeltaArgs &A, const DeltaBuf &B, char *lds) {
+    constexpr int MT = W::MT, KS = W::KS, DKP = 16 * MT;
+    char *pair = lds + W::kPairs + w.w * W::kPair;
+    const int tile = w.c0 / 16 + w.w;
+    const bool kept = tile < B.dvp / 16;
+    for (int64_t j = 0; j < w.chunks; ++j) {
+        W::next_chunk();
+        const char *x = lds + (W::STAGES == 2 ? j & 1 : 0) * W::kStage;
+        const float *f = (const float *)(x + W::kRows) + 4 * w.g;
+        const float *sc = (const float *)(x + W::kRows) + ROW_SCALARS * kC;
+        auto row = [&](int which, int i) { return *(const f32x4 *)(f + which * kC + 16 * i); };
+        const int64_t vh = (w.base + w.chunks - 1 - j) * A.Hv + w.h;
+        f32x4 d[4], y[4], f2[4], q[MT];
+        Split gb[KS], db[2];
+        typename W::Tri pf;
+        // P' dO (16-bit dO is exact in one half)
+        w.values(lds + W::kVals + (j & 1) * W::kTile, d);
+        w.template tri_load<true>(x + W::kP, pf.hi);
+        w.template tri_load<true>(x + W::kP + W::kLo, pf.lo);
+        const float ip = sc[SC_IP];
+        float id;
+        const float dmax = col_max(max_of(d));
+        split_by(d, pow2_to(dmax, kTop, &id), db);
+        W::template tri_mul<true, !W::SPLIT>(pf, db, y);
+        id *= ip;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= id;
+        W::put(pair + W::kPairTiles, y);
+        W::scalar(pair, 1) = dmax;
+        phase();
+        // Q' (f2 dO)
+        typename W::Cols qc[MT / 4];
+        w.cols_load(x + W::kIn / 2, 0, qc[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2[i] = row(ROW_F2, i);
+        W::hand_over();
+        W::get(pair, gb);
+        const float is = W::scalar(pair, 0);
+        if (kept) {
+            f32x4 s[MT];
+            W::unsplit(gb, is, s);
+            w.keep(B.G + vh * DKP * B.dvp, tile, s);
+            const float mx = tile_max(max_of(s));
+            if ((threadIdx.x & 63) == 0) B.Gmax[vh * (B.dvp / 16) + tile] = mx;
+        }
+        if (MT > 4) w.cols_load(x + W::kIn / 2, 4, qc[MT / 4 - 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] *= f2[i];
+        split_by(d, pow2_to(col_max(max_of(d)), kTop, &id), db);
+        phase();
+        zero(q);
+#pragma unroll
+        for (int i = 0; i < MT / 4; ++i) w.cols_mul(x + W::kIn / 2, 4 * i, qc[i], db, q);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) q[i] *= id;
+        W::put(pair, q);
+        W::hand_over();
+        phase();
+        // E, dV = b E
+        f32x4 e[4];
+        W::get(pair + W::kPairTiles, e);
+        if (kept) w.keep(B.E + vh * kC * B.dvp, tile, e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] *= row(ROW_B, i);
+        w.results(lds + W::kOuts + (j & 1) * W::kTile, e);
+    }
+    W::hand_over();
+}
+
+template <typename S, int DKP, int NW>
+__global__ __launch_bounds__(kScanBounds) void delta_scan_grad_kernel(DeltaArgs A, DeltaBuf B, int groups, bool vec) {
+    typedef Scan<S, DKP, NW> W;
+    __shared__ __align__(16) char lds[W::kLds];
+    W w;
+    if (!w.place(A, groups)) return;
+    if (w.role == 0) scan_grad_outputs<W, S>(w, A, B, lds);
+    else if (w.role == 1) scan_grad_state<W, S>(w, A, lds);
+    else w.template copy<true>(A, B, vec, lds);
 }
 
 template <typename S, int DKP, int NW>
@@ -565,7 +761,7 @@ hipError_t scan_run(const DeltaArgs &a, const DeltaBuf &b, bool grad, hipStream_
     const uintptr_t in = (uintptr_t)(grad ? a.d_o : a.v), out = (uintptr_t)(grad ? a.dv_out : a.o);
     const bool vec = a.dv * sizeof(S) % 16 == 0 && is % 16 == 0 && in % 16 == 0 && out % 16 == 0;
     auto run = [&](auto kern) {
-        hipLaunchKernelGGL(kern, grid, dim3(64 * NW + 64), 0, st, a, b, groups, vec);
+        hipLaunchKernelGGL(kern, grid, dim3(64 * (2 * NW + 1)), 0, st, a, b, groups, vec);
         return hipGetLastError();
     };
     if (grad) return run(delta_scan_grad_kernel<S, DKP, NW>);
