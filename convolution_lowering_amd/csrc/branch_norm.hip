@@ -12,7 +12,9 @@
 // ends.
 // Measured (bf16): forward 16384 x 4096 with x, h and a shared gate 107 us,
 // 5.0 TB/s; gradients of 8192 x 4096 110 + 7 us (82 us at a copy's rate);
-// 131072 x 128 gated rows 21 us forward, 37 + 7 us back.
+// 131072 x 128 gated rows 21 us forward, 37 + 7 us back.  Rows of odd widths
+// are read 16 bytes at a time as well: 72052 x 222 forward 35 us (128 MB), one
+// value at a time 66; 30001 x 1061 both ways 494 us, was 714.
 #include <algorithm>
 
 #include "mixer_internal.h"
@@ -55,28 +57,62 @@ __device__ __forceinline__ void act_grad(float z, int act, float *a, float *da) 
     *da = act == MIX_ACT_SILU ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
 }
 
-// The columns of a thread: V values from (i * TPR + lane) * V, i < NV.
-template <typename S, int V, int TPR, int NV>
-__device__ __forceinline__ void load_row(const S *p, int lane, int D, float (&f)[NV][V]) {
+// V values from column c of a row of D, at p.  ANY: rows that lie at any
+// multiple of a value's size (such an access still is one instruction), whose
+// last piece may hold fewer; what is past the row reads as zero.
+template <typename S, int V>
+struct __attribute__((packed, aligned(sizeof(S)))) AnyVec {
+    S v[V];
+};
+template <typename S, int V, bool ANY>
+__device__ __forceinline__ MixVec<S, V> piece(const S *p, int c, int D) {
+    MixVec<S, V> t = {};
+    if constexpr (!ANY) {
+        if (c < D) t = *(const MixVec<S, V> *)(p + c);
+    } else if (c + V <= D) {
+        const AnyVec<S, V> u = *(const AnyVec<S, V> *)(p + c);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < D) mix_load<S, V>(p + c, f[i]);
-        else
+        for (int j = 0; j < V; ++j) t.v[j] = u.v[j];
+    } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) f[i][j] = 0.f;
+        for (int j = 0; j < V; ++j)
+            if (c + j < D) t.v[j] = p[c + j];
     }
+    return t;
 }
-template <typename S, int V, int TPR, int NV>
-__device__ __forceinline__ void store_row(S *p, int lane, int D, const float (&f)[NV][V]) {
+template <typename S, int V, bool ANY>
+__device__ __forceinline__ void put_piece(S *p, int c, int D, const float (&f)[V]) {
+    if constexpr (!ANY) {
+        if (c < D) mix_store<S, V>(p + c, f);
+    } else if (c + V <= D) {
+        AnyVec<S, V> t;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (c < D) mix_store<S, V>(p + c, f[i]);
+        for (int j = 0; j < V; ++j) t.v[j] = mix_out<S>(f[j]);
+        *(AnyVec<S, V> *)(p + c) = t;
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (c + j < D) p[c + j] = mix_out<S>(f[j]);
     }
 }
 
-template <typename S, int V, int TPR, int NV>
+// The columns of a thread: V values from (i * TPR + lane) * V, i < NV.
+template <typename S, int V, int TPR, int NV, bool ANY>
+__device__ __forceinline__ void load_row(const S *p, int lane, int D, float (&f)[NV][V]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const MixVec<S, V> t = piece<S, V, ANY>(p, (i * TPR + lane) * V, D);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[i][j] = mix_f32(t.v[j]);
+    }
+}
+template <typename S, int V, int TPR, int NV, bool ANY>
+__device__ __forceinline__ void store_row(S *p, int lane, int D, const float (&f)[NV][V]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) put_piece<S, V, ANY>(p, (i * TPR + lane) * V, D, f[i]);
+}
+
+template <typename S, int V, int TPR, int NV, bool ANY>
 __global__ __launch_bounds__(block_of(TPR)) void branch_norm_fwd_kernel(NormArgs A) {
     constexpr int TB = block_of(TPR), ROWS = TB / TPR;
     __shared__ float red[TB / 64];
@@ -85,9 +121,9 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_fwd_kernel(NormArgs
     const bool live = row < A.R;  // a block of one row each is always live: the sums below meet all its threads
     const int64_t at = (live ? row : 0) * A.D;
     float r[NV][V], f[NV][V], w[NV][V];
-    load_row<S, V, TPR, NV>((const S *)A.y + at, lane, A.D, r);
-    if (A.gate) load_row<S, V, TPR, NV>((const S *)A.gate + (live ? row / A.rows_per_gate : 0) * A.D, lane, A.D, f);
-    load_row<S, V, TPR, NV>((const S *)A.w_post, lane, A.D, w);
+    load_row<S, V, TPR, NV, ANY>((const S *)A.y + at, lane, A.D, r);
+    if (A.gate) load_row<S, V, TPR, NV, ANY>((const S *)A.gate + (live ? row / A.rows_per_gate : 0) * A.D, lane, A.D, f);
+    load_row<S, V, TPR, NV, ANY>((const S *)A.w_post, lane, A.D, w);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -102,7 +138,7 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_fwd_kernel(NormArgs
             if (A.gate) r[i][j] *= act_of(f[i][j], A.act);
         }
     if (A.x) {
-        load_row<S, V, TPR, NV>((const S *)A.x + at, lane, A.D, f);
+        load_row<S, V, TPR, NV, ANY>((const S *)A.x + at, lane, A.D, f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -113,34 +149,31 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_fwd_kernel(NormArgs
 #pragma unroll
             for (int j = 0; j < V; ++j) r[i][j] *= A.alpha;
     }
-    if (live) store_row<S, V, TPR, NV>((S *)A.r + at, lane, A.D, r);
+    if (live) store_row<S, V, TPR, NV, ANY>((S *)A.r + at, lane, A.D, r);
     if (A.stats && live && lane == 0) A.stats[row] = rs;
     if (!A.w_next) return;
-    load_row<S, V, TPR, NV>((const S *)A.w_next, lane, A.D, w);
+    load_row<S, V, TPR, NV, ANY>((const S *)A.w_next, lane, A.D, w);
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            if ((i * TPR + lane) * V < A.D) ss = fmaf(r[i][j], r[i][j], ss);
+            if ((i * TPR + lane) * V + (ANY ? j : 0) < A.D) ss = fmaf(r[i][j], r[i][j], ss);
     const float rn = 1.f / sqrtf(row_sum<TPR>(ss, red) / A.D + A.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) r[i][j] *= rn * w[i][j];
-    if (live) store_row<S, V, TPR, NV>((S *)A.h + at, lane, A.D, r);
+    if (live) store_row<S, V, TPR, NV, ANY>((S *)A.h + at, lane, A.D, r);
     if (A.stats && live && lane == 0) A.stats[A.R + row] = rn;
 }
 
 // The block's sum of each column over the rows it held side by side, to p[D].
-template <int V, int TPR, int NV>
+template <int V, int TPR, int NV, bool ANY>
 __device__ __forceinline__ void block_sums(float (&s)[NV][V], float *p, int lane, int D) {
     if constexpr (TPR > 64) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lane) * V;
-            if (c < D) mix_store<float, V>(p + c, s[i]);
-        }
+        for (int i = 0; i < NV; ++i) put_piece<float, V, ANY>(p, (i * TPR + lane) * V, D, s[i]);
     } else {
         __shared__ float all[4][NV * TPR * V];  // one line a wavefront
 #pragma unroll
@@ -162,7 +195,7 @@ __device__ __forceinline__ void block_sums(float (&s)[NV][V], float *p, int lane
 // dy = rstd(y) (e - yn mean(e yn)), e = du w_post
 // r is built again from x and y: the rounded r would cost digits, and x is
 // the same number of bytes.
-template <typename S, int V, int TPR, int NV>
+template <typename S, int V, int TPR, int NV, bool ANY>
 __global__ __launch_bounds__(block_of(TPR)) void branch_norm_bwd_kernel(NormArgs A) {
     constexpr int TB = block_of(TPR), ROWS = TB / TPR;
     __shared__ float red[TB / 64];
@@ -178,9 +211,8 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_bwd_kernel(NormArgs
     auto fetch = [&](const void *p, int64_t at, Raw (&f)[NV]) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lane) * V;
             f[i] = Raw{};
-            if (p && c < A.D) f[i] = *(const Raw *)((const S *)p + at + c);
+            if (p) f[i] = piece<S, V, ANY>((const S *)p + at, (i * TPR + lane) * V, A.D);
         }
     };
     float sp[NV][V], sg[NV][V], sn[NV][V];
@@ -241,7 +273,7 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_bwd_kernel(NormArgs
 #pragma unroll
                 for (int j = 0; j < V; ++j) d[i][j] = fmaf(xs, e[i][j] - x[i][j] * dot, d[i][j]);
         }
-        if (A.dx && live) store_row<S, V, TPR, NV>((S *)A.dx + at, lane, A.D, d);
+        if (A.dx && live) store_row<S, V, TPR, NV, ANY>((S *)A.dx + at, lane, A.D, d);
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -261,18 +293,18 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_bwd_kernel(NormArgs
                 dot = fmaf(f, y[i][j], dot);
                 d[i][j] = f;
             }
-        if (per_row && live) store_row<S, V, TPR, NV>((S *)A.dgate + at, lane, A.D, g);
+        if (per_row && live) store_row<S, V, TPR, NV, ANY>((S *)A.dgate + at, lane, A.D, g);
         dot = row_sum<TPR>(dot, red) / A.D;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) d[i][j] = ys * (d[i][j] - y[i][j] * dot);
-        if (live) store_row<S, V, TPR, NV>((S *)A.dy + at, lane, A.D, d);
+        if (live) store_row<S, V, TPR, NV, ANY>((S *)A.dy + at, lane, A.D, d);
     }
-    block_sums<V, TPR, NV>(sp, A.part + (int64_t)blockIdx.x * A.D, lane, A.D);
+    block_sums<V, TPR, NV, ANY>(sp, A.part + (int64_t)blockIdx.x * A.D, lane, A.D);
     const int64_t plane = (int64_t)gridDim.x * A.D;
-    if (A.w_next) block_sums<V, TPR, NV>(sn, A.part + plane + (int64_t)blockIdx.x * A.D, lane, A.D);
-    if (A.gate && !per_row) block_sums<V, TPR, NV>(sg, A.part + 2 * plane + (int64_t)blockIdx.x * A.D, lane, A.D);
+    if (A.w_next) block_sums<V, TPR, NV, ANY>(sn, A.part + plane + (int64_t)blockIdx.x * A.D, lane, A.D);
+    if (A.gate && !per_row) block_sums<V, TPR, NV, ANY>(sg, A.part + 2 * plane + (int64_t)blockIdx.x * A.D, lane, A.D);
 }
 
 // Sums of the blocks' partial sums for one output row of D columns: 64
@@ -303,16 +335,16 @@ __global__ __launch_bounds__(1024) void branch_norm_sum_kernel(NormArgs A) {
     out[group * A.D + c] = mix_out<S>(s);
 }
 
-template <typename S, int V, int TPR, int NV, bool BWD>
+template <typename S, int V, int TPR, int NV, bool ANY, bool BWD>
 hipError_t norm_run(const NormArgs &a, hipStream_t st) {
     constexpr int TB = block_of(TPR), rows = TB / TPR;
     if constexpr (!BWD) {
-        hipLaunchKernelGGL((branch_norm_fwd_kernel<S, V, TPR, NV>), dim3((unsigned)((a.R + rows - 1) / rows)), dim3(TB),
+        hipLaunchKernelGGL((branch_norm_fwd_kernel<S, V, TPR, NV, ANY>), dim3((unsigned)((a.R + rows - 1) / rows)), dim3(TB),
                            0, st, a);
         return hipGetLastError();
     } else {
         if (a.R) {
-            hipLaunchKernelGGL((branch_norm_bwd_kernel<S, V, TPR, NV>), dim3(a.blocks), dim3(TB), 0, st, a);
+            hipLaunchKernelGGL((branch_norm_bwd_kernel<S, V, TPR, NV, ANY>), dim3(a.blocks), dim3(TB), 0, st, a);
             if (const hipError_t e = hipGetLastError()) return e;
         }
         const unsigned gates = a.gate && a.G != a.R ? (unsigned)a.G : 0;
@@ -324,28 +356,21 @@ hipError_t norm_run(const NormArgs &a, hipStream_t st) {
 // The fewest threads that hold a row in one 16-byte piece each, and more
 // pieces only past 1024 threads: registers are what the backward pass runs out
 // of (4096 bf16: 512 threads of one piece against 256 of two, 110 against 171
-// us).  Rows that cannot be read 16 bytes at a time take four values a thread.
-template <typename S, int V, bool BWD>
+// us).
+template <typename S, bool ANY, bool BWD>
 hipError_t norm_width(const NormArgs &a, hipStream_t st) {
-    if constexpr (V == 1) {
-        if (a.D <= 256) return norm_run<S, V, 64, 4, BWD>(a, st);
-        if (a.D <= 1024) return norm_run<S, V, 256, 4, BWD>(a, st);
-        if (a.D <= 4096) return norm_run<S, V, 1024, 4, BWD>(a, st);
-        if (a.D <= 8192) return norm_run<S, V, 1024, 8, BWD>(a, st);
-        return norm_run<S, V, 1024, 32, BWD>(a, st);
-    } else {
-        if (a.D <= 16 * V) return norm_run<S, V, 16, 1, BWD>(a, st);
-        if (a.D <= 32 * V) return norm_run<S, V, 32, 1, BWD>(a, st);
-        if (a.D <= 64 * V) return norm_run<S, V, 64, 1, BWD>(a, st);
-        if (a.D <= 128 * V) return norm_run<S, V, 128, 1, BWD>(a, st);
-        if (a.D <= 256 * V) return norm_run<S, V, 256, 1, BWD>(a, st);
-        if (a.D <= 512 * V) return norm_run<S, V, 512, 1, BWD>(a, st);
-        if (a.D <= 1024 * V) return norm_run<S, V, 1024, 1, BWD>(a, st);
-        if (a.D <= 2048 * V) return norm_run<S, V, 1024, 2, BWD>(a, st);
-        if constexpr (V == 4)
-            if (a.D > 4096 * V) return norm_run<S, V, 1024, 8, BWD>(a, st);  // to 32768 float32
-        return norm_run<S, V, 1024, 4, BWD>(a, st);
-    }
+    constexpr int V = 16 / sizeof(S);
+    if (a.D <= 16 * V) return norm_run<S, V, 16, 1, ANY, BWD>(a, st);
+    if (a.D <= 32 * V) return norm_run<S, V, 32, 1, ANY, BWD>(a, st);
+    if (a.D <= 64 * V) return norm_run<S, V, 64, 1, ANY, BWD>(a, st);
+    if (a.D <= 128 * V) return norm_run<S, V, 128, 1, ANY, BWD>(a, st);
+    if (a.D <= 256 * V) return norm_run<S, V, 256, 1, ANY, BWD>(a, st);
+    if (a.D <= 512 * V) return norm_run<S, V, 512, 1, ANY, BWD>(a, st);
+    if (a.D <= 1024 * V) return norm_run<S, V, 1024, 1, ANY, BWD>(a, st);
+    if (a.D <= 2048 * V) return norm_run<S, V, 1024, 2, ANY, BWD>(a, st);
+    if constexpr (V == 4)
+        if (a.D > 4096 * V) return norm_run<S, V, 1024, 8, ANY, BWD>(a, st);  // to 32768 float32
+    return norm_run<S, V, 1024, 4, ANY, BWD>(a, st);
 }
 
 template <typename S, bool BWD>
@@ -355,7 +380,7 @@ hipError_t norm_typed(const NormArgs &a, hipStream_t st) {
     for (const void *p : {a.x, a.y, a.w_post, a.gate, a.w_next, a.dr, a.dh, (const void *)a.r, (const void *)a.h,
                           (const void *)a.dx, (const void *)a.dy, (const void *)a.dgate})
         vec = vec && (uintptr_t)p % 16 == 0;
-    return vec ? norm_width<S, V, BWD>(a, st) : norm_width<S, 1, BWD>(a, st);
+    return vec ? norm_width<S, false, BWD>(a, st) : norm_width<S, true, BWD>(a, st);
 }
 
 }  // namespace
