@@ -8,8 +8,15 @@
 // The inverse is built from 16 x 16 diagonal blocks (substitution, a lane a
 // column) and joined twice, [A 0; B C]^-1 = [A' 0; -C' B A', C'], on the
 // float32 matrix cores.
-// Sums of g are held in float64: gam_i - gam_j loses too many digits in 32
-// bits where a chunk holds strong decays beside weak ones.
+// Sums of g are held in float64, and as two floats where differences of them
+// are taken: gam_i - gam_j loses too many digits in 32 bits where a chunk holds
+// strong decays beside weak ones.
+//
+// 16384 tokens, 16 and 32 heads of 128 (134 MB of q and k, 352 MB of operands
+// written, 99 us at a copy's rate): 149 us; 8192 tokens, 8 and 16 heads with
+// what the gradients need 58 us.  Bound by the barriers between a head's steps
+// (six, three blocks to a CU); the inverse by substitution alone, a lane a
+// column of the whole matrix, 246 us.
 #include "delta_chunk.h"
 
 namespace convlower {
@@ -87,7 +94,7 @@ __device__ __forceinline__ f32x4 mma32(float a, float b, f32x4 c) {
 
 // Both inverses of a chunk, from the strictly lower L ([64][kLd] in LDS) and
 // b: X[0] = (1 + L diag(b))^-1 and, WAYS = 2, X[1] = (1 + diag(b) L)^-1.
-// 256 threads, three barriers inside, none after.  m[way]: the largest value
+// 256 threads, two barriers inside, none after.  m[way]: the largest value
 // this thread wrote.
 //
 // A float32 product's left operand has row m, step s column 4 s + g in lane
@@ -183,8 +190,12 @@ __device__ __forceinline__ void store_tri(const float *x, const float *by, float
     }
 }
 
+// Bounds: the blocks that a CU's LDS and registers hold; a fourth, with the
+// registers that leaves it, gains nothing (151 against 149 us).
 template <typename S, int DKP, bool GRAD>
-__global__ __launch_bounds__(256, GRAD ? 2 : 3) void delta_prep_kernel(DeltaArgs A, DeltaBuf B, bool vec) {
+constexpr int kPrepBlocks = GRAD || (sizeof(S) == 4 && DKP == 128) ? 2 : 3;
+template <typename S, int DKP, bool GRAD>
+__global__ __launch_bounds__(256, kPrepBlocks<S, DKP, GRAD>) void delta_prep_kernel(DeltaArgs A, DeltaBuf B, bool vec) {
     constexpr bool SPLIT = sizeof(S) == 4;
     constexpr int LD = DKP + 8, KS = DKP / 32, PL = SPLIT ? 2 : 1, WAYS = GRAD ? 2 : 1;
     // q and k first, then a value head's L and inverses (P before those)
@@ -193,7 +204,7 @@ __global__ __launch_bounds__(256, GRAD ? 2 : 3) void delta_prep_kernel(DeltaArgs
     _Float16 *sk = (_Float16 *)both, *sq = sk + PL * kC * LD;
     float *lm = (float *)both, *xi = lm + kC * kLd;
     __shared__ __align__(16) float rk[kC], nk[kC], uq[kC], nq[kC], sb[4][kC], red[4][4], mfs[4][4];
-    __shared__ __align__(16) double sg[4][kC];
+    __shared__ __align__(16) float gh[4][kC], gl[4][kC];  // gam / log 2 in two floats
     const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const DeltaChunk ch = chunk_of(A.s, slot);
@@ -276,7 +287,9 @@ __global__ __launch_bounds__(256, GRAD ? 2 : 3) void delta_prep_kernel(DeltaArgs
                 if (lane >= d) s += o;
             }
             const double all = __shfl(s, 63, 64);
-            sg[w][lane] = s;
+            const double s2 = s * 1.4426950408889634;
+            gh[w][lane] = (float)s2;
+            gl[w][lane] = (float)(s2 - (double)(float)s2);
             sb[w][lane] = bt;
             const float rise = expf((float)s), last = expf((float)all);
             const float f1 = rk[lane] * rise, f2 = uq[lane] * A.scale * rise, f3 = rk[lane] * expf((float)(all - s));
@@ -311,14 +324,15 @@ __global__ __launch_bounds__(256, GRAD ? 2 : 3) void delta_prep_kernel(DeltaArgs
             for (int nt = 0; nt < 4; ++nt) {
                 if (nt > w) continue;
                 const int j = 16 * nt + m;
-                const double gj = sg[v][j];
-                const float bj = sb[v][j];
+                const float hj = gh[v][j], lj = gl[v][j], bj = sb[v][j];
+                const f32x4 hi = *(const f32x4 *)(gh[v] + row), li = *(const f32x4 *)(gl[v] + row);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = row + r;
-                    const float d = j <= i ? expf((float)(sg[v][i] - gj)) : 0.f;
-                    const float p = j <= i ? qk[nt][r] * d : 0.f;
-                    lm[i * kLd + j] = j < i ? kk[nt][r] * d : 0.f;
+                    const float d = __builtin_amdgcn_exp2f((hi[r] - hj) + (li[r] - lj));
+                    const bool in = nt < w || j <= i;
+                    const float p = in ? qk[nt][r] * d : 0.f;
+                    lm[i * kLd + j] = in && j != i ? kk[nt][r] * d : 0.f;
                     xi[i * kLd + j] = p;
                     mp = max2(mp, fabsf(p));
                     mpb = max2(mpb, fabsf(p * bj));
