@@ -190,13 +190,6 @@ __device__ __forceinline__ f32x4 mma2(f16x8 a, const Split &b, f32x4 c) { return
 __device__ __forceinline__ f32x4 mma3(f16x8 ah, f16x8 al, const Split &b, f32x4 c) {
     return mma(ah, b.hi, mma(ah, b.lo, mma(al, b.hi, c)));
 }
-// Left operand at p (its second half `half` values on where it has one).
-template <bool SPLIT>
-__device__ __forceinline__ f32x4 mma_in(const _Float16 *p, int half, const Split &b, f32x4 c) {
-    const f16x8 a = *(const f16x8 *)p;
-    if constexpr (SPLIT) return mma3(a, *(const f16x8 *)(p + half), b, c);
-    return mma2(a, b, c);
-}
 // (NaN if there is one: two values an instruction, without quieting them first)
 __device__ __forceinline__ float max2(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float max4(f32x4 v, float m) {

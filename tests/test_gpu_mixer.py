@@ -188,6 +188,8 @@ DELTA = [  # lens, Hk, Hv, dk, dv, dtype, state, packed, fp32 beta
     ([77], 1, 1, 1, 1, "bf16", True, False, True),
     ([300], 1, 4, 128, 256, "bf16", False, True, False),
     ([40, 90], 1, 2, 100, 130, "fp16", True, False, False),
+    ([700, 64, 321], 2, 2, 128, 80, "bf16", True, True, False),
+    ([400], 1, 3, 128, 128, "fp32", True, True, False),
 ]
 
 
@@ -204,7 +206,7 @@ def test_delta_rule_forward(case):
     _near(s, rs, "state")
 
 
-@pytest.mark.parametrize("L,rows,dk,dv,dtype", [(1, 5, 128, 128, "bf16"), (3, 2, 64, 64, "fp16"), (2, 3, 100, 30, "fp32"),
+@pytest.mark.parametrize("L,rows,dk,dv,dtype", [(1, 5, 128, 128, "bf16"), (6, 2, 128, 96, "bf16"), (3, 2, 64, 64, "fp16"), (2, 3, 100, 30, "fp32"),
                                                  (1, 1, 17, 7, "bf16")])
 def test_delta_rule_step_continues_the_sequence(L, rows, dk, dv, dtype):
     Hk, Hv, steps = 2, 4, 4
@@ -504,6 +506,29 @@ def test_branch_norm_forward_and_gradients(case):
             assert (got.double() - ref[id(leaf)]).abs().max() <= 128 * U * dr.abs().max() * 8
             continue
         _close(got, ref[id(leaf)], 256 + rows, name)
+
+
+@pytest.mark.parametrize("R,D,dtype", [(9, 1024, "bf16"), (70, 41, "fp16"), (3, 4099, "fp32"), (5, 7, "bf16")])
+def test_branch_norm_at_any_address(R, D, dtype):
+    """Rows that begin one, two or three values past a 16-byte boundary."""
+    _say("branch norm, any address", R, D, dtype)
+    g, t = _gen(13), T16[dtype]
+
+    def at(off, *shape):
+        n = torch.Size(shape).numel()
+        return torch.full((n + 16,), 7.0, device=DEV).to(t)[off:off + n].view(shape).copy_(_randn(g, *shape).to(t))
+
+    y, x, gate, w, wn = at(1, R, D), at(2, R, D), at(3, R, D), at(1, D), at(0, D)
+    dr, dh = at(3, R, D), at(1, R, D)
+    leaves = [z.double().requires_grad_(True) for z in (x, y, w, gate, wn)]
+    rr, rh = om.branch_norm(*leaves, 0.5, 1e-6, "silu")
+    r, h, stats = mixer.branch_norm_fwd(x, y, w, gate, wn, alpha=0.5, act="silu", save=True)
+    _close(r, rr.detach(), 128, "r")
+    _close(h, rh.detach(), 128, "h")
+    ref = torch.autograd.grad((rr * dr.double()).sum() + (rh * dh.double()).sum(), leaves)
+    grads = mixer.branch_norm_bwd(dr, dh, x, y, w, gate, wn, stats, alpha=0.5, act="silu")
+    for name, got, z in zip(("dx", "dy", "dw_post", "dgate", "dw_next"), grads, ref):
+        _close(got, z, 256 + (R if name.startswith("dw") else 0), name)
 
 
 def test_branch_norm_without_rows_and_without_gradients():
