@@ -149,6 +149,14 @@ __device__ __forceinline__ float pow2_to(float m, int t, float *inv) {
     *inv = __uint_as_float((uint32_t)(254 - e) << 23);
     return __uint_as_float((uint32_t)e << 23);
 }
+// A state's next power of two is ss, its present one 1 / is, and `last` what a
+// chunk leaves of it: the factor that takes it there.  Either power of two may
+// lie near the end of the range (a bound of zero gives the largest), their
+// product past it.  Taken in this order and held below infinity, what is zero
+// (a cleared state, `last` = 0, or one of zeros) stays zero; a state that is
+// neither, and so small that the limit is met, is below float32 anyway.
+__device__ __forceinline__ float held(float v) { return __builtin_elementwise_minimum(v, 0x1p126f); }
+__device__ __forceinline__ float state_step(float last, float is, float ss) { return held(last * is * ss); }
 constexpr int kTop = 11;     // split operands: largest value in [2^11, 2^12)
 constexpr int kBound = 14;   // those with a bound: the bound in [2^14, 2^15)
 // Rows of q and k: largest value in [1, 2).  What f16 then loses of a bf16 or

@@ -477,7 +477,7 @@ __device__ __forceinline__ void scan_state(const W &w, const DeltaArgs &A, char 
         // the next power of two, and the state in it
         float in;
         const float ss = pow2_to(smax * is * last + kRowSum * (zmax * bw), kBound, &in);
-        const float step = last * (ss * is);
+        const float step = state_step(last, is, ss);
         is = in;
 #pragma unroll
         for (int i = 0; i < MT; ++i) st[i] *= step;
@@ -489,12 +489,13 @@ __device__ __forceinline__ void scan_state(const W &w, const DeltaArgs &A, char 
         if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = y[i] * f3b[i];
-        wb[0] = split8(z[0], z[1], iz * ss);
+        const float sw = held(iz * ss);
+        wb[0] = split8(z[0], z[1], sw);
         W::hand_over();
         phase();
 #pragma unroll
         for (int i = 0; i < MT / 4; ++i) w.cols_step(x, 4 * i, 0, kc[i], wb[0], st);
-        wb[1] = split8(z[2], z[3], iz * ss);
+        wb[1] = split8(z[2], z[3], sw);
         phase();
         w.cols_step(x, 0, 1, kc[0], wb[1], st);
         phase();
@@ -640,7 +641,7 @@ __device__ __forceinline__ void scan_grad_state(const W &w, const DeltaArgs &A, 
         W::template tri_mul<true, false>(tf, eb, e);
         float ig;
         const float ss = pow2_to(gmax * is * last + kRowSum * (emax * bf1 + dmax * bf2), kBound, &ig);
-        const float step = last * (ss * is);
+        const float step = state_step(last, is, ss);
         is = ig;
 #pragma unroll
         for (int i = 0; i < MT; ++i) G[i] *= step;
