@@ -84,8 +84,10 @@ __device__ __forceinline__ Split slab_split(const _Float16 *hi, const _Float16 *
     return r;
 }
 
-// The sums of several value heads are kept in one place; what one head adds to
-// a dot product is the difference of two.
+// The sums of several value heads are kept in one place.  A head's own dot
+// products, which its decays' gradients are made of, are taken of what it adds
+// before that goes there: a difference of the sums would leave a small head
+// after a large one without digits, and a head of NaN none to any.
 template <typename S, int DKP>
 __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B, bool vec, bool vec_out) {
     constexpr bool SPLIT = sizeof(S) == 4;
@@ -94,14 +96,15 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
     constexpr int kState = 2 * kSlab * SLD * 2, kDF = 2 * kC * kLd * 4, kTok = 4 * kSlab * kTokLd * 2;
     // a slab of S or G, then D and F
     __shared__ __align__(16) char first[kState > kDF ? kState : kDF];
-    // U and dZ of a slab, then K and Q
-    __shared__ __align__(16) char second[kTok > IN ? kTok : IN];
+    // U and dZ of a slab
+    __shared__ __align__(16) char second[kTok];
+    __shared__ __align__(16) char kq[IN];  // K and Q, for the block's whole life
     _Float16 *sh = (_Float16 *)first, *sl = sh + kSlab * SLD;
     float *dm = (float *)first, *fm = dm + kC * kLd;
     _Float16 *uh = (_Float16 *)second, *ul = uh + kSlab * kTokLd, *eh = ul + kSlab * kTokLd, *el = eh + kSlab * kTokLd;
-    const char *kq = second;
     __shared__ __align__(16) float sb[kC], rise[kC], fall[kC], rk[kC], nk[kC], uq[kC], rq[kC], nq[kC], dgam[2][kC];
-    __shared__ __align__(16) float dbs[4][kC], red[8], mx[2][8], sums[2][2][kC];
+    __shared__ __align__(16) float dbs[4][kC], red[8], mx[2][8];
+    __shared__ __align__(16) float sums[2][2][kC];  // over the heads: q . dq and k . dk, a half of the columns each
     __shared__ double sg[kC];
     const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6 & 3), hf = __builtin_amdgcn_readfirstlane(tid >> 8);  // rows 16 w.., columns 16 MH hf..
@@ -120,31 +123,33 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
     // this wavefront's columns: where they begin in K' (fragments), in K (this lane's element) and in a slab of S
     const int fo0 = hf * (MH / 2) * 1024;
     const _Float16 *shh = sh + 16 * MH * hf, *slh = sl + 16 * MH * hf;
-    // x . (k or q with its norm; q with the scale too) of four rows, over this wavefront's columns
-    auto dot = [&](const char *x, const float *rho, const f32x4 (&v)[MH]) {
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < MH; ++i) {
-            const char *p = x + (w * KS + hf * (MH / 2)) * 1024 + (4 * g + 16 * (m >> 2)) * 16 + (m & 3) * 2 + (i / 2) * 1024 + (i & 1) * 8;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float u = (float)*(const _Float16 *)(p + r * 16);
-                if (SPLIT) u += (float)*(const _Float16 *)(p + MAT + r * 16);
-                sum[r] = fmaf(u, v[i][r], sum[r]);
-            }
-        }
-        sum *= *(const f32x4 *)(rho + 16 * w + 4 * g);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[r] = group_sum(sum[r]);
-        return sum;
+    // K's or Q's values where results lie: rows 16 w + 4 g .., column 16 i + m of this wavefront's
+    auto rows4 = [&](const char *x, int i) {
+        const char *p = x + (w * KS + hf * (MH / 2) + i / 2) * 1024 + tl + (i & 1) * 8;
+        auto read = [](const char *at) {
+            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)((lds_bytes)(lds_ptr_t)at));
+            return __builtin_convertvector(__builtin_bit_cast(f16x4, v), f32x4);
+        };
+        f32x4 v = read(p);
+        if (SPLIT) v += read(p + MAT);
+        return v;
     };
-    f32x4 dq[MH], dk[MH], gu[MH], dotq = {0.f, 0.f, 0.f, 0.f}, dotr = dotq, dotc = dotq;
+    // a row's dot product, its factor and the sum over its columns
+    auto whole = [&](f32x4 v, const float *rho) {
+        v *= *(const f32x4 *)(rho + 16 * w + 4 * g);
 #pragma unroll
-    for (int i = 0; i < MH; ++i) dq[i] = dk[i] = gu[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < 4; ++r) v[r] = group_sum(v[r]);
+        return v;
+    };
+    f32x4 dq[MH], dk[MH];
+#pragma unroll
+    for (int i = 0; i < MH; ++i) dq[i] = dk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int rep = A.Hv / A.Hk, slabs = B.dvp / kSlab;
     // What a slab begins with, fetched while the one before it is worked with.
     // Buffer loads: the base in scalar registers, one offset for all of them.
-    // (Any spill in here would wait for these loads.)
+    // A spill read back in here waits for these loads: with 16-bit inputs two
+    // registers spill, read only after the slabs; float32 ones of dk > 64 spill
+    // 40, two of them read in the slabs' loop and most between a head's products.
     const int l16 = lane * 16;
     auto load4 = [&](__amdgpu_buffer_rsrc_t r, int at) {
         return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, l16, at, 0));
@@ -197,7 +202,10 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             }
         }
     };
+    copy_in<8, IN / 1024>((const char *)B.kq + head * IN, kq);
     fetch(0, 0);
+    if (tid < 4 * kC) (&sums[0][0][0])[tid] = 0.f;
+    CONVLOWER_WAIT_VMCNT(0);  // the copies
     for (int v = 0; v < rep; ++v) {
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
@@ -214,6 +222,8 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         f32x4 dp[2], dl[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) dp[i] = dl[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // of this head: q . dq, k . dkr and k . dkc, this lane's columns and without the rows' factors
+        f32x4 pq = {0.f, 0.f, 0.f, 0.f}, pr = pq, pc = pq;
         float sgsum = 0.f;
         __syncthreads();
         const f32x4 up = *(const f32x4 *)(rise + 16 * w + 4 * g), down = *(const f32x4 *)(fall + 16 * w + 4 * g);
@@ -294,8 +304,10 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                     a = SPLIT ? mma_split(fo[s], x, a) : mma2(fo[s].hi, x, a);
                     b = mma_split(fe[s], x, b);
                 }
-                dq[i] += a * io;
-                dk[i] += b * je;
+                a *= io, b *= je;
+                dq[i] += a, dk[i] += b;
+                pq += rows4(kq + IN / 2, i) * a;
+                pr += rows4(kq, i) * b;
             }
             __syncthreads();
             float part = 0.f;
@@ -319,13 +331,14 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                 f32x4 a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < 2; ++s) a = mma_split(fu[s], slab_split<SLD>(shh, slh, i, s, so), a);
-                gu[i] += a * ju;
+                a *= ju;
+                dk[i] += a;
+                pc += rows4(kq, i) * a;
             }
         }
         __syncthreads();
         renew();
         const int row = 16 * w + m;  // this lane's row of left operands
-        copy_in<8, IN / 1024>((const char *)B.kq + head * IN, second);
         if (tid < ch.len) {
             const float db = (dbs[0][tid] + dbs[1][tid]) + (dbs[2][tid] + dbs[3][tid]);
             const int64_t th = (ch.t0 + tid) * A.Hv + h;
@@ -342,12 +355,11 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                 dm[i * kLd + j] = j <= i ? dp[t][r] * d : 0.f;
                 fm[i * kLd + j] = j < i ? dl[t][r] * d : 0.f;
             }
-        CONVLOWER_WAIT_VMCNT_LDS(0);  // the copies
         __syncthreads();
         // <S', G> = e^gam_C <S, G> + sum_j k_j . (its column part from the state)
         {
-            const f32x4 x = dot(kq, rk, gu) - dotc;
-            float end = last_v * sgsum + (m == 0 ? x[0] + x[1] + x[2] + x[3] : 0.f);
+            const f32x4 x = pc * *(const f32x4 *)(rk + 16 * w + 4 * g);
+            float end = last_v * sgsum + ((x[0] + x[1]) + (x[2] + x[3]));
 #pragma unroll
             for (int d = 32; d > 0; d >>= 1) end += __shfl_xor(end, d, 64);
             if (lane == 0) red[tid >> 6] = end;
@@ -379,8 +391,10 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                     b = mma(fb[s].hi, y, b);
                 }
             }
-            dq[i] += a * ia;
-            dk[i] += b * ib;
+            a *= ia, b *= ib;
+            dq[i] += a, dk[i] += b;
+            pq += rows4(kq + IN / 2, i) * a;
+            pr += rows4(kq, i) * b;
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -406,14 +420,18 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                     b = mma(fb[s].hi, trans_at(p + MAT, p + MAT + KS * 1024, i, tl), b);
                 }
             }
-            gu[i] += a * ia + b * ib;
+            a = a * ia + b * ib;
+            dk[i] += a;
+            pc += rows4(kq, i) * a;
         }
         renew();
-        const f32x4 oq = dotq, orr = dotr, oc = dotc;
-        dotq = dot(kq + IN / 2, rq, dq);
-        dotr = dot(kq, rk, dk);
-        dotc = dot(kq, rk, gu);
-        if (m == 0) *(f32x4 *)(dgam[hf] + 16 * w + 4 * g) = (dotq - oq) + (dotr - orr) - (dotc - oc);
+        pq = whole(pq, rq), pr = whole(pr, rk), pc = whole(pc, rk);
+        if (m == 0) {
+            const int at = 16 * w + 4 * g;
+            *(f32x4 *)(dgam[hf] + at) = pq + pr - pc;
+            *(f32x4 *)(sums[0][hf] + at) += pq;
+            *(f32x4 *)(sums[1][hf] + at) += pr + pc;
+        }
         __syncthreads();
         if (tid < 64) {  // sums from each token to the chunk's end
             double x = (double)dgam[0][lane] + dgam[1][lane];
@@ -465,14 +483,10 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
         __syncthreads();
     };
     const int at = 16 * w + 4 * g;
-    if (m == 0) *(f32x4 *)(sums[0][hf] + at) = dotq, *(f32x4 *)(sums[1][hf] + at) = dotr + dotc;
-    __syncthreads();
     const f32x4 sq = *(const f32x4 *)(sums[0][0] + at) + *(const f32x4 *)(sums[0][1] + at);
     const f32x4 sk = *(const f32x4 *)(sums[1][0] + at) + *(const f32x4 *)(sums[1][1] + at);
     leave(kq + IN / 2, uq, nq, dq, sq, A.scale, (S *)A.dq);
-#pragma unroll
-    for (int i = 0; i < MH; ++i) gu[i] += dk[i];
-    leave(kq, rk, nk, gu, sk, 1.f, (S *)A.dk_out);
+    leave(kq, rk, nk, dk, sk, 1.f, (S *)A.dk_out);
 }
 
 template <typename S, int DKP>

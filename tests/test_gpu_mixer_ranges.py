@@ -96,3 +96,127 @@ def test_delta_rule_gradients_of_a_cleared_chunk(kind, dtype):
     ref = torch.autograd.grad((ro * do.double()).sum() + (rs * ds.double()).sum(), leaves)
     for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta", "dstate"), got, ref):
         _near(x, y, name, 2e-5)
+
+
+# ------------------------------------- gated delta rule: parts far from others
+
+
+def _shared(dtype, heads=4, tokens=150):
+    q, k, v, g, beta, gen = _delta_inputs([tokens], 1, heads, 64, 64, dtype, packed=False, beta32=True)
+    return q, k, v, g, beta, _randn(gen, tokens, heads, 64), gen
+
+
+def _bwd(do, *five):
+    more = dict(scale=0.125, qk_norm=True)
+    _, _, saved = mixer.delta_rule_fwd(*five, save=True, **more)
+    return mixer.delta_rule_bwd(do, *five, saved, **more)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scales", [(1.0, 1e4, 1.0, 1e-2), (1e5, 1e-3, 1e-3, 1.0)])
+def test_delta_rule_gradients_of_heads_of_different_size(scales, dtype):
+    """Value heads that share a key: each one's decay and beta gradients keep
+    the digits of its own size."""
+    _say("delta, heads of different size", scales, dtype)
+    q, k, v, g, beta, do, _ = _shared(dtype)
+    do = (do * torch.tensor(scales, device=DEV)[None, :, None]).to(v.dtype)
+    got = _bwd(do, q, k, v, g, beta)
+    leaves = [z.double().requires_grad_(True) for z in (q, k, v, g, beta)]
+    ro, _ = om.delta_rule(*leaves, None, None, 0.125, True)
+    ref = torch.autograd.grad(ro, leaves, do.double())
+    for h in range(len(scales)):
+        for i, name in ((2, "dv"), (3, "dg"), (4, "dbeta")):
+            _near(got[i][:, h], ref[i][:, h], f"{name} of head {h}", 2e-5)
+    for i, name in ((0, "dq"), (1, "dk")):
+        _near(got[i], ref[i], name, 2e-5)
+
+
+def test_delta_rule_a_broken_head_leaves_the_others():
+    """One head's output gradient is NaN: the other heads' own gradients are
+    those of a call without it."""
+    q, k, v, g, beta, do, _ = _shared("bf16")
+    whole = do.to(v.dtype)
+    broken = whole.clone()
+    broken[:, 1] = float("nan")
+    a, b = _bwd(whole, q, k, v, g, beta), _bwd(broken, q, k, v, g, beta)
+    for h in (0, 2, 3):
+        for i, name in ((2, "dv"), (3, "dg"), (4, "dbeta")):
+            assert torch.equal(a[i][:, h], b[i][:, h]), f"{name} of head {h}"
+    assert b[3][:, 1].isnan().any()
+
+
+# ------------------------------------------- gated delta rule: counts and zeros
+
+
+@pytest.mark.parametrize("rep,dk,dv,dtype", [(6, 128, 128, "bf16"), (9, 40, 72, "fp32"), (5, 64, 64, "fp16")])
+def test_delta_rule_many_value_heads_of_one_key(rep, dk, dv, dtype):
+    _say("delta, value heads of one key", rep, dk, dv, dtype)
+    q, k, v, g, beta, gen = _delta_inputs([70, 9], 2, 2 * rep, dk, dv, dtype)
+    cu = _cu([70, 9])
+    do = _randn(gen, 79, 2 * rep, dv).to(v.dtype)
+    more = dict(cu_seqlens=cu, scale=0.2, qk_norm=True)
+    o, s, saved = mixer.delta_rule_fwd(q, k, v, g, beta, want_state=True, save=True, **more)
+    leaves = [z.double().requires_grad_(True) for z in (q, k, v, g, beta)]
+    ro, rs = om.delta_rule(*leaves, cu.tolist(), None, 0.2, True)
+    ref = torch.autograd.grad(ro, leaves, do.double())
+    got = mixer.delta_rule_bwd(do, q, k, v, g, beta, saved, **more)
+    _near(s, rs.detach(), "state")
+    for h in range(2 * rep):
+        _near(o[:, h], ro[:, h].detach(), f"o of head {h}")
+        for i, name in ((2, "dv"), (3, "dg"), (4, "dbeta")):
+            _near(got[i][:, h], ref[i][:, h], f"{name} of head {h}", 2e-5)
+    for i, name in ((0, "dq"), (1, "dk")):
+        _near(got[i], ref[i], name, 2e-5)
+
+
+@pytest.mark.parametrize("n", [65, 200, 4100])
+def test_delta_rule_many_sequences(n):
+    """More sequences than a wavefront looks at together, some of them empty;
+    each gives what it gives alone."""
+    _say("delta, sequences", n)
+    pick = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 4, (n,), generator=pick).tolist()
+    for i, ln in ((3, 70), (64, 1), (n - 1, 130)):
+        lens[i] = ln
+    q, k, v, g, beta, gen = _delta_inputs(lens, 1, 1, 32, 32, "bf16", packed=False)
+    state = _randn(gen, n, 1, 32, 32)
+    cu = _cu(lens)
+    at = cu.tolist()
+    o, s, saved = mixer.delta_rule_fwd(q, k, v, g, beta, cu_seqlens=cu, state=state, qk_norm=True, want_state=True,
+                                       save=True)
+    do = _randn(gen, *v.shape).to(v.dtype)
+    got = mixer.delta_rule_bwd(do, q, k, v, g, beta, saved, cu_seqlens=cu, qk_norm=True, want_dstate=True)
+    some = [0, 1, 2, 3, 62, 63, 64, n // 2, n - 2, n - 1]
+    for i in some:
+        a, e = at[i], at[i + 1]
+        if a == e:
+            assert torch.equal(s[i], state[i]) and (got[5][i] == 0).all()
+            continue
+        five = [z[a:e].contiguous() for z in (q, k, v, g, beta)]
+        o1, s1, saved1 = mixer.delta_rule_fwd(*five, state=state[i:i + 1], qk_norm=True, want_state=True, save=True)
+        assert torch.equal(o[a:e], o1) and torch.equal(s[i:i + 1], s1), f"sequence {i}"
+        g1 = mixer.delta_rule_bwd(do[a:e].contiguous(), *five, saved1, qk_norm=True, want_dstate=True)
+        for x, y in zip(got[:5], g1[:5]):
+            assert torch.equal(x[a:e], y), f"gradients of sequence {i}"
+        assert torch.equal(got[5][i:i + 1], g1[5])
+        ro, rs = _delta_ref(*five, None, state[i:i + 1], 32 ** -0.5, True)
+        _near(o1, ro, f"sequence {i}")
+        _near(s1, rs, f"state {i}")
+
+
+@pytest.mark.parametrize("form", ["chunks", "tokens"])
+def test_delta_rule_tokens_that_write_nothing(form):
+    """beta = 0 for some tokens, or all: the state only decays there."""
+    q, k, v, g, beta, gen = _delta_inputs([96], 1, 2, 64, 48, "bf16", packed=False)
+    beta[torch.rand(96, 2, generator=gen, device=DEV) < 0.5] = 0
+    beta[:, 1] = 0
+    state = _randn(gen, 1, 2, 64, 48)
+    ro, rs = _delta_ref(q, k, v, g, beta, None, state, 0.125, True)
+    if form == "chunks":
+        o, s, _ = mixer.delta_rule_fwd(q, k, v, g, beta, state=state, qk_norm=True, want_state=True)
+    else:
+        s = state.clone()
+        o = mixer.delta_rule_step(q[None], k[None], v[None], g[None], beta[None], s, scale=0.125, qk_norm=True)[0]
+    for h in range(2):
+        _near(o[:, h], ro[:, h], f"o of head {h}")
+        _near(s[:, h], rs[:, h], f"state of head {h}")
