@@ -81,17 +81,10 @@ enum TpRow {
     ROW_F1B = 5,  // f1 b
     ROW_SCALARS = 7,
 };
-// The scalars.  The largest values bound what a product's result can be, and
-// so give the next operand's power of two without looking at it: f16's range
-// leaves 17 bits of room above the 22 that are wanted.
 enum TpScalar {
     SC_LAST = 0,  // e^gam_C
     SC_IT = 1,    // 1 / (the inverse's factor)
     SC_IP = 2,    // 1 / (P's factor)
-    SC_T = 3,     // 64 max |inverse|
-    SC_TF3 = 4,   // 64 max |inverse| max |f3 b|
-    SC_TF1 = 5,   // 64 max |inverse| max |f1 b|
-    SC_F2 = 6,    // max |f2|
 };
 // P stands with its columns times b on the way forward (P U = (P b) Y).
 constexpr int kTpRows = 4 * kTri * kFrag * 2;  // bytes before the factors
@@ -157,8 +150,10 @@ __device__ __forceinline__ float pow2_to(float m, int t, float *inv) {
 // neither, and so small that the limit is met, is below float32 anyway.
 __device__ __forceinline__ float held(float v) { return __builtin_elementwise_minimum(v, 0x1p126f); }
 __device__ __forceinline__ float state_step(float last, float is, float ss) { return held(last * is * ss); }
-constexpr int kTop = 11;     // split operands: largest value in [2^11, 2^12)
-constexpr int kBound = 14;   // those with a bound: the bound in [2^14, 2^15)
+// Split operands: the largest value (of a state: what it can become in a
+// chunk) in [2^14, 2^15).  Halves reach down to 2^-25, so values down to 2^-17 of the
+// largest keep all 22 bits.
+constexpr int kTop = 14;
 // Rows of q and k: largest value in [1, 2).  What f16 then loses of a bf16 or
 // f16 row is below 2^-25 of its largest value.
 constexpr int kRowTop = 0;

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256, blocks_of(sizeof(S), DKP, GRAD)) void delta_pr
     __shared__ __align__(16) char both[kIn > kMat ? kIn : kMat];
     _Float16 *sk = (_Float16 *)both, *sq = sk + PL * kC * LD;
     float *lm = (float *)both, *xi = lm + kC * kLd;
-    __shared__ __align__(16) float rk[kC], nk[kC], uq[kC], nq[kC], sb[4][kC], red[4][4], mfs[4][4];
+    __shared__ __align__(16) float rk[kC], nk[kC], uq[kC], nq[kC], sb[4][kC], red[4][4];
     __shared__ __align__(16) float gh[4][kC], gl[4][kC];  // gam / log 2 in two floats
     const int slot = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -292,13 +292,11 @@ __global__ __launch_bounds__(256, blocks_of(sizeof(S), DKP, GRAD)) void delta_pr
             sb[w][lane] = bt;
             const float rise = expf((float)s), last = expf((float)all);
             const float f1 = rk[lane] * rise, f2 = uq[lane] * A.scale * rise, f3 = rk[lane] * expf((float)(all - s));
-            const float m0 = tile_max(fabsf(f3 * bt)), m1 = tile_max(fabsf(f1 * bt)), m2 = tile_max(fabsf(f2));
-            if (lane == 0) mfs[w][0] = m0, mfs[w][1] = m1;
             auto put = [&](char *p) {
                 float *f = (float *)(p + kTpRows) + lane;
                 f[ROW_F1 * kC] = f1, f[ROW_F2 * kC] = f2, f[ROW_F3 * kC] = f3, f[ROW_B * kC] = bt;
                 f[ROW_F3B * kC] = f3 * bt, f[ROW_F1B * kC] = f1 * bt;
-                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last, f[ROW_SCALARS * kC + SC_F2] = m2;
+                if (lane == 0) f[ROW_SCALARS * kC + SC_LAST] = last;
             };
             put(tp);
             if (GRAD) {
@@ -363,11 +361,7 @@ __global__ __launch_bounds__(256, blocks_of(sizeof(S), DKP, GRAD)) void delta_pr
                 const float big = max4(*(const f32x4 *)red[2 + way], 0.f);
                 sc = pow2_to(big, kTop, &inv);
                 store_tri(xi + way * kC * kLd, nullptr, sc, way ? tpg : tp);
-                if (tid == 0) {
-                    float *o = (float *)((way ? tpg : tp) + kTpRows) + ROW_SCALARS * kC;
-                    o[SC_IT] = inv;
-                    o[SC_T] = kC * big, o[SC_TF3] = kC * big * mfs[v][0], o[SC_TF1] = kC * big * mfs[v][1];
-                }
+                if (tid == 0) ((float *)((way ? tpg : tp) + kTpRows))[ROW_SCALARS * kC + SC_IT] = inv;
             }
         }
     }

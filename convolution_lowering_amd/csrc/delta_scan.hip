@@ -245,7 +245,7 @@ struct Scan {
 #pragma unroll
         for (int s = 0; s < KS; ++s) v[s].hi = frag_at(p + 2 * s * 1024), v[s].lo = frag_at(p + (2 * s + 1) * 1024);
     }
-    // A float a lane; which: 0 the state's measure, 1 and 2 of the chunk.
+    // A float a lane; which: 0 the state's measure, 1 of the chunk.
     __device__ __forceinline__ static float &scalar(char *pair, int which) {
         return ((float *)(pair + kPairRows) + which * 64)[threadIdx.x & 63];
     }
@@ -422,8 +422,10 @@ __device__ __forceinline__ void scan_state(const W &w, const DeltaArgs &A, char 
     constexpr int MT = W::MT, KS = W::KS;
     char *pair = lds + W::kPairs + w.w * W::kPair;
     // The state, each column times a power of two that keeps it in f16's
-    // range; is: the inverse.  What a chunk adds is bounded before it is
-    // known, and comes in the same measure.
+    // range; is: the inverse.  What a chunk adds comes in the same measure,
+    // which therefore follows from the largest of the state and of W, not from
+    // bounds on them: those are loose by up to 2^27 where a chunk's large
+    // values have decayed by its end, more than f16's range makes up for.
     f32x4 st[MT];
     Split sb[KS];
     w.load_state(A, A.state, st);
@@ -454,7 +456,7 @@ __device__ __forceinline__ void scan_state(const W &w, const DeltaArgs &A, char 
         w.values(lds + W::kVals + (c & 1) * W::kTile, z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f1[i] = row(ROW_F1, i);
-        const float last = sc[SC_LAST], it = sc[SC_IT], bw = sc[SC_TF3];
+        const float last = sc[SC_LAST], it = sc[SC_IT];
         w.template tri_load<false>(x + W::kTi, tf.hi);
         W::rows_mul(x, kf, sb, y);
         const float smax = col_max(max_of(st));
@@ -468,31 +470,27 @@ __device__ __forceinline__ void scan_state(const W &w, const DeltaArgs &A, char 
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] -= y[i] * (f1[i] * is);
         float iz;
-        const float zmax = col_max(max_of(z));
-        split_by(z, pow2_to(zmax, kTop, &iz), zb);
+        split_by(z, pow2_to(col_max(max_of(z)), kTop, &iz), zb);
         iz *= it;
         phase();
         // Y
         W::template tri_mul<false, false>(tf, zb, y);
-        // the next power of two, and the state in it
-        float in;
-        const float ss = pow2_to(smax * is * last + kRowSum * (zmax * bw), kBound, &in);
-        const float step = state_step(last, is, ss);
-        is = in;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) st[i] *= step;
         W::scalar(pair, 1) = iz;
-        W::scalar(pair, 2) = zmax;
         phase();
-        // W, and K' W into the state
+        // W, the next power of two, and K' W into the state in it
         W::put(pair + W::kPairTiles, y);
         if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = y[i] * f3b[i];
-        const float sw = held(iz * ss);
+        float in;
+        const float ss = pow2_to(smax * is * last + kRowSum * (col_max(max_of(z)) * iz), kTop, &in);
+        const float step = state_step(last, is, ss), sw = held(iz * ss);
+        is = in;
         wb[0] = split8(z[0], z[1], sw);
         W::hand_over();
         phase();
+#pragma unroll
+        for (int i = 0; i < MT; ++i) st[i] *= step;
 #pragma unroll
         for (int i = 0; i < MT / 4; ++i) w.cols_step(x, 4 * i, 0, kc[i], wb[0], st);
         wb[1] = split8(z[2], z[3], sw);
@@ -534,7 +532,7 @@ __device__ __forceinline__ void scan_outputs(const W &w, const DeltaArgs &A, con
         W::rows_load(x + W::kIn / 2, 0, KS, qf);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2[i] = *(const f32x4 *)(f + ROW_F2 * kC + 16 * i);
-        const float ip = sc[SC_IP], bt = sc[SC_T];
+        const float ip = sc[SC_IP];
         W::rows_mul(x + W::kIn / 2, qf, sb, o);
         phase();
         w.template tri_load<false>(x + W::kP, pf.hi);
@@ -554,10 +552,10 @@ __device__ __forceinline__ void scan_outputs(const W &w, const DeltaArgs &A, con
         phase();
         // P Y
         W::get(pair + W::kPairTiles, y);
-        const float iz = W::scalar(pair, 1), zmax = W::scalar(pair, 2);
+        const float iz = W::scalar(pair, 1);
         float iy;
-        split_by(y, iz * pow2_to(zmax * bt, kBound, &iy), yb);
-        iy *= ip;
+        split_by(y, pow2_to(col_max(max_of(y)), kTop, &iy), yb);
+        iy *= iz * ip;
         if constexpr (SAVE) {
             if (kept) {
                 f32x4 z[4];
@@ -613,7 +611,7 @@ __device__ __forceinline__ void scan_grad_state(const W &w, const DeltaArgs &A, 
         w.template tri_load<true>(x + W::kTi, tf.hi);
 #pragma unroll
         for (int i = 0; i < 4; ++i) f3[i] = row(ROW_F3, i);
-        const float last = sc[SC_LAST], it = sc[SC_IT], bf1 = sc[SC_TF1], bf2 = sc[SC_F2];
+        const float last = sc[SC_LAST], it = sc[SC_IT];
 #pragma unroll
         for (int s = 0; s < KS; ++s) gb[s] = split8(G[2 * s], G[2 * s + 1]);
         W::put(pair, gb);
@@ -634,28 +632,27 @@ __device__ __forceinline__ void scan_grad_state(const W &w, const DeltaArgs &A, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = e[i] * (f3[i] * is) + y[i];
         float ie;
-        const float emax = col_max(max_of(e));
-        split_by(e, pow2_to(emax, kTop, &ie), eb);
+        split_by(e, pow2_to(col_max(max_of(e)), kTop, &ie), eb);
         ie *= it;
         phase();
         W::template tri_mul<true, false>(tf, eb, e);
-        float ig;
-        const float ss = pow2_to(gmax * is * last + kRowSum * (emax * bf1 + dmax * bf2), kBound, &ig);
-        const float step = state_step(last, is, ss);
-        is = ig;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) G[i] *= step;
         phase();
         // dS = .. + Q' (f2 dO) - K' (f1 b E)
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] *= ie;
         W::put(pair + W::kPairTiles, e);
         if (MT > 4) w.cols_load(x, 4, kc[MT / 4 - 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = e[i] * f1b[i];
+        float ig;  // the next power of two, as for the state
+        const float ss = pow2_to(gmax * is * last + kRowSum * (col_max(max_of(y)) + dmax), kTop, &ig);
+        const float step = state_step(last, is, ss);
+        is = ig;
+        split_by(y, -ss, yb);
         W::hand_over();
         W::get(pair, q);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = e[i] * f1b[i];
-        split_by(y, -ss, yb);
+        for (int i = 0; i < MT; ++i) G[i] *= step;
 #pragma unroll
         for (int i = 0; i < MT; ++i) G[i] += q[i] * ss;
         phase();
@@ -690,12 +687,16 @@ __device__ __forceinline__ void scan_grad_outputs(const W &w, const DeltaArgs &A
         w.values(lds + W::kVals + (j & 1) * W::kTile, d);
         w.template tri_load<true>(x + W::kP, pf.hi);
         w.template tri_load<true>(x + W::kP + W::kLo, pf.lo);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2[i] = row(ROW_F2, i);
         const float ip = sc[SC_IP];
         float id;
-        const float dmax = col_max(max_of(d));
-        split_by(d, pow2_to(dmax, kTop, &id), db);
+        split_by(d, pow2_to(col_max(max_of(d)), kTop, &id), db);
         W::template tri_mul<true, !W::SPLIT>(pf, db, y);
         id *= ip;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] *= f2[i];
+        const float dmax = col_max(max_of(d));
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] *= id;
         W::put(pair + W::kPairTiles, y);
@@ -704,8 +705,6 @@ __device__ __forceinline__ void scan_grad_outputs(const W &w, const DeltaArgs &A
         // Q' (f2 dO)
         typename W::Cols qc[MT / 4];
         w.cols_load(x + W::kIn / 2, 0, qc[0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f2[i] = row(ROW_F2, i);
         W::hand_over();
         W::get(pair, gb);
         const float is = W::scalar(pair, 0);
@@ -717,9 +716,7 @@ __device__ __forceinline__ void scan_grad_outputs(const W &w, const DeltaArgs &A
             if ((threadIdx.x & 63) == 0) B.Gmax[vh * (B.dvp / 16) + tile] = mx;
         }
         if (MT > 4) w.cols_load(x + W::kIn / 2, 4, qc[MT / 4 - 1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] *= f2[i];
-        split_by(d, pow2_to(col_max(max_of(d)), kTop, &id), db);
+        split_by(d, pow2_to(dmax, kTop, &id), db);
         phase();
         zero(q);
 #pragma unroll

@@ -101,6 +101,54 @@ def test_delta_rule_gradients_of_a_cleared_chunk(kind, dtype):
 # ------------------------------------- gated delta rule: parts far from others
 
 
+def _room(large, ordinary):
+    """What an operand's split leaves out of a value that much smaller than
+    its column's largest: half of f16's smallest step, where the largest is at
+    2^11 or above; for two operands in series."""
+    return 2 * 2.0 ** -36 * large / ordinary
+
+
+@pytest.mark.parametrize("times", [1e2, 1e5])
+def test_delta_rule_a_large_value_that_decays(times):
+    """One token of a chunk holds values far above the others'; it has decayed
+    to nothing before the chunk ends.  The state after it is made of ordinary
+    tokens and keeps its digits."""
+    _say("delta, one large value", times)
+    q, k, v, g, beta, gen = _delta_inputs([256], 1, 2, 64, 64, "fp32", packed=False)
+    v = _randn(gen, 256, 2, 64)
+    g.fill_(-0.5)
+    v[2] *= times
+    v[130] *= times
+    o, s, _ = mixer.delta_rule_fwd(q, k, v, g, beta, qk_norm=True, want_state=True)
+    ro, rs = _delta_ref(q, k, v, g, beta, None, None, 0.125, True)
+    loose = 1e-5 + _room(v.abs().max().item(), 1.0)
+    for t in range(0, 256, 16):
+        _near(o[t:t + 16], ro[t:t + 16], f"o[{t}:]", loose)
+    _near(s, rs, "state", loose)
+    o, s, _ = mixer.delta_rule_fwd(*(z[:64].contiguous() for z in (q, k, v, g, beta)), qk_norm=True, want_state=True)
+    _near(s, _delta_ref(*(z[:64] for z in (q, k, v, g, beta)), None, None, 0.125, True)[1], "state of a chunk", loose)
+
+
+@pytest.mark.parametrize("times", [1e2, 1e5])
+def test_delta_rule_a_large_output_gradient_that_decays(times):
+    _say("delta, one large output gradient", times)
+    q, k, v, g, beta, gen = _delta_inputs([192], 1, 2, 64, 64, "fp32", packed=False)
+    g.fill_(-0.5)
+    do = _randn(gen, 192, 2, 64)
+    do[125] *= times
+    state = _randn(gen, 1, 2, 64, 64)
+    more = dict(scale=0.125, qk_norm=True)
+    _, _, saved = mixer.delta_rule_fwd(q, k, v, g, beta, state=state, save=True, **more)
+    got = mixer.delta_rule_bwd(do, q, k, v, g, beta, saved, want_dstate=True, **more)
+    leaves = [z.double().requires_grad_(True) for z in (q, k, v, g, beta, state)]
+    ro, _ = om.delta_rule(*leaves[:5], None, leaves[5], 0.125, True)
+    ref = torch.autograd.grad((ro * do.double()).sum(), leaves)
+    loose = 2e-5 + 2 * _room(do.abs().max().item(), 1.0)
+    for t in range(0, 192, 16):
+        _near(got[2][t:t + 16], ref[2][t:t + 16], f"dv[{t}:]", loose)
+    _near(got[5], ref[5], "dstate", loose)
+
+
 def _shared(dtype, heads=4, tokens=150):
     q, k, v, g, beta, gen = _delta_inputs([tokens], 1, heads, 64, 64, dtype, packed=False, beta32=True)
     return q, k, v, g, beta, _randn(gen, tokens, heads, 64), gen
