@@ -42,17 +42,19 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
+template <typename S>
 __device__ __forceinline__ float act_of(float z, int act) {
-    return act == MIX_ACT_NONE ? z : act == MIX_ACT_SILU ? z * mix_sigmoid(z) : mix_sigmoid(z);
+    return act == MIX_ACT_NONE ? z : act == MIX_ACT_SILU ? z * mix_sigmoid<S>(z) : mix_sigmoid<S>(z);
 }
 // Value and slope.
+template <typename S>
 __device__ __forceinline__ void act_grad(float z, int act, float *a, float *da) {
     if (act == MIX_ACT_NONE) {
         *a = z;
         *da = 1.f;
         return;
     }
-    const float s = mix_sigmoid(z);
+    const float s = mix_sigmoid<S>(z);
     *a = act == MIX_ACT_SILU ? z * s : s;
     *da = act == MIX_ACT_SILU ? s * (1.f + z * (1.f - s)) : s * (1.f - s);
 }
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_fwd_kernel(NormArgs
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             r[i][j] *= rs * w[i][j];
-            if (A.gate) r[i][j] *= act_of(f[i][j], A.act);
+            if (A.gate) r[i][j] *= act_of<S>(f[i][j], A.act);
         }
     if (A.x) {
         load_row<S, V, TPR, NV, ANY>((const S *)A.x + at, lane, A.D, f);
@@ -261,7 +263,7 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_bwd_kernel(NormArgs
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     float u = y[i][j] * mix_f32(w[i].v[j]);
-                    if (A.gate) u *= act_of(g[i][j], A.act);
+                    if (A.gate) u *= act_of<S>(g[i][j], A.act);
                     x[i][j] = fmaf(A.alpha, u, x[i][j]) * xs;  // (x reads as zero where there is none)
                     if (live) sn[i][j] = fmaf(e[i][j], x[i][j], sn[i][j]);
                     e[i][j] *= mix_f32(wn[i].v[j]);
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(block_of(TPR)) void branch_norm_bwd_kernel(NormArgs
                 float f = A.alpha * d[i][j];
                 if (A.gate) {
                     float a, da;
-                    act_grad(g[i][j], A.act, &a, &da);
+                    act_grad<S>(g[i][j], A.act, &a, &da);
                     g[i][j] = f * y[i][j] * wp * da;
                     if (live) sg[i][j] += g[i][j];
                     f *= a;

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(Conv1dArgs A) {
         taps<V, WT>(wt, b, hist, x, W, z);
         if (A.act == MIX_ACT_SILU)
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] *= mix_sigmoid(z[i]);
+            for (int i = 0; i < V; ++i) z[i] *= mix_sigmoid<S>(z[i]);
         mix_store<S, V>((S *)A.y + u * A.D + c0, z);
         push<V, WT>(hist, x);
     };
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(Conv1dArgs A) {
 }
 
 // dy of a token, whose inputs before it are in hist, becomes its dz.
-template <int V, int WT>
+template <typename S, int V, int WT>
 __device__ __forceinline__ void grad_z(const Conv1dArgs &A, const float (&wt)[WT][V], const float (&b)[V],
                                        const float (&hist)[WT][V], const float (&x)[V], int W, float (&dz)[V]) {
     if (A.act == MIX_ACT_SILU) {
@@ -165,7 +165,7 @@ __device__ __forceinline__ void grad_z(const Conv1dArgs &A, const float (&wt)[WT
         taps<V, WT>(wt, b, hist, x, W, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float s = mix_sigmoid(z[i]);
+            const float s = mix_sigmoid<S>(z[i]);
             dz[i] *= s * (1.f + z[i] * (1.f - s));
         }
     }
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(256) void conv1d_bwd_kernel(Conv1dArgs A) {
             if (p >= W - 1 || a + p >= e) continue;
             mix_load<S, V>((const S *)A.x + (a + p) * A.xs + c0, x);
             mix_load<S, V>((const S *)A.dy + (a + p) * A.dys + c0, dz);
-            grad_z<V, WT>(A, wt, b, hist, x, W, dz);
+            grad_z<S, V, WT>(A, wt, b, hist, x, W, dz);
             push<V, WT>(hist, x);
 #pragma unroll
             for (int j = 0; j < WT - 1; ++j)
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void conv1d_bwd_kernel(Conv1dArgs A) {
                 if (t < e) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) x[i] = mix_f32(rx.v[i]), dz[i] = mix_f32(ry.v[i]);
-                    grad_z<V, WT>(A, wt, b, hist, x, W, dz);
+                    grad_z<S, V, WT>(A, wt, b, hist, x, W, dz);
 #pragma unroll
                     for (int d = 0; d < WT; ++d) {
                         if (d >= W) continue;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(64) void conv1d_step_kernel(const S *x, int64_t xs,
     for (int j = 1; j < MIX_CONV1D_MAX_WIDTH; ++j)
         if (j < W) *(MixVec<S, V> *)(st + (int64_t)(j - 1) * D) = line[j];
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = act == MIX_ACT_SILU ? z[i] * mix_sigmoid(z[i]) : z[i];
+    for (int i = 0; i < V; ++i) f[i] = act == MIX_ACT_SILU ? z[i] * mix_sigmoid<S>(z[i]) : z[i];
     mix_store<S, V>(y + (int64_t)r * D + c0, f);
 }
 

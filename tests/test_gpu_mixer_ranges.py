@@ -268,3 +268,48 @@ def test_delta_rule_tokens_that_write_nothing(form):
     for h in range(2):
         _near(o[:, h], ro[:, h], f"o of head {h}")
         _near(s[:, h], rs[:, h], f"state of head {h}")
+
+
+# ----------------------------------------------------- float32 results' digits
+
+
+def _steps(got, ref):
+    """Largest distance in half steps of float32, of the results that are
+    not below its normal range."""
+    there = ref.abs() > 2.0 ** -126
+    return ((got.double() - ref).abs() / ref.abs())[there].max().item() * 2 ** 24
+
+
+def test_float32_activations_keep_their_digits():
+    """silu and sigmoid of exact inputs from -80 to 80.  The exponential is
+    good to two half steps, its sum with one, the quotient and the products
+    round once each, and the exponential's error counts in full: 8 half
+    steps."""
+    z = torch.linspace(-80, 80, 4001, device=DEV)
+    s = 1 / (1 + torch.exp(-z.double()))
+    one = torch.ones(z.numel(), 1, device=DEV)
+    y, _ = mixer.conv1d_causal_fwd(z[None], one, act="silu")
+    assert _steps(y[0], z.double() * s) <= 8
+    y = mixer.conv1d_causal_step(z[None], one, None, torch.zeros(1, 0, z.numel(), device=DEV), act="silu")
+    assert _steps(y[0], z.double() * s) <= 8
+    # rows of one value: y / rms(y) is 1 (eps = 0), so r is act(gate), and dgate its slope
+    yy, gate, w = torch.ones(z.numel(), 1, device=DEV), z[:, None].contiguous(), torch.ones(1, device=DEV)
+    for act, want, slope in (("silu", z.double() * s, s * (1 + z.double() * (1 - s))), ("sigmoid", s, s * (1 - s))):
+        r, _, stats = mixer.branch_norm_fwd(None, yy, w, gate, act=act, eps=0.0, save=True)
+        assert _steps(r[:, 0], want) <= 8, act
+        grads = mixer.branch_norm_bwd(yy, None, None, yy, w, gate, None, stats, act=act, eps=0.0)
+        # below zero the slope is a product of what is accurate; above, 1 - s is a difference
+        low = z < -2
+        assert _steps(grads[3][low, 0], slope[low]) <= 24, act
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_activations_at_the_ends_of_the_range(dtype):
+    t, inf, nan = T16[dtype], float("inf"), float("nan")
+    z = torch.tensor([inf, 3e38, 100.0, 0.0, -100.0, -3e38, nan], device=DEV).to(t)
+    one = torch.ones(7, 1, device=DEV, dtype=t)
+    y, _ = mixer.conv1d_causal_fwd(z[None], one, act="silu")
+    assert (y[0, :3] == z[:3]).all() and y[0, 3] == 0 and (y[0, 4:6].float().abs() < 1e-37).all() and y[0, 6].isnan()
+    z[5] = -inf
+    r, _, _ = mixer.branch_norm_fwd(None, one, one[:1, 0], z[:, None].contiguous(), act="sigmoid", eps=0.0)
+    assert (r[:3] == 1).all() and r[3] == 0.5 and (r[4:6].float() < 1e-37).all() and r[6].isnan()
