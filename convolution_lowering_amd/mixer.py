@@ -8,8 +8,9 @@ rule and the branch norm, over the C ABI of ``include/convlower_mixer.h``.
 
 As in the package's convolution binding, Python only checks and marshals:
 outputs and workspaces are allocated with torch on the stream the library
-launches on (`stream`, else torch's current one), and a failing call raises
-ConvLowerError, ValueError or TypeError before anything is launched.
+launches on (`stream`, else the current one of the tensors' device), and a
+failing call raises ConvLowerError, ValueError or TypeError before anything is
+launched.
 
 Tokens of several sequences are packed along one axis: ``[T, ...]`` with
 ``cu_seqlens`` (int32, N + 1 offsets on the device), or ``[B, L, ...]`` for B
@@ -125,10 +126,13 @@ _HERE = contextlib.nullcontext()
 
 
 def _on(stream, device):
-    """Where outputs and workspaces are allocated: torch's current stream as
-    it is (entering it again costs a one-token call a third of its time), or
-    the caller's."""
-    return _HERE if stream is None else torch.cuda.stream(stream)
+    """Where outputs and workspaces are allocated and the launch is made: on
+    the caller's stream, or the tensors' device and its current stream.  Where
+    that device is torch's current one there is nothing to enter (and entering
+    its stream again would cost a one-token call a third of its time)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return _HERE if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
 def _raw(stream, device):
@@ -232,9 +236,9 @@ def conv1d_causal_step(x, w, bias, pool, slots=None, *, act="silu", out=None, st
             _dense(pool, "pool", (P, W - 1, D), dt, dev), _dense(slots, "slots", (R,), torch.int32, dev))
     with _on(stream, dev):
         y = torch.empty((R, D), dtype=dt, device=dev) if out is None else out
-    _check("conv1d_causal_step",
-           _mixer_lib().conv1d_causal_step(*args, _dense(y, "out", (R, D), dt, dev), R, P, D, W, _act(act), code,
-                                           _raw(stream, dev)))
+        _check("conv1d_causal_step",
+               _mixer_lib().conv1d_causal_step(*args, _dense(y, "out", (R, D), dt, dev), R, P, D, W, _act(act), code,
+                                               _raw(stream, dev)))
     return y
 
 
@@ -339,10 +343,10 @@ def delta_rule_step(q, k, v, g, beta, pool, slots=None, *, scale=None, qk_norm=F
     sp = _dense(slots, "slots", (R,), torch.int32, dev)
     with _on(stream, dev):
         o = torch.empty(v.shape, dtype=q.dtype, device=dev) if out is None else out
-    _check("delta_rule_step",
-           _mixer_lib().delta_rule_step(*ptrs, pp, sp, _dense(o, "out", v.shape, q.dtype, dev), R, L, P, *sizes,
-                                        dk ** -0.5 if scale is None else scale, qk_norm, code, bcode,
-                                        _raw(stream, dev)))
+        _check("delta_rule_step",
+               _mixer_lib().delta_rule_step(*ptrs, pp, sp, _dense(o, "out", v.shape, q.dtype, dev), R, L, P, *sizes,
+                                            dk ** -0.5 if scale is None else scale, qk_norm, code, bcode,
+                                            _raw(stream, dev)))
     return o
 
 
