@@ -4,7 +4,7 @@ rule and the branch norm, over the C ABI of ``include/convlower_mixer.h``.
     conv1d_causal_fwd / _bwd / _step      silu(causal depthwise convolution)
     delta_rule_fwd / _bwd / _step         S <- e^g S + k (beta (v - e^g S'k))',  o = S'q
     branch_norm_fwd / _bwd                r = x + alpha act(gate) norm(y),  h = norm(r)
-    conv1d_causal, delta_rule, branch_norm   the same, differentiable by autograd
+    conv1d_causal, delta_rule, branch_norm   the same, differentiable (once) by autograd
 
 As in the package's convolution binding, Python only checks and marshals:
 outputs and workspaces are allocated with torch on the stream the library
@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -417,6 +418,37 @@ def branch_norm_bwd(dr, dh, x, y, w_post, gate, w_next, stats, *, alpha=1.0, eps
 # ------------------------------------------------------------- differentiable forms
 
 
+class _Last(torch.autograd.Function):
+    """A gradient, and the tensors it depends on: it has none itself."""
+
+    @staticmethod
+    def forward(ctx, g, *depends):
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the mixing operators can be differentiated once only")
+
+
+def differentiable_once(backward):
+    """For a backward function that calls the library: under create_graph its
+    gradients, which nothing records, would pass for constants; differentiated
+    again, they raise.  (torch's own decorator lets those pass whose output
+    gradient is a constant, as that of a sum is, and those that are asked for
+    certain inputs only.)"""
+
+    @functools.wraps(backward)
+    def wrapper(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        depends = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+        return tuple(None if g is None else _Last.apply(g.detach(), *depends) for g in out)
+
+    return wrapper
+
+
 class _Conv1d(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, state, cu_seqlens, act, want_state):
@@ -426,6 +458,7 @@ class _Conv1d(torch.autograd.Function):
         return y, out
 
     @staticmethod
+    @differentiable_once
     def backward(ctx, dy, dstate_out):
         x, w, bias, state, cu = ctx.saved_tensors
         dx, dw, db, ds = conv1d_causal_bwd(
@@ -444,13 +477,15 @@ class _DeltaRule(torch.autograd.Function):
     def forward(ctx, q, k, v, g, beta, state, cu_seqlens, scale, qk_norm, want_state):
         o, out, saved = delta_rule_fwd(q, k, v, g, beta, cu_seqlens=cu_seqlens, state=state, scale=scale,
                                        qk_norm=qk_norm, want_state=want_state, save=any(ctx.needs_input_grad))
-        ctx.save_for_backward(q, k, v, g, beta, cu_seqlens, saved)
+        # (the state is not needed, but what depends on it is to be known)
+        ctx.save_for_backward(q, k, v, g, beta, cu_seqlens, saved, state if ctx.needs_input_grad[5] else None)
         ctx.more = (scale, qk_norm, state is not None)
         return o, out
 
     @staticmethod
+    @differentiable_once
     def backward(ctx, do, dstate_out):
-        q, k, v, g, beta, cu, saved = ctx.saved_tensors
+        q, k, v, g, beta, cu, saved, _ = ctx.saved_tensors
         scale, qk_norm, has_state = ctx.more
         grads = delta_rule_bwd(do.contiguous(), q, k, v, g, beta, saved, cu_seqlens=cu, scale=scale, qk_norm=qk_norm,
                                dstate_out=None if dstate_out is None else dstate_out.contiguous(),
@@ -474,6 +509,7 @@ class _BranchNorm(torch.autograd.Function):
         return r, h
 
     @staticmethod
+    @differentiable_once
     def backward(ctx, dr, dh):
         x, y, w_post, gate, w_next, stats = ctx.saved_tensors
         dr, dh = (None if t is None else t.contiguous() for t in (dr, dh))

@@ -26,6 +26,7 @@ class _Project(torch.autograd.Function):
         return conv2d_fwd(x[None, None], w[:, None, None], layout="NHWC").view(x.shape[0], w.shape[0])
 
     @staticmethod
+    @mixer.differentiable_once
     def backward(ctx, dy):
         x, w = ctx.saved_tensors
         dy = dy.contiguous()
