@@ -341,8 +341,9 @@ template <typename S, int V, int TPR, int NV, bool ANY, bool BWD>
 hipError_t norm_run(const NormArgs &a, hipStream_t st) {
     constexpr int TB = block_of(TPR), rows = TB / TPR;
     if constexpr (!BWD) {
-        hipLaunchKernelGGL((branch_norm_fwd_kernel<S, V, TPR, NV, ANY>), dim3((unsigned)((a.R + rows - 1) / rows)), dim3(TB),
-                           0, st, a);
+        const int64_t blocks = (a.R + rows - 1) / rows;
+        if (!grid_fits(blocks, TB, 1)) return kTooLarge;
+        hipLaunchKernelGGL((branch_norm_fwd_kernel<S, V, TPR, NV, ANY>), dim3((unsigned)blocks), dim3(TB), 0, st, a);
         return hipGetLastError();
     } else {
         if (a.R) {

@@ -410,8 +410,10 @@ bool aligned16(std::initializer_list<const void *> ps) {
 template <typename S, int V>
 hipError_t fwd_typed(const Conv1dArgs &a, hipStream_t st) {
     const int cb = (a.D + 256 * V - 1) / (256 * V);
-    const dim3 grid(a.tiles + (a.state_out && a.W > 1 ? a.s.N : 0), cb);
-    if (!grid.x) return hipSuccess;
+    const int64_t all = (int64_t)a.tiles + (a.state_out && a.W > 1 ? a.s.N : 0);
+    if (!all) return hipSuccess;
+    if (!grid_fits(all, 256, cb)) return kTooLarge;
+    const dim3 grid((unsigned)all, cb);
     switch (a.W) {
         case 2: hipLaunchKernelGGL((conv1d_fwd_kernel<S, V, 2>), grid, dim3(256), 0, st, a); break;
         case 3: hipLaunchKernelGGL((conv1d_fwd_kernel<S, V, 3>), grid, dim3(256), 0, st, a); break;
@@ -424,9 +426,11 @@ hipError_t fwd_typed(const Conv1dArgs &a, hipStream_t st) {
 template <typename S, int V>
 hipError_t bwd_typed(const Conv1dArgs &a, hipStream_t st) {
     const int cb = (a.D + 64 * V - 1) / (64 * V);
-    const auto blocks = [](int64_t n) { return (unsigned)((n + kConvRuns - 1) / kConvRuns); };
-    const dim3 grid(blocks(a.tiles) + (a.dstate && a.W > 1 ? blocks(a.s.N) : 0), cb);
-    if (grid.x) {
+    const auto blocks = [](int64_t n) { return (n + kConvRuns - 1) / kConvRuns; };
+    const int64_t all = blocks(a.tiles) + (a.dstate && a.W > 1 ? blocks(a.s.N) : 0);
+    if (!grid_fits(all, 256, cb)) return kTooLarge;
+    const dim3 grid((unsigned)all, cb);
+    if (all) {
         switch (a.W) {
             case 2: hipLaunchKernelGGL((conv1d_bwd_kernel<S, V, 2>), grid, dim3(256), 0, st, a); break;
             case 3: hipLaunchKernelGGL((conv1d_bwd_kernel<S, V, 3>), grid, dim3(256), 0, st, a); break;
@@ -444,7 +448,9 @@ template <typename S>
 hipError_t step_typed(const void *x, int64_t xs, const void *w, const void *bias, void *pool, const int32_t *slots,
                       void *y, int R, int P, int D, int W, int act, hipStream_t st) {
     constexpr int V = 16 / sizeof(S);
-    if (D % V == 0 && xs % V == 0 && aligned16({x, pool, y}))
+    const bool vec = D % V == 0 && xs % V == 0 && aligned16({x, pool, y});
+    if (!grid_fits(R, 64, (D + 64 * (vec ? V : 1) - 1) / (64 * (vec ? V : 1)))) return kTooLarge;
+    if (vec)
         hipLaunchKernelGGL((conv1d_step_kernel<S, V>), dim3(R, (D + 64 * V - 1) / (64 * V)), dim3(64), 0, st,
                            (const S *)x, xs, (const S *)w, (const S *)bias, (S *)pool, slots, (S *)y, P, D, W, act);
     else

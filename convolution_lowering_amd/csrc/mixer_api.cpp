@@ -129,7 +129,9 @@ conv_status_t delta_bytes(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv
     return CONV_OK;
 }
 
-conv_status_t hip_status(hipError_t e) { return e == hipSuccess ? CONV_OK : CONV_ERR_HIP; }
+conv_status_t hip_status(hipError_t e) {
+    return e == hipSuccess ? CONV_OK : e == kTooLarge ? CONV_ERR_UNSUPPORTED : CONV_ERR_HIP;
+}
 
 }  // namespace
 }  // namespace convlower

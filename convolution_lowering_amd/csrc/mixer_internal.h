@@ -97,7 +97,14 @@ __device__ __forceinline__ int seq_of(const Seqs &s, int64_t t) {
     return lo;
 }
 
-// ---- launchers; dtype: conv_dtype_t (fp32, bf16, fp16)
+// ---- launchers; dtype: conv_dtype_t (fp32, bf16, fp16).  Before its first
+// launch a launcher looks whether its grids fit (threads of an axis are counted
+// in 32 bits, blocks of the second one go to 65536), and else returns
+// kTooLarge, which callers see as CONV_ERR_UNSUPPORTED.
+constexpr hipError_t kTooLarge = hipErrorInvalidConfiguration;
+inline bool grid_fits(int64_t blocks_x, int threads, int64_t blocks_y) {
+    return blocks_x * threads < (1LL << 32) && blocks_y <= 65536;
+}
 struct Conv1dArgs {
     const void *x, *w, *bias, *state, *dy, *dstate_out;
     void *y, *state_out, *dx, *dw, *dbias, *dstate;

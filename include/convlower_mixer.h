@@ -38,7 +38,9 @@ extern "C" {
 
 typedef enum { MIX_ACT_NONE = 0, MIX_ACT_SILU = 1, MIX_ACT_SIGMOID = 2 } mix_act_t;
 
-/* Limits, above which a call returns CONV_ERR_UNSUPPORTED. */
+/* Limits, above which a call returns CONV_ERR_UNSUPPORTED; so do more tokens,
+ * rows, requests or channels than one launch has threads for (2^32: some 2^30
+ * tokens of a convolution, 2^28 rows of up to 128 16-bit values of a norm). */
 #define MIX_CONV1D_MAX_WIDTH 8   /* taps of conv1d_causal_* */
 #define MIX_DELTA_MAX_DK 128     /* key head size of delta_rule_* */
 #define MIX_DELTA_MAX_DV 256     /* value head size of delta_rule_* */
