@@ -13,7 +13,7 @@ def test_conv_fwd_more_tokens_than_threads(bad):
     assert conv_fwd(**bad) == UNSUPPORTED
 
 
-@pytest.mark.parametrize("bad", [dict(D=(1 << 24) - 1, xs=1 << 24, nbytes=1 << 40)])
+@pytest.mark.parametrize("bad", [dict(D=(1 << 24) - 1, xs=1 << 24, dys=1 << 24, nbytes=1 << 40)])
 def test_conv_bwd_more_channels_than_blocks(bad):
     assert conv_bwd(**bad) == UNSUPPORTED
 
