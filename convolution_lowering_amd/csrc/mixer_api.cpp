@@ -48,7 +48,8 @@ conv_status_t delta_sizes(int Hk, int Hv, int dk, int dv, conv_dtype_t dtype, co
 conv_status_t norm_sizes(int64_t R, int D, int64_t G, bool gate, float eps, mix_act_t act, conv_dtype_t dtype) {
     if (R < 0 || D < 1 || !mix_dtype_ok(dtype) || !(eps >= 0.f)) return CONV_ERR_INVALID_ARG;
     if (act != MIX_ACT_NONE && act != MIX_ACT_SILU && act != MIX_ACT_SIGMOID) return CONV_ERR_INVALID_ARG;
-    if (gate && (G < 1 || (R % G && R) || (G > R && R))) return CONV_ERR_INVALID_ARG;
+    // (no rows: a gate of as many, or one that rows would share)
+    if (gate && (G < 0 || (R ? !G || G > R || R % G : false))) return CONV_ERR_INVALID_ARG;
     if (D > MIX_NORM_MAX_WIDTH || R > kMaxTokens || (gate && G != R && G > 60000)) return CONV_ERR_UNSUPPORTED;
     return CONV_OK;
 }
@@ -334,8 +335,9 @@ conv_status_t branch_norm_bwd(const void *dr, const void *dh, const void *x, con
     if (!pointers_ok({w_post, dw_post}, {dr, dh, x, y, gate, w_next, dx, dy, dgate, dw_next}, es))
         return CONV_ERR_INVALID_ARG;
     if (R && (!y || !dy || !stats || (uintptr_t)stats % 4)) return CONV_ERR_INVALID_ARG;
-    // each input's gradient goes with the input; dh only where there is an h
-    if ((gate != nullptr) != (dgate != nullptr) || (w_next != nullptr) != (dw_next != nullptr)) return CONV_ERR_INVALID_ARG;
+    // each input's gradient goes with the input (that of a gate without rows may be anywhere); dh only where there is an h
+    if ((!gate || G) && (gate != nullptr) != (dgate != nullptr)) return CONV_ERR_INVALID_ARG;
+    if ((w_next != nullptr) != (dw_next != nullptr)) return CONV_ERR_INVALID_ARG;
     if (R && (x != nullptr) != (dx != nullptr)) return CONV_ERR_INVALID_ARG;
     if (dh && !w_next) return CONV_ERR_INVALID_ARG;
     if ((uintptr_t)workspace % 16) return CONV_ERR_INVALID_ARG;

@@ -363,8 +363,8 @@ def _norm_args(x, y, w_post, gate, w_next, act):
     if gate is not None:
         if gate.dim() < 1 or gate.shape[-1] != D:
             raise ValueError(f"gate has shape {tuple(gate.shape)}: rows of {D} wanted")
-        G = gate.numel() // D
-        if G < 1 or R % G:
+        G = gate.numel() // D if D else 0
+        if R and (G < 1 or R % G):
             raise ValueError(f"{G} gate rows do not divide {R} rows")
         gp = _dense(gate, "gate", gate.shape, dt, dev)
     else:

@@ -313,3 +313,31 @@ def test_activations_at_the_ends_of_the_range(dtype):
     z[5] = -inf
     r, _, _ = mixer.branch_norm_fwd(None, one, one[:1, 0], z[:, None].contiguous(), act="sigmoid", eps=0.0)
     assert (r[:3] == 1).all() and r[3] == 0.5 and (r[4:6].float() < 1e-37).all() and r[6].isnan()
+
+
+# -------------------------------------------------------------- without rows
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_branch_norm_without_rows_but_with_a_gate(dtype):
+    """The gated norm of no tokens: a gate row for each of no rows, or a gate
+    that all would share."""
+    t = T16[dtype]
+    w = torch.ones(64, device=DEV, dtype=t)
+    y = torch.zeros(0, 64, device=DEV, dtype=t)
+    some = torch.zeros(4, 64, device=DEV, dtype=t)[:0]  # no rows of a buffer that is there
+    for gate in (y, some):
+        r, h, stats = mixer.branch_norm_fwd(y, y, w, gate, w, act="silu", save=True)
+        assert r.shape == h.shape == (0, 64)
+        grads = mixer.branch_norm_bwd(y, y, y, y, w, gate, w, stats, act="silu")
+        assert grads[3].shape == (0, 64)
+        assert (grads[2] == 0).all() and (grads[4] == 0).all()
+    gate = torch.ones(1, 64, device=DEV, dtype=t)
+    r, h, stats = mixer.branch_norm_fwd(y, y, w, gate, w, act="silu", save=True)
+    grads = mixer.branch_norm_bwd(y, y, y, y, w, gate, w, stats, act="silu")
+    assert all((z == 0).all() for z in grads[2:])
+    leaves = [z.clone().requires_grad_(True) for z in (y, w, y)]
+    r, _ = mixer.branch_norm(None, leaves[0], leaves[1], leaves[2], act="silu")
+    assert [z.shape for z in torch.autograd.grad(r.sum(), leaves)] == [z.shape for z in leaves]
+    with pytest.raises(ValueError):  # no gate rows for rows that are there
+        mixer.branch_norm_fwd(None, torch.ones(2, 64, device=DEV, dtype=t), w, gate[:0])

@@ -2,7 +2,7 @@
 here launches a kernel, and no pointer is dereferenced)."""
 import pytest
 
-from test_mixer_boundary import UNSUPPORTED, P, conv_bwd, conv_fwd, conv_step, norm_fwd
+from test_mixer_boundary import INVALID, OK, UNSUPPORTED, P, conv_bwd, conv_fwd, conv_step, norm_bwd, norm_fwd
 
 
 @pytest.mark.parametrize("bad", [
@@ -30,3 +30,17 @@ def test_conv_step_more_requests_than_threads(bad):
 ])
 def test_norm_fwd_more_rows_than_threads(bad):
     assert norm_fwd(**bad) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("gate,G,want", [(P, 0, OK), (P, 1, OK), (P, 5, OK), (None, 0, OK), (P, -1, INVALID)])
+def test_norm_without_rows(gate, G, want):
+    """No rows, and a gate of none (per row) or of any number (shared)."""
+    assert norm_fwd(gate=gate, G=G, R=0) == want
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(gate=P, dgate=None, G=1, R=0), INVALID), (dict(gate=P, dgate=P, G=-1, R=0), INVALID),
+    (dict(gate=P, dgate=P, G=0, R=4), INVALID), (dict(gate=None, dgate=P, G=4, R=0), INVALID),
+])
+def test_norm_bwd_gates_without_rows(bad, want):
+    assert norm_bwd(**bad) == want
