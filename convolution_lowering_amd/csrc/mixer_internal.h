@@ -148,8 +148,6 @@ struct DeltaArgs {
     float *pool;
     const int32_t *slots;
     int R, L, P;
-    // chunked form
-    void *ws, *saved;
 };
 // qk_norm's term under the root
 constexpr float kDeltaEps = 1e-6f;
