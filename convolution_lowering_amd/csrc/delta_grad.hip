@@ -147,9 +147,9 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
     const int rep = A.Hv / A.Hk, slabs = B.dvp / kSlab;
     // What a slab begins with, fetched while the one before it is worked with.
     // Buffer loads: the base in scalar registers, one offset for all of them.
-    // A spill read back in here waits for these loads: with 16-bit inputs two
-    // registers spill, read only after the slabs; float32 ones of dk > 64 spill
-    // 40, two of them read in the slabs' loop and most between a head's products.
+    // (A spill read back in here would wait for these loads; there is none, with
+    // the products inside the chunk kept to themselves below: mixed, float32
+    // inputs spilled 40 registers and took 213 us for 168.)
     const int l16 = lane * 16;
     auto load4 = [&](__amdgpu_buffer_rsrc_t r, int at) {
         return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, l16, at, 0));
@@ -205,7 +205,6 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
     copy_in<8, IN / 1024>((const char *)B.kq + head * IN, kq);
     fetch(0, 0);
     if (tid < 4 * kC) (&sums[0][0][0])[tid] = 0.f;
-    CONVLOWER_WAIT_VMCNT(0);  // the copies
     for (int v = 0; v < rep; ++v) {
         const int h = hk * rep + v;
         const int64_t vh = (int64_t)slot * A.Hv + h;
@@ -273,6 +272,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             }
             Split fo[2];
             f32x4 io = split_rows(xo, fo);
+            if (v == 0 && slab == 0) CONVLOWER_WAIT_VMCNT(0);  // K and Q are in LDS (all but G's slab was waited for above)
             if (slab + 1 < slabs) fetch(v, slab + 1);
             else if (v + 1 < rep) fetch(v + 1, 0);
             __syncthreads();
@@ -376,6 +376,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
                 xb[s][j] = fm[row * kLd + c] * rk[c];
             }
         f32x4 ia = split_rows(xa, fa), ib = split_rows(xb, fb);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < MH; ++i) {
             f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
@@ -396,6 +397,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             pq += rows4(kq + IN / 2, i) * a;
             pr += rows4(kq, i) * b;
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -406,6 +408,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaArgs A, DeltaBuf B
             }
         ia = split_rows(xa, fa);
         ib = split_rows(xb, fb);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < MH; ++i) {
             f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
