@@ -388,9 +388,11 @@ hipError_t norm_typed(const NormArgs &a, hipStream_t st) {
 
 }  // namespace
 
-// Blocks of the backward pass, each with rows of one gate row only: what the
-// CUs hold at 16 wavefronts each (a row's block has D / 512 of them, at least
-// four), and never more than rows; every block leaves a row of partial sums.
+// Blocks of the backward pass, each with rows of one gate row only, and never
+// more than rows; every block leaves a row of partial sums.  1024, 512 and 256 of
+// them give 16 wavefronts to a CU for 16-bit rows (whose blocks have D / 512
+// wavefronts, four for short rows) but for widths of 513 to 1024, blocks of two
+// wavefronts and so 8 to a CU; float32 rows have blocks twice as large.
 void branch_norm_bwd_plan(int64_t R, int D, int64_t G, int *per_group, int *blocks) {
     const int64_t groups = G == R ? 1 : G;
     const int64_t span = groups ? R / groups : 0;

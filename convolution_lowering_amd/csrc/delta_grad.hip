@@ -20,7 +20,7 @@
 // before the products of these.
 //
 // 8192 tokens, 8 and 16 heads of 128 x 128 (400 MB of S, G, Y and E: 82 us at a
-// copy's rate): 207 us.  Bound by the way through LDS (write, barrier, read, for
+// copy's rate): 206 us.  Bound by the way through LDS (write, barrier, read, for
 // operands that serve one product each) with one block of eight wavefronts a
 // CU; four wavefronts of all key columns each spill, 339 us.
 #include "delta_chunk.h"

@@ -13,8 +13,8 @@
 // strong decays beside weak ones.
 //
 // 16384 tokens, 16 and 32 heads of 128 (134 MB of q and k, 352 MB of operands
-// written, 99 us at a copy's rate): 149 us; 8192 tokens, 8 and 16 heads with
-// what the gradients need 58 us.  Bound by the barriers between a head's steps
+// written, 99 us at a copy's rate): 143 us; 8192 tokens, 8 and 16 heads with
+// what the gradients need 57 us.  Bound by the barriers between a head's steps
 // (six, three blocks to a CU); the inverse by substitution alone, a lane a
 // column of the whole matrix, 246 us.
 #include "delta_chunk.h"
@@ -191,7 +191,7 @@ __device__ __forceinline__ void store_tri(const float *x, const float *by, float
 }
 
 // Bounds: the blocks that a CU's LDS and registers hold; a fourth, with the
-// registers that leaves it, gains nothing (151 against 149 us).
+// registers that leaves it, gains nothing (151 us where three took 149).
 constexpr int blocks_of(int bytes, int dkp, bool grad) { return grad || (bytes == 4 && dkp == 128) ? 2 : 3; }
 template <typename S, int DKP, bool GRAD>
 __global__ __launch_bounds__(256, blocks_of(sizeof(S), DKP, GRAD)) void delta_prep_kernel(DeltaArgs A, DeltaBuf B, bool vec) {

@@ -23,10 +23,10 @@
 // same bytes by the transposing LDS read.
 //
 // 16384 tokens in 6 sequences, the longest of 129 chunks, 32 heads of 128 x 128:
-// 300 us, 4400 cycles a chunk of which the chain's products are 1312 (82 of
+// 300 us, 4450 cycles a chunk of which the chain's products are 1312 (82 of
 // 16x16x32); one wavefront doing all of it 338 us, without the lines brought to
 // L2 322 us.  32 chunks x 64 heads, with what is kept for the gradients (200 MB)
-// 92 us, was 111; back 106 us, was 113.  Two more pairs of columns in a block do
+// 91 us, was 111; back 103 us, was 113.  Two more pairs of columns in a block do
 // not fit LDS, and a wavefront's columns cannot be fewer than a product's 16.
 #include "delta_chunk.h"
 
@@ -249,8 +249,9 @@ struct Scan {
     __device__ __forceinline__ static float &scalar(char *pair, int which) {
         return ((float *)(pair + kPairRows) + which * 64)[threadIdx.x & 63];
     }
-    // The state that a pair's operands stand for, 16 rows by 16 (22 bits: what
-    // the gradients' products take of it).
+    // The state that a pair's operands stand for, 16 rows by 16.  22 bits: all
+    // that the gradients' products take of it, and its float32 values would be
+    // another 8 KB a pair to hand over.
     __device__ __forceinline__ static void unsplit(const Split (&b)[KS], float is, f32x4 (&v)[MT]) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)

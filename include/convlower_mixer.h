@@ -25,7 +25,8 @@
  *   (head h at h * head_size).  Buffers without a stride are dense.
  * Dtype      CONV_DTYPE_FP32, _BF16 or _FP16 for every tensor not said to be
  *   fp32.  Sums, states and statistics are fp32; each result is rounded once,
- *   to nearest-even.
+ *   to nearest-even.  The chunked delta rule multiplies operands of 22 bits
+ *   (see there).
  */
 #ifndef CONVLOWER_MIXER_H
 #define CONVLOWER_MIXER_H
@@ -90,7 +91,18 @@ conv_status_t conv1d_causal_step(const void *x, int64_t x_stride, const void *w,
  *
  * delta_rule_fwd works on chunks of 64 tokens.  saved: NULL, or a buffer of
  * saved_bytes (from the size query) that delta_rule_bwd of the same inputs
- * takes. */
+ * takes.
+ *
+ * Digits     The chunked form's products take their operands in two halves, 22
+ *   bits: q, k and what is made of them (16-bit q and k are exact), v - S'k, u,
+ *   d_o, the state, and the states and gradients that are saved.  They are
+ *   added up in fp32, and the state that is carried is fp32.  Float32 results
+ *   are off by less than 1e-6 of the norm of a head; a value keeps all 22 bits
+ *   while it is not below 2^-17 of the largest of its column in the chunk.
+ *   The decays' gradients are sums in which large terms cancel: their error is
+ *   relative to the terms.  The token form is fp32 throughout.
+ * Infinities and NaN in a token's inputs may reach the chunk's tokens before
+ *   it as well; never another sequence, nor, but through q and k, another head. */
 conv_status_t delta_rule_fwd_workspace_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
                                             size_t *bytes_out);
 conv_status_t delta_rule_saved_size(int64_t T, int N, int Hk, int Hv, int dk, int dv, conv_dtype_t dtype,
