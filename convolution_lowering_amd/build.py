@@ -42,7 +42,13 @@ def _units():
              ("delta_prep", "delta_prep.hip", []),
              ("delta_scan", "delta_scan.hip", []),
              ("delta_grad", "delta_grad.hip", []),
-             ("branch_norm", "branch_norm.hip", [])]
+             ("branch_norm", "branch_norm.hip", []),
+             ("ffn_api", "ffn_api.cpp", []),
+             ("ffn_back", "ffn_back.hip", []),
+             ("ffn_w4", "ffn_w4.hip", []),
+             ("norm_quant", "norm_quant.hip", [])]
+    for dt, tag in ((1, "bf16"), (2, "f16"), (0, "f32"), (3, "fp8")):  # FFN_DTYPE: a conv_dtype_t
+        units.append((f"ffn_gated_{tag}", "ffn_gated.hip", [f"-DFFN_DTYPE={dt}"]))
     for dt, tag in ((1, "bf16"), (2, "f16"), (0, "f32")):  # IGEMM_DTYPE: 0 fp32, 1 bf16, 2 fp16
         for feed in range(10):  # the Feed values of conv_internal.h
             units.append((f"igemm_{tag}_feed{feed}", "igemm_inst.hip",

@@ -1,0 +1,227 @@
+// The C ABI of include/convlower_ffn.h: argument checks and launches.  Every
+// check is on the host, before the first launch.
+#include <initializer_list>
+
+#include "ffn_internal.h"
+
+namespace convlower {
+namespace {
+
+constexpr int64_t kMaxRows = (1LL << 31) - 1 - 256;
+constexpr int64_t kMaxBackTokens = 1 << 21;  // a row of tokens is addressed by 32-bit byte offsets, 192 rows at once
+
+bool ffn_dtype_ok(conv_dtype_t d) { return d == CONV_DTYPE_FP32 || d == CONV_DTYPE_BF16 || d == CONV_DTYPE_FP16; }
+size_t bytes_of(conv_dtype_t d) { return d == CONV_DTYPE_FP32 ? 4 : 2; }
+bool act_ok(ffn_act_t a) {
+    return a == FFN_ACT_NONE || a == FFN_ACT_SILU || a == FFN_ACT_SIGMOID || a == FFN_ACT_GELU;
+}
+// Whether every pointer of `must` is there and all are aligned to `es` bytes.
+bool pointers_ok(std::initializer_list<const void *> must, std::initializer_list<const void *> may, size_t es) {
+    for (const void *p : must)
+        if (!p || (uintptr_t)p % es) return false;
+    for (const void *p : may)
+        if ((uintptr_t)p % es) return false;
+    return true;
+}
+conv_status_t hip_status(hipError_t e) {
+    return e == hipSuccess ? CONV_OK : e == kTooLarge ? CONV_ERR_UNSUPPORTED : CONV_ERR_HIP;
+}
+
+conv_status_t ffn_sizes(int64_t T, int D, int F, ffn_act_t act, int64_t stride) {
+    if (T < 0 || D < 1 || F < 1 || !act_ok(act) || stride < D) return CONV_ERR_INVALID_ARG;
+    if (T > kMaxRows || D > FFN_MAX_WIDTH || F > FFN_MAX_WIDTH || stride > FFN_MAX_WIDTH) return CONV_ERR_UNSUPPORTED;
+    return CONV_OK;
+}
+int64_t saved_pitch(int F) { return (F + 3) / 4 * 4; }
+
+// Rows of the workspace are whole 128-byte pieces.
+int64_t padded(int64_t n, conv_dtype_t dtype) {
+    const int64_t piece = 128 / (int64_t)bytes_of(dtype);
+    return (n + piece - 1) / piece * piece;
+}
+// Gives b its parts of the workspace at p; returns the bytes (p null: only that).
+size_t lay_out(FfnBack *b, conv_dtype_t dtype, void *p) {
+    const size_t es = bytes_of(dtype);
+    b->Fp = (int)padded(b->F, dtype);
+    b->Tp = padded(b->T, dtype);
+    size_t at = 0;
+    auto take = [&](int64_t rows, int64_t width) {
+        void *r = p ? (char *)p + at : nullptr;
+        at += ((size_t)rows * (size_t)width * es + 255) / 256 * 256;
+        return r;
+    };
+    b->dgu = take(b->T, 2 * (int64_t)b->Fp);
+    b->dguT = take(2 * (int64_t)b->F, b->Tp);
+    b->xT = take(b->D, b->Tp);
+    b->wT = take(b->D, 2 * (int64_t)b->Fp);
+    return at;
+}
+
+conv_status_t w4_check(const void *x, int64_t x_stride, const void *y, int64_t R, int D, int F, int group,
+                       conv_dtype_t dtype) {
+    if (R < 0 || D < 1 || F < 1 || D % 8 || x_stride < D || !ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return CONV_ERR_INVALID_ARG;
+    if (R > kMaxRows || D > FFN_MAX_WIDTH || F > FFN_MAX_WIDTH || x_stride > FFN_MAX_WIDTH) return CONV_ERR_UNSUPPORTED;
+    if (R && !pointers_ok({x, y}, {}, bytes_of(dtype))) return CONV_ERR_INVALID_ARG;
+    return CONV_OK;
+}
+bool w4_weights_ok(const void *w, const void *scales, const void *zeros, conv_dtype_t dtype) {
+    return pointers_ok({w}, {}, 4) && pointers_ok({scales}, {zeros}, bytes_of(dtype));
+}
+
+}  // namespace
+
+hipError_t launch_ffn_gated_f32(const FfnGemmArgs &a, bool saving, hipStream_t st);
+hipError_t launch_ffn_gated_bf16(const FfnGemmArgs &a, bool saving, hipStream_t st);
+hipError_t launch_ffn_gated_f16(const FfnGemmArgs &a, bool saving, hipStream_t st);
+hipError_t launch_ffn_gated_fp8(const FfnGemmArgs &a, int out_dtype, hipStream_t st);
+hipError_t launch_ffn_plain_f32(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_plain_bf16(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_plain_f16(const FfnGemmArgs &a, hipStream_t st);
+
+hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int out_dtype, hipStream_t st) {
+    if (dtype == CONV_DTYPE_FP8_E4M3) return launch_ffn_gated_fp8(a, out_dtype, st);
+    if (dtype == CONV_DTYPE_FP32) return launch_ffn_gated_f32(a, e == FFN_SAVING, st);
+    if (dtype == CONV_DTYPE_FP16) return launch_ffn_gated_f16(a, e == FFN_SAVING, st);
+    return launch_ffn_gated_bf16(a, e == FFN_SAVING, st);
+}
+hipError_t launch_ffn_plain(const FfnGemmArgs &a, int dtype, hipStream_t st) {
+    if (dtype == CONV_DTYPE_FP32) return launch_ffn_plain_f32(a, st);
+    if (dtype == CONV_DTYPE_FP16) return launch_ffn_plain_f16(a, st);
+    return launch_ffn_plain_bf16(a, st);
+}
+
+}  // namespace convlower
+
+using namespace convlower;
+
+extern "C" {
+
+conv_status_t gated_ffn_saved_size(int64_t T, int F, size_t *bytes_out) {
+    if (!bytes_out || T < 0 || F < 1) return CONV_ERR_INVALID_ARG;
+    if (T > kMaxRows || F > FFN_MAX_WIDTH) return CONV_ERR_UNSUPPORTED;
+    *bytes_out = (size_t)T * 2 * (size_t)saved_pitch(F) * sizeof(float);
+    return CONV_OK;
+}
+
+conv_status_t gated_ffn_fwd(const void *x, int64_t x_stride, const void *w_gate, const void *w_up, void *h, void *saved,
+                            size_t saved_bytes, int64_t T, int D, int F, ffn_act_t act, conv_dtype_t dtype,
+                            conv_stream_t stream) {
+    if (!ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
+    conv_status_t st = ffn_sizes(T, D, F, act, x_stride);
+    if (st != CONV_OK) return st;
+    size_t keep = 0;
+    if ((st = gated_ffn_saved_size(T, F, &keep)) != CONV_OK) return st;
+    if (!T) return CONV_OK;
+    if (!pointers_ok({x, w_gate, w_up, h}, {}, bytes_of(dtype)) || (uintptr_t)saved % 16) return CONV_ERR_INVALID_ARG;
+    if (saved && saved_bytes < keep) return CONV_ERR_WORKSPACE;
+    FfnGemmArgs a{};
+    a.a = x, a.b0 = w_gate, a.b1 = w_up, a.as = x_stride, a.bs = D, a.M = T, a.N = F, a.K = D, a.act = act, a.out = h;
+    a.saved = (float *)saved, a.pitch = saved_pitch(F);
+    return hip_status(launch_ffn_gated(a, saved ? FFN_SAVING : FFN_GATED, dtype, dtype, (hipStream_t)stream));
+}
+
+conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t dtype, size_t *bytes_out) {
+    if (!bytes_out || !ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
+    const conv_status_t st = ffn_sizes(T, D, F, FFN_ACT_NONE, D);
+    if (st != CONV_OK) return st;
+    if (T > kMaxBackTokens) return CONV_ERR_UNSUPPORTED;
+    FfnBack b{};
+    b.T = T, b.D = D, b.F = F;
+    *bytes_out = lay_out(&b, dtype, nullptr);
+    return CONV_OK;
+}
+
+conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, int64_t x_stride, const void *w_gate,
+                            const void *w_up, const void *saved, size_t saved_bytes, void *dx, void *dw_gate,
+                            void *dw_up, int64_t T, int D, int F, ffn_act_t act, conv_dtype_t dtype,
+                            conv_stream_t stream, void *workspace, size_t workspace_bytes) {
+    if (!ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
+    conv_status_t st = ffn_sizes(T, D, F, act, x_stride);
+    if (st != CONV_OK) return st;
+    const size_t es = bytes_of(dtype);
+    if (!pointers_ok({w_gate, w_up, dw_gate, dw_up}, {dh, x, dx}, es) || dh_stride < F) return CONV_ERR_INVALID_ARG;
+    if (T && (!dh || !x || !dx)) return CONV_ERR_INVALID_ARG;
+    if (!pointers_ok({}, {saved, workspace}, 16)) return CONV_ERR_INVALID_ARG;
+    if (dh_stride > FFN_MAX_WIDTH) return CONV_ERR_UNSUPPORTED;
+    size_t need = 0, keep = 0;
+    if ((st = gated_ffn_saved_size(T, F, &keep)) != CONV_OK) return st;
+    if ((st = gated_ffn_bwd_workspace_size(T, D, F, dtype, &need)) != CONV_OK) return st;
+    if (!workspace || workspace_bytes < need || (T && (!saved || saved_bytes < keep))) return CONV_ERR_WORKSPACE;
+    FfnBack b{};
+    b.dh = dh, b.x = x, b.w_gate = w_gate, b.w_up = w_up, b.dhs = dh_stride, b.xs = x_stride;
+    b.saved = (const float *)saved, b.pitch = saved_pitch(F), b.T = T, b.D = D, b.F = F, b.act = act;
+    lay_out(&b, dtype, workspace);
+    hipError_t e = launch_ffn_back_prep(b, dtype, (hipStream_t)stream);
+    if (e == hipSuccess && T) {  // dx = [dg du] [w_gate; w_up]
+        FfnGemmArgs a{};
+        a.a = b.dgu, a.b0 = a.b1 = b.wT, a.as = a.bs = 2 * (int64_t)b.Fp, a.M = T, a.N = D, a.K = 2 * b.Fp;
+        a.out = dx, a.split = T;
+        e = launch_ffn_plain(a, dtype, (hipStream_t)stream);
+    }
+    if (e == hipSuccess) {  // [dw_gate; dw_up] = [dg du]' x
+        FfnGemmArgs a{};
+        a.a = b.dguT, a.b0 = a.b1 = b.xT, a.as = a.bs = b.Tp, a.M = 2 * (int64_t)F, a.N = D, a.K = (int)b.Tp;
+        a.out = dw_gate, a.out2 = dw_up, a.split = F;
+        e = launch_ffn_plain(a, dtype, (hipStream_t)stream);
+    }
+    return hip_status(e);
+}
+
+conv_status_t gated_ffn8_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *w_gate,
+                             const float *gate_scale, const void *w_up, const float *up_scale, void *h, int64_t T,
+                             int D, int F, ffn_act_t act, conv_dtype_t dtype, conv_stream_t stream) {
+    if (dtype != CONV_DTYPE_BF16 && dtype != CONV_DTYPE_FP16) return CONV_ERR_INVALID_ARG;
+    const conv_status_t st = ffn_sizes(T, D, F, act, x_stride);
+    if (st != CONV_OK) return st;
+    if (!T) return CONV_OK;
+    if (!x || !w_gate || !w_up || !pointers_ok({x_scale, gate_scale, up_scale}, {}, 4) || !pointers_ok({h}, {}, 2))
+        return CONV_ERR_INVALID_ARG;
+    FfnGemmArgs a{};
+    a.a = x, a.b0 = w_gate, a.b1 = w_up, a.as = x_stride, a.bs = D, a.M = T, a.N = F, a.K = D, a.act = act, a.out = h;
+    a.a_scale = x_scale, a.b0_scale = gate_scale, a.b1_scale = up_scale;
+    return hip_status(launch_ffn_gated(a, FFN_SCALED, CONV_DTYPE_FP8_E4M3, dtype, (hipStream_t)stream));
+}
+
+conv_status_t linear_w4_fwd(const void *x, int64_t x_stride, const void *w, const void *scales, const void *zeros,
+                            void *y, int64_t R, int D, int F, int group, conv_dtype_t dtype, conv_stream_t stream) {
+    const conv_status_t st = w4_check(x, x_stride, y, R, D, F, group, dtype);
+    if (st != CONV_OK || !R) return st;
+    if (!w4_weights_ok(w, scales, zeros, dtype)) return CONV_ERR_INVALID_ARG;
+    W4Args a{};
+    a.x = x, a.xs = x_stride, a.w[0] = (const uint8_t *)w, a.scales[0] = scales, a.zeros[0] = zeros, a.y = y;
+    a.R = R, a.D = D, a.F = F, a.groups = (D + group - 1) / group;
+    return hip_status(launch_w4(a, group, false, dtype, (hipStream_t)stream));
+}
+
+conv_status_t gated_ffn_w4_fwd(const void *x, int64_t x_stride, const void *w_gate, const void *gate_scales,
+                               const void *gate_zeros, const void *w_up, const void *up_scales, const void *up_zeros,
+                               void *h, int64_t R, int D, int F, int group, ffn_act_t act, conv_dtype_t dtype,
+                               conv_stream_t stream) {
+    const conv_status_t st = w4_check(x, x_stride, h, R, D, F, group, dtype);
+    if (st != CONV_OK) return st;
+    if (!act_ok(act)) return CONV_ERR_INVALID_ARG;
+    if (!R) return CONV_OK;
+    if (!w4_weights_ok(w_gate, gate_scales, gate_zeros, dtype) || !w4_weights_ok(w_up, up_scales, up_zeros, dtype) ||
+        (gate_zeros != nullptr) != (up_zeros != nullptr))
+        return CONV_ERR_INVALID_ARG;
+    W4Args a{};
+    a.x = x, a.xs = x_stride, a.y = h, a.R = R, a.D = D, a.F = F, a.groups = (D + group - 1) / group, a.act = act;
+    a.w[0] = (const uint8_t *)w_gate, a.scales[0] = gate_scales, a.zeros[0] = gate_zeros;
+    a.w[1] = (const uint8_t *)w_up, a.scales[1] = up_scales, a.zeros[1] = up_zeros;
+    return hip_status(launch_w4(a, group, true, dtype, (hipStream_t)stream));
+}
+
+conv_status_t norm_quant_fwd(const void *x, const void *res, const void *w, void *r, void *q, float *scale, int64_t R,
+                             int D, float eps, conv_dtype_t dtype, conv_stream_t stream) {
+    if (R < 0 || D < 1 || !ffn_dtype_ok(dtype) || !(eps >= 0.f)) return CONV_ERR_INVALID_ARG;
+    if (D > FFN_MAX_NORM_WIDTH || R > kMaxRows) return CONV_ERR_UNSUPPORTED;
+    if (!R) return CONV_OK;
+    if (!pointers_ok({x, w}, {res, r}, bytes_of(dtype)) || !q || !pointers_ok({scale}, {}, 4) || (r && !res))
+        return CONV_ERR_INVALID_ARG;
+    NormQuantArgs a{};
+    a.x = x, a.res = res, a.w = w, a.r = r, a.q = (uint8_t *)q, a.scale = scale, a.R = R, a.D = D, a.eps = eps;
+    return hip_status(launch_norm_quant(a, dtype, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,113 @@
+// Internal declarations of the feed-forward operators (convlower_ffn.h).
+#pragma once
+
+#include "convlower_ffn.h"
+#include "igemm_impl.h"
+#include "mixer_internal.h"
+
+namespace convlower {
+
+// ---- the gate's activation: value, and value and slope.  S: the type whose
+// digits the result needs (mix_sigmoid).  In the tanh form's polynomial z stops
+// at +-30, far past where the sigmoid is 0 or 1 in 32 bits, so that no z
+// overflows it.
+template <typename S>
+__device__ __forceinline__ float gelu_gate(float z, float *inner) {
+    constexpr float k2c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float c = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -30.f), 30.f);
+    *inner = c * k2c * fmaf(0.134145f, c * c, 1.f);  // z times the argument's slope
+    return mix_sigmoid<S>(c * k2c * fmaf(0.044715f, c * c, 1.f));
+}
+template <typename S>
+__device__ __forceinline__ float ffn_act(float z, int act) {
+    float inner;
+    switch (act) {
+        case FFN_ACT_SILU: return z * mix_sigmoid<S>(z);
+        case FFN_ACT_SIGMOID: return mix_sigmoid<S>(z);
+        case FFN_ACT_GELU: return z * gelu_gate<S>(z, &inner);
+        default: return z;
+    }
+}
+template <typename S>
+__device__ __forceinline__ void ffn_act_grad(float z, int act, float *a, float *da) {
+    if (act == FFN_ACT_NONE) {
+        *a = z;
+        *da = 1.f;
+    } else if (act == FFN_ACT_GELU) {
+        float inner;
+        const float p = gelu_gate<S>(z, &inner);
+        *a = z * p;
+        *da = fmaf(p * (1.f - p), inner, p);
+    } else {
+        const float p = mix_sigmoid<S>(z);
+        *a = act == FFN_ACT_SILU ? z * p : p;
+        *da = act == FFN_ACT_SILU ? p * fmaf(z, 1.f - p, 1.f) : p * (1.f - p);
+    }
+}
+
+// V consecutive elements at any multiple of an element's size.
+template <typename S, int V>
+struct __attribute__((packed, aligned(sizeof(S)))) FfnAnyVec {
+    S v[V];
+};
+
+// ---- products of rows: out[m][n] = sum_k a[m][k] b[n][k], both k-contiguous
+enum FfnEpilogue {
+    FFN_GATED,   // h = act(a b0') * (a b1')
+    FFN_SAVING,  // ... and both products, fp32
+    FFN_SCALED,  // ... each times its row's and its column's factor (8-bit operands)
+    FFN_PLAIN,   // out = a b0', rows from `split` on to out2
+};
+struct FfnGemmArgs {
+    const void *a, *b0, *b1;
+    int64_t as, bs;  // row strides, elements
+    int64_t M;
+    int N, K;  // columns (of each of b0, b1), products summed
+    int act;
+    void *out, *out2;  // [M][N]
+    int64_t split;
+    float *saved;  // [2][M][pitch]
+    int64_t pitch;
+    const float *a_scale, *b0_scale, *b1_scale;
+};
+hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int out_dtype, hipStream_t st);
+hipError_t launch_ffn_plain(const FfnGemmArgs &a, int dtype, hipStream_t st);
+
+// What the backward pass lays out in its workspace: rows of K are whole pieces
+// of 128 bytes, zeros behind the last value.
+struct FfnBack {
+    const void *dh, *x, *w_gate, *w_up;
+    int64_t dhs, xs;
+    const float *saved;
+    int64_t pitch;
+    void *dgu;   // [T][2][Fp]: gradients of g and of u
+    void *dguT;  // [2][F][Tp]
+    void *xT;    // [D][Tp]
+    void *wT;    // [D][2][Fp]
+    int64_t T, Tp;
+    int D, F, Fp, act;
+};
+hipError_t launch_ffn_back_prep(const FfnBack &a, int dtype, hipStream_t st);
+
+struct W4Args {
+    const void *x;
+    const uint8_t *w[2];
+    const void *scales[2], *zeros[2];
+    void *y;
+    int64_t xs, R;
+    int D, F, groups, act;
+};
+hipError_t launch_w4(const W4Args &a, int group, bool gated, int dtype, hipStream_t st);
+
+struct NormQuantArgs {
+    const void *x, *res, *w;
+    void *r;
+    uint8_t *q;
+    float *scale;
+    int64_t R;
+    int D;
+    float eps;
+};
+hipError_t launch_norm_quant(const NormQuantArgs &a, int dtype, hipStream_t st);
+
+}  // namespace convlower
