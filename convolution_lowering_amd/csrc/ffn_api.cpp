@@ -8,7 +8,6 @@ namespace convlower {
 namespace {
 
 constexpr int64_t kMaxRows = (1LL << 31) - 1 - 256;
-constexpr int64_t kMaxBackTokens = 1 << 21;  // a row of tokens is addressed by 32-bit byte offsets, 192 rows at once
 
 bool ffn_dtype_ok(conv_dtype_t d) { return d == CONV_DTYPE_FP32 || d == CONV_DTYPE_BF16 || d == CONV_DTYPE_FP16; }
 size_t bytes_of(conv_dtype_t d) { return d == CONV_DTYPE_FP32 ? 4 : 2; }
@@ -34,27 +33,11 @@ conv_status_t ffn_sizes(int64_t T, int D, int F, ffn_act_t act, int64_t stride) 
 }
 int64_t saved_pitch(int F) { return (F + 3) / 4 * 4; }
 
-// Rows of the workspace are whole 128-byte pieces.
-int64_t padded(int64_t n, conv_dtype_t dtype) {
-    const int64_t piece = 128 / (int64_t)bytes_of(dtype);
-    return (n + piece - 1) / piece * piece;
-}
-// Gives b its parts of the workspace at p; returns the bytes (p null: only that).
-size_t lay_out(FfnBack *b, conv_dtype_t dtype, void *p) {
-    const size_t es = bytes_of(dtype);
-    b->Fp = (int)padded(b->F, dtype);
-    b->Tp = padded(b->T, dtype);
-    size_t at = 0;
-    auto take = [&](int64_t rows, int64_t width) {
-        void *r = p ? (char *)p + at : nullptr;
-        at += ((size_t)rows * (size_t)width * es + 255) / 256 * 256;
-        return r;
-    };
-    b->dgu = take(b->T, 2 * (int64_t)b->Fp);
-    b->dguT = take(2 * (int64_t)b->F, b->Tp);
-    b->xT = take(b->D, b->Tp);
-    b->wT = take(b->D, 2 * (int64_t)b->Fp);
-    return at;
+// The workspace of the backward pass: the gradients of g and u, rows of whole
+// 128-byte pieces.
+int padded(int F, conv_dtype_t dtype) {
+    const int piece = dtype == CONV_DTYPE_FP32 ? 32 : 64;
+    return (F + piece - 1) / piece * piece;
 }
 
 conv_status_t w4_check(const void *x, int64_t x_stride, const void *y, int64_t R, int D, int F, int group,
@@ -75,9 +58,12 @@ hipError_t launch_ffn_gated_f32(const FfnGemmArgs &a, bool saving, hipStream_t s
 hipError_t launch_ffn_gated_bf16(const FfnGemmArgs &a, bool saving, hipStream_t st);
 hipError_t launch_ffn_gated_f16(const FfnGemmArgs &a, bool saving, hipStream_t st);
 hipError_t launch_ffn_gated_fp8(const FfnGemmArgs &a, int out_dtype, hipStream_t st);
-hipError_t launch_ffn_plain_f32(const FfnGemmArgs &a, hipStream_t st);
-hipError_t launch_ffn_plain_bf16(const FfnGemmArgs &a, hipStream_t st);
-hipError_t launch_ffn_plain_f16(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_dx_f32(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_dw_f32(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_dx_bf16(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_dw_bf16(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_dx_f16(const FfnGemmArgs &a, hipStream_t st);
+hipError_t launch_ffn_dw_f16(const FfnGemmArgs &a, hipStream_t st);
 
 hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int out_dtype, hipStream_t st) {
     if (dtype == CONV_DTYPE_FP8_E4M3) return launch_ffn_gated_fp8(a, out_dtype, st);
@@ -85,10 +71,15 @@ hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int 
     if (dtype == CONV_DTYPE_FP16) return launch_ffn_gated_f16(a, e == FFN_SAVING, st);
     return launch_ffn_gated_bf16(a, e == FFN_SAVING, st);
 }
-hipError_t launch_ffn_plain(const FfnGemmArgs &a, int dtype, hipStream_t st) {
-    if (dtype == CONV_DTYPE_FP32) return launch_ffn_plain_f32(a, st);
-    if (dtype == CONV_DTYPE_FP16) return launch_ffn_plain_f16(a, st);
-    return launch_ffn_plain_bf16(a, st);
+hipError_t launch_ffn_dx(const FfnGemmArgs &a, int dtype, hipStream_t st) {
+    if (dtype == CONV_DTYPE_FP32) return launch_ffn_dx_f32(a, st);
+    if (dtype == CONV_DTYPE_FP16) return launch_ffn_dx_f16(a, st);
+    return launch_ffn_dx_bf16(a, st);
+}
+hipError_t launch_ffn_dw(const FfnGemmArgs &a, int dtype, hipStream_t st) {
+    if (dtype == CONV_DTYPE_FP32) return launch_ffn_dw_f32(a, st);
+    if (dtype == CONV_DTYPE_FP16) return launch_ffn_dw_f16(a, st);
+    return launch_ffn_dw_bf16(a, st);
 }
 
 }  // namespace convlower
@@ -125,10 +116,7 @@ conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t
     if (!bytes_out || !ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
     const conv_status_t st = ffn_sizes(T, D, F, FFN_ACT_NONE, D);
     if (st != CONV_OK) return st;
-    if (T > kMaxBackTokens) return CONV_ERR_UNSUPPORTED;
-    FfnBack b{};
-    b.T = T, b.D = D, b.F = F;
-    *bytes_out = lay_out(&b, dtype, nullptr);
+    *bytes_out = (size_t)T * 2 * (size_t)padded(F, dtype) * bytes_of(dtype);
     return CONV_OK;
 }
 
@@ -147,23 +135,23 @@ conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, in
     size_t need = 0, keep = 0;
     if ((st = gated_ffn_saved_size(T, F, &keep)) != CONV_OK) return st;
     if ((st = gated_ffn_bwd_workspace_size(T, D, F, dtype, &need)) != CONV_OK) return st;
-    if (!workspace || workspace_bytes < need || (T && (!saved || saved_bytes < keep))) return CONV_ERR_WORKSPACE;
-    FfnBack b{};
-    b.dh = dh, b.x = x, b.w_gate = w_gate, b.w_up = w_up, b.dhs = dh_stride, b.xs = x_stride;
-    b.saved = (const float *)saved, b.pitch = saved_pitch(F), b.T = T, b.D = D, b.F = F, b.act = act;
-    lay_out(&b, dtype, workspace);
-    hipError_t e = launch_ffn_back_prep(b, dtype, (hipStream_t)stream);
+    if (T && (!workspace || workspace_bytes < need || !saved || saved_bytes < keep)) return CONV_ERR_WORKSPACE;
+    const int Fp = padded(F, dtype), piece = dtype == CONV_DTYPE_FP32 ? 32 : 64;
+    FfnGateGrad d{};
+    d.dh = dh, d.dhs = dh_stride, d.saved = (const float *)saved, d.pitch = saved_pitch(F), d.dgu = workspace;
+    d.T = T, d.F = F, d.Fp = Fp, d.act = act;
+    hipError_t e = launch_ffn_gate_grad(d, dtype, (hipStream_t)stream);
+    FfnGemmArgs a{};
+    a.a = workspace, a.as = 2 * (int64_t)Fp, a.bs = D, a.N = D;
     if (e == hipSuccess && T) {  // dx = [dg du] [w_gate; w_up]
-        FfnGemmArgs a{};
-        a.a = b.dgu, a.b0 = a.b1 = b.wT, a.as = a.bs = 2 * (int64_t)b.Fp, a.M = T, a.N = D, a.K = 2 * b.Fp;
-        a.out = dx, a.split = T;
-        e = launch_ffn_plain(a, dtype, (hipStream_t)stream);
+        a.b0 = w_gate, a.b1 = w_up, a.M = T, a.K = 2 * Fp, a.ktsplit = Fp / piece, a.brows = F;
+        a.out = dx, a.split = T, a.rows = T;
+        e = launch_ffn_dx(a, dtype, (hipStream_t)stream);
     }
     if (e == hipSuccess) {  // [dw_gate; dw_up] = [dg du]' x
-        FfnGemmArgs a{};
-        a.a = b.dguT, a.b0 = a.b1 = b.xT, a.as = a.bs = b.Tp, a.M = 2 * (int64_t)F, a.N = D, a.K = (int)b.Tp;
-        a.out = dw_gate, a.out2 = dw_up, a.split = F;
-        e = launch_ffn_plain(a, dtype, (hipStream_t)stream);
+        a.b0 = a.b1 = x, a.bs = x_stride, a.M = 2 * (int64_t)Fp, a.K = (int)T, a.ktsplit = INT32_MAX, a.brows = (int)T;
+        a.out = dw_gate, a.out2 = dw_up, a.split = Fp, a.rows = F;
+        e = launch_ffn_dw(a, dtype, (hipStream_t)stream);
     }
     return hip_status(e);
 }

@@ -1,102 +1,83 @@
-// What the gradients of the gated product need laid out before their products:
-// the gradients of g and u,
+// The gradients of g and u, which the products for dx and for the weights' gradients
+// take:
 //
-//   du = dh act(g),   dg = dh u act'(g),
+//   du = dh act(g),   dg = dh u act'(g).
 //
-// along the features (for dx) and along the tokens (for the weights'), and x and
-// the weights with their other axis contiguous.  HBM bound; tiles of 64 x 64 pass
-// through LDS.
+// HBM bound: each thread takes 16 bytes of results of both.  They are rounded to
+// the operands' type, which is what the matrix instructions take.
+#include <type_traits>
+
 #include "ffn_internal.h"
 
 namespace convlower {
 namespace {
 
-constexpr int kTile = 64;
-
-// One tile transposed: from in[r][c] (R x C, any addresses) to out[c][r], rows of
-// out up to Rp, zeros from R on.
-template <typename S>
-__device__ __forceinline__ void transpose_tile(const S *in, int64_t is, int64_t R, int C, S *out, int64_t os, int64_t Rp,
-                                               int64_t r0, int c0, S (&buf)[kTile][kTile + 2]) {
-    const int x = threadIdx.x & 63, y0 = threadIdx.x >> 6;
-    for (int y = y0; y < kTile; y += 4) {
-        S v = S(0);
-        if (r0 + y < R && c0 + x < C) v = in[(r0 + y) * is + c0 + x];
-        buf[y][x] = v;
-    }
-    __syncthreads();
-    for (int y = y0; y < kTile; y += 4)
-        if (c0 + y < C && r0 + x < Rp) out[(int64_t)(c0 + y) * os + r0 + x] = buf[x][y];
-}
-
-template <typename S>
-__global__ __launch_bounds__(256) void ffn_transpose_kernel(const S *in, int64_t is, int64_t R, int C, S *out, int64_t os,
-                                                            int64_t Rp) {
-    __shared__ S buf[kTile][kTile + 2];
-    transpose_tile<S>(in, is, R, C, out, os, Rp, (int64_t)blockIdx.x * kTile, blockIdx.y * kTile, buf);
-}
-
-template <typename S>
-__global__ __launch_bounds__(256) void ffn_gate_grad_kernel(FfnBack A) {
-    __shared__ S bg[kTile][kTile + 2], bu[kTile][kTile + 2];
-    const int x = threadIdx.x & 63, y0 = threadIdx.x >> 6;
-    const int64_t t0 = (int64_t)blockIdx.x * kTile;
-    const int f0 = blockIdx.y * kTile;
-    const S *dh = (const S *)A.dh;
-    for (int y = y0; y < kTile; y += 4) {
-        const int64_t t = t0 + y;
-        const int f = f0 + x;
-        float dg = 0.f, du = 0.f;
-        if (t < A.T && f < A.F) {
-            const float g = A.saved[t * A.pitch + f], u = A.saved[(A.T + t) * A.pitch + f], d = mix_f32(dh[t * A.dhs + f]);
+template <typename S, int ACT>
+__device__ __forceinline__ void gate_grad(const FfnGateGrad &A) {
+    constexpr int V = 16 / (int)sizeof(S);
+    const int per = A.Fp / V;
+    const int64_t total = A.T * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per;
+        const int f = (int)(i - t * per) * V;
+        const float *g = A.saved + t * A.pitch + f, *u = g + A.T * A.pitch;
+        const S *dh = (const S *)A.dh + t * A.dhs + f;
+        float gv[V] = {}, uv[V] = {}, d[V] = {};
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+            if (f + j < A.pitch) {  // (rows of the saved values are whole 16-byte pieces)
+                const float4 x = *(const float4 *)(g + j), y = *(const float4 *)(u + j);
+                gv[j] = x.x, gv[j + 1] = x.y, gv[j + 2] = x.z, gv[j + 3] = x.w;
+                uv[j] = y.x, uv[j + 1] = y.y, uv[j + 2] = y.z, uv[j + 3] = y.w;
+            }
+        if (f + V <= A.F) {
+            const FfnAnyVec<S, V> x = *(const FfnAnyVec<S, V> *)dh;
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = mix_f32(x.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (f + j < A.F) d[j] = mix_f32(dh[j]);
+        }
+        float dg[V], du[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
             float a, slope;
-            ffn_act_grad<S>(g, A.act, &a, &slope);
-            dg = d * u * slope;
-            du = d * a;
+            ffn_act_grad<S>(gv[j], ACT, &a, &slope);
+            const bool in = f + j < A.F;
+            dg[j] = in ? d[j] * uv[j] * slope : 0.f;
+            du[j] = in ? d[j] * a : 0.f;
         }
-        bg[y][x] = mix_out<S>(dg);
-        bu[y][x] = mix_out<S>(du);
-        if (t < A.T && f < A.Fp) {
-            S *row = (S *)A.dgu + t * 2 * A.Fp + f;
-            row[0] = bg[y][x];
-            row[A.Fp] = bu[y][x];
-        }
+        S *out = (S *)A.dgu + t * 2 * A.Fp + f;
+        mix_store<S, V>(out, dg);
+        mix_store<S, V>(out + A.Fp, du);
     }
-    __syncthreads();
-    for (int y = y0; y < kTile; y += 4)
-        if (f0 + y < A.F && t0 + x < A.Tp) {
-            S *row = (S *)A.dguT + (int64_t)(f0 + y) * A.Tp + t0 + x;
-            row[0] = bg[x][y];
-            row[(int64_t)A.F * A.Tp] = bu[x][y];
-        }
+}
+template <typename S, int ACT>
+__global__ __launch_bounds__(256) void ffn_gate_grad_kernel(FfnGateGrad A) {
+    gate_grad<S, ACT>(A);
 }
 
 template <typename S>
-hipError_t back_prep(const FfnBack &a, hipStream_t st) {
-    const int64_t tt = a.Tp / kTile + (a.Tp % kTile != 0);
-    const int ft = (a.Fp + kTile - 1) / kTile, dt = (a.D + kTile - 1) / kTile, wt = (a.Fp + kTile - 1) / kTile;
-    if (!grid_fits(tt, 256, ft > dt ? ft : dt) || !grid_fits(wt, 256, dt)) return kTooLarge;
-    if (tt) {
-        hipLaunchKernelGGL((ffn_gate_grad_kernel<S>), dim3((unsigned)tt, ft), dim3(256), 0, st, a);
-        if (const hipError_t e = hipGetLastError()) return e;
-        hipLaunchKernelGGL((ffn_transpose_kernel<S>), dim3((unsigned)tt, dt), dim3(256), 0, st, (const S *)a.x, a.xs, a.T, a.D,
-                           (S *)a.xT, a.Tp, a.Tp);
-        if (const hipError_t e = hipGetLastError()) return e;
+hipError_t run(const FfnGateGrad &a, hipStream_t st) {
+    const int64_t blocks = (a.T * (a.Fp / (16 / (int)sizeof(S))) + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20));
+    switch (a.act) {
+        case FFN_ACT_SILU: hipLaunchKernelGGL((ffn_gate_grad_kernel<S, FFN_ACT_SILU>), grid, dim3(256), 0, st, a); break;
+        case FFN_ACT_SIGMOID: hipLaunchKernelGGL((ffn_gate_grad_kernel<S, FFN_ACT_SIGMOID>), grid, dim3(256), 0, st, a); break;
+        case FFN_ACT_GELU: hipLaunchKernelGGL((ffn_gate_grad_kernel<S, FFN_ACT_GELU>), grid, dim3(256), 0, st, a); break;
+        default: hipLaunchKernelGGL((ffn_gate_grad_kernel<S, FFN_ACT_NONE>), grid, dim3(256), 0, st, a);
     }
-    for (int h = 0; h < 2; ++h) {
-        hipLaunchKernelGGL((ffn_transpose_kernel<S>), dim3(wt, dt), dim3(256), 0, st, (const S *)(h ? a.w_up : a.w_gate),
-                           (int64_t)a.D, (int64_t)a.F, a.D, (S *)a.wT + (int64_t)h * a.Fp, 2 * (int64_t)a.Fp, (int64_t)a.Fp);
-        if (const hipError_t e = hipGetLastError()) return e;
-    }
-    return hipSuccess;
+    return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_ffn_back_prep(const FfnBack &a, int dtype, hipStream_t st) {
-    if (dtype == CONV_DTYPE_FP32) return back_prep<float>(a, st);
-    if (dtype == CONV_DTYPE_FP16) return back_prep<_Float16>(a, st);
-    return back_prep<uint16_t>(a, st);
+hipError_t launch_ffn_gate_grad(const FfnGateGrad &a, int dtype, hipStream_t st) {
+    if (!a.T) return hipSuccess;
+    if (dtype == CONV_DTYPE_FP32) return run<float>(a, st);
+    if (dtype == CONV_DTYPE_FP16) return run<_Float16>(a, st);
+    return run<uint16_t>(a, st);
 }
 
 }  // namespace convlower

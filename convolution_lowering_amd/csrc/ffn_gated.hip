@@ -6,8 +6,8 @@ namespace convlower {
 
 #if FFN_DTYPE == 3
 hipError_t launch_ffn_gated_fp8(const FfnGemmArgs &a, int out_dtype, hipStream_t st) {
-    return out_dtype == CONV_DTYPE_FP16 ? ffn_run<uint8_t, _Float16, FFN_SCALED>(a, st)
-                                        : ffn_run<uint8_t, uint16_t, FFN_SCALED>(a, st);
+    return out_dtype == CONV_DTYPE_FP16 ? ffn_run<uint8_t, _Float16, FFN_SCALED, false, false>(a, st)
+                                        : ffn_run<uint8_t, uint16_t, FFN_SCALED, false, false>(a, st);
 }
 #else
 #if FFN_DTYPE == 0
@@ -21,10 +21,14 @@ typedef uint16_t ffn_t;
 typedef _Float16 ffn_t;
 #endif
 hipError_t FFN_NAME(launch_ffn_gated)(const FfnGemmArgs &a, bool saving, hipStream_t st) {
-    return saving ? ffn_run<ffn_t, ffn_t, FFN_SAVING>(a, st) : ffn_run<ffn_t, ffn_t, FFN_GATED>(a, st);
+    return saving ? ffn_run<ffn_t, ffn_t, FFN_SAVING, false, false>(a, st)
+                  : ffn_run<ffn_t, ffn_t, FFN_GATED, false, false>(a, st);
 }
-hipError_t FFN_NAME(launch_ffn_plain)(const FfnGemmArgs &a, hipStream_t st) {
-    return ffn_run<ffn_t, ffn_t, FFN_PLAIN>(a, st);
+hipError_t FFN_NAME(launch_ffn_dx)(const FfnGemmArgs &a, hipStream_t st) {
+    return ffn_run<ffn_t, ffn_t, FFN_PLAIN, false, true>(a, st);
+}
+hipError_t FFN_NAME(launch_ffn_dw)(const FfnGemmArgs &a, hipStream_t st) {
+    return ffn_run<ffn_t, ffn_t, FFN_PLAIN, true, true>(a, st);
 }
 #endif
 

@@ -1,16 +1,27 @@
-// Products of rows on the matrix cores: every a[m] with every b[n], both
-// contiguous along what is summed.  A K tile is 128 bytes of each row (64
-// 16-bit values, 32 float32, 128 e4m3), in LDS as 8 chunks of 16 bytes.
+// Products on the matrix cores: out[m][n] = sum_k a[m][k] b[n][k].  An operand
+// lies with its k together ("rows of k": activations and weights on the way
+// forward) or with its m or n together ("rows of m": what the gradients' products
+// sum over runs down the columns of the same tensors).
 //
-// Chunk c of row r lies in slot 8 r + (c ^ (r / 2) % 8): a fragment read takes
-// 16 rows of one chunk, and this puts them on the 16 groups of banks of a 256-byte
-// line.  Which values a lane's chunk holds does not matter to a sum as long as
-// both operands agree, so all types read the same two chunks of a row, c = lane
-// / 16 and that plus 4, and differ only in the instruction that takes them.
+// A K tile is 128 bytes of each row of k (64 16-bit values, 32 float32, 128 e4m3),
+// or as many rows of m.  In LDS it lies in regions of W rows or columns:
+//   * rows of k: W rows of 8 chunks of 16 bytes; chunk c of row r in slot 8 r + (c
+//     ^ (r / 2) % 8).  A fragment read takes 16 rows of one chunk: this puts them on
+//     the 16 groups of banks of a 256-byte line.  Which values a lane's chunk holds
+//     does not matter to a sum as long as both operands agree, so all types read
+//     the same two chunks of a row, c = lane / 16 and that plus 4, and differ only in
+//     the instruction that takes them.
+//   * rows of m: one LDS row for each k.  16-bit fragments come by the transposing
+//     read: 16 lanes read 16 columns of four rows and each gets its column of
+//     them, the same values a chunk of k would hold.  float32 ones are read one by
+//     one (their matrix instructions are 16 times slower).  Chunks are exchanged
+//     within a row so that the rows of one read lie on different banks.
 //
-// The rows of b are the matrix instruction's left operand, so that a lane's four
-// results are four neighbours of one output row.
+// b is the matrix instruction's left operand, so that a lane's four results are
+// four neighbours of one output row.
 #pragma once
+
+#include <type_traits>
 
 #include "ffn_internal.h"
 
@@ -26,15 +37,89 @@ __device__ __forceinline__ void ffn_mma(const uint4 (&b)[2], const uint4 (&a)[2]
         i32x8_t x, y;
         __builtin_memcpy(&x, &b, 32);
         __builtin_memcpy(&y, &a, 32);
-        // (e4m3 both; the scale operands are unused exponents of 1)
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+        // (e4m3 both; without block scales, which zeros ask for)
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, 0, 0, 0);
+    } else if constexpr (sizeof(S) == 4) {
+        // The tile's 32 products are added up by themselves: in one chain of K
+        // additions a float32 result loses sqrt(K / 32) times as much.
+        f32x4_t part = {};
+        MfmaShape<S, 16>::mma(b[0], a[0], part);
+        MfmaShape<S, 16>::mma(b[1], a[1], part);
+        acc += part;
     } else {
         MfmaShape<S, 16>::mma(b[0], a[0], acc);
         MfmaShape<S, 16>::mma(b[1], a[1], acc);
     }
 }
 
-__device__ __forceinline__ int ffn_slot(int r, int c) { return r * 8 + (c ^ ((r >> 1) & 7)); }
+// 16 bytes at an address in LDS.
+__device__ __forceinline__ uint4 lds_at(uint32_t at) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) u32x4 *)at);
+}
+
+// A region of W rows of k, or of W columns of rows of m (MM).
+template <typename S, bool MM, int W>
+struct FfnRegion {
+    static constexpr int ES = (int)sizeof(S);
+    static constexpr int KROWS = 128 / ES;               // rows of m in a K tile
+    static constexpr int PITCH = MM ? W * ES : 128;      // bytes of an LDS row
+    static constexpr int CHUNKS = PITCH / 16;
+    static constexpr int LOADS = W / 8;                  // 1 KB loads that fill it
+    static constexpr int ROWS_PER_LOAD = 64 / CHUNKS;
+    __device__ static __forceinline__ int swizzle(int row) {
+        if constexpr (!MM) return (row >> 1) & 7;
+        else if constexpr (ES == 4) return 4 * ((row >> 2) & 3);
+        else if constexpr (W == 128) return 2 * ((row & 3) | (((row >> 3) & 1) << 2));
+        else return 2 * (((row >> 1) & 1) | (((row >> 3) & 1) << 1));
+    }
+    // Which LDS row, and which of its chunks, lane `lane` of load q brings.
+    __device__ static __forceinline__ int load_row(int q, int lane) { return q * ROWS_PER_LOAD + lane / CHUNKS; }
+    __device__ static __forceinline__ int load_chunk(int q, int lane) {
+        return (lane % CHUNKS) ^ swizzle(load_row(q, lane));
+    }
+};
+
+// A wavefront's fragments of NT tiles of 16, from row or column `first` of a region.
+template <typename S, bool MM, int W, int NT>
+struct FfnFragments {
+    using R = FfnRegion<S, MM, W>;
+    uint32_t at[MM ? NT : 2];
+    __device__ __forceinline__ void init(uint32_t region, int first, int lane) {
+        const int g = lane >> 4, t = lane & 15;
+        if constexpr (!MM) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) at[j] = region + (first + t) * 128 + (((j * 4 + g) ^ (t >> 1)) * 16);
+        } else if constexpr (R::ES == 2) {
+            const int row = 8 * g + (t >> 2);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                at[i] = region + row * R::PITCH + ((((first >> 3) + 2 * i) ^ R::swizzle(row)) + ((t & 3) >> 1)) * 16 + (t & 1) * 8;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                at[i] = region + 4 * g * R::PITCH + ((((first >> 2) + 4 * i) ^ (4 * g)) + (t >> 2)) * 16 + (t & 3) * 4;
+        }
+    }
+    // Chunk j of tile i; add: the stage, or another region like this one.
+    __device__ __forceinline__ uint4 get(int i, int j, uint32_t add) const {
+        if constexpr (!MM) {
+            return lds_at(at[j] + add + i * 2048);
+        } else if constexpr (R::ES == 2) {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 *ptr;
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(at[i] + add + 32 * j * R::PITCH));
+            const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(at[i] + add + (32 * j + 4) * R::PITCH));
+            return __builtin_bit_cast(uint4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = *(const __attribute__((address_space(3))) uint32_t *)(at[i] + add + (16 * j + e) * R::PITCH);
+            return make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+};
 
 // Tiles in an order that keeps what the blocks of one XCD work on at a time
 // nearly square: XCD x (blocks x, x + 8, ...) has a contiguous run of the list,
@@ -60,7 +145,7 @@ __device__ __forceinline__ void ffn_put4(O *row, int n, int N, const float (&v)[
             if (n + i < N) row[n + i] = mix_out<O>(v[i]);
     }
 }
-template <typename O, FfnEpilogue EPI>
+template <typename O, FfnEpilogue EPI, int ACT>
 __device__ __forceinline__ void ffn_gated_out(const FfnGemmArgs &A, int64_t m, int n, const f32x4_t &ga,
                                               const f32x4_t &ua) {
     float g[4], u[4], h[4];
@@ -81,29 +166,62 @@ __device__ __forceinline__ void ffn_gated_out(const FfnGemmArgs &A, int64_t m, i
         store4(p + A.M * A.pitch, u[0], u[1], u[2], u[3]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = ffn_act<O>(g[i], A.act) * u[i];
+    for (int i = 0; i < 4; ++i) h[i] = ffn_act<O>(g[i], ACT) * u[i];
     ffn_put4((O *)A.out + m * A.N, n, A.N, h);
+}
+// f with the activation as a constant: one branch for all results.
+template <typename F>
+__device__ __forceinline__ void ffn_with_act(int act, F &&f) {
+    switch (act) {
+        case FFN_ACT_SILU: f(std::integral_constant<int, FFN_ACT_SILU>()); break;
+        case FFN_ACT_SIGMOID: f(std::integral_constant<int, FFN_ACT_SIGMOID>()); break;
+        case FFN_ACT_GELU: f(std::integral_constant<int, FFN_ACT_GELU>()); break;
+        default: f(std::integral_constant<int, FFN_ACT_NONE>());
+    }
 }
 template <typename O>
 __device__ __forceinline__ void ffn_plain_out(const FfnGemmArgs &A, int64_t m, int n, const f32x4_t &acc) {
     const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
-    O *row = m < A.split ? (O *)A.out + m * A.N : (O *)A.out2 + (m - A.split) * A.N;
-    ffn_put4(row, n, A.N, v);
+    const bool second = m >= A.split;
+    const int64_t row = second ? m - A.split : m;
+    if (row < A.rows) ffn_put4((O *)(second ? A.out2 : A.out) + row * A.N, n, A.N, v);
 }
 
-// ---- the loop for any size: four wavefronts, 2 x 2, over BM rows of a and BH
-// of each of b0 and b1 (or 2 BH of b0 alone).  Rows at multiples of 16 bytes are
+// Where tile kt of b's rows of m lies: `rows` of them in b0, then as many in b1
+// from tile `ktsplit` on.
+struct FfnTileAt {
+    const char *p;
+    int left;  // rows there are from here on
+};
+template <typename S>
+__device__ __forceinline__ FfnTileAt ffn_tile_of_b(const FfnGemmArgs &A, int kt) {
+    const int k = kt < A.ktsplit ? kt : kt - A.ktsplit, krows = 128 / (int)sizeof(S);
+    return {(const char *)(kt < A.ktsplit ? A.b0 : A.b1) + (int64_t)k * krows * A.bs * (int64_t)sizeof(S), A.brows - k * krows};
+}
+// `cols` values of each of a tile's rows of m, as a buffer.
+template <typename S>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ffn_rows_of_m(const char *p, int left, uint32_t step, int cols) {
+    constexpr int KROWS = 128 / (int)sizeof(S);
+    const int n = left < KROWS ? left : KROWS;
+    return make_rsrc(n > 0 ? p : nullptr, n > 0 ? (uint32_t)(n - 1) * step + (uint32_t)cols * (uint32_t)sizeof(S) : 0u);
+}
+
+// ---- the loop for any size: four wavefronts, 2 x 2, over BM of a's m and BH of
+// each of b0 and b1 (or 2 BH of b0 alone).  Chunks at multiples of 16 bytes are
 // copied into LDS by the load instructions that write there (three stages, two
-// tiles under way); others (ANY) pass through registers, one tile ahead, their
-// last values one by one.
-template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY>
+// tiles under way); others (ANY) pass through registers, one tile ahead, the last
+// values of a row one by one.
+template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY, bool AM, bool BMM>
 __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
-    constexpr int V = 16 / (int)sizeof(S), ROWS = BM + 2 * BH, ST = ANY ? 2 : 3;
-    constexpr int IPW = ROWS / 32;              // 1 KB loads of a wavefront per tile
-    constexpr int TM = BM / 32, TN = BH / 32;   // 16-row tiles of a wavefront: of a, and of each half of b
     constexpr bool PLAIN = EPI == FFN_PLAIN;
-    static_assert(ROWS % 32 == 0 && BM % 32 == 0 && BH % 32 == 0, "loads and wavefronts split evenly");
-    __shared__ uint4 lds[ST][ROWS * 8];
+    constexpr int ES = (int)sizeof(S), V = 16 / ES, ST = ANY ? 2 : 3;
+    constexpr int TM = BM / 32, TN = BH / 32;  // 16-wide tiles of a wavefront: of a, and of each half of b
+    using RA = FfnRegion<S, AM, BM>;
+    using RB = FfnRegion<S, BMM, 2 * BH>;
+    constexpr int IA = RA::LOADS / 4, IB = RB::LOADS / 4, IPW = IA + IB;  // loads of a wavefront per tile
+    static_assert(BM % 32 == 0 && BH % 32 == 0 && (PLAIN || !BMM), "loads and wavefronts split evenly");
+    constexpr uint32_t STAGE = (BM + 2 * BH) * 128;
+    __shared__ alignas(16) char lds[ST * STAGE];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int mt, nt;
@@ -111,158 +229,209 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
     ffn_tile((int)((A.M + BM - 1) / BM), (A.N + BN - 1) / BN, 8, &mt, &nt);
     const int64_t m0 = (int64_t)mt * BM;
     const int n0 = nt * BN;
-    const uint32_t kbytes = (uint32_t)A.K * (uint32_t)sizeof(S), abytes = (uint32_t)(A.as * sizeof(S)),
-                   bbytes = (uint32_t)(A.bs * sizeof(S));
-    const int nk = (int)((kbytes + 127) / 128);
+    const uint32_t kbytes = (uint32_t)A.K * ES, abytes = (uint32_t)(A.as * ES), bbytes = (uint32_t)(A.bs * ES);
+    const int nk = (A.K + RA::KROWS - 1) / RA::KROWS;
+    const int am = (int)min((int64_t)BM, A.M - m0);  // a's m that are there
+    const char *abase = (const char *)A.a + m0 * (AM ? ES : A.as * ES);
 
-    // Bases of the three groups of rows and how many rows are there.
-    const char *base[3] = {(const char *)A.a + m0 * A.as * (int64_t)sizeof(S),
-                           (const char *)A.b0 + (int64_t)n0 * A.bs * (int64_t)sizeof(S),
-                           (const char *)(PLAIN ? A.b0 : A.b1) + (int64_t)(n0 + (PLAIN ? BH : 0)) * A.bs * (int64_t)sizeof(S)};
-    const int have[3] = {(int)min((int64_t)BM, A.M - m0), min(BH, A.N - n0), min(BH, A.N - n0 - (PLAIN ? BH : 0))};
-
-    // Load i of this wavefront covers rows 8 (4 i + wave) + lane / 8 of one group; each lane always has the same chunk.
-    const int chunk = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
-    auto part_of = [&](int row) { return row < BM ? 0 : row < BM + BH ? 1 : 2; };
-    auto row_in = [&](int row) { return row < BM ? row : row < BM + BH ? row - BM : row - BM - BH; };
-
+    // Load i of this wavefront is load 4 i + wave of its region.
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
     f32x4_t acc[TM][2][TN] = {};
     const int wm = wave >> 1, wn = wave & 1;
-    auto compute = [&](const uint4 *st) {
+    FfnFragments<S, AM, BM, TM> fa;
+    FfnFragments<S, BMM, 2 * BH, TN> fb[2];
+    fa.init(lds0, wm * TM * 16, lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fb[h].init(lds0 + BM * 128, h * BH + wn * TN * 16, lane);
+    auto compute = [&](uint32_t stage) {
         uint4 b[2][TN][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int t = 0; t < TN; ++t)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    b[h][t][j] = st[ffn_slot(BM + h * BH + (wn * TN + t) * 16 + (lane & 15), j * 4 + (lane >> 4))];
+                for (int j = 0; j < 2; ++j) b[h][t][j] = fb[h].get(t, j, stage);
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
             uint4 a[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) a[j] = st[ffn_slot((wm * TM + t) * 16 + (lane & 15), j * 4 + (lane >> 4))];
+            for (int j = 0; j < 2; ++j) a[j] = fa.get(t, j, stage);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int f = 0; f < TN; ++f) ffn_mma<S>(b[h][f], a, acc[t][h][f]);
         }
     };
+    auto next = [](uint32_t stage) { return stage + STAGE == ST * STAGE ? 0u : stage + STAGE; };
 
     if constexpr (!ANY) {
-        __amdgpu_buffer_rsrc_t rs[3];
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-            rs[p] = make_rsrc(base[p], have[p] > 0 ? (uint32_t)(have[p] - 1) * (p ? bbytes : abytes) + kbytes : 0u);
+        const int gate = min(BH, A.N - n0), up = min(BH, A.N - n0 - (PLAIN ? BH : 0));
+        const int64_t up0 = (int64_t)(n0 + (PLAIN ? BH : 0)) * A.bs * ES;
+        const __amdgpu_buffer_rsrc_t ka = make_rsrc(abase, (uint32_t)(am - 1) * abytes + kbytes),
+                                     kg = make_rsrc((const char *)A.b0 + (int64_t)n0 * A.bs * ES, (uint32_t)(gate - 1) * bbytes + kbytes),
+                                     ku = make_rsrc((const char *)(PLAIN ? A.b0 : A.b1) + (up > 0 ? up0 : 0),
+                                                    up > 0 ? (uint32_t)(up - 1) * bbytes + kbytes : 0u);
         uint32_t off[IPW];
 #pragma unroll
         for (int i = 0; i < IPW; ++i) {
-            const int row = 8 * (4 * i + wave) + (lane >> 3), p = part_of(32 * i);
-            off[i] = (uint32_t)row_in(row) * (p ? bbytes : abytes) + chunk * 16;
+            const bool of_a = i < IA;
+            const int q = 4 * (of_a ? i : i - IA) + wave;
+            const int row = of_a ? RA::load_row(q, lane) : RB::load_row(q, lane);
+            const int chunk = of_a ? RA::load_chunk(q, lane) : RB::load_chunk(q, lane);
+            if (of_a ? AM : BMM) {
+                const bool in = chunk * V < (of_a ? am : A.N - n0);
+                off[i] = in ? (uint32_t)row * (of_a ? abytes : bbytes) + chunk * 16 : kOutOfRange;
+            } else {
+                off[i] = (uint32_t)(of_a ? row : row % BH) * (of_a ? abytes : bbytes) + chunk * 16;
+            }
         }
-        auto issue = [&](int kt) {  // tiles past the end and what lies behind a row read as zeros
+        // (in rows of k all loads of a lane bring the same chunk, as 8 q + lane / 8 keep (row / 2) % 8)
+        const uint32_t chunk = (uint32_t)FfnRegion<S, false, 128>::load_chunk(wave, lane) * 16;
+        auto issue = [&](int kt, uint32_t stage) {  // tiles past the end and what lies behind a row read as zeros
             const uint32_t at = (uint32_t)kt * 128;
-            const bool in = at + chunk * 16 < kbytes;
-            const uint32_t dst = (uint32_t)(uintptr_t)(lds_ptr_t)&lds[kt % ST][0] + wave * 1024;
+            const bool in = at + chunk < kbytes;
+            const uint32_t dst = lds0 + stage + wave * 1024;
+            __amdgpu_buffer_rsrc_t ma, mb;
+            if constexpr (AM) ma = ffn_rows_of_m<S>(abase + (int64_t)kt * RA::KROWS * abytes, A.K - kt * RA::KROWS, abytes, (int)(A.M - m0));
+            if constexpr (BMM) {
+                const FfnTileAt b = ffn_tile_of_b<S>(A, kt);
+                mb = ffn_rows_of_m<S>(b.p + (int64_t)n0 * ES, kt < nk ? b.left : 0, bbytes, A.N - n0);
+            }
 #pragma unroll
             for (int i = 0; i < IPW; ++i) {
-                const int p = part_of(32 * i);
-                lds_dma16(rs[p], in ? off[i] + at : kOutOfRange, dst + i * 4096);
+                if (i < IA) {
+                    if constexpr (AM) lds_dma16(ma, off[i], dst + i * 4096);
+                    else lds_dma16(ka, in ? off[i] + at : kOutOfRange, dst + i * 4096);
+                } else {
+                    if constexpr (BMM) lds_dma16(mb, off[i], dst + i * 4096);
+                    else lds_dma16(i - IA < BH / 32 ? kg : ku, in ? off[i] + at : kOutOfRange, dst + i * 4096);
+                }
             }
         };
-        if (nk > 0) {
-            issue(0);
-            issue(1);
-        }
+        issue(0, 0);
+        issue(1, STAGE);
+        uint32_t stage = 0, filled = 2 * STAGE;
+#pragma nounroll
         for (int kt = 0; kt < nk; ++kt) {
             CONVLOWER_WAIT_VMCNT_LDS(IPW);
             block_barrier();  // tile kt has landed for all, and nobody reads tile kt - 1's stage any more
             __builtin_amdgcn_sched_barrier(0);
-            issue(kt + 2);
+            issue(kt + 2, filled);
             __builtin_amdgcn_sched_barrier(0);
-            compute(lds[kt % ST]);
+            compute(stage);
             __builtin_amdgcn_sched_barrier(0);
+            stage = next(stage);
+            filled = next(filled);
         }
         CONVLOWER_WAIT_VMCNT(0);  // no load may still write LDS when the block ends
     } else {
         uint4 reg[IPW];
+        // V values of a row from value k on, of which there are `have`.
+        auto values = [&](const char *row, int k, int have) {
+            const S *src = (const S *)row + k;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (k + V <= have) {
+                const FfnAnyVec<S, V> t = *(const FfnAnyVec<S, V> *)src;
+                __builtin_memcpy(&v, &t, 16);
+            } else if (k < have) {
+                S t[V] = {};
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (k + j < have) t[j] = src[j];
+                __builtin_memcpy(&v, t, 16);
+            }
+            return v;
+        };
         auto fetch = [&](int kt) {
-            const int k = kt * (128 / (int)sizeof(S)) + chunk * V;
 #pragma unroll
             for (int i = 0; i < IPW; ++i) {
-                const int row = 8 * (4 * i + wave) + (lane >> 3), p = part_of(32 * i), in = row_in(row);
+                const bool of_a = i < IA;
+                const int q = 4 * (of_a ? i : i - IA) + wave;
+                const int row = of_a ? RA::load_row(q, lane) : RB::load_row(q, lane);
+                const int first = (of_a ? RA::load_chunk(q, lane) : RB::load_chunk(q, lane)) * V;
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (in < have[p] && k < A.K) {
-                    const S *src = (const S *)base[p] + (int64_t)in * (p ? A.bs : A.as) + k;
-                    if (k + V <= A.K) {
-                        const FfnAnyVec<S, V> t = *(const FfnAnyVec<S, V> *)src;
-                        __builtin_memcpy(&v, &t, 16);
-                    } else {
-                        S t[V] = {};
-#pragma unroll
-                        for (int j = 0; j < V; ++j)
-                            if (k + j < A.K) t[j] = src[j];
-                        __builtin_memcpy(&v, t, 16);
+                if (of_a ? AM : BMM) {
+                    const char *p = abase + (int64_t)kt * RA::KROWS * abytes;
+                    int left = A.K - kt * RA::KROWS, cols = am;
+                    if (!of_a) {
+                        const FfnTileAt b = ffn_tile_of_b<S>(A, kt);
+                        p = b.p + (int64_t)n0 * ES, left = b.left, cols = A.N - n0;
                     }
+                    if (row < left) v = values(p + (int64_t)row * (of_a ? abytes : bbytes), first, cols);
+                } else {
+                    const bool up = !of_a && !PLAIN && row >= BH;
+                    const int64_t r = of_a ? m0 + row : n0 + (up ? row - BH : row);
+                    const char *p = (const char *)(of_a ? A.a : up ? A.b1 : A.b0) + r * (of_a ? A.as : A.bs) * ES;
+                    if (r < (of_a ? A.M : (int64_t)A.N)) v = values(p, kt * RA::KROWS + first, A.K);
                 }
                 reg[i] = v;
             }
         };
-        auto keep = [&](int kt) {
+        auto keep = [&](uint32_t stage) {
 #pragma unroll
-            for (int i = 0; i < IPW; ++i) lds[kt % ST][(4 * i + wave) * 64 + lane] = reg[i];
+            for (int i = 0; i < IPW; ++i) *(uint4 *)(lds + stage + (4 * i + wave) * 1024 + lane * 16) = reg[i];
         };
         if (nk > 0) {
             fetch(0);
             keep(0);
         }
+        uint32_t stage = 0;
+#pragma nounroll
         for (int kt = 0; kt < nk; ++kt) {
             __syncthreads();
             if (kt + 1 < nk) fetch(kt + 1);
-            compute(lds[kt % ST]);
-            if (kt + 1 < nk) keep(kt + 1);
+            compute(stage);
+            stage = next(stage);
+            if (kt + 1 < nk) keep(stage);
         }
     }
 
+    auto results = [&](auto act) {
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        const int64_t m = m0 + (wm * TM + t) * 16 + (lane & 15);
-        if (m >= A.M) continue;
+        for (int t = 0; t < TM; ++t) {
+            const int64_t m = m0 + (wm * TM + t) * 16 + (lane & 15);
+            if (m >= A.M) continue;
 #pragma unroll
-        for (int f = 0; f < TN; ++f) {
-            const int n = n0 + (wn * TN + f) * 16 + 4 * (lane >> 4);
-            if constexpr (PLAIN) {
-                if (n < A.N) ffn_plain_out<O>(A, m, n, acc[t][0][f]);
-                if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[t][1][f]);
-            } else if (n < A.N) {
-                ffn_gated_out<O, EPI>(A, m, n, acc[t][0][f], acc[t][1][f]);
+            for (int f = 0; f < TN; ++f) {
+                const int n = n0 + (wn * TN + f) * 16 + 4 * (lane >> 4);
+                if constexpr (PLAIN) {
+                    if (n < A.N) ffn_plain_out<O>(A, m, n, acc[t][0][f]);
+                    if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[t][1][f]);
+                } else if (n < A.N) {
+                    ffn_gated_out<O, EPI, decltype(act)::value>(A, m, n, acc[t][0][f], acc[t][1][f]);
+                }
             }
         }
-    }
+    };
+    if constexpr (PLAIN) results(0);
+    else ffn_with_act(A.act, results);
 }
-template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY>
+template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY, bool AM, bool BMM>
 __global__ __launch_bounds__(256) void ffn_small_kernel(FfnGemmArgs A) {
-    ffn_small_body<S, O, EPI, BM, BH, ANY>(A);
+    ffn_small_body<S, O, EPI, BM, BH, ANY, AM, BMM>(A);
 }
 
-// ---- the large tile: 256 rows of a by 128 of each half of b, one block of
+// ---- the large tile: 256 of a's m by 128 of each half of b, one block of
 // eight wavefronts on a CU, two on each SIMD, each with 128 x (32 + 32) of the
 // tile.  Wavefronts 0-3 and 4-7 alternate: while one group multiplies, the other
 // reads LDS and issues loads, with a barrier at each change, so that a SIMD's
 // matrix core always has a wavefront whose operands are in registers.
 //
 // A wavefront goes through a K tile in four phases, (A0, B0), (A0, B1), (A1, B1),
-// (A1, B0): A0, A1 are the halves of its rows of a, B0 and B1 its rows of the
+// (A1, B0): A0, A1 are the halves of its part of a, B0 and B1 its parts of the
 // halves of b.  Each of the four is 16 KB of a stage, its own region; there are
 // two stages, and a region takes the tile after next as soon as both groups
 // have read it.  Two 1 KB loads of each phase and wavefront fill one region, in
 // the order in which they are read, five phases ahead: the wait at the end of a
 // phase's reads leaves ten loads under way.
-template <typename S, typename O, FfnEpilogue EPI>
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
 __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
-    constexpr int BM = 256, BH = 128;
+    constexpr int BM = 256, BH = 128, ES = (int)sizeof(S), V = 16 / ES;
     constexpr bool PLAIN = EPI == FFN_PLAIN;
+    static_assert(PLAIN || !BMM, "two matrices of rows of k, or one of either kind");
     constexpr uint32_t REGION = 16384, STAGE = 4 * REGION;
+    using RA = FfnRegion<S, AM, 128>;
+    using RB = FfnRegion<S, BMM, 128>;
     __shared__ alignas(16) char lds[2 * STAGE];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -271,56 +440,91 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
     ffn_tile((int)((A.M + BM - 1) / BM), (A.N + BN - 1) / BN, 8, &mt, &nt);
     const int64_t m0 = (int64_t)mt * BM;
     const int n0 = nt * BN;
-    const uint32_t kbytes = (uint32_t)A.K * (uint32_t)sizeof(S), abytes = (uint32_t)(A.as * sizeof(S)),
-                   bbytes = (uint32_t)(A.bs * sizeof(S));
-    const int nk = (int)((kbytes + 127) / 128);
+    const uint32_t kbytes = (uint32_t)A.K * ES, abytes = (uint32_t)(A.as * ES), bbytes = (uint32_t)(A.bs * ES);
+    const int nk = (A.K + RA::KROWS - 1) / RA::KROWS;
 
     auto rows_at = [&](const void *p, int64_t first, int64_t rows, int64_t most, uint32_t step) {
         const int64_t n = rows - first < most ? rows - first : most;
         return make_rsrc((const char *)p + (n > 0 ? first : 0) * (int64_t)step, n > 0 ? (uint32_t)(n - 1) * step + kbytes : 0u);
     };
-    // Regions 0, 1: the first and second 64 of each 128 rows of a; 2, 3: the halves of b.
-    const __amdgpu_buffer_rsrc_t rs[4] = {rows_at(A.a, m0, A.M, 192, abytes), rows_at(A.a, m0 + 64, A.M, 192, abytes),
-                                          rows_at(A.b0, n0, A.N, BH, bbytes),
-                                          rows_at(PLAIN ? A.b0 : A.b1, n0 + (PLAIN ? BH : 0), A.N, BH, bbytes)};
+    // Regions 0, 1: the first and second 64 of each 128 of a; 2, 3: the halves of b.
+    __amdgpu_buffer_rsrc_t rs[4];
+    if constexpr (!AM) rs[0] = rows_at(A.a, m0, A.M, 192, abytes), rs[1] = rows_at(A.a, m0 + 64, A.M, 192, abytes);
+    if constexpr (!BMM) {
+        rs[2] = rows_at(A.b0, n0, A.N, BH, bbytes);
+        rs[3] = rows_at(PLAIN ? A.b0 : A.b1, n0 + (PLAIN ? BH : 0), A.N, BH, bbytes);
+    }
 
-    // Load j of this wavefront: rows 16 wave + 8 j + lane / 8 of a region.
-    uint32_t off[2][2];  // [of a, of b][j]
-    int chunk[2];
+    // Load j of this wavefront is load 2 wave + j of a region.
+    uint32_t off[4][2];  // rows of k: the same for both regions of an operand
+    uint32_t chunk[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        chunk[j] = (lane & 7) ^ (4 * j + (lane >> 4));
-        const int row = 16 * wave + 8 * j + (lane >> 3);
-        off[0][j] = (uint32_t)((row >> 6) * 128 + (row & 63)) * abytes + chunk[j] * 16;
-        off[1][j] = (uint32_t)row * bbytes + chunk[j] * 16;
+        const int q = 2 * wave + j;
+        chunk[j] = (uint32_t)FfnRegion<S, false, 128>::load_chunk(q, lane) * 16;
+        const int ra = RA::load_row(q, lane), ca = RA::load_chunk(q, lane) * V;
+        const int rb = RB::load_row(q, lane), cb = RB::load_chunk(q, lane) * V;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (AM) {
+                const int col = (ca >> 6) * 128 + (ca & 63) + 64 * h;
+                off[h][j] = m0 + col < A.M ? (uint32_t)ra * abytes + col * ES : kOutOfRange;
+            } else {
+                off[h][j] = (uint32_t)((ra >> 6) * 128 + (ra & 63)) * abytes + ca * ES;
+            }
+            if constexpr (BMM) {
+                const int col = cb + 128 * h;
+                off[2 + h][j] = n0 + col < A.N ? (uint32_t)rb * bbytes + col * ES : kOutOfRange;
+            } else {
+                off[2 + h][j] = (uint32_t)rb * bbytes + cb * ES;
+            }
+        }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
-    auto issue = [&](int region, int kt) {
+    auto issue = [&](auto region_c, int kt) {
+        constexpr int region = decltype(region_c)::value;
         const uint32_t at = (uint32_t)kt * 128, dst = lds0 + (kt & 1) * STAGE + region * REGION + wave * 2048;
+        if constexpr (region < 2 ? AM : BMM) {
+            __amdgpu_buffer_rsrc_t r;
+            if constexpr (region < 2) {
+                const char *p = (const char *)A.a + m0 * ES + (int64_t)kt * RA::KROWS * abytes;
+                r = ffn_rows_of_m<S>(p, A.K - kt * RA::KROWS, abytes, (int)min(A.M - m0, (int64_t)BM));
+            } else {
+                const FfnTileAt b = ffn_tile_of_b<S>(A, kt);
+                r = ffn_rows_of_m<S>(b.p + (int64_t)n0 * ES, kt < nk ? b.left : 0, bbytes, A.N - n0 < BN ? A.N - n0 : BN);
+            }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            lds_dma16(rs[region], at + chunk[j] * 16 < kbytes ? off[region >> 1][j] + at : kOutOfRange, dst + j * 1024);
+            for (int j = 0; j < 2; ++j) lds_dma16(r, off[region][j], dst + j * 1024);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                lds_dma16(rs[region], at + chunk[j] < kbytes ? off[region][j] + at : kOutOfRange, dst + j * 1024);
+        }
     };
+    constexpr std::integral_constant<int, 0> A0;
+    constexpr std::integral_constant<int, 1> A1;
+    constexpr std::integral_constant<int, 2> B0;
+    constexpr std::integral_constant<int, 3> B1;
 
     const int wm = wave >> 2, wn = wave & 3;
     f32x4_t acc[2][2][4][2] = {};  // [half of a][half of b][tile of a][tile of b]
     uint4 fa[4][2], fb[2][2][2];
-    // Fragments of a region's rows r0 + 16 t + lane % 16.
-    auto frag = [&](int stage, int region, int r0, int t, int j) {
-        return *(const uint4 *)(lds + stage * STAGE + region * REGION + (r0 + 16 * t + (lane & 15)) * 128 +
-                                ((j * 4 + (lane >> 4)) ^ ((lane & 15) >> 1)) * 16);
-    };
-    auto read_a = [&](int stage, int h) {
+    FfnFragments<S, AM, 128, 4> pa;
+    FfnFragments<S, BMM, 128, 2> pb;
+    pa.init(lds0, wm * 64, lane);
+    pb.init(lds0 + 2 * REGION, wn * 32, lane);
+    uint32_t stage = 0;
+    auto read_a = [&](int h) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fa[t][j] = frag(stage, h, wm * 64, t, j);
+            for (int j = 0; j < 2; ++j) fa[t][j] = pa.get(t, j, stage + h * REGION);
     };
-    auto read_b = [&](int stage, int h) {
+    auto read_b = [&](int h) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[h][t][j] = frag(stage, 2 + h, wn * 32, t, j);
+            for (int j = 0; j < 2; ++j) fb[h][t][j] = pb.get(t, j, stage + h * REGION);
     };
     auto multiply = [&](int ha, int hb) {
         // This wavefront's reads have come, and all but its last ten loads.
@@ -329,103 +533,103 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
 #pragma unroll
             for (int f = 0; f < 2; ++f) ffn_mma<S>(fb[hb][f], fa[t], acc[ha][hb][t][f]);
+            if constexpr (ES == 4) __builtin_amdgcn_sched_barrier(0);  // (else the tiles' own sums are kept side by side, and spill)
+        }
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         block_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto tile = [&](int kt, int stage) {
-        read_a(stage, 0);
-        read_b(stage, 0);
-        issue(1, kt + 1);
-        multiply(0, 0);
-        read_b(stage, 1);
-        issue(0, kt + 2);
-        multiply(0, 1);
-        read_a(stage, 1);
-        issue(2, kt + 2);
-        multiply(1, 1);
-        issue(3, kt + 2);
-        multiply(1, 0);
-    };
 
-    issue(0, 0);
-    issue(2, 0);
-    issue(3, 0);
-    issue(1, 0);
-    issue(0, 1);
-    issue(2, 1);
-    issue(3, 1);
+    issue(A0, 0);
+    issue(B0, 0);
+    issue(B1, 0);
+    issue(A1, 0);
+    issue(A0, 1);
+    issue(B0, 1);
+    issue(B1, 1);
     CONVLOWER_WAIT_VMCNT(10);
     block_barrier();
     if (wave >= 4) block_barrier();
-    // (an odd number of tiles ends with one of zeros)
-    for (int kt = 0; kt < nk; kt += 2) {
-        tile(kt, 0);
-        tile(kt + 1, 1);
+#pragma nounroll
+    for (int kt = 0; kt < nk; ++kt) {
+        read_a(0);
+        read_b(0);
+        issue(A1, kt + 1);
+        multiply(0, 0);
+        read_b(1);
+        issue(A0, kt + 2);
+        multiply(0, 1);
+        read_a(1);
+        issue(B0, kt + 2);
+        multiply(1, 1);
+        issue(B1, kt + 2);
+        multiply(1, 0);
+        stage ^= STAGE;
     }
     if (wave < 4) block_barrier();
     CONVLOWER_WAIT_VMCNT(0);  // no load may still write LDS when the block ends
 
+    auto results = [&](auto act) {
 #pragma unroll
-    for (int ha = 0; ha < 2; ++ha)
+        for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int64_t m = m0 + wm * 128 + ha * 64 + 16 * t + (lane & 15);
-            if (m >= A.M) continue;
+            for (int t = 0; t < 4; ++t) {
+                const int64_t m = m0 + wm * 128 + ha * 64 + 16 * t + (lane & 15);
+                if (m >= A.M) continue;
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int n = n0 + wn * 32 + 16 * f + 4 * (lane >> 4);
-                if constexpr (PLAIN) {
-                    if (n < A.N) ffn_plain_out<O>(A, m, n, acc[ha][0][t][f]);
-                    if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[ha][1][t][f]);
-                } else if (n < A.N) {
-                    ffn_gated_out<O, EPI>(A, m, n, acc[ha][0][t][f], acc[ha][1][t][f]);
+                for (int f = 0; f < 2; ++f) {
+                    const int n = n0 + wn * 32 + 16 * f + 4 * (lane >> 4);
+                    if constexpr (PLAIN) {
+                        if (n < A.N) ffn_plain_out<O>(A, m, n, acc[ha][0][t][f]);
+                        if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[ha][1][t][f]);
+                    } else if (n < A.N) {
+                        ffn_gated_out<O, EPI, decltype(act)::value>(A, m, n, acc[ha][0][t][f], acc[ha][1][t][f]);
+                    }
                 }
             }
-        }
+    };
+    if constexpr (PLAIN) results(0);
+    else ffn_with_act(A.act, results);
 }
-template <typename S, typename O, FfnEpilogue EPI>
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
 __global__ __launch_bounds__(512) void ffn_large_kernel(FfnGemmArgs A) {
-    ffn_large_body<S, O, EPI>(A);
+    ffn_large_body<S, O, EPI, AM, BMM>(A);
 }
 
 // ---- launches
-template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY>
+template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY, bool AM, bool BMM>
 hipError_t ffn_run_small(const FfnGemmArgs &a, hipStream_t st) {
     constexpr int BN = EPI == FFN_PLAIN ? 2 * BH : BH;
     const int64_t blocks = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
     if (!grid_fits(blocks, 256, 1)) return kTooLarge;
-    hipLaunchKernelGGL((ffn_small_kernel<S, O, EPI, BM, BH, ANY>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((ffn_small_kernel<S, O, EPI, BM, BH, ANY, AM, BMM>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     return hipGetLastError();
 }
-template <typename S, typename O, FfnEpilogue EPI>
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
 hipError_t ffn_run_large(const FfnGemmArgs &a, hipStream_t st) {
     constexpr int BN = EPI == FFN_PLAIN ? 256 : 128;
     const int64_t blocks = ((a.M + 255) / 256) * ((a.N + BN - 1) / BN);
     if (!grid_fits(blocks, 512, 1)) return kTooLarge;
-    hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI>), dim3((unsigned)blocks), dim3(512), 0, st, a);
+    hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI, AM, BMM>), dim3((unsigned)blocks), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
-template <typename S, typename O, FfnEpilogue EPI>
+// AM, BMM: a, b as rows of m (of columns that are there: M and N values wide).
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
 hipError_t ffn_run(const FfnGemmArgs &a, hipStream_t st) {
-    bool vec = a.K % (16 / (int)sizeof(S)) == 0 && a.as * sizeof(S) % 16 == 0 && a.bs * sizeof(S) % 16 == 0;
+    constexpr int V = 16 / (int)sizeof(S), BN = EPI == FFN_PLAIN ? 2 : 1;
+    bool vec = (AM && BMM ? 0 : a.K) % V == 0 && (AM ? a.M : 0) % V == 0 && (BMM ? a.N : 0) % V == 0 && a.as % V == 0 && a.bs % V == 0;
     for (const void *p : {a.a, a.b0, a.b1}) vec = vec && (uintptr_t)p % 16 == 0;
-    constexpr int BN = EPI == FFN_PLAIN ? 2 : 1;
-    if (vec) {
-        const int64_t large = ((a.M + 255) / 256) * ((a.N + 128 * BN - 1) / (128 * BN));
-        if (large >= 192) return ffn_run_large<S, O, EPI>(a, st);
-        const int64_t mid = ((a.M + 127) / 128) * ((a.N + 64 * BN - 1) / (64 * BN));
-        if (mid >= 256) return ffn_run_small<S, O, EPI, 128, 64, false>(a, st);
-        return ffn_run_small<S, O, EPI, 64, 32, false>(a, st);
-    }
-    // (the backward pass lays its operands out aligned)
-    if constexpr (EPI == FFN_PLAIN) return hipErrorInvalidValue;
-    else return ffn_run_small<S, O, EPI, 64, 32, true>(a, st);
+    if (!vec) return ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
+    const int64_t large = ((a.M + 255) / 256) * ((a.N + 128 * BN - 1) / (128 * BN));
+    if (large >= 192) return ffn_run_large<S, O, EPI, AM, BMM>(a, st);
+    const int64_t mid = ((a.M + 127) / 128) * ((a.N + 64 * BN - 1) / (64 * BN));
+    if (mid >= 256) return ffn_run_small<S, O, EPI, 128, 64, false, AM, BMM>(a, st);
+    return ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
 }
 
 }  // namespace

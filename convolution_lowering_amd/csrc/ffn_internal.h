@@ -51,43 +51,43 @@ struct __attribute__((packed, aligned(sizeof(S)))) FfnAnyVec {
     S v[V];
 };
 
-// ---- products of rows: out[m][n] = sum_k a[m][k] b[n][k], both k-contiguous
+// ---- products: out[m][n] = sum_k a[m][k] b[n][k] (ffn_gemm.h)
 enum FfnEpilogue {
     FFN_GATED,   // h = act(a b0') * (a b1')
     FFN_SAVING,  // ... and both products, fp32
     FFN_SCALED,  // ... each times its row's and its column's factor (8-bit operands)
-    FFN_PLAIN,   // out = a b0', rows from `split` on to out2
+    FFN_PLAIN,   // out = a b0'
 };
 struct FfnGemmArgs {
     const void *a, *b0, *b1;
-    int64_t as, bs;  // row strides, elements
+    int64_t as, bs;  // strides of rows of k or of rows of m, elements
     int64_t M;
     int N, K;  // columns (of each of b0, b1), products summed
+    // b as rows of m: `brows` of them in b0, and from K tile `ktsplit` on in b1
+    int ktsplit, brows;
     int act;
-    void *out, *out2;  // [M][N]
-    int64_t split;
+    // plain: row m < rows of out, row m - split < rows of out2; other rows go nowhere
+    void *out, *out2;  // [..][N]
+    int64_t split, rows;
     float *saved;  // [2][M][pitch]
     int64_t pitch;
     const float *a_scale, *b0_scale, *b1_scale;
 };
 hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int out_dtype, hipStream_t st);
-hipError_t launch_ffn_plain(const FfnGemmArgs &a, int dtype, hipStream_t st);
+hipError_t launch_ffn_dx(const FfnGemmArgs &a, int dtype, hipStream_t st);  // a: rows of k, b: rows of m
+hipError_t launch_ffn_dw(const FfnGemmArgs &a, int dtype, hipStream_t st);  // both: rows of m
 
-// What the backward pass lays out in its workspace: rows of K are whole pieces
-// of 128 bytes, zeros behind the last value.
-struct FfnBack {
-    const void *dh, *x, *w_gate, *w_up;
-    int64_t dhs, xs;
+// The gradients of g and u, [T][2][Fp], zeros from F to Fp.
+struct FfnGateGrad {
+    const void *dh;
+    int64_t dhs;
     const float *saved;
     int64_t pitch;
-    void *dgu;   // [T][2][Fp]: gradients of g and of u
-    void *dguT;  // [2][F][Tp]
-    void *xT;    // [D][Tp]
-    void *wT;    // [D][2][Fp]
-    int64_t T, Tp;
-    int D, F, Fp, act;
+    void *dgu;
+    int64_t T;
+    int F, Fp, act;
 };
-hipError_t launch_ffn_back_prep(const FfnBack &a, int dtype, hipStream_t st);
+hipError_t launch_ffn_gate_grad(const FfnGateGrad &a, int dtype, hipStream_t st);
 
 struct W4Args {
     const void *x;
