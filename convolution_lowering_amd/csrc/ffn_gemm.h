@@ -55,7 +55,8 @@ __device__ __forceinline__ void ffn_mma(const uint4 (&b)[2], const uint4 (&a)[2]
 // 16 bytes at an address in LDS.
 __device__ __forceinline__ uint4 lds_at(uint32_t at) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) u32x4 *)at);
+    const u32x4 v = *(const __attribute__((address_space(3))) u32x4 *)at;
+    return __builtin_bit_cast(uint4, v);
 }
 
 // A region of W rows of k, or of W columns of rows of m (MM).
@@ -100,6 +101,16 @@ struct FfnFragments {
             for (int i = 0; i < NT; ++i)
                 at[i] = region + 4 * g * R::PITCH + ((((first >> 2) + 4 * i) ^ (4 * g)) + (t >> 2)) * 16 + (t & 3) * 4;
         }
+    }
+    // The same `by` times 64 KB on.  A read's constant offset reaches that far, and
+    // what lies further would cost the compiler one register a fragment; behind
+    // the asm these addresses are registers of their own (with known alignment).
+    __device__ __forceinline__ FfnFragments moved(uint32_t by) const {
+        FfnFragments f = *this;
+        asm("" : "+v"(by));
+#pragma unroll
+        for (int i = 0; i < (MM ? NT : 2); ++i) f.at[i] += by << 16;
+        return f;
     }
     // Chunk j of tile i; add: the stage, or another region like this one.
     __device__ __forceinline__ uint4 get(int i, int j, uint32_t add) const {
@@ -417,13 +428,16 @@ __global__ __launch_bounds__(256) void ffn_small_kernel(FfnGemmArgs A) {
 // reads LDS and issues loads, with a barrier at each change, so that a SIMD's
 // matrix core always has a wavefront whose operands are in registers.
 //
-// A wavefront goes through a K tile in four phases, (A0, B0), (A0, B1), (A1, B1),
-// (A1, B0): A0, A1 are the halves of its part of a, B0 and B1 its parts of the
-// halves of b.  Each of the four is 16 KB of a stage, its own region; there are
-// two stages, and a region takes the tile after next as soon as both groups
-// have read it.  Two 1 KB loads of each phase and wavefront fill one region, in
-// the order in which they are read, five phases ahead: the wait at the end of a
-// phase's reads leaves ten loads under way.
+// A wavefront goes through a K tile in four phases, (A0, F), (A0, L), (A1, L),
+// (A1, F): A0, A1 are the halves of its part of a; F and L, the first and the
+// last, its parts of b's halves, B0 and B1 in even tiles, B1 and B0 in odd ones. The
+// next tile's F is then this tile's L, whose registers are free one phase early,
+// and each phase reads one region: L and A1 for the next phase of the tile, F and
+// A0 for the next tile's.  Each region is 16 KB of a stage; there are two stages,
+// and a region takes the tile after next as soon as both groups have read it. Two
+// 1 KB loads of each phase and wavefront fill one region, in the order in which
+// they are read, seven phases ahead: the wait at the end of a phase's reads
+// leaves twelve loads under way.
 template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
 __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
     constexpr int BM = 256, BH = 128, ES = (int)sizeof(S), V = 16 / ES;
@@ -481,7 +495,7 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
         }
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
-    auto issue = [&](auto region_c, int kt) {
+    auto issue = [&](auto region_c, int kt) {  // tiles past the end read as zeros
         constexpr int region = decltype(region_c)::value;
         const uint32_t at = (uint32_t)kt * 128, dst = lds0 + (kt & 1) * STAGE + region * REGION + wave * 2048;
         if constexpr (region < 2 ? AM : BMM) {
@@ -501,34 +515,30 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
                 lds_dma16(rs[region], at + chunk[j] < kbytes ? off[region][j] + at : kOutOfRange, dst + j * 1024);
         }
     };
-    constexpr std::integral_constant<int, 0> A0;
-    constexpr std::integral_constant<int, 1> A1;
-    constexpr std::integral_constant<int, 2> B0;
-    constexpr std::integral_constant<int, 3> B1;
-
     const int wm = wave >> 2, wn = wave & 3;
     f32x4_t acc[2][2][4][2] = {};  // [half of a][half of b][tile of a][tile of b]
     uint4 fa[4][2], fb[2][2][2];
-    FfnFragments<S, AM, 128, 4> pa;
-    FfnFragments<S, BMM, 128, 2> pb;
-    pa.init(lds0, wm * 64, lane);
-    pb.init(lds0 + 2 * REGION, wn * 32, lane);
-    uint32_t stage = 0;
-    auto read_a = [&](int h) {
+    FfnFragments<S, AM, 128, 4> pa[2];
+    FfnFragments<S, BMM, 128, 2> pb[2];
+    pa[0].init(lds0, wm * 64, lane);
+    pb[0].init(lds0 + 2 * REGION, wn * 32, lane);
+    pa[1] = pa[0].moved(STAGE >> 16);
+    pb[1] = pb[0].moved(STAGE >> 16);
+    auto read_a = [&](int h, int stage) {
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fa[t][j] = pa.get(t, j, stage + h * REGION);
+            for (int j = 0; j < 2; ++j) fa[t][j] = pa[stage].get(t, j, h * REGION);
     };
-    auto read_b = [&](int h) {
+    auto read_b = [&](int h, int stage) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[h][t][j] = pb.get(t, j, stage + h * REGION);
+            for (int j = 0; j < 2; ++j) fb[h][t][j] = pb[stage].get(t, j, h * REGION);
     };
     auto multiply = [&](int ha, int hb) {
-        // This wavefront's reads have come, and all but its last ten loads.
-        CONVLOWER_WAIT_VMCNT_LDS(10);
+        // This wavefront's reads have come, and all but its last twelve loads.
+        CONVLOWER_WAIT_VMCNT_LDS(12);
         block_barrier();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
@@ -543,33 +553,45 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
         block_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
+    auto tile = [&](int kt, auto odd) {
+        constexpr int F = decltype(odd)::value, L = 1 - F;
+        read_a(0, F);
+        issue(std::integral_constant<int, 2 + F>(), kt + 2);
+        multiply(0, F);
+        read_b(L, F);
+        issue(std::integral_constant<int, 0>(), kt + 2);
+        multiply(0, L);
+        read_a(1, F);
+        issue(std::integral_constant<int, 2 + L>(), kt + 2);
+        multiply(1, L);
+        read_b(L, L);
+        issue(std::integral_constant<int, 1>(), kt + 2);
+        multiply(1, F);
+    };
+    constexpr std::integral_constant<int, 0> even;
+    constexpr std::integral_constant<int, 1> odd;
 
-    issue(A0, 0);
-    issue(B0, 0);
-    issue(B1, 0);
-    issue(A1, 0);
-    issue(A0, 1);
-    issue(B0, 1);
-    issue(B1, 1);
-    CONVLOWER_WAIT_VMCNT(10);
+    issue(std::integral_constant<int, 2>(), 0);
+    issue(std::integral_constant<int, 0>(), 0);
+    issue(std::integral_constant<int, 3>(), 0);
+    issue(std::integral_constant<int, 1>(), 0);
+    issue(std::integral_constant<int, 3>(), 1);
+    issue(std::integral_constant<int, 0>(), 1);
+    issue(std::integral_constant<int, 2>(), 1);
+    issue(std::integral_constant<int, 1>(), 1);
+    CONVLOWER_WAIT_VMCNT(14);
+    block_barrier();
+    read_b(0, 0);
+    CONVLOWER_WAIT_VMCNT_LDS(12);
     block_barrier();
     if (wave >= 4) block_barrier();
+    int kt = 0;
 #pragma nounroll
-    for (int kt = 0; kt < nk; ++kt) {
-        read_a(0);
-        read_b(0);
-        issue(A1, kt + 1);
-        multiply(0, 0);
-        read_b(1);
-        issue(A0, kt + 2);
-        multiply(0, 1);
-        read_a(1);
-        issue(B0, kt + 2);
-        multiply(1, 1);
-        issue(B1, kt + 2);
-        multiply(1, 0);
-        stage ^= STAGE;
+    for (; kt + 1 < nk; kt += 2) {
+        tile(kt, even);
+        tile(kt + 1, odd);
     }
+    if (kt < nk) tile(kt, even);
     if (wave < 4) block_barrier();
     CONVLOWER_WAIT_VMCNT(0);  // no load may still write LDS when the block ends
 
@@ -626,7 +648,8 @@ hipError_t ffn_run(const FfnGemmArgs &a, hipStream_t st) {
     for (const void *p : {a.a, a.b0, a.b1}) vec = vec && (uintptr_t)p % 16 == 0;
     if (!vec) return ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
     const int64_t large = ((a.M + 255) / 256) * ((a.N + 128 * BN - 1) / (128 * BN));
-    if (large >= 192) return ffn_run_large<S, O, EPI, AM, BMM>(a, st);
+    if constexpr (sizeof(S) < 4 || !BMM)
+        if (large >= 192) return ffn_run_large<S, O, EPI, AM, BMM>(a, st);
     const int64_t mid = ((a.M + 127) / 128) * ((a.N + 64 * BN - 1) / (64 * BN));
     if (mid >= 256) return ffn_run_small<S, O, EPI, 128, 64, false, AM, BMM>(a, st);
     return ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
