@@ -52,6 +52,17 @@ __device__ __forceinline__ void ffn_mma(const uint4 (&b)[2], const uint4 (&a)[2]
     }
 }
 
+// lds_dma16 (igemm_dma.h) of rows that begin `at` bytes further on.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void ffn_dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t at, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(lds_base)), "s"(__builtin_amdgcn_readfirstlane(at))
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // 16 bytes at an address in LDS.
 __device__ __forceinline__ uint4 lds_at(uint32_t at) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -102,14 +113,14 @@ struct FfnFragments {
                 at[i] = region + 4 * g * R::PITCH + ((((first >> 2) + 4 * i) ^ (4 * g)) + (t >> 2)) * 16 + (t & 3) * 4;
         }
     }
-    // The same `by` times 64 KB on.  A read's constant offset reaches that far, and
-    // what lies further would cost the compiler one register a fragment; behind
-    // the asm these addresses are registers of their own (with known alignment).
+    // The same `by` times 4 KB on.  A read's constant offset reaches 64 KB, and what
+    // lies further would cost the compiler one register a fragment; behind the
+    // asm these addresses are registers of their own (with known alignment).
     __device__ __forceinline__ FfnFragments moved(uint32_t by) const {
         FfnFragments f = *this;
         asm("" : "+v"(by));
 #pragma unroll
-        for (int i = 0; i < (MM ? NT : 2); ++i) f.at[i] += by << 16;
+        for (int i = 0; i < (MM ? NT : 2); ++i) f.at[i] += by << 12;
         return f;
     }
     // Chunk j of tile i; add: the stage, or another region like this one.
@@ -198,24 +209,30 @@ __device__ __forceinline__ void ffn_plain_out(const FfnGemmArgs &A, int64_t m, i
     if (row < A.rows) ffn_put4((O *)(second ? A.out2 : A.out) + row * A.N, n, A.N, v);
 }
 
-// Where tile kt of b's rows of m lies: `rows` of them in b0, then as many in b1
-// from tile `ktsplit` on.
-struct FfnTileAt {
-    const char *p;
-    int left;  // rows there are from here on
+// The K tiles of an operand of rows of m, one after another: `rows` of them from
+// p0 and, from tile `split` on, as many from p1, `width` bytes of each.
+template <typename S>
+struct FfnRowsOfM {
+    static constexpr int KROWS = 128 / (int)sizeof(S);
+    const char *p, *p1;
+    uint32_t step, behind;  // behind: what of a row is past its `width` bytes
+    int rows, left, until;  // left: rows from here on; until: tiles before p1's
+    __device__ __forceinline__ void init(const void *p0, const void *p1_, int64_t stride, int rows_, int64_t width, int split) {
+        p = (const char *)p0, p1 = (const char *)p1_, step = (uint32_t)(stride * (int64_t)sizeof(S));
+        behind = step - (uint32_t)(width * (int64_t)sizeof(S));
+        rows = left = rows_, until = split;
+    }
+    __device__ __forceinline__ void next() {
+        const bool other = --until == 0;
+        p = other ? p1 : p + (uint64_t)step * KROWS;
+        left = other ? rows : left - KROWS;
+    }
+    // The tile as a buffer: no bytes where no rows are left.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile() const {
+        const int n = left < KROWS ? left : KROWS;
+        return make_rsrc(p, n > 0 ? (uint32_t)n * step - behind : 0u);
+    }
 };
-template <typename S>
-__device__ __forceinline__ FfnTileAt ffn_tile_of_b(const FfnGemmArgs &A, int kt) {
-    const int k = kt < A.ktsplit ? kt : kt - A.ktsplit, krows = 128 / (int)sizeof(S);
-    return {(const char *)(kt < A.ktsplit ? A.b0 : A.b1) + (int64_t)k * krows * A.bs * (int64_t)sizeof(S), A.brows - k * krows};
-}
-// `cols` values of each of a tile's rows of m, as a buffer.
-template <typename S>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t ffn_rows_of_m(const char *p, int left, uint32_t step, int cols) {
-    constexpr int KROWS = 128 / (int)sizeof(S);
-    const int n = left < KROWS ? left : KROWS;
-    return make_rsrc(n > 0 ? p : nullptr, n > 0 ? (uint32_t)(n - 1) * step + (uint32_t)cols * (uint32_t)sizeof(S) : 0u);
-}
 
 // ---- the loop for any size: four wavefronts, 2 x 2, over BM of a's m and BH of
 // each of b0 and b1 (or 2 BH of b0 alone).  Chunks at multiples of 16 bytes are
@@ -244,6 +261,9 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
     const int nk = (A.K + RA::KROWS - 1) / RA::KROWS;
     const int am = (int)min((int64_t)BM, A.M - m0);  // a's m that are there
     const char *abase = (const char *)A.a + m0 * (AM ? ES : A.as * ES);
+    FfnRowsOfM<S> ma, mb;
+    if constexpr (AM) ma.init(abase, nullptr, A.as, A.K, A.M - m0, INT32_MAX);
+    if constexpr (BMM) mb.init((const char *)A.b0 + (int64_t)n0 * ES, (const char *)A.b1 + (int64_t)n0 * ES, A.bs, A.brows, A.N - n0, A.ktsplit);
 
     // Load i of this wavefront is load 4 i + wave of its region.
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
@@ -302,20 +322,17 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
             const uint32_t at = (uint32_t)kt * 128;
             const bool in = at + chunk < kbytes;
             const uint32_t dst = lds0 + stage + wave * 1024;
-            __amdgpu_buffer_rsrc_t ma, mb;
-            if constexpr (AM) ma = ffn_rows_of_m<S>(abase + (int64_t)kt * RA::KROWS * abytes, A.K - kt * RA::KROWS, abytes, (int)(A.M - m0));
-            if constexpr (BMM) {
-                const FfnTileAt b = ffn_tile_of_b<S>(A, kt);
-                mb = ffn_rows_of_m<S>(b.p + (int64_t)n0 * ES, kt < nk ? b.left : 0, bbytes, A.N - n0);
-            }
+            __amdgpu_buffer_rsrc_t ta, tb;
+            if constexpr (AM) ta = ma.tile(), ma.next();
+            if constexpr (BMM) tb = mb.tile(), mb.next();
 #pragma unroll
             for (int i = 0; i < IPW; ++i) {
                 if (i < IA) {
-                    if constexpr (AM) lds_dma16(ma, off[i], dst + i * 4096);
-                    else lds_dma16(ka, in ? off[i] + at : kOutOfRange, dst + i * 4096);
+                    if constexpr (AM) lds_dma16(ta, off[i], dst + i * 4096);
+                    else ffn_dma16(ka, in ? off[i] : kOutOfRange, at, dst + i * 4096);
                 } else {
-                    if constexpr (BMM) lds_dma16(mb, off[i], dst + i * 4096);
-                    else lds_dma16(i - IA < BH / 32 ? kg : ku, in ? off[i] + at : kOutOfRange, dst + i * 4096);
+                    if constexpr (BMM) lds_dma16(tb, off[i], dst + i * 4096);
+                    else ffn_dma16(i - IA < BH / 32 ? kg : ku, in ? off[i] : kOutOfRange, at, dst + i * 4096);
                 }
             }
         };
@@ -362,13 +379,8 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
                 const int first = (of_a ? RA::load_chunk(q, lane) : RB::load_chunk(q, lane)) * V;
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (of_a ? AM : BMM) {
-                    const char *p = abase + (int64_t)kt * RA::KROWS * abytes;
-                    int left = A.K - kt * RA::KROWS, cols = am;
-                    if (!of_a) {
-                        const FfnTileAt b = ffn_tile_of_b<S>(A, kt);
-                        p = b.p + (int64_t)n0 * ES, left = b.left, cols = A.N - n0;
-                    }
-                    if (row < left) v = values(p + (int64_t)row * (of_a ? abytes : bbytes), first, cols);
+                    const FfnRowsOfM<S> &m = of_a ? ma : mb;
+                    if (row < m.left) v = values(m.p + (int64_t)row * m.step, first, of_a ? am : A.N - n0);
                 } else {
                     const bool up = !of_a && !PLAIN && row >= BH;
                     const int64_t r = of_a ? m0 + row : n0 + (up ? row - BH : row);
@@ -377,6 +389,8 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
                 }
                 reg[i] = v;
             }
+            if constexpr (AM) ma.next();
+            if constexpr (BMM) mb.next();
         };
         auto keep = [&](uint32_t stage) {
 #pragma unroll
@@ -422,30 +436,37 @@ __global__ __launch_bounds__(256) void ffn_small_kernel(FfnGemmArgs A) {
     ffn_small_body<S, O, EPI, BM, BH, ANY, AM, BMM>(A);
 }
 
-// ---- the large tile: 256 of a's m by 128 of each half of b, one block of
-// eight wavefronts on a CU, two on each SIMD, each with 128 x (32 + 32) of the
-// tile.  Wavefronts 0-3 and 4-7 alternate: while one group multiplies, the other
-// reads LDS and issues loads, with a barrier at each change, so that a SIMD's
-// matrix core always has a wavefront whose operands are in registers.
+// ---- large tiles: one block of eight wavefronts on a CU, two on each SIMD, WM x 8 /
+// WM over 32 WM TA of a's m by 16 (8 / WM) TB of each half of b.  Wavefronts 0-3 and
+// 4-7 alternate: while one group multiplies, the other reads LDS and issues loads,
+// with a barrier at each change, so that a SIMD's matrix core always has a
+// wavefront whose operands are in registers.
 //
 // A wavefront goes through a K tile in four phases, (A0, F), (A0, L), (A1, L),
 // (A1, F): A0, A1 are the halves of its part of a; F and L, the first and the
 // last, its parts of b's halves, B0 and B1 in even tiles, B1 and B0 in odd ones. The
 // next tile's F is then this tile's L, whose registers are free one phase early,
 // and each phase reads one region: L and A1 for the next phase of the tile, F and
-// A0 for the next tile's.  Each region is 16 KB of a stage; there are two stages,
-// and a region takes the tile after next as soon as both groups have read it. Two
-// 1 KB loads of each phase and wavefront fill one region, in the order in which
-// they are read, seven phases ahead: the wait at the end of a phase's reads
-// leaves twelve loads under way.
-template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
+// A0 for the next tile's.  There are two stages, and a region takes the tile after
+// next as soon as both groups have read it.  Every wavefront's loads of a phase
+// fill one region, in the order in which they are read, seven phases ahead: the
+// wait at the end of a phase's reads leaves those of six under way.
+template <int WM_, int TA_, int TB_>
+struct FfnLarge {
+    static constexpr int WM = WM_, WN = 8 / WM_, TA = TA_, TB = TB_;
+    static constexpr int RA = WM * TA * 16, RB = WN * TB * 16;  // rows of a region
+    static constexpr int BM = 2 * RA, BH = RB;
+};
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM, typename C>
 __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
-    constexpr int BM = 256, BH = 128, ES = (int)sizeof(S), V = 16 / ES;
+    constexpr int BM = C::BM, BH = C::BH, TA = C::TA, TB = C::TB, ES = (int)sizeof(S), V = 16 / ES;
     constexpr bool PLAIN = EPI == FFN_PLAIN;
     static_assert(PLAIN || !BMM, "two matrices of rows of k, or one of either kind");
-    constexpr uint32_t REGION = 16384, STAGE = 4 * REGION;
-    using RA = FfnRegion<S, AM, 128>;
-    using RB = FfnRegion<S, BMM, 128>;
+    constexpr uint32_t SIZE_A = C::RA * 128, SIZE_B = C::RB * 128, STAGE = 2 * (SIZE_A + SIZE_B);
+    using RA = FfnRegion<S, AM, C::RA>;
+    using RB = FfnRegion<S, BMM, C::RB>;
+    constexpr int LA = RA::LOADS / 8, LB = RB::LOADS / 8;  // a wavefront's loads of a region
+    static_assert(LA * 8 == RA::LOADS && LB * 8 == RB::LOADS && STAGE % 4096 == 0, "regions split evenly");
     __shared__ alignas(16) char lds[2 * STAGE];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -461,91 +482,95 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
         const int64_t n = rows - first < most ? rows - first : most;
         return make_rsrc((const char *)p + (n > 0 ? first : 0) * (int64_t)step, n > 0 ? (uint32_t)(n - 1) * step + kbytes : 0u);
     };
-    // Regions 0, 1: the first and second 64 of each 128 of a; 2, 3: the halves of b.
+    // Regions 0, 1: the first and second half of each wavefront's part of a; 2, 3: the halves of b.
     __amdgpu_buffer_rsrc_t rs[4];
-    if constexpr (!AM) rs[0] = rows_at(A.a, m0, A.M, 192, abytes), rs[1] = rows_at(A.a, m0 + 64, A.M, 192, abytes);
+    constexpr int HA = TA * 16;  // a half
+    if constexpr (!AM) rs[0] = rows_at(A.a, m0, A.M, BM - HA, abytes), rs[1] = rows_at(A.a, m0 + HA, A.M, BM - HA, abytes);
     if constexpr (!BMM) {
         rs[2] = rows_at(A.b0, n0, A.N, BH, bbytes);
         rs[3] = rows_at(PLAIN ? A.b0 : A.b1, n0 + (PLAIN ? BH : 0), A.N, BH, bbytes);
     }
 
-    // Load j of this wavefront is load 2 wave + j of a region.
-    uint32_t off[4][2];  // rows of k: the same for both regions of an operand
-    uint32_t chunk[2];
+    // Load j of this wavefront is load LA wave + j, or LB wave + j, of a region.
+    uint32_t off_a[2][LA], off_b[2][LB];  // rows of k: the same for both regions of an operand
+    uint32_t chunk_a[LA], chunk_b[LB];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int q = 2 * wave + j;
-        chunk[j] = (uint32_t)FfnRegion<S, false, 128>::load_chunk(q, lane) * 16;
-        const int ra = RA::load_row(q, lane), ca = RA::load_chunk(q, lane) * V;
-        const int rb = RB::load_row(q, lane), cb = RB::load_chunk(q, lane) * V;
+    for (int j = 0; j < LA; ++j) {
+        const int q = LA * wave + j, row = RA::load_row(q, lane), c = RA::load_chunk(q, lane) * V;
+        chunk_a[j] = c * ES;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if constexpr (AM) {
-                const int col = (ca >> 6) * 128 + (ca & 63) + 64 * h;
-                off[h][j] = m0 + col < A.M ? (uint32_t)ra * abytes + col * ES : kOutOfRange;
-            } else {
-                off[h][j] = (uint32_t)((ra >> 6) * 128 + (ra & 63)) * abytes + ca * ES;
-            }
-            if constexpr (BMM) {
-                const int col = cb + 128 * h;
-                off[2 + h][j] = n0 + col < A.N ? (uint32_t)rb * bbytes + col * ES : kOutOfRange;
-            } else {
-                off[2 + h][j] = (uint32_t)rb * bbytes + cb * ES;
-            }
+            const int m = AM ? c : row, at = m / HA * 2 * HA + m % HA + (AM ? h * HA : 0);
+            if constexpr (AM) off_a[h][j] = m0 + at < A.M ? (uint32_t)row * abytes + at * ES : kOutOfRange;
+            else off_a[h][j] = (uint32_t)at * abytes + c * ES;
         }
     }
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+        const int q = LB * wave + j, row = RB::load_row(q, lane), c = RB::load_chunk(q, lane) * V;
+        chunk_b[j] = c * ES;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (BMM) off_b[h][j] = n0 + c + h * BH < A.N ? (uint32_t)row * bbytes + (c + h * BH) * ES : kOutOfRange;
+            else off_b[h][j] = (uint32_t)row * bbytes + c * ES;
+        }
+    }
+    FfnRowsOfM<S> ma, mb;
+    if constexpr (AM) ma.init((const char *)A.a + m0 * ES, nullptr, A.as, A.K, min(A.M - m0, (int64_t)BM), INT32_MAX);
+    if constexpr (BMM)
+        mb.init((const char *)A.b0 + (int64_t)n0 * ES, (const char *)A.b1 + (int64_t)n0 * ES, A.bs, A.brows, min(A.N - n0, BN), A.ktsplit);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
-    auto issue = [&](auto region_c, int kt) {  // tiles past the end read as zeros
-        constexpr int region = decltype(region_c)::value;
-        const uint32_t at = (uint32_t)kt * 128, dst = lds0 + (kt & 1) * STAGE + region * REGION + wave * 2048;
-        if constexpr (region < 2 ? AM : BMM) {
-            __amdgpu_buffer_rsrc_t r;
-            if constexpr (region < 2) {
-                const char *p = (const char *)A.a + m0 * ES + (int64_t)kt * RA::KROWS * abytes;
-                r = ffn_rows_of_m<S>(p, A.K - kt * RA::KROWS, abytes, (int)min(A.M - m0, (int64_t)BM));
-            } else {
-                const FfnTileAt b = ffn_tile_of_b<S>(A, kt);
-                r = ffn_rows_of_m<S>(b.p + (int64_t)n0 * ES, kt < nk ? b.left : 0, bbytes, A.N - n0 < BN ? A.N - n0 : BN);
-            }
+    auto issue = [&](auto region_c, auto stage_c, int kt) {  // tiles past the end read as zeros
+        constexpr int region = decltype(region_c)::value, h = region & 1;
+        constexpr bool of_a = region < 2;
+        const uint32_t at = (uint32_t)kt * 128,
+                       dst = lds0 + decltype(stage_c)::value * STAGE + (of_a ? h * SIZE_A : 2 * SIZE_A + h * SIZE_B) + wave * ((of_a ? LA : LB) * 1024);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) lds_dma16(r, off[region][j], dst + j * 1024);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                lds_dma16(rs[region], at + chunk[j] < kbytes ? off[region][j] + at : kOutOfRange, dst + j * 1024);
+        for (int j = 0; j < (of_a ? LA : LB); ++j) {
+            const uint32_t off = of_a ? off_a[h][j] : off_b[h][j];
+            if constexpr (of_a ? AM : BMM) lds_dma16(rs[region], off, dst + j * 1024);
+            else ffn_dma16(rs[region], at + (of_a ? chunk_a[j] : chunk_b[j]) < kbytes ? off : kOutOfRange, at, dst + j * 1024);
         }
     };
-    const int wm = wave >> 2, wn = wave & 3;
-    f32x4_t acc[2][2][4][2] = {};  // [half of a][half of b][tile of a][tile of b]
-    uint4 fa[4][2], fb[2][2][2];
-    FfnFragments<S, AM, 128, 4> pa[2];
-    FfnFragments<S, BMM, 128, 2> pb[2];
-    pa[0].init(lds0, wm * 64, lane);
-    pb[0].init(lds0 + 2 * REGION, wn * 32, lane);
-    pa[1] = pa[0].moved(STAGE >> 16);
-    pb[1] = pb[0].moved(STAGE >> 16);
+    // The next tile of an operand of rows of m.
+    auto turn_a = [&] {
+        if constexpr (AM) rs[0] = rs[1] = ma.tile(), ma.next();
+    };
+    auto turn_b = [&] {
+        if constexpr (BMM) rs[2] = rs[3] = mb.tile(), mb.next();
+    };
+
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    f32x4_t acc[2][2][TA][TB] = {};  // [half of a][half of b][tile of a][tile of b]
+    uint4 fa[TA][2], fb[2][TB][2];
+    FfnFragments<S, AM, C::RA, TA> pa[2];
+    FfnFragments<S, BMM, C::RB, TB> pb[2];
+    pa[0].init(lds0, wm * HA, lane);
+    pb[0].init(lds0 + 2 * SIZE_A, wn * TB * 16, lane);
+    pa[1] = pa[0].moved(STAGE / 4096);
+    pb[1] = pb[0].moved(STAGE / 4096);
     auto read_a = [&](int h, int stage) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < TA; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fa[t][j] = pa[stage].get(t, j, h * REGION);
+            for (int j = 0; j < 2; ++j) fa[t][j] = pa[stage].get(t, j, h * SIZE_A);
     };
     auto read_b = [&](int h, int stage) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < TB; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[h][t][j] = pb[stage].get(t, j, h * REGION);
+            for (int j = 0; j < 2; ++j) fb[h][t][j] = pb[stage].get(t, j, h * SIZE_B);
     };
     auto multiply = [&](int ha, int hb) {
-        // This wavefront's reads have come, and all but its last twelve loads.
-        CONVLOWER_WAIT_VMCNT_LDS(12);
+        // This wavefront's reads have come, and all but its loads of the last six phases.
+        CONVLOWER_WAIT_VMCNT_LDS(3 * (LA + LB));
         block_barrier();
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < TA; ++t) {
 #pragma unroll
-            for (int f = 0; f < 2; ++f) ffn_mma<S>(fb[hb][f], fa[t], acc[ha][hb][t][f]);
+            for (int f = 0; f < TB; ++f) ffn_mma<S>(fb[hb][f], fa[t], acc[ha][hb][t][f]);
             if constexpr (ES == 4) __builtin_amdgcn_sched_barrier(0);  // (else the tiles' own sums are kept side by side, and spill)
         }
         __builtin_amdgcn_s_setprio(0);
@@ -553,36 +578,46 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
         block_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    auto tile = [&](int kt, auto odd) {
-        constexpr int F = decltype(odd)::value, L = 1 - F;
-        read_a(0, F);
-        issue(std::integral_constant<int, 2 + F>(), kt + 2);
-        multiply(0, F);
-        read_b(L, F);
-        issue(std::integral_constant<int, 0>(), kt + 2);
-        multiply(0, L);
-        read_a(1, F);
-        issue(std::integral_constant<int, 2 + L>(), kt + 2);
-        multiply(1, L);
-        read_b(L, L);
-        issue(std::integral_constant<int, 1>(), kt + 2);
-        multiply(1, F);
-    };
     constexpr std::integral_constant<int, 0> even;
     constexpr std::integral_constant<int, 1> odd;
+    constexpr std::integral_constant<int, 0> A0;
+    constexpr std::integral_constant<int, 1> A1;
+    constexpr std::integral_constant<int, 2> B0;
+    constexpr std::integral_constant<int, 3> B1;
+    auto tile = [&](int kt, auto parity) {
+        constexpr int F = decltype(parity)::value, L = 1 - F;
+        read_a(0, F);
+        turn_b();
+        issue(std::integral_constant<int, 2 + F>(), parity, kt + 2);
+        multiply(0, F);
+        read_b(L, F);
+        turn_a();
+        issue(A0, parity, kt + 2);
+        multiply(0, L);
+        read_a(1, F);
+        issue(std::integral_constant<int, 2 + L>(), parity, kt + 2);
+        multiply(1, L);
+        read_b(L, L);
+        issue(A1, parity, kt + 2);
+        multiply(1, F);
+    };
 
-    issue(std::integral_constant<int, 2>(), 0);
-    issue(std::integral_constant<int, 0>(), 0);
-    issue(std::integral_constant<int, 3>(), 0);
-    issue(std::integral_constant<int, 1>(), 0);
-    issue(std::integral_constant<int, 3>(), 1);
-    issue(std::integral_constant<int, 0>(), 1);
-    issue(std::integral_constant<int, 2>(), 1);
-    issue(std::integral_constant<int, 1>(), 1);
-    CONVLOWER_WAIT_VMCNT(14);
+    turn_a();
+    turn_b();
+    issue(B0, even, 0);
+    issue(A0, even, 0);
+    issue(B1, even, 0);
+    issue(A1, even, 0);
+    turn_a();
+    turn_b();
+    issue(B1, odd, 1);
+    issue(A0, odd, 1);
+    issue(B0, odd, 1);
+    issue(A1, odd, 1);
+    CONVLOWER_WAIT_VMCNT(4 * LA + 3 * LB);
     block_barrier();
     read_b(0, 0);
-    CONVLOWER_WAIT_VMCNT_LDS(12);
+    CONVLOWER_WAIT_VMCNT_LDS(3 * (LA + LB));
     block_barrier();
     if (wave >= 4) block_barrier();
     int kt = 0;
@@ -599,12 +634,12 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
 #pragma unroll
         for (int ha = 0; ha < 2; ++ha)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int64_t m = m0 + wm * 128 + ha * 64 + 16 * t + (lane & 15);
+            for (int t = 0; t < TA; ++t) {
+                const int64_t m = m0 + (wm * 2 + ha) * HA + 16 * t + (lane & 15);
                 if (m >= A.M) continue;
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const int n = n0 + wn * 32 + 16 * f + 4 * (lane >> 4);
+                for (int f = 0; f < TB; ++f) {
+                    const int n = n0 + (wn * TB + f) * 16 + 4 * (lane >> 4);
                     if constexpr (PLAIN) {
                         if (n < A.N) ffn_plain_out<O>(A, m, n, acc[ha][0][t][f]);
                         if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[ha][1][t][f]);
@@ -617,10 +652,12 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
     if constexpr (PLAIN) results(0);
     else ffn_with_act(A.act, results);
 }
-template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM, typename C>
 __global__ __launch_bounds__(512) void ffn_large_kernel(FfnGemmArgs A) {
-    ffn_large_body<S, O, EPI, AM, BMM>(A);
+    ffn_large_body<S, O, EPI, AM, BMM, C>(A);
 }
+typedef FfnLarge<2, 4, 2> FfnTile256x128;  // 128 x (32 + 32) of a wavefront
+typedef FfnLarge<4, 2, 2> FfnTile256x64;   // 64 x (32 + 32)
 
 // ---- launches
 template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY, bool AM, bool BMM>
@@ -631,12 +668,12 @@ hipError_t ffn_run_small(const FfnGemmArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((ffn_small_kernel<S, O, EPI, BM, BH, ANY, AM, BMM>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     return hipGetLastError();
 }
-template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
+template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM, typename C>
 hipError_t ffn_run_large(const FfnGemmArgs &a, hipStream_t st) {
-    constexpr int BN = EPI == FFN_PLAIN ? 256 : 128;
-    const int64_t blocks = ((a.M + 255) / 256) * ((a.N + BN - 1) / BN);
+    constexpr int BN = EPI == FFN_PLAIN ? 2 * C::BH : C::BH;
+    const int64_t blocks = ((a.M + C::BM - 1) / C::BM) * ((a.N + BN - 1) / BN);
     if (!grid_fits(blocks, 512, 1)) return kTooLarge;
-    hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI, AM, BMM>), dim3((unsigned)blocks), dim3(512), 0, st, a);
+    hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI, AM, BMM, C>), dim3((unsigned)blocks), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
@@ -649,7 +686,7 @@ hipError_t ffn_run(const FfnGemmArgs &a, hipStream_t st) {
     if (!vec) return ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
     const int64_t large = ((a.M + 255) / 256) * ((a.N + 128 * BN - 1) / (128 * BN));
     if constexpr (sizeof(S) < 4 || !BMM)
-        if (large >= 192) return ffn_run_large<S, O, EPI, AM, BMM>(a, st);
+        if (large >= 192) return ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x128>(a, st);
     const int64_t mid = ((a.M + 127) / 128) * ((a.N + 64 * BN - 1) / (64 * BN));
     if (mid >= 256) return ffn_run_small<S, O, EPI, 128, 64, false, AM, BMM>(a, st);
     return ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
