@@ -1,5 +1,7 @@
 // The C ABI of include/convlower_ffn.h: argument checks and launches.  Every
 // check is on the host, before the first launch.
+#include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "ffn_internal.h"
@@ -33,12 +35,14 @@ conv_status_t ffn_sizes(int64_t T, int D, int F, ffn_act_t act, int64_t stride) 
 }
 int64_t saved_pitch(int F) { return (F + 3) / 4 * 4; }
 
-// The workspace of the backward pass: the gradients of g and u, rows of whole
-// 128-byte pieces.
+// The workspace of the backward pass holds the gradients of g and u, rows of whole
+// 128-byte pieces, and then the parts' sums of either product.
 int padded(int F, conv_dtype_t dtype) {
     const int piece = dtype == CONV_DTYPE_FP32 ? 32 : 64;
     return (F + piece - 1) / piece * piece;
 }
+
+size_t dgu_bytes(int64_t T, int F, conv_dtype_t dtype) { return (size_t)T * 2 * (size_t)padded(F, dtype) * bytes_of(dtype); }
 
 conv_status_t w4_check(const void *x, int64_t x_stride, const void *y, int64_t R, int D, int F, int group,
                        conv_dtype_t dtype) {
@@ -53,6 +57,45 @@ bool w4_weights_ok(const void *w, const void *scales, const void *zeros, conv_dt
 }
 
 }  // namespace
+
+// The time of a product is that of the blocks of one CU, one K tile after another.
+// A block's K tile of 128 bytes takes, in hundredths of a microsecond (bf16, all
+// CUs at work; 256 x 128 is the tile's rows of a by columns of each half of b):
+//   256 x 128  115, one block on a CU at a time;
+//   256 x 64    82;
+//   128 x 64    62, two at once 100;
+//   64 x 32     42, two 56, three 94.
+// (4096 to 10240 features, fwd: 200 tokens 74, 55, 66, 72 us in this order, 512: 80, 108,
+// 101, 149, 128: 71, 51, 46, 60; 2048 to 4096: 400 tokens 38, 28, 20, 29, 200: 37, 27, 19,
+// 16.)  float32 tiles take what their matrix instructions do, 16 times a 16-bit
+// tile's 16 cycles each.  A product that needs no second matrix (plain) may share
+// its K tiles out to several grids, whose float32 sums are written, read and added
+// by one more launch: 4 us and 8 bytes a value and grid at 4 TB/s.  (200 tokens, 4096
+// wide, 20480 summed: 135 us in one grid of 64 x 32, 42 in eight of 256 x 64.)
+FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec) {
+    static const struct {
+        int m, n;
+        double at[3];  // of one, two, three blocks on a CU
+        int most;
+    } kTiles[] = {{256, 128, {1.15}, 1}, {256, 64, {0.82}, 1}, {128, 64, {0.62, 1.00}, 2}, {64, 32, {0.42, 0.56, 0.94}, 3}};
+    const int per = 128 / value_bytes, nk = K ? (K - 1) / per + 1 : 1;
+    FfnPlan best{FFN_TILE_64x32, 1};
+    double least = 1e300;
+    for (int t = vec ? 0 : 3; t < 4; ++t) {
+        const int n = plain ? 2 * kTiles[t].n : kTiles[t].n;
+        const double blocks = (double)((M + kTiles[t].m - 1) / kTiles[t].m) * ((N + n - 1) / n);
+        for (int s = 1; s <= (plain ? 32 : 1) && (s == 1 || nk / s >= 4); ++s) {
+            const double on = std::ceil(blocks * s / 256);  // blocks of a CU
+            const int most = kTiles[t].most, rest = (int)std::fmod(on, most);
+            double tile = (on - rest) / most * kTiles[t].at[most - 1] + (rest ? kTiles[t].at[rest - 1] : 0.0);
+            if (value_bytes == 4) tile = on * kTiles[t].m * kTiles[t].n * 2 / 65536.0 * 7.2;
+            double us = tile * ((nk + s - 1) / s + 2);
+            if (s > 1) us += 4 + (double)s * M * ffn_part_pitch(N) * 8 / 4e6;
+            if (us < least) least = us, best = {t, s};
+        }
+    }
+    return best;
+}
 
 hipError_t launch_ffn_gated_f32(const FfnGemmArgs &a, bool saving, hipStream_t st);
 hipError_t launch_ffn_gated_bf16(const FfnGemmArgs &a, bool saving, hipStream_t st);
@@ -116,7 +159,14 @@ conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t
     if (!bytes_out || !ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
     const conv_status_t st = ffn_sizes(T, D, F, FFN_ACT_NONE, D);
     if (st != CONV_OK) return st;
-    *bytes_out = (size_t)T * 2 * (size_t)padded(F, dtype) * bytes_of(dtype);
+    const int es = (int)bytes_of(dtype), Fp = padded(F, dtype);
+    size_t part = 0;
+    for (int vec = 0; vec < 2; ++vec) {
+        const int dx = ffn_plan(T, D, 2 * Fp, es, true, vec).splits, dw = ffn_plan(2 * (int64_t)Fp, D, (int)T, es, true, vec).splits;
+        if (dx > 1) part = std::max(part, (size_t)dx * T * ffn_part_pitch(D) * 4);
+        if (dw > 1) part = std::max(part, (size_t)dw * 2 * Fp * ffn_part_pitch(D) * 4);
+    }
+    *bytes_out = T ? dgu_bytes(T, F, dtype) + part : 0;
     return CONV_OK;
 }
 
@@ -143,6 +193,7 @@ conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, in
     hipError_t e = launch_ffn_gate_grad(d, dtype, (hipStream_t)stream);
     FfnGemmArgs a{};
     a.a = workspace, a.as = 2 * (int64_t)Fp, a.bs = D, a.N = D;
+    if (T) a.part = (float *)((char *)workspace + dgu_bytes(T, F, dtype));
     if (e == hipSuccess && T) {  // dx = [dg du] [w_gate; w_up]
         a.b0 = w_gate, a.b1 = w_up, a.M = T, a.K = 2 * Fp, a.ktsplit = Fp / piece, a.brows = F;
         a.out = dx, a.split = T, a.rows = T;

@@ -203,6 +203,10 @@ __device__ __forceinline__ void ffn_with_act(int act, F &&f) {
 }
 template <typename O>
 __device__ __forceinline__ void ffn_plain_out(const FfnGemmArgs &A, int64_t m, int n, const f32x4_t &acc) {
+    if (A.splits > 1) {  // this part's sums; their rows are whole 16-byte pieces
+        *(float4 *)(A.part + ((int64_t)blockIdx.y * A.M + m) * ffn_part_pitch(A.N) + n) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        return;
+    }
     const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
     const bool second = m >= A.split;
     const int64_t row = second ? m - A.split : m;
@@ -217,10 +221,14 @@ struct FfnRowsOfM {
     const char *p, *p1;
     uint32_t step, behind;  // behind: what of a row is past its `width` bytes
     int rows, left, until;  // left: rows from here on; until: tiles before p1's
-    __device__ __forceinline__ void init(const void *p0, const void *p1_, int64_t stride, int rows_, int64_t width, int split) {
-        p = (const char *)p0, p1 = (const char *)p1_, step = (uint32_t)(stride * (int64_t)sizeof(S));
+    __device__ __forceinline__ void init(const void *p0, const void *p1_, int64_t stride, int rows_, int64_t width, int split, int first) {
+        step = (uint32_t)(stride * (int64_t)sizeof(S));
         behind = step - (uint32_t)(width * (int64_t)sizeof(S));
-        rows = left = rows_, until = split;
+        const bool other = first >= split;
+        first -= other ? split : 0;
+        p = (const char *)(other ? p1_ : p0) + (uint64_t)step * KROWS * (uint32_t)first;
+        p1 = (const char *)p1_, rows = rows_, left = rows_ - first * KROWS;
+        until = other ? INT32_MAX : split - first;
     }
     __device__ __forceinline__ void next() {
         const bool other = --until == 0;
@@ -258,12 +266,14 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
     const int64_t m0 = (int64_t)mt * BM;
     const int n0 = nt * BN;
     const uint32_t kbytes = (uint32_t)A.K * ES, abytes = (uint32_t)(A.as * ES), bbytes = (uint32_t)(A.bs * ES);
-    const int nk = (A.K + RA::KROWS - 1) / RA::KROWS;
+    const int tiles = (A.K + RA::KROWS - 1) / RA::KROWS;
+    const int k0 = PLAIN ? (int)((int64_t)tiles * blockIdx.y / A.splits) : 0;  // this part's tiles
+    const int nk = (PLAIN ? (int)((int64_t)tiles * (blockIdx.y + 1) / A.splits) : tiles) - k0;
     const int am = (int)min((int64_t)BM, A.M - m0);  // a's m that are there
     const char *abase = (const char *)A.a + m0 * (AM ? ES : A.as * ES);
     FfnRowsOfM<S> ma, mb;
-    if constexpr (AM) ma.init(abase, nullptr, A.as, A.K, A.M - m0, INT32_MAX);
-    if constexpr (BMM) mb.init((const char *)A.b0 + (int64_t)n0 * ES, (const char *)A.b1 + (int64_t)n0 * ES, A.bs, A.brows, A.N - n0, A.ktsplit);
+    if constexpr (AM) ma.init(abase, nullptr, A.as, A.K, A.M - m0, INT32_MAX, k0);
+    if constexpr (BMM) mb.init((const char *)A.b0 + (int64_t)n0 * ES, (const char *)A.b1 + (int64_t)n0 * ES, A.bs, A.brows, A.N - n0, A.ktsplit, k0);
 
     // Load i of this wavefront is load 4 i + wave of its region.
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
@@ -319,7 +329,7 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
         // (in rows of k all loads of a lane bring the same chunk, as 8 q + lane / 8 keep (row / 2) % 8)
         const uint32_t chunk = (uint32_t)FfnRegion<S, false, 128>::load_chunk(wave, lane) * 16;
         auto issue = [&](int kt, uint32_t stage) {  // tiles past the end and what lies behind a row read as zeros
-            const uint32_t at = (uint32_t)kt * 128;
+            const uint32_t at = (uint32_t)(k0 + kt) * 128;
             const bool in = at + chunk < kbytes;
             const uint32_t dst = lds0 + stage + wave * 1024;
             __amdgpu_buffer_rsrc_t ta, tb;
@@ -385,7 +395,7 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
                     const bool up = !of_a && !PLAIN && row >= BH;
                     const int64_t r = of_a ? m0 + row : n0 + (up ? row - BH : row);
                     const char *p = (const char *)(of_a ? A.a : up ? A.b1 : A.b0) + r * (of_a ? A.as : A.bs) * ES;
-                    if (r < (of_a ? A.M : (int64_t)A.N)) v = values(p, kt * RA::KROWS + first, A.K);
+                    if (r < (of_a ? A.M : (int64_t)A.N)) v = values(p, (k0 + kt) * RA::KROWS + first, A.K);
                 }
                 reg[i] = v;
             }
@@ -476,7 +486,9 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
     const int64_t m0 = (int64_t)mt * BM;
     const int n0 = nt * BN;
     const uint32_t kbytes = (uint32_t)A.K * ES, abytes = (uint32_t)(A.as * ES), bbytes = (uint32_t)(A.bs * ES);
-    const int nk = (A.K + RA::KROWS - 1) / RA::KROWS;
+    const int tiles = (A.K + RA::KROWS - 1) / RA::KROWS;
+    const int k0 = PLAIN ? (int)((int64_t)tiles * blockIdx.y / A.splits) : 0;  // this part's tiles
+    const int nk = (PLAIN ? (int)((int64_t)tiles * (blockIdx.y + 1) / A.splits) : tiles) - k0;
 
     auto rows_at = [&](const void *p, int64_t first, int64_t rows, int64_t most, uint32_t step) {
         const int64_t n = rows - first < most ? rows - first : most;
@@ -516,14 +528,14 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
         }
     }
     FfnRowsOfM<S> ma, mb;
-    if constexpr (AM) ma.init((const char *)A.a + m0 * ES, nullptr, A.as, A.K, min(A.M - m0, (int64_t)BM), INT32_MAX);
+    if constexpr (AM) ma.init((const char *)A.a + m0 * ES, nullptr, A.as, A.K, min(A.M - m0, (int64_t)BM), INT32_MAX, k0);
     if constexpr (BMM)
-        mb.init((const char *)A.b0 + (int64_t)n0 * ES, (const char *)A.b1 + (int64_t)n0 * ES, A.bs, A.brows, min(A.N - n0, BN), A.ktsplit);
+        mb.init((const char *)A.b0 + (int64_t)n0 * ES, (const char *)A.b1 + (int64_t)n0 * ES, A.bs, A.brows, min(A.N - n0, BN), A.ktsplit, k0);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t)lds;
     auto issue = [&](auto region_c, auto stage_c, int kt) {  // tiles past the end read as zeros
         constexpr int region = decltype(region_c)::value, h = region & 1;
         constexpr bool of_a = region < 2;
-        const uint32_t at = (uint32_t)kt * 128,
+        const uint32_t at = (uint32_t)(k0 + kt) * 128,
                        dst = lds0 + decltype(stage_c)::value * STAGE + (of_a ? h * SIZE_A : 2 * SIZE_A + h * SIZE_B) + wave * ((of_a ? LA : LB) * 1024);
 #pragma unroll
         for (int j = 0; j < (of_a ? LA : LB); ++j) {
@@ -658,38 +670,67 @@ __global__ __launch_bounds__(512) void ffn_large_kernel(FfnGemmArgs A) {
 }
 typedef FfnLarge<2, 4, 2> FfnTile256x128;  // 128 x (32 + 32) of a wavefront
 typedef FfnLarge<4, 2, 2> FfnTile256x64;   // 64 x (32 + 32)
+typedef FfnLarge<2, 2, 1> FfnTile128x64;   // 64 x (16 + 16), two blocks on a CU
+
+// out from the parts' sums, added in their order.
+template <typename O>
+__global__ __launch_bounds__(256) void ffn_sum_kernel(FfnGemmArgs A) {
+    const int64_t pitch = ffn_part_pitch(A.N), per = pitch / 4, total = A.M * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / per;
+        const int n = (int)(i - m * per) * 4;
+        const bool second = m >= A.split;
+        const int64_t row = second ? m - A.split : m;
+        if (row >= A.rows) continue;
+        float v[4] = {};
+        for (int s = 0; s < A.splits; ++s) {
+            const float4 x = *(const float4 *)(A.part + (s * A.M + m) * pitch + n);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        }
+        ffn_put4((O *)(second ? A.out2 : A.out) + row * A.N, n, A.N, v);
+    }
+}
 
 // ---- launches
 template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY, bool AM, bool BMM>
 hipError_t ffn_run_small(const FfnGemmArgs &a, hipStream_t st) {
     constexpr int BN = EPI == FFN_PLAIN ? 2 * BH : BH;
     const int64_t blocks = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
-    if (!grid_fits(blocks, 256, 1)) return kTooLarge;
-    hipLaunchKernelGGL((ffn_small_kernel<S, O, EPI, BM, BH, ANY, AM, BMM>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    if (!grid_fits(blocks, 256, a.splits)) return kTooLarge;
+    hipLaunchKernelGGL((ffn_small_kernel<S, O, EPI, BM, BH, ANY, AM, BMM>), dim3((unsigned)blocks, a.splits), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM, typename C>
 hipError_t ffn_run_large(const FfnGemmArgs &a, hipStream_t st) {
     constexpr int BN = EPI == FFN_PLAIN ? 2 * C::BH : C::BH;
     const int64_t blocks = ((a.M + C::BM - 1) / C::BM) * ((a.N + BN - 1) / BN);
-    if (!grid_fits(blocks, 512, 1)) return kTooLarge;
-    hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI, AM, BMM, C>), dim3((unsigned)blocks), dim3(512), 0, st, a);
+    if (!grid_fits(blocks, 512, a.splits)) return kTooLarge;
+    hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI, AM, BMM, C>), dim3((unsigned)blocks, a.splits), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
 // AM, BMM: a, b as rows of m (of columns that are there: M and N values wide).
 template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
-hipError_t ffn_run(const FfnGemmArgs &a, hipStream_t st) {
-    constexpr int V = 16 / (int)sizeof(S), BN = EPI == FFN_PLAIN ? 2 : 1;
+hipError_t ffn_run(FfnGemmArgs a, hipStream_t st) {
+    constexpr int V = 16 / (int)sizeof(S);
+    constexpr bool PLAIN = EPI == FFN_PLAIN;
     bool vec = (AM && BMM ? 0 : a.K) % V == 0 && (AM ? a.M : 0) % V == 0 && (BMM ? a.N : 0) % V == 0 && a.as % V == 0 && a.bs % V == 0;
     for (const void *p : {a.a, a.b0, a.b1}) vec = vec && (uintptr_t)p % 16 == 0;
-    if (!vec) return ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
-    const int64_t large = ((a.M + 255) / 256) * ((a.N + 128 * BN - 1) / (128 * BN));
-    if constexpr (sizeof(S) < 4 || !BMM)
-        if (large >= 192) return ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x128>(a, st);
-    const int64_t mid = ((a.M + 127) / 128) * ((a.N + 64 * BN - 1) / (64 * BN));
-    if (mid >= 256) return ffn_run_small<S, O, EPI, 128, 64, false, AM, BMM>(a, st);
-    return ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
+    const FfnPlan plan = ffn_plan(a.M, a.N, a.K, (int)sizeof(S), PLAIN, vec);
+    a.splits = plan.splits;
+    hipError_t e;
+    if (!vec) e = ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
+    else if (plan.tile == FFN_TILE_256x128) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x128>(a, st);
+    else if (plan.tile == FFN_TILE_256x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x64>(a, st);
+    else if (plan.tile == FFN_TILE_128x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile128x64>(a, st);
+    else e = ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
+    if constexpr (PLAIN) {
+        if (e != hipSuccess || a.splits == 1) return e;
+        const int64_t blocks = (a.M * (ffn_part_pitch(a.N) / 4) + 255) / 256;
+        hipLaunchKernelGGL((ffn_sum_kernel<O>), dim3((unsigned)(blocks < 1 << 16 ? blocks : 1 << 16)), dim3(256), 0, st, a);
+        return hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace

@@ -121,7 +121,7 @@ def test_gate_values(act, t):
 
 
 BACK = [(1, 64, 64), (2, 1, 3), (5, 24, 40), (17, 72, 33), (64, 128, 64), (65, 130, 129), (130, 250, 77), (333, 96, 700),
-        (260, 2200, 900), (2600, 64, 1100)]
+        (260, 2200, 900), (2600, 64, 1100), (40, 200, 5000), (33, 77, 2500), (9000, 40, 50), (5000, 33, 70)]
 
 
 @pytest.mark.parametrize("t", DTYPES, ids=str)
