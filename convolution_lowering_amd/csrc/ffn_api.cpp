@@ -228,7 +228,8 @@ conv_status_t linear_w4_fwd(const void *x, int64_t x_stride, const void *w, cons
     if (st != CONV_OK || !R) return st;
     if (!w4_weights_ok(w, scales, zeros, dtype)) return CONV_ERR_INVALID_ARG;
     W4Args a{};
-    a.x = x, a.xs = x_stride, a.w[0] = (const uint8_t *)w, a.scales[0] = scales, a.zeros[0] = zeros, a.y = y;
+    a.x = x, a.xs = x_stride, a.w[0] = (const uint8_t *)w, a.scales[0] = scales, a.y = y;
+    a.has_zeros = zeros != nullptr, a.zeros[0] = zeros ? zeros : scales;
     a.R = R, a.D = D, a.F = F, a.groups = (D + group - 1) / group;
     return hip_status(launch_w4(a, group, false, dtype, (hipStream_t)stream));
 }
@@ -246,8 +247,9 @@ conv_status_t gated_ffn_w4_fwd(const void *x, int64_t x_stride, const void *w_ga
         return CONV_ERR_INVALID_ARG;
     W4Args a{};
     a.x = x, a.xs = x_stride, a.y = h, a.R = R, a.D = D, a.F = F, a.groups = (D + group - 1) / group, a.act = act;
-    a.w[0] = (const uint8_t *)w_gate, a.scales[0] = gate_scales, a.zeros[0] = gate_zeros;
-    a.w[1] = (const uint8_t *)w_up, a.scales[1] = up_scales, a.zeros[1] = up_zeros;
+    a.w[0] = (const uint8_t *)w_gate, a.scales[0] = gate_scales, a.w[1] = (const uint8_t *)w_up, a.scales[1] = up_scales;
+    a.has_zeros = gate_zeros != nullptr;
+    a.zeros[0] = gate_zeros ? gate_zeros : gate_scales, a.zeros[1] = up_zeros ? up_zeros : up_scales;
     return hip_status(launch_w4(a, group, true, dtype, (hipStream_t)stream));
 }
 

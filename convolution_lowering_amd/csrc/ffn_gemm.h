@@ -52,24 +52,6 @@ __device__ __forceinline__ void ffn_mma(const uint4 (&b)[2], const uint4 (&a)[2]
     }
 }
 
-// lds_dma16 (igemm_dma.h) of rows that begin `at` bytes further on.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void ffn_dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t at, uint32_t lds_base) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
-                 :
-                 : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(lds_base)), "s"(__builtin_amdgcn_readfirstlane(at))
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// 16 bytes at an address in LDS.
-__device__ __forceinline__ uint4 lds_at(uint32_t at) {
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const u32x4 v = *(const __attribute__((address_space(3))) u32x4 *)at;
-    return __builtin_bit_cast(uint4, v);
-}
-
 // A region of W rows of k, or of W columns of rows of m (MM).
 template <typename S, bool MM, int W>
 struct FfnRegion {
@@ -126,7 +108,7 @@ struct FfnFragments {
     // Chunk j of tile i; add: the stage, or another region like this one.
     __device__ __forceinline__ uint4 get(int i, int j, uint32_t add) const {
         if constexpr (!MM) {
-            return lds_at(at[j] + add + i * 2048);
+            return ffn_lds_at(at[j] + add + i * 2048);
         } else if constexpr (R::ES == 2) {
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 *ptr;

@@ -51,6 +51,24 @@ struct __attribute__((packed, aligned(sizeof(S)))) FfnAnyVec {
     S v[V];
 };
 
+// lds_dma16 (igemm_dma.h) of rows that begin `at` bytes further on.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void ffn_dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t at, uint32_t lds_base) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+                 :
+                 : "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(lds_base)), "s"(__builtin_amdgcn_readfirstlane(at))
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// 16 bytes at an address in LDS.
+__device__ __forceinline__ uint4 ffn_lds_at(uint32_t at) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 v = *(const __attribute__((address_space(3))) u32x4 *)at;
+    return __builtin_bit_cast(uint4, v);
+}
+
 // ---- products: out[m][n] = sum_k a[m][k] b[n][k] (ffn_gemm.h)
 enum FfnEpilogue {
     FFN_GATED,   // h = act(a b0') * (a b1')
@@ -108,6 +126,7 @@ struct W4Args {
     void *y;
     int64_t xs, R;
     int D, F, groups, act;
+    int has_zeros;  // (without, zeros point to the scales)
 };
 hipError_t launch_w4(const W4Args &a, int group, bool gated, int dtype, hipStream_t st);
 

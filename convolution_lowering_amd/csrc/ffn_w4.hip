@@ -12,14 +12,16 @@
 //     eight values of a fragment are put in the same order.
 //   * fp32 x: three bf16 parts of 8 bits each, cut, not rounded, so that they add
 //     up to x exactly; codes as integers (128 would cost seven of the sum's digits).
-// A block has 16 FT features of each matrix; its wavefronts share out the 128-value
-// pieces of the rows, and their sums meet in LDS in a fixed order.
+// A block has 16 features of each matrix; its wavefronts share out the 128-value
+// pieces of the rows and run apart from one another, their sums meet in LDS in a
+// fixed order.  Codes and x go from memory to registers, the next pieces' on their
+// way and no branch between them (each would end in a wait for all of them); scales
+// pass through LDS.
 #include "ffn_internal.h"
 
 namespace convlower {
 namespace {
 
-constexpr int kWaves = 8;
 constexpr int kPiece = 128;  // values of a row that a wavefront takes at once: 16 bytes of codes a lane
 
 template <typename S>
@@ -52,30 +54,28 @@ __device__ __forceinline__ uint4 w4_codes(uint32_t d) {
                           __builtin_amdgcn_perm(f[5], f[4], 0x07060302), __builtin_amdgcn_perm(f[7], f[6], 0x07060302));
     }
 }
-// Eight values of x as fragments, in the codes' order.
-template <typename S>
-__device__ __forceinline__ void w4_x(const FfnAnyVec<S, 8> &v, uint4 (&out)[W4Type<S>::PARTS]) {
-    if constexpr (sizeof(S) == 2) {
-        uint4 t;
-        __builtin_memcpy(&t, &v, 16);
-        out[0] = make_uint4(__builtin_amdgcn_perm(t.z, t.x, 0x05040100), __builtin_amdgcn_perm(t.z, t.x, 0x07060302),
-                            __builtin_amdgcn_perm(t.w, t.y, 0x05040100), __builtin_amdgcn_perm(t.w, t.y, 0x07060302));
-    } else {
-        uint32_t p[3][8];
+// Eight 16-bit values of x in the codes' order.
+__device__ __forceinline__ uint4 w4_order(const uint4 &t) {
+    return make_uint4(__builtin_amdgcn_perm(t.z, t.x, 0x05040100), __builtin_amdgcn_perm(t.z, t.x, 0x07060302),
+                      __builtin_amdgcn_perm(t.w, t.y, 0x05040100), __builtin_amdgcn_perm(t.w, t.y, 0x07060302));
+}
+// Eight float32 values as three bf16 fragments.
+__device__ __forceinline__ void w4_parts(const uint4 &lo, const uint4 &hi, uint4 (&out)[3]) {
+    const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t p[3][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float x = v.v[i];
+    for (int i = 0; i < 8; ++i) {
+        float x = __uint_as_float(v[i]);
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                p[k][i] = __float_as_uint(x) & 0xffff0000u;
-                x -= __uint_as_float(p[k][i]);
-            }
+        for (int k = 0; k < 3; ++k) {
+            p[k][i] = __float_as_uint(x) & 0xffff0000u;
+            x -= __uint_as_float(p[k][i]);
         }
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            out[k] = make_uint4(__builtin_amdgcn_perm(p[k][1], p[k][0], 0x07060302), __builtin_amdgcn_perm(p[k][3], p[k][2], 0x07060302),
-                                __builtin_amdgcn_perm(p[k][5], p[k][4], 0x07060302), __builtin_amdgcn_perm(p[k][7], p[k][6], 0x07060302));
     }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        out[k] = make_uint4(__builtin_amdgcn_perm(p[k][1], p[k][0], 0x07060302), __builtin_amdgcn_perm(p[k][3], p[k][2], 0x07060302),
+                            __builtin_amdgcn_perm(p[k][5], p[k][4], 0x07060302), __builtin_amdgcn_perm(p[k][7], p[k][6], 0x07060302));
 }
 // d[j] of lane row q (16 lanes) becomes d[q] of lane row j.
 __device__ __forceinline__ void w4_transpose(uint32_t (&d)[4]) {
@@ -86,114 +86,177 @@ __device__ __forceinline__ void w4_transpose(uint32_t (&d)[4]) {
     d[0] = c[0], d[1] = c[1], d[2] = e[0], d[3] = e[1];
 }
 
-// NT: 16-token tiles; FT: 16-feature tiles of each of NM matrices.
-template <typename S, int NT, int FT, int GROUP, bool GATED>
+constexpr int kScaleBytes = 16384;  // scales and zero points in LDS at a time
+
+template <typename S>
+struct W4Scale {
+    S scale, zero;
+};
+
+// NT: 16-token tiles, all of them a wavefront's; WAVES of them share out the pieces.
+// VEC: rows of x at multiples of 4 bytes.
+template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC>
 __device__ __forceinline__ void w4_body(const W4Args &A) {
     using T = W4Type<S>;
-    constexpr int NM = GATED ? 2 : 1, TILES = NM * FT, SUB = kPiece / GROUP, STEPS = 4 / SUB;
-    constexpr int AHEAD = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // pieces under way
+    constexpr int NM = GATED ? 2 : 1, SUB = kPiece / GROUP, STEPS = 4 / SUB;
+    constexpr int ES = (int)sizeof(S), UNIT = 16 / ES, XL = ES / 2;  // values of a 16-byte load, loads of eight
+    constexpr int AHEAD = NT * XL * NM * (SUB == 4 ? 2 : 1) <= 2 ? 2 : 1;                      // pieces under way beside the one worked with
+    constexpr int THREADS = WAVES * 64, ROWS = 16 * NM;
+    constexpr int SPAN = kScaleBytes / (ROWS * SUB * (int)sizeof(W4Scale<S>)) / (WAVES * AHEAD) * AHEAD;  // turns whose scales have room
+    constexpr int PER = SPAN * WAVES * SUB;                          // scales of a row and span
+    static_assert(SPAN >= AHEAD, "scales have room");
     typedef MfmaShape<typename T::mma_t, 16> MF;
-    __shared__ f32x4_t sums[kWaves][TILES][64];
+    __shared__ W4Scale<S> scales[ROWS * PER];
+    __shared__ f32x4_t sums[WAVES][NM][64];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane >> 4;
-    const int f0 = blockIdx.x * 16 * FT;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
+    const int f0 = blockIdx.x * 16;
     const int64_t r0 = (int64_t)blockIdx.y * 16 * NT;
-    const int pieces = (A.D + kPiece - 1) / kPiece;
-    const int first = (int)((int64_t)pieces * wave / kWaves), last = (int)((int64_t)pieces * (wave + 1) / kWaves);
+    const int rows = (int)min((int64_t)16 * NT, A.R - r0);
+    const int full = A.D / kPiece, turns = (full + WAVES - 1) / WAVES;  // whole pieces of a row
     const int64_t pitch = A.D / 2;
 
+    // ---- loads: what is not there (rows, pieces) reads as zeros
+    __amdgpu_buffer_rsrc_t rw[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) rw[m] = make_rsrc(A.w[m] + f0 * pitch, (uint32_t)(min(16, A.F - f0) * pitch));
+    const S *const x0 = (const S *)A.x + r0 * A.xs;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(x0, (uint32_t)(((int64_t)(rows - 1) * A.xs + A.D) * ES));
+    const uint32_t code_at = (uint32_t)((lane & 15) * pitch) + q * 16;
+    uint32_t x_at[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x_at[n] = (uint32_t)((16 * n + (lane & 15)) * A.xs * ES);
+    const int x_first = SUB == 1 ? q * 32 : q * 8;  // value of a piece; chunk j begins x_step values further on
+    constexpr int x_step = SUB == 1 ? 8 : 32;
     struct Piece {
-        uint32_t w[TILES][4];
-        S s[TILES][SUB], z[TILES][SUB];
-        FfnAnyVec<S, 8> x[NT][4];
-    } buf[AHEAD];
-    auto load = [&](Piece &p, int at) {
-        const int d0 = at * kPiece;
-        if (at >= last) return;
+        uint32_t w[NM][4];
+        uint4 x[NT][4][XL];
+    };
+    auto load_x = [&](Piece &p, int piece) {
+        const int left = A.D - piece * kPiece;
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-            const int m = t / FT;
-            const int f = min(f0 + (t % FT) * 16 + (lane & 15), A.F - 1);
-            const uint8_t *row = A.w[m] + f * pitch + (d0 + q * 32) / 2;
-            if (d0 + q * 32 + 32 <= A.D) {
-                const FfnAnyVec<uint32_t, 4> v = *(const FfnAnyVec<uint32_t, 4> *)row;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p.w[t][j] = v.v[j];
-            } else {
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p.w[t][j] = d0 + q * 32 + j * 8 < A.D ? *(const uint32_t *)(row + j * 4) : 0u;
-            }
+                for (int e = 0; e < XL; ++e) {
+                    const int d = x_first + j * x_step + e * UNIT;
+                    if constexpr (VEC) {
+                        p.x[n][j][e] = __builtin_bit_cast(
+                            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(d < left ? x_at[n] + d * ES : kOutOfRange), piece * kPiece * ES, 0));
+                    } else {  // (the first eight values in their place, and zeros)
+                        const bool in = 16 * n + (lane & 15) < rows && d < left;
+                        const FfnAnyVec<S, UNIT> v = *(const FfnAnyVec<S, UNIT> *)(x0 + (in ? (16 * n + (lane & 15)) * A.xs + piece * kPiece + d : 0));
+                        __builtin_memcpy(&p.x[n][j][e], &v, 16);
+                        if (!in) p.x[n][j][e] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+    };
+    auto load = [&](Piece &p, int turn) {
+        const int piece = turn * WAVES + wave;
 #pragma unroll
-            for (int g = 0; g < SUB; ++g) {
-                const int64_t i = (int64_t)f * A.groups + min(at * SUB + g, A.groups - 1);
-                p.s[t][g] = ((const S *)A.scales[m])[i];
-                if (A.zeros[m]) p.z[t][g] = ((const S *)A.zeros[m])[i];
-            }
+        for (int m = 0; m < NM; ++m) {
+            const uint4 v = __builtin_bit_cast(
+                uint4, __builtin_amdgcn_raw_buffer_load_b128(rw[m], (int)(piece < full ? code_at : kOutOfRange), piece * (kPiece / 2), 0));
+            p.w[m][0] = v.x, p.w[m][1] = v.y, p.w[m][2] = v.z, p.w[m][3] = v.w;
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int64_t r = r0 + 16 * n + (lane & 15);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int d = d0 + (SUB == 1 ? q * 32 + j * 8 : j * 32 + q * 8);
-                FfnAnyVec<S, 8> v = {};
-                if (r < A.R && d < A.D) v = *(const FfnAnyVec<S, 8> *)((const S *)A.x + r * A.xs + d);
-                p.x[n][j] = v;
+        load_x(p, piece);
+    };
+    auto scales_of = [&](int turn) {  // of the span that begins with this turn
+        const int g0 = turn * WAVES * SUB, per = min(PER, (A.groups + SUB - 1) / SUB * SUB - g0);
+#pragma unroll 4
+        for (int u = threadIdx.x; u < ROWS * per; u += THREADS) {
+            const int row = u / per, g = g0 + u % per;
+            const bool up = GATED && row >= 16;
+            W4Scale<S> v = {S(0), S(0)};
+            if (g < A.groups) {
+                const int64_t at = (int64_t)min(f0 + (row & 15), A.F - 1) * A.groups + g;
+                v.scale = ((const S *)(up ? A.scales[1] : A.scales[0]))[at];
+                v.zero = A.has_zeros ? ((const S *)(up ? A.zeros[1] : A.zeros[0]))[at] : mix_out<S>(8.f);
             }
+            scales[row * PER + g - g0] = v;
         }
     };
 
-    f32x4_t acc[NT][TILES] = {};
-    uint4 ones;
-    {
-        constexpr uint32_t one = __is_same(S, _Float16) ? 0x3c003c00u : 0x3f803f80u;
-        ones = make_uint4(one, one, one, one);
-    }
-    auto work = [&](Piece &p) {
+    f32x4_t acc[NT][NM] = {};
+    constexpr uint32_t one = __is_same(S, _Float16) ? 0x3c003c00u : 0x3f803f80u;
+    const uint4 ones = make_uint4(one, one, one, one);
+    // Piece `in` of the span; if not `there`, to no effect (a code of 0 is not a weight of 0).
+    auto work = [&](Piece &p, int in, bool there) {
         if constexpr (SUB > 1) {  // a product's 32 values lie in one group
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) w4_transpose(p.w[t]);
+            for (int m = 0; m < NM; ++m) w4_transpose(p.w[m]);
         }
 #pragma unroll
         for (int g = 0; g < SUB; ++g) {
-            f32x4_t part[NT][TILES] = {}, all[NT] = {};
+            f32x4_t part[NT][NM] = {}, all[NT] = {};
 #pragma unroll
             for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
-                uint4 c[TILES];
+                uint4 codes[NM];
 #pragma unroll
-                for (int t = 0; t < TILES; ++t) c[t] = w4_codes<S>(p.w[t][j]);
+                for (int m = 0; m < NM; ++m) codes[m] = w4_codes<S>(p.w[m][j]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     uint4 x[T::PARTS];
-                    w4_x<S>(p.x[n][j], x);
+                    if constexpr (ES == 2) x[0] = w4_order(p.x[n][j][0]);
+                    else w4_parts(p.x[n][j][0], p.x[n][j][XL - 1], x);
 #pragma unroll
                     for (int k = 0; k < T::PARTS; ++k) {
                         MF::mma(x[k], ones, all[n]);
 #pragma unroll
-                        for (int t = 0; t < TILES; ++t) MF::mma(x[k], c[t], part[n][t]);
+                        for (int m = 0; m < NM; ++m) MF::mma(x[k], codes[m], part[n][m]);
                     }
                 }
             }
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-                const float s = mix_f32(p.s[t][g]), z = T::OFFSET + (A.zeros[t / FT] ? mix_f32(p.z[t][g]) : 8.f);
+            for (int m = 0; m < NM; ++m) {
+                const W4Scale<S> sz = scales[(m * 16 + (lane & 15)) * PER + in * SUB + g];
+                const float s = there ? mix_f32(sz.scale) : 0.f, z = there ? T::OFFSET + mix_f32(sz.zero) : 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][t][i] = fmaf(s, fmaf(-z, all[n][i], part[n][t][i]), acc[n][t][i]);
+                    for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(s, fmaf(-z, all[n][i], part[n][m][i]), acc[n][m][i]);
             }
+            __builtin_amdgcn_sched_barrier(0);  // (one group's operands at a time: there are no registers for more)
         }
     };
 
+    Piece piece[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) load(buf[i], first + i);
-    for (int at = first; at < last; at += AHEAD) {
+    for (int i = 0; i < AHEAD; ++i) load(piece[i], i);
+    scales_of(0);
+    __syncthreads();
+    int in_span = 0;
+#pragma nounroll
+    for (int turn = 0; turn < turns; turn += AHEAD) {
+        if (in_span == SPAN) {
+            __syncthreads();  // nobody reads the last span's scales any more
+            scales_of(turn);
+            __syncthreads();
+            in_span = 0;
+        }
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (at + i < last) {
-                work(buf[i]);
-                load(buf[i], at + i + AHEAD);
-            }
+        for (int i = 0; i < AHEAD; ++i) {
+            work(piece[i], (in_span + i) * WAVES + wave, (turn + i) * WAVES + wave < full);
+            load(piece[i], turn + i + AHEAD);
+        }
+        in_span += AHEAD;
+    }
+    if (A.D % kPiece) {  // what is left of a row, word by word
+        const int first = full / (SPAN * WAVES) * SPAN;
+        __syncthreads();
+        scales_of(first);
+        __syncthreads();
+        if (full % WAVES == wave) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    piece[0].w[m][j] = __builtin_amdgcn_raw_buffer_load_b32(
+                        rw[m], (int)(full * kPiece + q * 32 + j * 8 < A.D ? code_at + j * 4 : kOutOfRange), full * (kPiece / 2), 0);
+            load_x(piece[0], full);
+            work(piece[0], full - first * WAVES, true);
+        }
     }
 
     // Result: lane l holds feature l % 16 and tokens 4 (l / 16) .. + 3 of a tile.
@@ -201,40 +264,54 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     for (int n = 0; n < NT; ++n) {
         if (n) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) sums[wave][t][lane] = acc[n][t];
+        for (int m = 0; m < NM; ++m) sums[wave][m][lane] = acc[n][m];
         __syncthreads();
-        for (int i = threadIdx.x; i < FT * 256; i += kWaves * 64) {
-            const int f = (i & 15) + 16 * (i >> 8), tok = (i >> 4) & 15, at = (tok >> 2) * 16 + (i & 15);
-            const int64_t r = r0 + 16 * n + tok;
-            if (r >= A.R || f0 + f >= A.F) continue;
+        const int tok = threadIdx.x >> 4, f = threadIdx.x & 15, at = (tok >> 2) * 16 + f;
+        const int64_t r = r0 + 16 * n + tok;
+        if (tok < 16 && r < A.R && f0 + f < A.F) {
             float y[NM];
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
                 y[m] = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) y[m] += sums[w][m * FT + (i >> 8)][at][tok & 3];
+                for (int w = 0; w < WAVES; ++w) y[m] += sums[w][m][at][tok & 3];
             }
             ((S *)A.y)[r * A.F + f0 + f] = mix_out<S>(GATED ? ffn_act<S>(y[0], A.act) * y[NM - 1] : y[0]);
         }
     }
 }
-template <typename S, int NT, int FT, int GROUP, bool GATED>
-__global__ __launch_bounds__(kWaves * 64) void w4_kernel(W4Args A) {
-    w4_body<S, NT, FT, GROUP, GATED>(A);
+template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC>
+__global__ __launch_bounds__(WAVES * 64, NT == 1 ? (GROUP == 128 ? 4 : 3) : NT == 2 && GROUP == 128 ? 3 : 2) void w4_kernel(W4Args A) {
+    w4_body<S, NT, WAVES, GROUP, GATED, VEC>(A);
 }
 
-template <typename S, int NT, int FT, int GROUP, bool GATED>
+template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC>
 hipError_t w4_run(const W4Args &a, hipStream_t st) {
-    const int64_t x = (a.F + 16 * FT - 1) / (16 * FT), y = (a.R + 16 * NT - 1) / (16 * NT);
-    if (!grid_fits(x, kWaves * 64, y)) return kTooLarge;
-    hipLaunchKernelGGL((w4_kernel<S, NT, FT, GROUP, GATED>), dim3((unsigned)x, (unsigned)y), dim3(kWaves * 64), 0, st, a);
+    const int64_t x = (a.F + 15) / 16, y = (a.R + 16 * NT - 1) / (16 * NT);
+    if (!grid_fits(x, WAVES * 64, y)) return kTooLarge;
+    hipLaunchKernelGGL((w4_kernel<S, NT, WAVES, GROUP, GATED, VEC>), dim3((unsigned)x, (unsigned)y), dim3(WAVES * 64), 0, st, a);
     return hipGetLastError();
+}
+// Blocks of four wavefronts where there are enough of them for every CU to hold two or
+// more, so that all are there at once (640 blocks of 16 gated features, R = 1: 15.1 us
+// against 25 with eight wavefronts); eight where there are few (256 blocks, R = 1, 4096
+// wide: 5.4 us against 7.1 with sixteen).  Four token tiles at once but for the
+// groups whose sums do not fit the registers (gated, 32: 64 tokens 114 us, two by two 84).
+template <typename S, int NT, int GROUP, bool GATED>
+hipError_t w4_waves(const W4Args &a, hipStream_t st) {
+    return a.F >= 6144 ? w4_run<S, NT, 4, GROUP, GATED, true>(a, st) : w4_run<S, NT, 8, GROUP, GATED, true>(a, st);
 }
 template <typename S, int GROUP, bool GATED>
 hipError_t w4_tokens(const W4Args &a, hipStream_t st) {
-    if (a.R <= 16) return w4_run<S, 1, 1, GROUP, GATED>(a, st);
-    if (a.R <= 32) return w4_run<S, 2, 1, GROUP, GATED>(a, st);
-    return w4_run<S, 4, 1, GROUP, GATED>(a, st);
+    if constexpr (sizeof(S) == 4) {
+        return w4_waves<S, 1, GROUP, GATED>(a, st);
+    } else {
+        if ((uintptr_t)a.x % 4 || a.xs % 2) return w4_run<S, 1, 8, GROUP, GATED, false>(a, st);
+        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED>(a, st);
+        if (a.R <= 32 || (GROUP == 32 && GATED)) return w4_waves<S, 2, GROUP, GATED>(a, st);
+        if constexpr (GROUP != 32 || !GATED) return w4_waves<S, 4, GROUP, GATED>(a, st);
+    }
+    return hipErrorInvalidValue;
 }
 template <typename S>
 hipError_t w4_typed(const W4Args &a, int group, bool gated, hipStream_t st) {

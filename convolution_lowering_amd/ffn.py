@@ -73,6 +73,13 @@ def _rows(t, name, dtype, device):
     one dense row; the axes before it lie at one stride."""
     if t.dim() < 1:
         raise ValueError(f"{name} is [..., D]")
+    if t.is_contiguous():  # (the common case, without views: a one-token call is half checks)
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}, expected {device}, a GPU")
+        D = t.shape[-1]
+        return t.data_ptr(), D, t.numel() // D if D else 0
     if t.dim() > 2:
         try:
             t = t.view(-1, t.shape[-1])
@@ -81,6 +88,14 @@ def _rows(t, name, dtype, device):
     elif t.dim() == 1:
         t = t[None]
     return (*_tokens(t, name, 1, dtype, device), t.shape[0])
+
+
+def _out(out, like, shape, device):
+    """The result: the caller's tensor, checked, or a new one of `like`'s type."""
+    if out is None:
+        return like.new_empty(shape)
+    _dense(out, "out", shape, like.dtype, device)
+    return out
 
 
 # ------------------------------------------------------------ gated product
@@ -105,7 +120,7 @@ def gated_ffn_fwd(x, w_gate, w_up, *, act="silu", save=False, stream=None):
     code, xp, xs, gp, up, T, D, F = _ffn_args(x, w_gate, w_up)
     a, dev = _act(act), x.device
     with _on(stream, dev):
-        h = torch.empty((*x.shape[:-1], F), dtype=x.dtype, device=dev)
+        h = x.new_empty((*x.shape[:-1], F))
         saved = _bytes(max(16, _size("gated_ffn_saved_size", T, F)), dev) if save else None
         _check("gated_ffn_fwd",
                _ffn_lib().gated_ffn_fwd(xp, xs, gp, up, h.data_ptr(), _ptr(saved), saved.numel() if save else 0, T, D, F,
@@ -207,10 +222,9 @@ def linear_w4_fwd(x, w, scales, zeros=None, *, group=128, out=None, stream=None)
     xp, xs, R = _rows(x, "x", x.dtype, dev)
     shape = (*x.shape[:-1], F)
     with _on(stream, dev):
-        y = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
-        _check("linear_w4_fwd",
-               _ffn_lib().linear_w4_fwd(xp, xs, *ptrs, _dense(y, "out", shape, x.dtype, dev), R, D, F, group, code,
-                                        _raw(stream, dev)))
+        y = _out(out, x, shape, dev)
+        st = _ffn_lib().linear_w4_fwd(xp, xs, *ptrs, y.data_ptr(), R, D, F, group, code, _raw(stream, dev))
+    _check("linear_w4_fwd", st)
     return y
 
 
@@ -228,10 +242,9 @@ def gated_ffn_w4_fwd(x, w_gate, gate_scales, w_up, up_scales, gate_zeros=None, u
     xp, xs, R = _rows(x, "x", x.dtype, dev)
     shape = (*x.shape[:-1], F)
     with _on(stream, dev):
-        h = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
-        _check("gated_ffn_w4_fwd",
-               _ffn_lib().gated_ffn_w4_fwd(xp, xs, *gate, *up, _dense(h, "out", shape, x.dtype, dev), R, D, F, group, a,
-                                           code, _raw(stream, dev)))
+        h = _out(out, x, shape, dev)
+        st = _ffn_lib().gated_ffn_w4_fwd(xp, xs, *gate, *up, h.data_ptr(), R, D, F, group, a, code, _raw(stream, dev))
+    _check("gated_ffn_w4_fwd", st)
     return h
 
 
@@ -272,16 +285,16 @@ def norm_quant_fwd(x, w, res=None, *, eps=1e-6, want_r=True, stream=None):
     res in x's dtype, None without res or where it is not wanted."""
     if x.dim() < 1:
         raise ValueError("x is [..., D]")
-    D, dt, dev = x.shape[-1], x.dtype, x.device
-    code = _code(x, "x")
+    shape, dt, dev = x.shape, x.dtype, x.device
+    D, code = shape[-1], _code(x, "x")
     if D < 1:
         raise ValueError("rows without values")
     R = x.numel() // D
-    ptrs = (_dense(x, "x", x.shape, dt, dev), _dense(res, "res", x.shape, dt, dev), _dense(w, "w", (D,), dt, dev))
+    ptrs = (_dense(x, "x", shape, dt, dev), _dense(res, "res", shape, dt, dev), _dense(w, "w", (D,), dt, dev))
     with _on(stream, dev):
-        q = torch.empty(x.shape, dtype=E4M3, device=dev)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        r = torch.empty(x.shape, dtype=dt, device=dev) if res is not None and want_r else None
+        q = torch.empty_like(x, dtype=E4M3)
+        scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        r = torch.empty_like(x) if res is not None and want_r else None
         _check("norm_quant_fwd",
                _ffn_lib().norm_quant_fwd(*ptrs, _ptr(r), q.data_ptr(), scale.data_ptr(), R, D, eps, code,
                                          _raw(stream, dev)))
