@@ -3,18 +3,23 @@
     h -> q, k, v, z, decay and b     1x1 channels-last convolutions (conv2d_fwd)
     q, k, v -> short causal convolution -> gated delta rule
     -> norm of each head, gated by silu(z) -> 1x1 convolution
+    -> norm, gate and residual sum, and the next norm
+    with `ffn`, the feed-forward half:
+    -> both projections, activation and product -> 1x1 convolution
     -> norm, gate and residual sum, and the next block's norm
 
 ``MixerBlock.forward`` is differentiable and takes packed sequences (prompts,
 training); ``MixerBlock.step`` takes one token for each request and keeps the
-requests' states in pools.  ``python -m convolution_lowering_amd.mixer_block``
-runs both and a few training steps.
+requests' states in pools.  ``MixerBlock.quantize`` makes the feed-forward
+weights for serving: 8 bits, which ``MixerBlock.prompts`` takes, and 4 bits,
+which ``step`` then takes.  ``python -m convolution_lowering_amd.mixer_block``
+runs all of it and a few training steps.
 """
 from __future__ import annotations
 
 import torch
 
-from . import conv2d_fwd, mixer
+from . import conv2d_fwd, ffn as feed_forward, mixer
 
 
 class _Project(torch.autograd.Function):
@@ -42,7 +47,10 @@ def project(x, w):
 
 
 class MixerBlock(torch.nn.Module):
-    def __init__(self, width=512, qk_heads=2, v_heads=4, head=64, taps=4, dtype=torch.bfloat16, device="cuda", seed=0):
+    """ffn: the hidden size of a feed-forward half, None for none; act: its gate."""
+
+    def __init__(self, width=512, qk_heads=2, v_heads=4, head=64, taps=4, dtype=torch.bfloat16, device="cuda", seed=0,
+                 ffn=None, act="silu"):
         super().__init__()
         g = torch.Generator(device=device).manual_seed(seed)
 
@@ -62,6 +70,12 @@ class MixerBlock(torch.nn.Module):
         # decays -exp(a_log) softplus(.. + dt_bias), float32
         self.a_log = torch.nn.Parameter(torch.rand(v_heads, generator=g, device=device))
         self.dt_bias = torch.nn.Parameter(torch.full((v_heads,), -3.0, device=device))
+        self.ffn, self.act, self.w8, self.w4 = ffn, act, None, None
+        if ffn:
+            self.w_ffn_gate, self.w_ffn_up = weight(ffn, width, fan=width), weight(ffn, width, fan=width)
+            self.w_ffn_down = weight(width, ffn, fan=ffn)
+            self.n_ffn_post, self.n_ffn_next = ones(width), ones(width)
+            self.ffn_gate = torch.nn.Parameter(torch.full((1, width), 0.5, device=device, dtype=dtype))
 
     def _inputs(self, h):
         gates = project(h, self.w_gates)
@@ -74,15 +88,59 @@ class MixerBlock(torch.nn.Module):
         q, k, v = mixed.split((n, n, self.v_heads * self.head), -1)
         return (q.unflatten(-1, (-1, self.head)), k.unflatten(-1, (-1, self.head)), v.unflatten(-1, (-1, self.head)))
 
-    def _finish(self, x, o, z):
+    def _branch(self, x, o, z):
         o, _ = mixer.branch_norm(None, o.reshape(-1, self.head), self.n_head, z.reshape(-1, self.head), act="silu")
-        y = project(o.view(x.shape[0], -1), self.w_out)
-        return mixer.branch_norm(x, y, self.n_post, self.gate, self.n_next, alpha=1.0)
+        return project(o.view(x.shape[0], -1), self.w_out)
+
+    def _finish(self, x, o, z):
+        x, h = mixer.branch_norm(x, self._branch(x, o, z), self.n_post, self.gate, self.n_next, alpha=1.0)
+        if not self.ffn:
+            return x, h
+        return self._ffn_end(x, project(feed_forward.gated_ffn(h, self.w_ffn_gate, self.w_ffn_up, act=self.act), self.w_ffn_down))
+
+    def _finish8(self, x, o, z):
+        """_finish with the feed-forward product in 8 bits: the sum's norm
+        leaves 8-bit rows."""
+        u, _ = mixer.branch_norm(None, self._branch(x, o, z), self.n_post, self.gate)
+        q, scale, x = feed_forward.norm_quant_fwd(x, self.n_next, u)
+        h = feed_forward.gated_ffn8_fwd(q, scale, *self.w8, act=self.act, dtype=x.dtype)
+        return self._ffn_end(x, project(h, self.w_ffn_down))
+
+    def _finish4(self, x, o, z):
+        """_finish with the feed-forward weights in 4 bits."""
+        x, h = mixer.branch_norm(x, self._branch(x, o, z), self.n_post, self.gate, self.n_next, alpha=1.0)
+        (gate, sg, zg), (up, su, zu), down = self.w4
+        h = feed_forward.gated_ffn_w4_fwd(h, gate, sg, up, su, zg, zu, group=self.group, act=self.act)
+        return self._ffn_end(x, feed_forward.linear_w4_fwd(h, *down, group=self.group))
+
+    def _ffn_end(self, x, y):
+        return mixer.branch_norm(x, y, self.n_ffn_post, self.ffn_gate, self.n_ffn_next, alpha=1.0)
+
+    def quantize(self, group=64):
+        """Copies of the feed-forward weights for serving: 8 bits for
+        ``prompts`` (bfloat16 and float16 blocks), 4 bits with groups of
+        `group` for ``step``."""
+        if not self.ffn:
+            raise ValueError("a block without a feed-forward half")
+        self.group = group
+        self.w8 = (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up))
+        self.w4 = tuple(feed_forward.quantize_w4(w, group, zeros=True)
+                        for w in (self.w_ffn_gate, self.w_ffn_up, self.w_ffn_down))
 
     def forward(self, x, h, cu_seqlens=None, states=None, want_states=False):
         """x: the residual stream [T, width], h: its norm; returns the next
         ones and, with want_states, (last conv inputs, delta states) of each
         sequence.  states: those of an earlier call on the same sequences."""
+        return self._sequences(x, h, cu_seqlens, states, want_states, self._finish)
+
+    @torch.no_grad()
+    def prompts(self, x, h, cu_seqlens=None, states=None, want_states=False):
+        """forward with the 8-bit weights of ``quantize``."""
+        if self.w8 is None:
+            raise ValueError("no 8-bit weights: call quantize first")
+        return self._sequences(x, h, cu_seqlens, states, want_states, self._finish8)
+
+    def _sequences(self, x, h, cu_seqlens, states, want_states, finish):
         qkv, z, decay, b = self._inputs(h)
         conv0, delta0 = states if states is not None else (None, None)
         mixed, conv1 = mixer.conv1d_causal(qkv, self.w_conv, self.b_conv, cu_seqlens=cu_seqlens, state=conv0,
@@ -90,7 +148,7 @@ class MixerBlock(torch.nn.Module):
         q, k, v = self._heads(mixed)
         o, delta1 = mixer.delta_rule(q, k, v, decay, b, cu_seqlens=cu_seqlens, state=delta0, qk_norm=True,
                                      want_state=want_states)
-        x, h = self._finish(x, o, z)
+        x, h = finish(x, o, z)
         return (x, h, (conv1, delta1)) if want_states else (x, h)
 
     def pools(self, slots):
@@ -102,12 +160,38 @@ class MixerBlock(torch.nn.Module):
     @torch.no_grad()
     def step(self, x, h, pools, slots=None):
         """One token for each request: x, h [R, width]; request r's states are
-        pools[..][slots[r]], moved on in place."""
+        pools[..][slots[r]], moved on in place.  The feed-forward weights are
+        those of 4 bits once ``quantize`` has made them."""
         qkv, z, decay, b = self._inputs(h)
         mixed = mixer.conv1d_causal_step(qkv, self.w_conv, self.b_conv, pools[0], slots)
         q, k, v = self._heads(mixed)
         o = mixer.delta_rule_step(q, k, v, decay, b, pools[1], slots, qk_norm=True)
-        return self._finish(x, o, z)
+        return self._finish(x, o, z) if self.w4 is None else self._finish4(x, o, z)
+
+
+def _serve(block, x, cu, prompts):
+    """Prompts, then four tokens each; returns the last tokens' norms."""
+    h = mixer.branch_norm_fwd(None, x, block.n_next)[0]
+    _, _, states = prompts(x, h, cu, want_states=True)
+    pools = block.pools(8)
+    slots = torch.tensor([3, 0, 6], dtype=torch.int32, device="cuda")
+    for pool, state in zip(pools, states):
+        pool[slots.long()] = state
+    for _ in range(4):
+        token = torch.randn(3, block.width, device="cuda").bfloat16()
+        _, out = block.step(token, mixer.branch_norm_fwd(None, token, block.n_next)[0], pools, slots)
+    return out
+
+
+def _train(block, x, cu, target):
+    opt = torch.optim.SGD(block.parameters(), lr=0.5)
+    for i in range(5):
+        _, h1 = block(x, mixer.branch_norm(None, x, block.n_next)[0], cu)
+        loss = (h1.float() - target.float()).pow(2).mean()
+        opt.zero_grad()
+        loss.backward()
+        opt.step()
+        print(f"training step {i}: loss {loss.item():.4f}")
 
 
 def main():
@@ -117,25 +201,16 @@ def main():
     cu = torch.tensor([0, 37, 237, 242], dtype=torch.int32, device="cuda")
     x = torch.randn(sum(lens), block.width, device="cuda").bfloat16()
     with torch.no_grad():
-        h = mixer.branch_norm_fwd(None, x, block.n_next)[0]
-        _, _, states = block(x, h, cu, want_states=True)
-        pools = block.pools(8)
-        slots = torch.tensor([3, 0, 6], dtype=torch.int32, device="cuda")
-        for pool, state in zip(pools, states):
-            pool[slots.long()] = state
-        for _ in range(4):
-            token = torch.randn(3, block.width, device="cuda").bfloat16()
-            _, out = block.step(token, mixer.branch_norm_fwd(None, token, block.n_next)[0], pools, slots)
+        out = _serve(block, x, cu, block)
     print(f"prompts of {lens} tokens, then 4 tokens each: rms {out.float().pow(2).mean().sqrt().item():.4f}")
     target = torch.randn_like(x)
-    opt = torch.optim.SGD(block.parameters(), lr=0.5)
-    for i in range(5):
-        _, h1 = block(x, mixer.branch_norm(None, x, block.n_next)[0], cu)
-        loss = (h1.float() - target.float()).pow(2).mean()
-        opt.zero_grad()
-        loss.backward()
-        opt.step()
-        print(f"training step {i}: loss {loss.item():.4f}")
+    _train(block, x, cu, target)
+    block = MixerBlock(ffn=1536)
+    print("with a feed-forward half")
+    _train(block, x, cu, target)
+    block.quantize()
+    out = _serve(block, x, cu, block.prompts)
+    print(f"prompts in 8 bits, tokens in 4: rms {out.float().pow(2).mean().sqrt().item():.4f}")
 
 
 if __name__ == "__main__":
