@@ -59,36 +59,44 @@ bool w4_weights_ok(const void *w, const void *scales, const void *zeros, conv_dt
 }  // namespace
 
 // The time of a product is that of the blocks of one CU, one K tile after another.
-// A block's K tile of 128 bytes takes, in hundredths of a microsecond (bf16, all
-// CUs at work; 256 x 128 is the tile's rows of a by columns of each half of b):
-//   256 x 128  115, one block on a CU at a time;
-//   256 x 64    82;
-//   128 x 64    62, two at once 100;
-//   64 x 32     42, two 56, three 94.
-// (4096 to 10240 features, fwd: 200 tokens 74, 55, 66, 72 us in this order, 512: 80, 108,
-// 101, 149, 128: 71, 51, 46, 60; 2048 to 4096: 400 tokens 38, 28, 20, 29, 200: 37, 27, 19,
-// 16.)  float32 tiles take what their matrix instructions do, 16 times a 16-bit
-// tile's 16 cycles each.  A product that needs no second matrix (plain) may share
-// its K tiles out to several grids, whose float32 sums are written, read and added
-// by one more launch: 4 us and 8 bytes a value and grid at 4 TB/s.  (200 tokens, 4096
-// wide, 20480 summed: 135 us in one grid of 64 x 32, 42 in eight of 256 x 64.)
-FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec) {
+// A block's K tile of 128 bytes takes, in microseconds (bf16, all CUs at work; 256 x
+// 128 is the tile's rows of a by columns of each half of b):
+//   256 x 128  1.15, one block on a CU at a time;
+//   256 x 64   0.82;
+//   128 x 64   0.62, two at once 1.00;
+//   64 x 32    0.42, two 0.56, three 0.94;
+//   32 x 32    0.27, two 0.34, three 0.45, four 0.60.
+// (forward, 4096 to 10240 features: 512 tokens 80, 108, 101, 149, 198 us in this order, 200
+// tokens 74, 55, 66, 72, 99, 128 tokens 71, 51, 46, 60, 67; 2048 to 4096: 400 tokens 38, 28,
+// 20, 29, 32, 200 tokens 37, 27, 19, 16, 21, 64 tokens 35, 26, 18, 14, 11.)  float32 tiles
+// take what their matrix instructions do, 16 times a 16-bit tile's 16 cycles each.  Rows
+// at any address (64 x 32 only) wait for their way through registers: 2.0, two at
+// once 2.1, three 2.4 (gradients of 768 tokens, 500 to 800 features: 77 us with the
+// times of aligned rows, 42 with these).  A
+// product that needs no second matrix (plain) may share its K tiles out to several
+// grids, whose float32 sums are written, read and added by one more launch: 4 us and
+// 8 bytes a value and grid at 4 TB/s.  (Both gradients' products of 200 tokens, 4096
+// wide and 10240: 246 us in one grid of 64 x 32 each, 160 as chosen here.)
+FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec, bool a_of_m) {
     static const struct {
         int m, n;
-        double at[3];  // of one, two, three blocks on a CU
+        double at[4];  // of one, two, three, four blocks on a CU
         int most;
-    } kTiles[] = {{256, 128, {1.15}, 1}, {256, 64, {0.82}, 1}, {128, 64, {0.62, 1.00}, 2}, {64, 32, {0.42, 0.56, 0.94}, 3}};
+    } kTiles[] = {{256, 128, {1.15}, 1}, {256, 64, {0.82}, 1}, {128, 64, {0.62, 1.00}, 2}, {64, 32, {0.42, 0.56, 0.94}, 3},
+                  {32, 32, {0.27, 0.34, 0.45, 0.60}, 4}};
     const int per = 128 / value_bytes, nk = K ? (K - 1) / per + 1 : 1;
     FfnPlan best{FFN_TILE_64x32, 1};
     double least = 1e300;
-    for (int t = vec ? 0 : 3; t < 4; ++t) {
+    for (int t = vec ? 0 : 3; t < (vec && !a_of_m ? 5 : 4); ++t) {
         const int n = plain ? 2 * kTiles[t].n : kTiles[t].n;
         const double blocks = (double)((M + kTiles[t].m - 1) / kTiles[t].m) * ((N + n - 1) / n);
         for (int s = 1; s <= (plain ? 32 : 1) && (s == 1 || nk / s >= 4); ++s) {
             const double on = std::ceil(blocks * s / 256);  // blocks of a CU
             const int most = kTiles[t].most, rest = (int)std::fmod(on, most);
-            double tile = (on - rest) / most * kTiles[t].at[most - 1] + (rest ? kTiles[t].at[rest - 1] : 0.0);
-            if (value_bytes == 4) tile = on * kTiles[t].m * kTiles[t].n * 2 / 65536.0 * 7.2;
+            static const double kAny[] = {2.0, 2.1, 2.4};
+            const double *at = vec ? kTiles[t].at : kAny;
+            double tile = (on - rest) / most * at[most - 1] + (rest ? at[rest - 1] : 0.0);
+            if (value_bytes == 4 && vec) tile = on * kTiles[t].m * kTiles[t].n * 2 / 65536.0 * 7.2;
             double us = tile * ((nk + s - 1) / s + 2);
             if (s > 1) us += 4 + (double)s * M * ffn_part_pitch(N) * 8 / 4e6;
             if (us < least) least = us, best = {t, s};
@@ -162,7 +170,7 @@ conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t
     const int es = (int)bytes_of(dtype), Fp = padded(F, dtype);
     size_t part = 0;
     for (int vec = 0; vec < 2; ++vec) {
-        const int dx = ffn_plan(T, D, 2 * Fp, es, true, vec).splits, dw = ffn_plan(2 * (int64_t)Fp, D, (int)T, es, true, vec).splits;
+        const int dx = ffn_plan(T, D, 2 * Fp, es, true, vec, false).splits, dw = ffn_plan(2 * (int64_t)Fp, D, (int)T, es, true, vec, true).splits;
         if (dx > 1) part = std::max(part, (size_t)dx * T * ffn_part_pitch(D) * 4);
         if (dw > 1) part = std::max(part, (size_t)dw * 2 * Fp * ffn_part_pitch(D) * 4);
     }

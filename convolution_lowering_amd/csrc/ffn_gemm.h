@@ -698,14 +698,15 @@ hipError_t ffn_run(FfnGemmArgs a, hipStream_t st) {
     constexpr bool PLAIN = EPI == FFN_PLAIN;
     bool vec = (AM && BMM ? 0 : a.K) % V == 0 && (AM ? a.M : 0) % V == 0 && (BMM ? a.N : 0) % V == 0 && a.as % V == 0 && a.bs % V == 0;
     for (const void *p : {a.a, a.b0, a.b1}) vec = vec && (uintptr_t)p % 16 == 0;
-    const FfnPlan plan = ffn_plan(a.M, a.N, a.K, (int)sizeof(S), PLAIN, vec);
+    const FfnPlan plan = ffn_plan(a.M, a.N, a.K, (int)sizeof(S), PLAIN, vec, AM);
     a.splits = plan.splits;
-    hipError_t e;
+    hipError_t e = hipErrorInvalidValue;
     if (!vec) e = ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
     else if (plan.tile == FFN_TILE_256x128) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x128>(a, st);
     else if (plan.tile == FFN_TILE_256x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x64>(a, st);
     else if (plan.tile == FFN_TILE_128x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile128x64>(a, st);
-    else e = ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
+    else if (AM || plan.tile == FFN_TILE_64x32) e = ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
+    else if constexpr (!AM) e = ffn_run_small<S, O, EPI, 32, 32, false, AM, BMM>(a, st);
     if constexpr (PLAIN) {
         if (e != hipSuccess || a.splits == 1) return e;
         const int64_t blocks = (a.M * (ffn_part_pitch(a.N) / 4) + 255) / 256;

@@ -97,12 +97,12 @@ struct FfnGemmArgs {
 __host__ __device__ inline int64_t ffn_part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
 
 // The tile and the number of parts of a product.  vec: rows at multiples of 16
-// bytes (else only the smallest tile's loop is there).
-enum FfnTileKind { FFN_TILE_256x128, FFN_TILE_256x64, FFN_TILE_128x64, FFN_TILE_64x32 };  // of m, of each half of b
+// bytes (else there is a loop for 64 x 32 only); a_of_m: a as rows of m (not 32 x 32).
+enum FfnTileKind { FFN_TILE_256x128, FFN_TILE_256x64, FFN_TILE_128x64, FFN_TILE_64x32, FFN_TILE_32x32 };  // of m, of each half of b
 struct FfnPlan {
     int tile, splits;
 };
-FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec);
+FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec, bool a_of_m);
 hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int out_dtype, hipStream_t st);
 hipError_t launch_ffn_dx(const FfnGemmArgs &a, int dtype, hipStream_t st);  // a: rows of k, b: rows of m
 hipError_t launch_ffn_dw(const FfnGemmArgs &a, int dtype, hipStream_t st);  // both: rows of m
