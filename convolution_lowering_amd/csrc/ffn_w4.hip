@@ -15,8 +15,14 @@
 // A block has 16 features of each matrix; its wavefronts share out the 128-value
 // pieces of the rows and run apart from one another, their sums meet in LDS in a
 // fixed order.  Codes and x go from memory to registers, the next pieces' on their
-// way and no branch between them (each would end in a wait for all of them); scales
-// pass through LDS.
+// way and no branch between them (each would end in a wait for all of them).  They
+// are loaded along the rows, neighbouring lanes side by side, and come into the
+// matrix instructions' order (neighbouring lanes in different rows) by LDS: loaded
+// in that order each lane's 16 bytes are an access of its own to the first cache, which
+// bounds the kernel from some 8 tokens on (4096 to 10240 gated, bf16, groups of 128: 16 and
+// 32 tokens 22 and 33 us, by LDS 16 and 25).  Up to 4 tokens there is little of x, and
+// both are loaded in that order (DIRECT; 1 token 15 us, by LDS 17).  Scales pass
+// through LDS as well.
 #include "ffn_internal.h"
 
 namespace convlower {
@@ -86,7 +92,7 @@ __device__ __forceinline__ void w4_transpose(uint32_t (&d)[4]) {
     d[0] = c[0], d[1] = c[1], d[2] = e[0], d[3] = e[1];
 }
 
-constexpr int kScaleBytes = 16384;  // scales and zero points in LDS at a time
+constexpr int kScaleBytes = 8192;  // scales and zero points in LDS at a time (32 gated tokens, groups of 128: 24 us, with 16 KB 30)
 
 template <typename S>
 struct W4Scale {
@@ -95,7 +101,7 @@ struct W4Scale {
 
 // NT: 16-token tiles, all of them a wavefront's; WAVES of them share out the pieces.
 // VEC: rows of x at multiples of 4 bytes.
-template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC>
+template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC, bool DIRECT>
 __device__ __forceinline__ void w4_body(const W4Args &A) {
     using T = W4Type<S>;
     constexpr int NM = GATED ? 2 : 1, SUB = kPiece / GROUP, STEPS = 4 / SUB;
@@ -107,7 +113,9 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     static_assert(SPAN >= AHEAD, "scales have room");
     typedef MfmaShape<typename T::mma_t, 16> MF;
     __shared__ W4Scale<S> scales[ROWS * PER];
-    __shared__ f32x4_t sums[WAVES][NM][64];
+    // a wavefront's piece of x and of codes; in the end its sums
+    constexpr int ROOM = ((DIRECT ? 0 : NT * 16 * kPiece * ES) + NM * 1024) / 16;
+    __shared__ uint4 turned[WAVES][ROOM];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
     const int f0 = blockIdx.x * 16;
@@ -122,45 +130,58 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     for (int m = 0; m < NM; ++m) rw[m] = make_rsrc(A.w[m] + f0 * pitch, (uint32_t)(min(16, A.F - f0) * pitch));
     const S *const x0 = (const S *)A.x + r0 * A.xs;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(x0, (uint32_t)(((int64_t)(rows - 1) * A.xs + A.D) * ES));
-    const uint32_t code_at = (uint32_t)((lane & 15) * pitch) + q * 16;
-    uint32_t x_at[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) x_at[n] = (uint32_t)((16 * n + (lane & 15)) * A.xs * ES);
-    const int x_first = SUB == 1 ? q * 32 : q * 8;  // value of a piece; chunk j begins x_step values further on
-    constexpr int x_step = SUB == 1 ? 8 : 32;
+    // Load i of a tile's x: rows RPL i + lane / UNITS, unit lane % UNITS of a piece; of
+    // codes: row lane / 4, 16 bytes lane % 4.  In LDS unit u of row r lies in place u ^ r,
+    // 16 bytes c of row r of codes in c ^ r / 4, so that both ways take all banks.
+    constexpr int UNITS = kPiece / UNIT, RPL = 64 / UNITS, LOADS = 16 / RPL;
+    const uint32_t code_at = DIRECT ? (uint32_t)((lane & 15) * pitch) + q * 16 : (uint32_t)((lane >> 2) * pitch) + (lane & 3) * 16;
+    const int code_first = (DIRECT ? q : lane & 3) * 32;  // its first value of a piece
+    auto unit_of = [&](int i) {
+        if constexpr (!DIRECT) return lane % UNITS;
+        const int j = i / XL;
+        return (SUB == 1 ? q * 4 + j : j * 4 + q) * XL + i % XL;
+    };
+    auto row_of = [&](int i) { return DIRECT ? lane & 15 : RPL * i + lane / UNITS; };
     struct Piece {
-        uint32_t w[NM][4];
-        uint4 x[NT][4][XL];
+        uint4 w[NM], x[NT][LOADS];
     };
     auto load_x = [&](Piece &p, int piece) {
-        const int left = A.D - piece * kPiece;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < XL; ++e) {
-                    const int d = x_first + j * x_step + e * UNIT;
-                    if constexpr (VEC) {
-                        p.x[n][j][e] = __builtin_bit_cast(
-                            uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(d < left ? x_at[n] + d * ES : kOutOfRange), piece * kPiece * ES, 0));
-                    } else {  // (the first eight values in their place, and zeros)
-                        const bool in = 16 * n + (lane & 15) < rows && d < left;
-                        const FfnAnyVec<S, UNIT> v = *(const FfnAnyVec<S, UNIT> *)(x0 + (in ? (16 * n + (lane & 15)) * A.xs + piece * kPiece + d : 0));
-                        __builtin_memcpy(&p.x[n][j][e], &v, 16);
-                        if (!in) p.x[n][j][e] = make_uint4(0, 0, 0, 0);
-                    }
+            for (int i = 0; i < LOADS; ++i) {
+                const int row = 16 * n + row_of(i), unit = unit_of(i);
+                const bool in = piece * kPiece + unit * UNIT < A.D;
+                if constexpr (VEC) {
+                    p.x[n][i] = __builtin_bit_cast(
+                        uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(in ? (uint32_t)(row * A.xs * ES) + unit * 16 : kOutOfRange), piece * kPiece * ES, 0));
+                } else {  // (the first values in their place, and zeros)
+                    const bool here = in && row < rows;
+                    const FfnAnyVec<S, UNIT> v = *(const FfnAnyVec<S, UNIT> *)(x0 + (here ? row * A.xs + piece * kPiece + unit * UNIT : 0));
+                    __builtin_memcpy(&p.x[n][i], &v, 16);
+                    if (!here) p.x[n][i] = make_uint4(0, 0, 0, 0);
                 }
+            }
     };
     auto load = [&](Piece &p, int turn) {
         const int piece = turn * WAVES + wave;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const uint4 v = __builtin_bit_cast(
+        for (int m = 0; m < NM; ++m)
+            p.w[m] = __builtin_bit_cast(
                 uint4, __builtin_amdgcn_raw_buffer_load_b128(rw[m], (int)(piece < full ? code_at : kOutOfRange), piece * (kPiece / 2), 0));
-            p.w[m][0] = v.x, p.w[m][1] = v.y, p.w[m][2] = v.z, p.w[m][3] = v.w;
-        }
         load_x(p, piece);
+    };
+    // This wavefront's piece in LDS, and its way there.
+    uint4 *const mine = turned[wave];
+    const int code_to = (lane >> 2) * 4 + ((lane & 3) ^ (lane >> 4)), code_from = (lane & 15) * 4 + (q ^ ((lane & 15) >> 2));
+    auto turn_x = [&](const Piece &p) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int row = row_of(i);
+                mine[(n * 16 + row) * UNITS + (unit_of(i) ^ row)] = p.x[n][i];
+            }
     };
     auto scales_of = [&](int turn) {  // of the span that begins with this turn
         const int g0 = turn * WAVES * SUB, per = min(PER, (A.groups + SUB - 1) / SUB * SUB - g0);
@@ -182,10 +203,18 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     constexpr uint32_t one = __is_same(S, _Float16) ? 0x3c003c00u : 0x3f803f80u;
     const uint4 ones = make_uint4(one, one, one, one);
     // Piece `in` of the span; if not `there`, to no effect (a code of 0 is not a weight of 0).
-    auto work = [&](Piece &p, int in, bool there) {
-        if constexpr (SUB > 1) {  // a product's 32 values lie in one group
+    auto work = [&](const Piece &p, int in, bool there) {
+        if constexpr (!DIRECT) {
+            turn_x(p);
 #pragma unroll
-            for (int m = 0; m < NM; ++m) w4_transpose(p.w[m]);
+            for (int m = 0; m < NM; ++m) mine[NT * 16 * UNITS + m * 64 + code_to] = p.w[m];
+        }
+        uint32_t w[NM][4];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const uint4 v = DIRECT ? p.w[m] : mine[NT * 16 * UNITS + m * 64 + code_from];
+            w[m][0] = v.x, w[m][1] = v.y, w[m][2] = v.z, w[m][3] = v.w;
+            if constexpr (SUB > 1) w4_transpose(w[m]);  // a product's 32 values lie in one group
         }
 #pragma unroll
         for (int g = 0; g < SUB; ++g) {
@@ -194,12 +223,16 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
             for (int j = g * STEPS; j < (g + 1) * STEPS; ++j) {
                 uint4 codes[NM];
 #pragma unroll
-                for (int m = 0; m < NM; ++m) codes[m] = w4_codes<S>(p.w[m][j]);
+                for (int m = 0; m < NM; ++m) codes[m] = w4_codes<S>(w[m][j]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
+                    const int first = (SUB == 1 ? q * 4 + j : j * 4 + q) * XL, row = lane & 15;
+                    const uint4 *at = mine + (n * 16 + row) * UNITS;
                     uint4 x[T::PARTS];
-                    if constexpr (ES == 2) x[0] = w4_order(p.x[n][j][0]);
-                    else w4_parts(p.x[n][j][0], p.x[n][j][XL - 1], x);
+                    if constexpr (DIRECT && ES == 2) x[0] = w4_order(p.x[n][j]);
+                    else if constexpr (DIRECT) w4_parts(p.x[n][j * XL], p.x[n][j * XL + XL - 1], x);
+                    else if constexpr (ES == 2) x[0] = w4_order(at[first ^ row]);
+                    else w4_parts(at[first ^ row], at[(first + 1) ^ row], x);
 #pragma unroll
                     for (int k = 0; k < T::PARTS; ++k) {
                         MF::mma(x[k], ones, all[n]);
@@ -249,22 +282,26 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
         __syncthreads();
         if (full % WAVES == wave) {
 #pragma unroll
-            for (int m = 0; m < NM; ++m)
+            for (int m = 0; m < NM; ++m) {
+                uint32_t v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    piece[0].w[m][j] = __builtin_amdgcn_raw_buffer_load_b32(
-                        rw[m], (int)(full * kPiece + q * 32 + j * 8 < A.D ? code_at + j * 4 : kOutOfRange), full * (kPiece / 2), 0);
+                    v[j] = __builtin_amdgcn_raw_buffer_load_b32(
+                        rw[m], (int)(full * kPiece + code_first + j * 8 < A.D ? code_at + j * 4 : kOutOfRange), full * (kPiece / 2), 0);
+                piece[0].w[m] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
             load_x(piece[0], full);
             work(piece[0], full - first * WAVES, true);
         }
     }
 
     // Result: lane l holds feature l % 16 and tokens 4 (l / 16) .. + 3 of a tile.
+    static_assert(NM * 64 <= ROOM, "the sums' room");
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (n) __syncthreads();
 #pragma unroll
-        for (int m = 0; m < NM; ++m) sums[wave][m][lane] = acc[n][m];
+        for (int m = 0; m < NM; ++m) mine[m * 64 + lane] = __builtin_bit_cast(uint4, acc[n][m]);
         __syncthreads();
         const int tok = threadIdx.x >> 4, f = threadIdx.x & 15, at = (tok >> 2) * 16 + f;
         const int64_t r = r0 + 16 * n + tok;
@@ -274,22 +311,22 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
             for (int m = 0; m < NM; ++m) {
                 y[m] = 0.f;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) y[m] += sums[w][m][at][tok & 3];
+                for (int w = 0; w < WAVES; ++w) y[m] += ((const float *)&turned[w][m * 64 + at])[tok & 3];
             }
             ((S *)A.y)[r * A.F + f0 + f] = mix_out<S>(GATED ? ffn_act<S>(y[0], A.act) * y[NM - 1] : y[0]);
         }
     }
 }
-template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC>
+template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC, bool DIRECT>
 __global__ __launch_bounds__(WAVES * 64, NT == 1 ? (GROUP == 128 ? 4 : 3) : NT == 2 && GROUP == 128 ? 3 : 2) void w4_kernel(W4Args A) {
-    w4_body<S, NT, WAVES, GROUP, GATED, VEC>(A);
+    w4_body<S, NT, WAVES, GROUP, GATED, VEC, DIRECT>(A);
 }
 
-template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC>
+template <typename S, int NT, int WAVES, int GROUP, bool GATED, bool VEC, bool DIRECT>
 hipError_t w4_run(const W4Args &a, hipStream_t st) {
     const int64_t x = (a.F + 15) / 16, y = (a.R + 16 * NT - 1) / (16 * NT);
     if (!grid_fits(x, WAVES * 64, y)) return kTooLarge;
-    hipLaunchKernelGGL((w4_kernel<S, NT, WAVES, GROUP, GATED, VEC>), dim3((unsigned)x, (unsigned)y), dim3(WAVES * 64), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<S, NT, WAVES, GROUP, GATED, VEC, DIRECT>), dim3((unsigned)x, (unsigned)y), dim3(WAVES * 64), 0, st, a);
     return hipGetLastError();
 }
 // Blocks of four wavefronts where there are enough of them for every CU to hold two or
@@ -297,19 +334,22 @@ hipError_t w4_run(const W4Args &a, hipStream_t st) {
 // against 25 with eight wavefronts); eight where there are few (256 blocks, R = 1, 4096
 // wide: 5.4 us against 7.1 with sixteen).  Four token tiles at once but for the
 // groups whose sums do not fit the registers (gated, 32: 64 tokens 114 us, two by two 84).
-template <typename S, int NT, int GROUP, bool GATED>
+template <typename S, int NT, int GROUP, bool GATED, bool DIRECT>
 hipError_t w4_waves(const W4Args &a, hipStream_t st) {
-    return a.F >= 6144 ? w4_run<S, NT, 4, GROUP, GATED, true>(a, st) : w4_run<S, NT, 8, GROUP, GATED, true>(a, st);
+    return a.F >= 6144 ? w4_run<S, NT, 4, GROUP, GATED, true, DIRECT>(a, st) : w4_run<S, NT, 8, GROUP, GATED, true, DIRECT>(a, st);
 }
 template <typename S, int GROUP, bool GATED>
 hipError_t w4_tokens(const W4Args &a, hipStream_t st) {
     if constexpr (sizeof(S) == 4) {
-        return w4_waves<S, 1, GROUP, GATED>(a, st);
+        return a.R <= 4 ? w4_waves<S, 1, GROUP, GATED, true>(a, st) : w4_waves<S, 1, GROUP, GATED, false>(a, st);
     } else {
-        if ((uintptr_t)a.x % 4 || a.xs % 2) return w4_run<S, 1, 8, GROUP, GATED, false>(a, st);
-        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED>(a, st);
-        if (a.R <= 32 || (GROUP == 32 && GATED)) return w4_waves<S, 2, GROUP, GATED>(a, st);
-        if constexpr (GROUP != 32 || !GATED) return w4_waves<S, 4, GROUP, GATED>(a, st);
+        if ((uintptr_t)a.x % 4 || a.xs % 2) return w4_run<S, 1, 8, GROUP, GATED, false, false>(a, st);
+        if (a.R <= 4) return w4_waves<S, 1, GROUP, GATED, true>(a, st);
+        // (gated groups of 32 are bound by their scales' arithmetic: 32 tokens 57 us by LDS, 42 in that order)
+        constexpr bool direct = GROUP == 32 && GATED;
+        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED, direct>(a, st);
+        if (direct || a.R <= 32) return w4_waves<S, 2, GROUP, GATED, direct>(a, st);
+        if constexpr (!direct) return w4_waves<S, 4, GROUP, GATED, false>(a, st);
     }
     return hipErrorInvalidValue;
 }
