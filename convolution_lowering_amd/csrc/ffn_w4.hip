@@ -345,11 +345,10 @@ hipError_t w4_tokens(const W4Args &a, hipStream_t st) {
     } else {
         if ((uintptr_t)a.x % 4 || a.xs % 2) return w4_run<S, 1, 8, GROUP, GATED, false, false>(a, st);
         if (a.R <= 4) return w4_waves<S, 1, GROUP, GATED, true>(a, st);
-        // (gated groups of 32 are bound by their scales' arithmetic: 32 tokens 57 us by LDS, 42 in that order)
-        constexpr bool direct = GROUP == 32 && GATED;
-        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED, direct>(a, st);
-        if (direct || a.R <= 32) return w4_waves<S, 2, GROUP, GATED, direct>(a, st);
-        if constexpr (!direct) return w4_waves<S, 4, GROUP, GATED, false>(a, st);
+        // Gated groups of 32 spend their time on scales, not loads: 16 tokens 35 us, by LDS 38.
+        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED, GROUP == 32 && GATED>(a, st);
+        if (a.R <= 32 || (GROUP == 32 && GATED)) return w4_waves<S, 2, GROUP, GATED, false>(a, st);
+        if constexpr (GROUP != 32 || !GATED) return w4_waves<S, 4, GROUP, GATED, false>(a, st);
     }
     return hipErrorInvalidValue;
 }
