@@ -110,7 +110,7 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     constexpr int THREADS = WAVES * 64, ROWS = 16 * NM;
     constexpr int SPAN = kScaleBytes / (ROWS * SUB * (int)sizeof(W4Scale<S>)) / (WAVES * AHEAD) * AHEAD;  // turns whose scales have room
     constexpr int PER = SPAN * WAVES * SUB;                          // scales of a row and span
-    static_assert(SPAN >= AHEAD, "scales have room");
+    static_assert(SPAN >= AHEAD && PER % 16 == 0, "scales have room");
     typedef MfmaShape<typename T::mma_t, 16> MF;
     __shared__ W4Scale<S> scales[ROWS * PER];
     // a wavefront's piece of x and of codes; in the end its sums
@@ -183,6 +183,8 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
                 mine[(n * 16 + row) * UNITS + (unit_of(i) ^ row)] = p.x[n][i];
             }
     };
+    // (16 rows of one group lie on different banks: gated groups of 32, one token 27.5 us, unmixed 34.7)
+    auto scale_at = [](int row, int g) { return row * PER + (g ^ (row & 15)); };
     auto scales_of = [&](int turn) {  // of the span that begins with this turn
         const int g0 = turn * WAVES * SUB, per = min(PER, (A.groups + SUB - 1) / SUB * SUB - g0);
 #pragma unroll 4
@@ -195,7 +197,7 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
                 v.scale = ((const S *)(up ? A.scales[1] : A.scales[0]))[at];
                 v.zero = A.has_zeros ? ((const S *)(up ? A.zeros[1] : A.zeros[0]))[at] : mix_out<S>(8.f);
             }
-            scales[row * PER + g - g0] = v;
+            scales[scale_at(row, g - g0)] = v;
         }
     };
 
@@ -243,7 +245,7 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
             }
 #pragma unroll
             for (int m = 0; m < NM; ++m) {
-                const W4Scale<S> sz = scales[(m * 16 + (lane & 15)) * PER + in * SUB + g];
+                const W4Scale<S> sz = scales[scale_at(m * 16 + (lane & 15), in * SUB + g)];
                 const float s = there ? mix_f32(sz.scale) : 0.f, z = there ? T::OFFSET + mix_f32(sz.zero) : 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
