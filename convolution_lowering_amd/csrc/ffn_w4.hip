@@ -20,9 +20,15 @@
 // matrix instructions' order (neighbouring lanes in different rows) by LDS: loaded
 // in that order each lane's 16 bytes are an access of its own to the first cache, which
 // bounds the kernel from some 8 tokens on (4096 to 10240 gated, bf16, groups of 128: 16 and
-// 32 tokens 22 and 33 us, by LDS 16 and 25).  Up to 4 tokens there is little of x, and
+// 32 tokens 22 and 33 us, by LDS 16.6 and 22.6).  Up to 4 tokens there is little of x, and
 // both are loaded in that order (DIRECT; 1 token 15 us, by LDS 17).  Scales pass
 // through LDS as well.
+//
+// Inside a captured graph, bf16: 10240 to 4096, groups of 128: 1 token 8.4 us, of 21.6
+// MB (2.6 TB/s; the launch and the first pieces' way are 5 of them), 32 tokens 15.6, 64
+// tokens 24.9.  4096 to 10240 gated, groups of 128: 1 token 15.0 us (43 MB, 2.9 TB/s), 32
+// tokens 22.6, 64 tokens 40; groups of 32: 27.8, 52, 74, bound by the arithmetic on
+// scales, which is four times as much.
 #include "ffn_internal.h"
 
 namespace convlower {
@@ -335,7 +341,8 @@ hipError_t w4_run(const W4Args &a, hipStream_t st) {
 // more, so that all are there at once (640 blocks of 16 gated features, R = 1: 15.1 us
 // against 25 with eight wavefronts); eight where there are few (256 blocks, R = 1, 4096
 // wide: 5.4 us against 7.1 with sixteen).  Four token tiles at once but for the
-// groups whose sums do not fit the registers (gated, 32: 64 tokens 114 us, two by two 84).
+// groups whose sums do not fit the registers (gated, 32, 64 tokens: two by two 74 us;
+// with the scales' rows still on one bank 84, and 114 four at once).
 template <typename S, int NT, int GROUP, bool GATED, bool DIRECT>
 hipError_t w4_waves(const W4Args &a, hipStream_t st) {
     return a.F >= 6144 ? w4_run<S, NT, 4, GROUP, GATED, true, DIRECT>(a, st) : w4_run<S, NT, 8, GROUP, GATED, true, DIRECT>(a, st);
@@ -347,8 +354,7 @@ hipError_t w4_tokens(const W4Args &a, hipStream_t st) {
     } else {
         if ((uintptr_t)a.x % 4 || a.xs % 2) return w4_run<S, 1, 8, GROUP, GATED, false, false>(a, st);
         if (a.R <= 4) return w4_waves<S, 1, GROUP, GATED, true>(a, st);
-        // Gated groups of 32 spend their time on scales, not loads: 16 tokens 35 us, by LDS 38.
-        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED, GROUP == 32 && GATED>(a, st);
+        if (a.R <= 16) return w4_waves<S, 1, GROUP, GATED, false>(a, st);
         if (a.R <= 32 || (GROUP == 32 && GATED)) return w4_waves<S, 2, GROUP, GATED, false>(a, st);
         if constexpr (GROUP != 32 || !GATED) return w4_waves<S, 4, GROUP, GATED, false>(a, st);
     }

