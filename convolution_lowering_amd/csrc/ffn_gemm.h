@@ -26,7 +26,7 @@
 // 1420 TFLOP/s); 8192 tokens e4m3 509 to 590 (2330 to 2700); training, 8192 tokens, 4096 to
 // 8192: forward with g and u saved 940 us (1170; 768 MB written), dx 730 (1500), dw 790
 // (1390); 200 tokens 59 us, 4 tokens 38 (168 MB of weights, 4.4 TB/s).  The matrix
-// cores are busy 62 to 75 % of the time, no LDS access meets another's bank.
+// cores are busy 64 to 87 % of the time, no LDS access meets another's bank.
 #pragma once
 
 #include <type_traits>
