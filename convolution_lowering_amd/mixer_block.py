@@ -119,7 +119,8 @@ class MixerBlock(torch.nn.Module):
     def quantize(self, group=64):
         """Copies of the feed-forward weights for serving: 8 bits for
         ``prompts`` (bfloat16 and float16 blocks), 4 bits with groups of
-        `group` for ``step``."""
+        `group` for ``step``.  To be called again when the weights have
+        changed, or moved."""
         if not self.ffn:
             raise ValueError("a block without a feed-forward half")
         self.group = group

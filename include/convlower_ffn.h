@@ -69,10 +69,10 @@ conv_status_t gated_ffn8_fwd(const void *x, int64_t x_stride, const float *x_sca
  *   y[r,f] = sum_d x[r,d] scales[f, d / group] (code[f,d] - zeros[f, d / group])
  * x [R][D] (x_stride), D a multiple of 8; w [F][D/2] bytes, at a multiple of 4,
  * each with the codes (0..15) of two neighbours, the earlier one in the low half;
- * scales and zeros
- * [F][ceil(D / group)] in dtype, zeros NULL: 8; group 32, 64 or 128; y [R][F].
- * Made for a few tokens; more take the weights again for each 64 (float32: 16).  A
- * row of x that holds an infinity or a NaN gives NaN. */
+ * scales and zeros [F][ceil(D / group)] in dtype, zeros NULL: 8; group 32, 64 or
+ * 128; y [R][F].  Made for a few tokens: each 64 take the weights again (gated
+ * groups of 32: each 32; float32, and 16-bit rows at odd multiples of 2 bytes:
+ * each 16).  A row of x that holds an infinity or a NaN gives NaN. */
 conv_status_t linear_w4_fwd(const void *x, int64_t x_stride, const void *w, const void *scales, const void *zeros,
                             void *y, int64_t R, int D, int F, int group, conv_dtype_t dtype, conv_stream_t stream);
 
