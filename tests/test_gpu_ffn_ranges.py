@@ -85,6 +85,24 @@ def test_long_rows_of_codes(size):
 
 
 @pytest.mark.parametrize("t", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("tokens", [1, 4, 5, 16, 17, 32, 33, 65])
+def test_many_features_of_codes(tokens, group, t):
+    """As many features as have blocks of half the size, on both sides of each
+    number of tokens at which they are shared out another way."""
+    D, F = 264 + 8 * (tokens % 3), 6150
+    say("many features of codes", tokens, D, F, group, t)
+    (cg, sg, zg), (cu, su, zu) = (weights4(F, D, group, tokens % 2 == 0, t, s) for s in (2, 3))
+    x = torch.randn(tokens, D, generator=gen(6), device=DEV).to(t)
+    xd = x.double()
+    wg, wu = of.weights_w4(cg, sg, zg, group), of.weights_w4(cu, su, zu, group)
+    eg, eu = w4_tolerance(xd, wg, sg, zg, group, t), w4_tolerance(xd, wu, su, zu, group, t)
+    want, g, u = of.gated_ffn(xd, wg, wu, "silu")
+    near(ffn.linear_w4_fwd(x, cg, sg, zg, group=group), g, eg + half(t) * g.abs() * 1.01 + tiny(t), "y")
+    near(ffn.gated_ffn_w4_fwd(x, cg, sg, cu, su, zg, zu, group=group), want, gated_tolerance(g, u, eg, eu, "silu", t), "h")
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16, torch.float32], ids=str)
 def test_rows_at_any_address(t):
     """x, dh and weights one value past a multiple of 16 bytes, and rows of 4-bit
     products' x that begin at odd ones: the same results as in their place."""
