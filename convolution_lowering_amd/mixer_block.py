@@ -46,6 +46,40 @@ def project(x, w):
     return _Project.apply(x, w)
 
 
+def _capturing(t):
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
+def _renewed(old, new):
+    """`new`, written into the tensors of `old` where those are of its shapes,
+    types and device.  Both: tensors, None, or tuples of them."""
+    if isinstance(new, tuple):
+        return tuple(map(_renewed, old if old is not None else (None,) * len(new), new))
+    if old is None or new is None or (old.shape, old.dtype, old.device) != (new.shape, new.dtype, new.device):
+        return new
+    if old.is_inference() and not torch.is_inference_mode_enabled():  # (not to be written to)
+        return new
+    return old.copy_(new)
+
+
+class _Copied:
+    """Which weights copies were made of, and in which state."""
+
+    def __init__(self, weights=()):
+        self.weights, self.stamps = weights, self._stamps(weights)
+
+    @staticmethod
+    def _stamps(weights):
+        return [(None if w.is_inference() else w._version, w.device, w.dtype) for w in weights]
+
+    def still(self, weights):
+        return (len(self.weights) == len(weights) and all(a is b for a, b in zip(self.weights, weights)) and
+                self.stamps == self._stamps(weights))
+
+    def __reduce__(self):  # a copied or loaded block counts its weights' versions anew
+        return _Copied, ()
+
+
 class MixerBlock(torch.nn.Module):
     """ffn: the hidden size of a feed-forward half, None for none; act: its gate."""
 
@@ -70,7 +104,7 @@ class MixerBlock(torch.nn.Module):
         # decays -exp(a_log) softplus(.. + dt_bias), float32
         self.a_log = torch.nn.Parameter(torch.rand(v_heads, generator=g, device=device))
         self.dt_bias = torch.nn.Parameter(torch.full((v_heads,), -3.0, device=device))
-        self.ffn, self.act, self.w8, self.w4 = ffn, act, None, None
+        self.ffn, self.act, self.w8, self.w4, self._copied = ffn, act, None, None, None
         if ffn:
             self.w_ffn_gate, self.w_ffn_up = weight(ffn, width, fan=width), weight(ffn, width, fan=width)
             self.w_ffn_down = weight(width, ffn, fan=ffn)
@@ -119,14 +153,31 @@ class MixerBlock(torch.nn.Module):
     def quantize(self, group=64):
         """Copies of the feed-forward weights for serving: 8 bits for
         ``prompts`` (bfloat16 and float16 blocks), 4 bits with groups of
-        `group` for ``step``.  To be called again when the weights have
-        changed, or moved."""
+        `group` for ``step``.  Where the weights have changed since (a training
+        step, load_state_dict, another device or type), ``prompts`` and ``step``
+        make the copies again, in place where they fit, so that a captured
+        ``step`` takes the new ones too; what is written past autograd's
+        knowledge (``.data``) asks for a call of this."""
         if not self.ffn:
             raise ValueError("a block without a feed-forward half")
         self.group = group
-        self.w8 = (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up))
-        self.w4 = tuple(feed_forward.quantize_w4(w, group, zeros=True)
-                        for w in (self.w_ffn_gate, self.w_ffn_up, self.w_ffn_down))
+        self.w8 = _renewed(self.w8, (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up)))
+        self.w4 = _renewed(self.w4, tuple(feed_forward.quantize_w4(w, group, zeros=True) for w in self._ffn_weights()))
+        self._copied = _Copied(self._ffn_weights())
+
+    def _ffn_weights(self):
+        return self.w_ffn_gate, self.w_ffn_up, self.w_ffn_down
+
+    def _refresh(self):
+        """The copies of the weights as they are now."""
+        if self._copied is None or self._copied.still(self._ffn_weights()):
+            return
+        if _capturing(self.w_ffn_gate):
+            raise RuntimeError("the weights have changed since quantize: call it before the capture")
+        kept = self.w8, self.w4
+        self.quantize(self.group)
+        # (what a caller has taken out stays out)
+        self.w8, self.w4 = (None if old is None else new for old, new in zip(kept, (self.w8, self.w4)))
 
     def forward(self, x, h, cu_seqlens=None, states=None, want_states=False):
         """x: the residual stream [T, width], h: its norm; returns the next
@@ -139,6 +190,7 @@ class MixerBlock(torch.nn.Module):
         """forward with the 8-bit weights of ``quantize``."""
         if self.w8 is None:
             raise ValueError("no 8-bit weights: call quantize first")
+        self._refresh()
         return self._sequences(x, h, cu_seqlens, states, want_states, self._finish8)
 
     def _sequences(self, x, h, cu_seqlens, states, want_states, finish):
@@ -163,6 +215,8 @@ class MixerBlock(torch.nn.Module):
         """One token for each request: x, h [R, width]; request r's states are
         pools[..][slots[r]], moved on in place.  The feed-forward weights are
         those of 4 bits once ``quantize`` has made them."""
+        if self.w4 is not None:
+            self._refresh()
         qkv, z, decay, b = self._inputs(h)
         mixed = mixer.conv1d_causal_step(qkv, self.w_conv, self.b_conv, pools[0], slots)
         q, k, v = self._heads(mixed)
