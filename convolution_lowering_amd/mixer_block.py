@@ -160,9 +160,9 @@ class MixerBlock(torch.nn.Module):
         knowledge (``.data``) asks for a call of this."""
         if not self.ffn:
             raise ValueError("a block without a feed-forward half")
-        self.group = group
-        self.w8 = _renewed(self.w8, (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up)))
-        self.w4 = _renewed(self.w4, tuple(feed_forward.quantize_w4(w, group, zeros=True) for w in self._ffn_weights()))
+        w4 = tuple(feed_forward.quantize_w4(w, group, zeros=True) for w in self._ffn_weights())  # (refuses first)
+        w8 = (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up))
+        self.group, self.w8, self.w4 = group, _renewed(self.w8, w8), _renewed(self.w4, w4)
         self._copied = _Copied(self._ffn_weights())
 
     def _ffn_weights(self):

@@ -117,3 +117,18 @@ def test_other_ways(monkeypatch):
     written(block)
     serve(block)
     assert current(block)
+
+
+def test_a_refused_call_changes_nothing(monkeypatch):
+    """A group that there is not, and widths that 4 bits do not take, leave the
+    copies and their group as they were."""
+    block = block_of(monkeypatch)
+    block.quantize(32)
+    with pytest.raises(ValueError):
+        block.quantize(48)
+    assert block.group == 32 and current(block)
+    serve(block)
+    odd = MixerBlock(width=64, ffn=97, device="cpu")
+    with pytest.raises(ValueError):
+        odd.quantize(32)
+    assert odd.w8 is None and odd.w4 is None
