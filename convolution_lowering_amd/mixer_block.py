@@ -53,9 +53,11 @@ def _capturing(t):
 def _renewed(old, new):
     """`new`, written into the tensors of `old` where those are of its shapes,
     types and device.  Both: tensors, None, or tuples of them."""
+    if new is None:
+        return None
     if isinstance(new, tuple):
         return tuple(map(_renewed, old if old is not None else (None,) * len(new), new))
-    if old is None or new is None or (old.shape, old.dtype, old.device) != (new.shape, new.dtype, new.device):
+    if old is None or (old.shape, old.dtype, old.device) != (new.shape, new.dtype, new.device):
         return new
     if old.is_inference() and not torch.is_inference_mode_enabled():  # (not to be written to)
         return new
@@ -150,18 +152,25 @@ class MixerBlock(torch.nn.Module):
     def _ffn_end(self, x, y):
         return mixer.branch_norm(x, y, self.n_ffn_post, self.ffn_gate, self.n_ffn_next, alpha=1.0)
 
-    def quantize(self, group=64):
+    def quantize(self, group=64, bits=(8, 4)):
         """Copies of the feed-forward weights for serving: 8 bits for
         ``prompts`` (bfloat16 and float16 blocks), 4 bits with groups of
-        `group` for ``step``.  Where the weights have changed since (a training
+        `group` for ``step``.  bits: which of them; without 4, ``step`` stays
+        with the weights themselves, which past some 64 requests are faster
+        than 4-bit ones.  Where the weights have changed since (a training
         step, load_state_dict, another device or type), ``prompts`` and ``step``
         make the copies again, in place where they fit, so that a captured
         ``step`` takes the new ones too; what is written past autograd's
         knowledge (``.data``) asks for a call of this."""
         if not self.ffn:
             raise ValueError("a block without a feed-forward half")
-        w4 = tuple(feed_forward.quantize_w4(w, group, zeros=True) for w in self._ffn_weights())  # (refuses first)
-        w8 = (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up))
+        if not set(bits) <= {8, 4} or not bits:
+            raise ValueError(f"bits {bits!r}: 8, 4 or both wanted")
+        w8 = w4 = None
+        if 4 in bits:  # (refuses first)
+            w4 = tuple(feed_forward.quantize_w4(w, group, zeros=True) for w in self._ffn_weights())
+        if 8 in bits:
+            w8 = (*feed_forward.quantize_rows(self.w_ffn_gate), *feed_forward.quantize_rows(self.w_ffn_up))
         self.group, self.w8, self.w4 = group, _renewed(self.w8, w8), _renewed(self.w4, w4)
         self._copied = _Copied(self._ffn_weights())
 
@@ -174,10 +183,7 @@ class MixerBlock(torch.nn.Module):
             return
         if _capturing(self.w_ffn_gate):
             raise RuntimeError("the weights have changed since quantize: call it before the capture")
-        kept = self.w8, self.w4
-        self.quantize(self.group)
-        # (what a caller has taken out stays out)
-        self.w8, self.w4 = (None if old is None else new for old, new in zip(kept, (self.w8, self.w4)))
+        self.quantize(self.group, [n for n, w in ((8, self.w8), (4, self.w4)) if w is not None])
 
     def forward(self, x, h, cu_seqlens=None, states=None, want_states=False):
         """x: the residual stream [T, width], h: its norm; returns the next

@@ -132,3 +132,24 @@ def test_a_refused_call_changes_nothing(monkeypatch):
     with pytest.raises(ValueError):
         odd.quantize(32)
     assert odd.w8 is None and odd.w4 is None
+
+
+def test_only_the_copies_asked_for(monkeypatch):
+    """8 bits alone, at any width, leave step with the weights themselves; 4 bits
+    alone leave no prompts."""
+    block = block_of(monkeypatch)
+    block.quantize(bits=(8,))
+    assert block.w8 is not None and block.w4 is None
+    written(block)
+    block.prompts(None, None)
+    assert block.w4 is None and torch.equal(block.w8[1], ffn.quantize_rows(block.w_ffn_gate)[1])
+    block.quantize(32, bits=(4,))
+    assert block.w8 is None and block.w4 is not None
+    with pytest.raises(ValueError):
+        block.prompts(None, None)
+    odd = MixerBlock(width=64, ffn=97, device="cpu")
+    odd.quantize(bits=(8,))
+    assert odd.w8 is not None
+    for bad in ((), (16,), (8, 2)):
+        with pytest.raises(ValueError):
+            block.quantize(bits=bad)
