@@ -135,10 +135,10 @@ class MixerBlock(torch.nn.Module):
         return self._ffn_end(x, project(feed_forward.gated_ffn(h, self.w_ffn_gate, self.w_ffn_up, act=self.act), self.w_ffn_down))
 
     def _finish8(self, x, o, z):
-        """_finish with the feed-forward product in 8 bits: the sum's norm
-        leaves 8-bit rows."""
-        u, _ = mixer.branch_norm(None, self._branch(x, o, z), self.n_post, self.gate)
-        q, scale, x = feed_forward.norm_quant_fwd(x, self.n_next, u)
+        """_finish with the feed-forward product in 8 bits: the residual
+        stream is the same to the bit, and its norm leaves 8-bit rows."""
+        x, _ = mixer.branch_norm(x, self._branch(x, o, z), self.n_post, self.gate, alpha=1.0)
+        q, scale, _ = feed_forward.norm_quant_fwd(x, self.n_next)
         h = feed_forward.gated_ffn8_fwd(q, scale, *self.w8, act=self.act, dtype=x.dtype)
         return self._ffn_end(x, project(h, self.w_ffn_down))
 

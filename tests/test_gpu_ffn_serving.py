@@ -50,3 +50,17 @@ def test_prompts_and_steps_after_training():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, want[2:]))
+
+
+@torch.no_grad()
+def test_prompts_keep_the_residual_stream():
+    """With a closed feed-forward gate the residual stream of 8-bit prompts is that
+    of the block, bit for bit: the branch is added before anything is rounded."""
+    block = MixerBlock(width=128, seed=4, ffn=192)
+    block.ffn_gate.zero_()
+    block.quantize(bits=(8,))
+    x = prepared(2, 70)
+    h = mixer.branch_norm_fwd(None, x, block.n_next)[0]
+    want, got = block(x, h), block.prompts(x, h)
+    assert not torch.equal(want[0], x)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
