@@ -150,8 +150,8 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, saved, *, act="silu", stream=None):
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, act):
-        h, saved = gated_ffn_fwd(x, w_gate, w_up, act=act, save=any(ctx.needs_input_grad))
+    def forward(ctx, x, w_gate, w_up, act, save):
+        h, saved = gated_ffn_fwd(x, w_gate, w_up, act=act, save=save)
         ctx.save_for_backward(x, w_gate, w_up, saved)
         ctx.act = act
         return h
@@ -160,12 +160,14 @@ class _GatedFfn(torch.autograd.Function):
     @differentiable_once
     def backward(ctx, dh):
         x, w_gate, w_up, saved = ctx.saved_tensors
-        return (*gated_ffn_bwd(dh.contiguous(), x, w_gate, w_up, saved, act=ctx.act), None)
+        return (*gated_ffn_bwd(dh.contiguous(), x, w_gate, w_up, saved, act=ctx.act), None, None)
 
 
 def gated_ffn(x, w_gate, w_up, *, act="silu"):
     """gated_ffn_fwd as an autograd function; returns h."""
-    return _GatedFfn.apply(x, w_gate, w_up, act)
+    # (inside the function needs_input_grad counts parameters under no_grad too)
+    save = torch.is_grad_enabled() and any(t.requires_grad for t in (x, w_gate, w_up))
+    return _GatedFfn.apply(x, w_gate, w_up, act, save)
 
 
 def gated_ffn8_fwd(x, x_scale, w_gate, gate_scale, w_up, up_scale, *, act="silu", dtype=torch.bfloat16, stream=None):
