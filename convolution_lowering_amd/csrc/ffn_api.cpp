@@ -77,13 +77,16 @@ bool w4_weights_ok(const void *w, const void *scales, const void *zeros, conv_dt
 // grids, whose float32 sums are written, read and added by one more launch: 4 us and
 // 8 bytes a value and grid at 4 TB/s.  (Both gradients' products of 200 tokens, 4096
 // wide and 10240: 246 us in one grid of 64 x 32 each, 160 as chosen here.)
+static const struct {
+    int m, n;
+    double at[4];  // of one, two, three, four blocks on a CU
+    int most, threads;
+} kTiles[] = {{256, 128, {1.15}, 1, 512},
+              {256, 64, {0.82}, 1, 512},
+              {128, 64, {0.62, 1.00}, 2, 512},
+              {64, 32, {0.42, 0.56, 0.94}, 3, 256},
+              {32, 32, {0.27, 0.34, 0.45, 0.60}, 4, 256}};
 FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec, bool a_of_m) {
-    static const struct {
-        int m, n;
-        double at[4];  // of one, two, three, four blocks on a CU
-        int most;
-    } kTiles[] = {{256, 128, {1.15}, 1}, {256, 64, {0.82}, 1}, {128, 64, {0.62, 1.00}, 2}, {64, 32, {0.42, 0.56, 0.94}, 3},
-                  {32, 32, {0.27, 0.34, 0.45, 0.60}, 4}};
     const int per = 128 / value_bytes, nk = K ? (K - 1) / per + 1 : 1;
     FfnPlan best{FFN_TILE_64x32, 1};
     double least = 1e300;
@@ -103,6 +106,17 @@ FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec,
         }
     }
     return best;
+}
+
+bool ffn_choose(FfnGemmArgs &a, int dtype, bool plain, bool a_of_m, bool b_of_m) {
+    const int es = dtype == CONV_DTYPE_FP8_E4M3 ? 1 : (int)bytes_of((conv_dtype_t)dtype), V = 16 / es;
+    a.vec = (a_of_m && b_of_m ? 0 : a.K) % V == 0 && (a_of_m ? a.M : 0) % V == 0 && (b_of_m ? a.N : 0) % V == 0 && a.as % V == 0 && a.bs % V == 0;
+    for (const void *p : {a.a, a.b0, a.b1}) a.vec = a.vec && (uintptr_t)p % 16 == 0;
+    const FfnPlan plan = ffn_plan(a.M, a.N, a.K, es, plain, a.vec, a_of_m);
+    a.tile = plan.tile, a.splits = plan.splits;
+    const auto &t = kTiles[plan.tile];
+    const int n = plain ? 2 * t.n : t.n;
+    return grid_fits(((a.M + t.m - 1) / t.m) * ((a.N + n - 1) / n), t.threads, a.splits);
 }
 
 hipError_t launch_ffn_gated_f32(const FfnGemmArgs &a, bool saving, hipStream_t st);
@@ -160,6 +174,7 @@ conv_status_t gated_ffn_fwd(const void *x, int64_t x_stride, const void *w_gate,
     FfnGemmArgs a{};
     a.a = x, a.b0 = w_gate, a.b1 = w_up, a.as = x_stride, a.bs = D, a.M = T, a.N = F, a.K = D, a.act = act, a.out = h;
     a.saved = (float *)saved, a.pitch = saved_pitch(F);
+    if (!ffn_choose(a, dtype, false, false, false)) return CONV_ERR_UNSUPPORTED;
     return hip_status(launch_ffn_gated(a, saved ? FFN_SAVING : FFN_GATED, dtype, dtype, (hipStream_t)stream));
 }
 
@@ -198,20 +213,21 @@ conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, in
     FfnGateGrad d{};
     d.dh = dh, d.dhs = dh_stride, d.saved = (const float *)saved, d.pitch = saved_pitch(F), d.dgu = workspace;
     d.T = T, d.F = F, d.Fp = Fp, d.act = act;
-    hipError_t e = launch_ffn_gate_grad(d, dtype, (hipStream_t)stream);
     FfnGemmArgs a{};
-    a.a = workspace, a.as = 2 * (int64_t)Fp, a.bs = D, a.N = D;
+    a.a = workspace, a.as = 2 * (int64_t)Fp, a.N = D;
     if (T) a.part = (float *)((char *)workspace + dgu_bytes(T, F, dtype));
-    if (e == hipSuccess && T) {  // dx = [dg du] [w_gate; w_up]
-        a.b0 = w_gate, a.b1 = w_up, a.M = T, a.K = 2 * Fp, a.ktsplit = Fp / piece, a.brows = F;
-        a.out = dx, a.split = T, a.rows = T;
-        e = launch_ffn_dx(a, dtype, (hipStream_t)stream);
-    }
-    if (e == hipSuccess) {  // [dw_gate; dw_up] = [dg du]' x
-        a.b0 = a.b1 = x, a.bs = x_stride, a.M = 2 * (int64_t)Fp, a.K = (int)T, a.ktsplit = INT32_MAX, a.brows = (int)T;
-        a.out = dw_gate, a.out2 = dw_up, a.split = Fp, a.rows = F;
-        e = launch_ffn_dw(a, dtype, (hipStream_t)stream);
-    }
+    // dx = [dg du] [w_gate; w_up]
+    FfnGemmArgs x1 = a;
+    x1.b0 = w_gate, x1.b1 = w_up, x1.bs = D, x1.M = T, x1.K = 2 * Fp, x1.ktsplit = Fp / piece, x1.brows = F;
+    x1.out = dx, x1.split = T, x1.rows = T;
+    // [dw_gate; dw_up] = [dg du]' x
+    FfnGemmArgs w1 = a;
+    w1.b0 = w1.b1 = x, w1.bs = x_stride, w1.M = 2 * (int64_t)Fp, w1.K = (int)T, w1.ktsplit = INT32_MAX, w1.brows = (int)T;
+    w1.out = dw_gate, w1.out2 = dw_up, w1.split = Fp, w1.rows = F;
+    if ((T && !ffn_choose(x1, dtype, true, false, true)) || !ffn_choose(w1, dtype, true, true, true)) return CONV_ERR_UNSUPPORTED;
+    hipError_t e = launch_ffn_gate_grad(d, dtype, (hipStream_t)stream);
+    if (e == hipSuccess && T) e = launch_ffn_dx(x1, dtype, (hipStream_t)stream);
+    if (e == hipSuccess) e = launch_ffn_dw(w1, dtype, (hipStream_t)stream);
     return hip_status(e);
 }
 
@@ -227,6 +243,7 @@ conv_status_t gated_ffn8_fwd(const void *x, int64_t x_stride, const float *x_sca
     FfnGemmArgs a{};
     a.a = x, a.b0 = w_gate, a.b1 = w_up, a.as = x_stride, a.bs = D, a.M = T, a.N = F, a.K = D, a.act = act, a.out = h;
     a.a_scale = x_scale, a.b0_scale = gate_scale, a.b1_scale = up_scale;
+    if (!ffn_choose(a, CONV_DTYPE_FP8_E4M3, false, false, false)) return CONV_ERR_UNSUPPORTED;
     return hip_status(launch_ffn_gated(a, FFN_SCALED, CONV_DTYPE_FP8_E4M3, dtype, (hipStream_t)stream));
 }
 

@@ -686,7 +686,6 @@ template <typename S, typename O, FfnEpilogue EPI, int BM, int BH, bool ANY, boo
 hipError_t ffn_run_small(const FfnGemmArgs &a, hipStream_t st) {
     constexpr int BN = EPI == FFN_PLAIN ? 2 * BH : BH;
     const int64_t blocks = ((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
-    if (!grid_fits(blocks, 256, a.splits)) return kTooLarge;
     hipLaunchKernelGGL((ffn_small_kernel<S, O, EPI, BM, BH, ANY, AM, BMM>), dim3((unsigned)blocks, a.splits), dim3(256), 0, st, a);
     return hipGetLastError();
 }
@@ -694,28 +693,21 @@ template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM, typename C
 hipError_t ffn_run_large(const FfnGemmArgs &a, hipStream_t st) {
     constexpr int BN = EPI == FFN_PLAIN ? 2 * C::BH : C::BH;
     const int64_t blocks = ((a.M + C::BM - 1) / C::BM) * ((a.N + BN - 1) / BN);
-    if (!grid_fits(blocks, 512, a.splits)) return kTooLarge;
     hipLaunchKernelGGL((ffn_large_kernel<S, O, EPI, AM, BMM, C>), dim3((unsigned)blocks, a.splits), dim3(512), 0, st, a);
     return hipGetLastError();
 }
 
 // AM, BMM: a, b as rows of m (of columns that are there: M and N values wide).
 template <typename S, typename O, FfnEpilogue EPI, bool AM, bool BMM>
-hipError_t ffn_run(FfnGemmArgs a, hipStream_t st) {
-    constexpr int V = 16 / (int)sizeof(S);
-    constexpr bool PLAIN = EPI == FFN_PLAIN;
-    bool vec = (AM && BMM ? 0 : a.K) % V == 0 && (AM ? a.M : 0) % V == 0 && (BMM ? a.N : 0) % V == 0 && a.as % V == 0 && a.bs % V == 0;
-    for (const void *p : {a.a, a.b0, a.b1}) vec = vec && (uintptr_t)p % 16 == 0;
-    const FfnPlan plan = ffn_plan(a.M, a.N, a.K, (int)sizeof(S), PLAIN, vec, AM);
-    a.splits = plan.splits;
+hipError_t ffn_run(const FfnGemmArgs &a, hipStream_t st) {
     hipError_t e = hipErrorInvalidValue;
-    if (!vec) e = ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
-    else if (plan.tile == FFN_TILE_256x128) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x128>(a, st);
-    else if (plan.tile == FFN_TILE_256x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x64>(a, st);
-    else if (plan.tile == FFN_TILE_128x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile128x64>(a, st);
-    else if (AM || plan.tile == FFN_TILE_64x32) e = ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
+    if (!a.vec) e = ffn_run_small<S, O, EPI, 64, 32, true, AM, BMM>(a, st);
+    else if (a.tile == FFN_TILE_256x128) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x128>(a, st);
+    else if (a.tile == FFN_TILE_256x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile256x64>(a, st);
+    else if (a.tile == FFN_TILE_128x64) e = ffn_run_large<S, O, EPI, AM, BMM, FfnTile128x64>(a, st);
+    else if (AM || a.tile == FFN_TILE_64x32) e = ffn_run_small<S, O, EPI, 64, 32, false, AM, BMM>(a, st);
     else if constexpr (!AM) e = ffn_run_small<S, O, EPI, 32, 32, false, AM, BMM>(a, st);
-    if constexpr (PLAIN) {
+    if constexpr (EPI == FFN_PLAIN) {
         if (e != hipSuccess || a.splits == 1) return e;
         const int64_t blocks = (a.M * (ffn_part_pitch(a.N) / 4) + 255) / 256;
         hipLaunchKernelGGL((ffn_sum_kernel<O>), dim3((unsigned)(blocks < 1 << 16 ? blocks : 1 << 16)), dim3(256), 0, st, a);

@@ -90,8 +90,9 @@ struct FfnGemmArgs {
     float *saved;  // [2][M][pitch]
     int64_t pitch;
     const float *a_scale, *b0_scale, *b1_scale;
-    // plain: the K tiles shared out to `splits` grids, whose sums go to part
-    int splits;
+    // how the product is made (ffn_choose); plain: the K tiles shared out to `splits` grids, whose sums go to part
+    bool vec;
+    int tile, splits;
     float *part;  // [splits][M][ffn_part_pitch(N)]
 };
 __host__ __device__ inline int64_t ffn_part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
@@ -103,6 +104,10 @@ struct FfnPlan {
     int tile, splits;
 };
 FfnPlan ffn_plan(int64_t M, int N, int K, int value_bytes, bool plain, bool vec, bool a_of_m);
+// The plan of a product, into a; a_of_m, b_of_m: operands as rows of m.  False:
+// one launch does not hold its blocks.
+bool ffn_choose(FfnGemmArgs &a, int dtype, bool plain, bool a_of_m, bool b_of_m);
+// The launches take a plan that was chosen.
 hipError_t launch_ffn_gated(const FfnGemmArgs &a, FfnEpilogue e, int dtype, int out_dtype, hipStream_t st);
 hipError_t launch_ffn_dx(const FfnGemmArgs &a, int dtype, hipStream_t st);  // a: rows of k, b: rows of m
 hipError_t launch_ffn_dw(const FfnGemmArgs &a, int dtype, hipStream_t st);  // both: rows of m
