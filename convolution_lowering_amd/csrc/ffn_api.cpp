@@ -193,16 +193,16 @@ conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t
     return CONV_OK;
 }
 
-conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, int64_t x_stride, const void *w_gate,
-                            const void *w_up, const void *saved, size_t saved_bytes, void *dx, void *dw_gate,
-                            void *dw_up, int64_t T, int D, int F, ffn_act_t act, conv_dtype_t dtype,
-                            conv_stream_t stream, void *workspace, size_t workspace_bytes) {
+conv_status_t gated_ffn_bwd_some(const void *dh, int64_t dh_stride, const void *x, int64_t x_stride,
+                                 const void *w_gate, const void *w_up, const void *saved, size_t saved_bytes, void *dx,
+                                 void *dw_gate, void *dw_up, int64_t T, int D, int F, ffn_act_t act,
+                                 conv_dtype_t dtype, conv_stream_t stream, void *workspace, size_t workspace_bytes) {
     if (!ffn_dtype_ok(dtype)) return CONV_ERR_INVALID_ARG;
     conv_status_t st = ffn_sizes(T, D, F, act, x_stride);
     if (st != CONV_OK) return st;
     const size_t es = bytes_of(dtype);
-    if (!pointers_ok({w_gate, w_up, dw_gate, dw_up}, {dh, x, dx}, es) || dh_stride < F) return CONV_ERR_INVALID_ARG;
-    if (T && (!dh || !x || !dx)) return CONV_ERR_INVALID_ARG;
+    if (!pointers_ok({w_gate, w_up}, {dh, x, dx, dw_gate, dw_up}, es) || dh_stride < F) return CONV_ERR_INVALID_ARG;
+    if ((T && (!dh || !x)) || !dw_gate != !dw_up) return CONV_ERR_INVALID_ARG;
     if (!pointers_ok({}, {saved, workspace}, 16)) return CONV_ERR_INVALID_ARG;
     if (dh_stride > FFN_MAX_WIDTH) return CONV_ERR_UNSUPPORTED;
     size_t need = 0, keep = 0;
@@ -224,11 +224,23 @@ conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, in
     FfnGemmArgs w1 = a;
     w1.b0 = w1.b1 = x, w1.bs = x_stride, w1.M = 2 * (int64_t)Fp, w1.K = (int)T, w1.ktsplit = INT32_MAX, w1.brows = (int)T;
     w1.out = dw_gate, w1.out2 = dw_up, w1.split = Fp, w1.rows = F;
-    if ((T && !ffn_choose(x1, dtype, true, false, true)) || !ffn_choose(w1, dtype, true, true, true)) return CONV_ERR_UNSUPPORTED;
+    const bool want_dx = T && dx, want_dw = dw_gate;
+    if (want_dx && !ffn_choose(x1, dtype, true, false, true)) return CONV_ERR_UNSUPPORTED;
+    if (want_dw && !ffn_choose(w1, dtype, true, true, true)) return CONV_ERR_UNSUPPORTED;
+    if (!want_dx && !want_dw) return CONV_OK;
     hipError_t e = launch_ffn_gate_grad(d, dtype, (hipStream_t)stream);
-    if (e == hipSuccess && T) e = launch_ffn_dx(x1, dtype, (hipStream_t)stream);
-    if (e == hipSuccess) e = launch_ffn_dw(w1, dtype, (hipStream_t)stream);
+    if (e == hipSuccess && want_dx) e = launch_ffn_dx(x1, dtype, (hipStream_t)stream);
+    if (e == hipSuccess && want_dw) e = launch_ffn_dw(w1, dtype, (hipStream_t)stream);
     return hip_status(e);
+}
+
+conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, int64_t x_stride, const void *w_gate,
+                            const void *w_up, const void *saved, size_t saved_bytes, void *dx, void *dw_gate,
+                            void *dw_up, int64_t T, int D, int F, ffn_act_t act, conv_dtype_t dtype,
+                            conv_stream_t stream, void *workspace, size_t workspace_bytes) {
+    if ((T && !dx) || !dw_gate || !dw_up) return CONV_ERR_INVALID_ARG;
+    return gated_ffn_bwd_some(dh, dh_stride, x, x_stride, w_gate, w_up, saved, saved_bytes, dx, dw_gate, dw_up, T, D, F, act,
+                              dtype, stream, workspace, workspace_bytes);
 }
 
 conv_status_t gated_ffn8_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *w_gate,

@@ -32,8 +32,8 @@ MAX_WIDTH, MAX_NORM_WIDTH = 1 << 20, 32768
 GROUPS = (32, 64, 128)
 E4M3 = torch.float8_e4m3fn
 # Every symbol include/convlower_ffn.h declares.
-EXPORTS = ("gated_ffn_saved_size", "gated_ffn_fwd", "gated_ffn_bwd_workspace_size", "gated_ffn_bwd", "gated_ffn8_fwd",
-           "linear_w4_fwd", "gated_ffn_w4_fwd", "norm_quant_fwd")
+EXPORTS = ("gated_ffn_saved_size", "gated_ffn_fwd", "gated_ffn_bwd_workspace_size", "gated_ffn_bwd", "gated_ffn_bwd_some",
+           "gated_ffn8_fwd", "linear_w4_fwd", "gated_ffn_w4_fwd", "norm_quant_fwd")
 _lib = None
 
 
@@ -45,7 +45,7 @@ def _ffn_lib():
         L.gated_ffn_saved_size.argtypes = [l, i, ctypes.POINTER(z)]
         L.gated_ffn_fwd.argtypes = [vp, l] + [vp] * 4 + [z, l] + [i] * 4 + [vp]
         L.gated_ffn_bwd_workspace_size.argtypes = [l, i, i, i, ctypes.POINTER(z)]
-        L.gated_ffn_bwd.argtypes = [vp, l, vp, l] + [vp] * 3 + [z] + [vp] * 3 + [l] + [i] * 4 + [vp, vp, z]
+        L.gated_ffn_bwd.argtypes = L.gated_ffn_bwd_some.argtypes = [vp, l, vp, l] + [vp] * 3 + [z] + [vp] * 3 + [l] + [i] * 4 + [vp, vp, z]
         L.gated_ffn8_fwd.argtypes = [vp, l] + [vp] * 6 + [l] + [i] * 4 + [vp]
         L.linear_w4_fwd.argtypes = [vp, l] + [vp] * 4 + [l] + [i] * 4 + [vp]
         L.gated_ffn_w4_fwd.argtypes = [vp, l] + [vp] * 7 + [l] + [i] * 5 + [vp]
@@ -128,9 +128,10 @@ def gated_ffn_fwd(x, w_gate, w_up, *, act="silu", save=False, stream=None):
     return h, saved
 
 
-def gated_ffn_bwd(dh, x, w_gate, w_up, saved, *, act="silu", stream=None):
-    """Gradients of gated_ffn_fwd: (dx, dw_gate, dw_up).  saved: what the
-    forward call with save=True returned for the same inputs."""
+def gated_ffn_bwd(dh, x, w_gate, w_up, saved, *, act="silu", want_dx=True, want_dw=True, stream=None):
+    """Gradients of gated_ffn_fwd: (dx, dw_gate, dw_up), None for what is not
+    wanted.  saved: what the forward call with save=True returned for the same
+    inputs."""
     code, xp, xs, gp, up, T, D, F = _ffn_args(x, w_gate, w_up)
     a, dt, dev = _act(act), x.dtype, x.device
     if dh.shape != (*x.shape[:-1], F):
@@ -138,13 +139,13 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, saved, *, act="silu", stream=None):
     dp, ds, _ = _rows(dh, "dh", dt, dev)
     sp = _dense(saved, "saved", saved.shape, torch.uint8, dev)
     with _on(stream, dev):
-        dx = torch.empty(x.shape, dtype=dt, device=dev)
-        dg, du = (torch.empty((F, D), dtype=dt, device=dev) for _ in range(2))
+        dx = torch.empty(x.shape, dtype=dt, device=dev) if want_dx else None
+        dg, du = (torch.empty((F, D), dtype=dt, device=dev) if want_dw else None for _ in range(2))
         ws = _bytes(_size("gated_ffn_bwd_workspace_size", T, D, F, code), dev)
         _check("gated_ffn_bwd",
-               _ffn_lib().gated_ffn_bwd(dp, ds, xp, xs, gp, up, sp, saved.numel(), dx.data_ptr(), dg.data_ptr(),
-                                        du.data_ptr(), T, D, F, a, code, _raw(stream, dev), _ptr(ws),
-                                        ws.numel() if ws is not None else 0))
+               _ffn_lib().gated_ffn_bwd_some(dp, ds, xp, xs, gp, up, sp, saved.numel(), _ptr(dx), _ptr(dg), _ptr(du), T,
+                                             D, F, a, code, _raw(stream, dev), _ptr(ws),
+                                             ws.numel() if ws is not None else 0))
     return dx, dg, du
 
 
@@ -160,7 +161,9 @@ class _GatedFfn(torch.autograd.Function):
     @differentiable_once
     def backward(ctx, dh):
         x, w_gate, w_up, saved = ctx.saved_tensors
-        return (*gated_ffn_bwd(dh.contiguous(), x, w_gate, w_up, saved, act=ctx.act), None, None)
+        want = ctx.needs_input_grad
+        return (*gated_ffn_bwd(dh.contiguous(), x, w_gate, w_up, saved, act=ctx.act, want_dx=want[0],
+                               want_dw=want[1] or want[2]), None, None)
 
 
 def gated_ffn(x, w_gate, w_up, *, act="silu"):

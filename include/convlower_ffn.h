@@ -56,6 +56,12 @@ conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, in
                             const void *w_up, const void *saved, size_t saved_bytes, void *dx, void *dw_gate,
                             void *dw_up, int64_t T, int D, int F, ffn_act_t act, conv_dtype_t dtype,
                             conv_stream_t stream, void *workspace, size_t workspace_bytes);
+/* The same for frozen weights or an input without a gradient: dx, or dw_gate
+ * and dw_up together, may be NULL, and their product is left out. */
+conv_status_t gated_ffn_bwd_some(const void *dh, int64_t dh_stride, const void *x, int64_t x_stride,
+                                 const void *w_gate, const void *w_up, const void *saved, size_t saved_bytes, void *dx,
+                                 void *dw_gate, void *dw_up, int64_t T, int D, int F, ffn_act_t act,
+                                 conv_dtype_t dtype, conv_stream_t stream, void *workspace, size_t workspace_bytes);
 
 /* The product on 8 bits: x [T][D] (x_stride), w_gate and w_up [F][D] are e4m3
  * (CONV_DTYPE_FP8_E4M3); a value stands for itself times its row's scale,
