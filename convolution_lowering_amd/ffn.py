@@ -137,7 +137,10 @@ def gated_ffn_bwd(dh, x, w_gate, w_up, saved, *, act="silu", want_dx=True, want_
     if dh.shape != (*x.shape[:-1], F):
         raise ValueError(f"dh has shape {tuple(dh.shape)}, expected {(*x.shape[:-1], F)}")
     dp, ds, _ = _rows(dh, "dh", dt, dev)
-    sp = _dense(saved, "saved", saved.shape, torch.uint8, dev)
+    if saved is None:
+        raise ValueError("saved: gated_ffn_fwd returns it with save=True")
+    # (its layout goes by T and F: that of another call would be read wrongly)
+    sp = _dense(saved, "saved", (max(16, _size("gated_ffn_saved_size", T, F)),), torch.uint8, dev)
     with _on(stream, dev):
         dx = torch.empty(x.shape, dtype=dt, device=dev) if want_dx else None
         dg, du = (torch.empty((F, D), dtype=dt, device=dev) if want_dw else None for _ in range(2))

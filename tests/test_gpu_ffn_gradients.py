@@ -31,3 +31,18 @@ def test_a_frozen_layer():
     got, = torch.autograd.grad(ffn.gated_ffn(x, wg, wu).sum(), x)
     wg.requires_grad_(True)
     assert torch.equal(torch.autograd.grad(ffn.gated_ffn(x, wg, wu).sum(), (x, wg))[0], got)
+
+
+def test_saved_of_another_call():
+    """What the forward call did not save, or saved for another number of tokens or
+    features, is refused."""
+    x, wg, wu = inputs(12, 40, 24, torch.bfloat16)
+    dh = torch.zeros(12, 24, dtype=torch.bfloat16, device=DEV)
+    h, saved = ffn.gated_ffn_fwd(x, wg, wu, save=True)
+    for bad in (ffn.gated_ffn_fwd(x, wg, wu)[1], torch.cat((saved, saved)), saved[:-16],
+                ffn.gated_ffn_fwd(x[:11], wg, wu, save=True)[1], saved.view(2, -1), saved.cpu()):
+        with pytest.raises(ValueError):
+            ffn.gated_ffn_bwd(dh, x, wg, wu, bad)
+    with pytest.raises(TypeError):
+        ffn.gated_ffn_bwd(dh, x, wg, wu, saved.view(torch.float32))
+    ffn.gated_ffn_bwd(dh, x, wg, wu, saved)
