@@ -1,9 +1,11 @@
 """Gradients of the gated product: those that are wanted."""
+import math
+
 import pytest
 import torch
 
 from convolution_lowering_amd import ffn
-from test_gpu_ffn import DEV, DTYPES, gen, inputs, say
+from test_gpu_ffn import DEV, DTYPES, gen, half, inputs, near, say, tiny
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +48,32 @@ def test_saved_of_another_call():
     with pytest.raises(TypeError):
         ffn.gated_ffn_bwd(dh, x, wg, wu, saved.view(torch.float32))
     ffn.gated_ffn_bwd(dh, x, wg, wu, saved)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu", "gelu"])
+@pytest.mark.parametrize("t", DTYPES, ids=str)
+def test_slopes_alone(act, t):
+    """The gate's slope by itself, relative to its own size: one product for each
+    feature (x = u = 1), so that dw_gate is the slope, rounded to t.
+
+    p = 1 / (1 + e^-v) and q = 1 - p: the exponential is off by 2^-22 |v| of
+    itself, which changes p by q times that and q by p times that; instructions
+    are good to 2^-20 for results of 16 bits, 2^-21 for float32."""
+    z = torch.linspace(-40, 40, 641, device=DEV) if t != torch.float16 else torch.linspace(-9, 9, 289, device=DEV)
+    z = z.to(t)[:, None].contiguous()
+    one = torch.ones(1, 1, dtype=t, device=DEV)
+    wu = torch.ones_like(z)
+    _, saved = ffn.gated_ffn_fwd(one, z, wu, act=act, save=True)
+    _, dg, _ = ffn.gated_ffn_bwd(torch.ones(1, z.shape[0], dtype=t, device=DEV), one, z, wu, saved, act=act)
+    zd = z.double()
+    c = 2 * math.sqrt(2 / math.pi)
+    v = c * (zd + 0.044715 * zd ** 3) if act == "gelu" else zd
+    inner = {"sigmoid": torch.ones_like(zd), "silu": zd, "gelu": c * (zd + 3 * 0.044715 * zd ** 3)}[act]
+    p, q = 1 / (1 + torch.exp(-v)), 1 / (1 + torch.exp(v))
+    fast = 2.0 ** -20 if t != torch.float32 else 2.0 ** -21
+    wp, wq = fast + 2.0 ** -22 * v.abs() * q, fast + 2.0 ** -22 * v.abs() * p
+    turn, rest = p * q * inner, 0 * p if act == "sigmoid" else p  # the slope is their sum
+    tol = (wp + wq + 2.0 ** -21) * turn.abs() + (wp + 2.0 ** -22) * rest
+    want = turn + rest
+    # below the smallest normal numbers (of float32, in which e^-v is taken) nothing has to be kept
+    near(dg, want, tol + half(t) * want.abs() * 1.01 + tiny(t) + 1e-34, "dw_gate")
