@@ -36,13 +36,15 @@ conv_status_t ffn_sizes(int64_t T, int D, int F, ffn_act_t act, int64_t stride) 
 int64_t saved_pitch(int F) { return (F + 3) / 4 * 4; }
 
 // The workspace of the backward pass holds the gradients of g and u, rows of whole
-// 128-byte pieces, and then the parts' sums of either product.
+// 128-byte pieces, what fp16 keeps of their range, and then the parts' sums of either
+// product.
 int padded(int F, conv_dtype_t dtype) {
     const int piece = dtype == CONV_DTYPE_FP32 ? 32 : 64;
     return (F + piece - 1) / piece * piece;
 }
 
 size_t dgu_bytes(int64_t T, int F, conv_dtype_t dtype) { return (size_t)T * 2 * (size_t)padded(F, dtype) * bytes_of(dtype); }
+size_t range_bytes(conv_dtype_t dtype) { return dtype == CONV_DTYPE_FP16 ? (kFfnRangeAt + kFfnRangeBlocks) * sizeof(float) : 0; }
 
 conv_status_t w4_check(const void *x, int64_t x_stride, const void *y, int64_t R, int D, int F, int group,
                        conv_dtype_t dtype) {
@@ -189,7 +191,7 @@ conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t
         if (dx > 1) part = std::max(part, (size_t)dx * T * ffn_part_pitch(D) * 4);
         if (dw > 1) part = std::max(part, (size_t)dw * 2 * Fp * ffn_part_pitch(D) * 4);
     }
-    *bytes_out = T ? dgu_bytes(T, F, dtype) + part : 0;
+    *bytes_out = T ? dgu_bytes(T, F, dtype) + range_bytes(dtype) + part : 0;
     return CONV_OK;
 }
 
@@ -215,7 +217,11 @@ conv_status_t gated_ffn_bwd_some(const void *dh, int64_t dh_stride, const void *
     d.T = T, d.F = F, d.Fp = Fp, d.act = act;
     FfnGemmArgs a{};
     a.a = workspace, a.as = 2 * (int64_t)Fp, a.N = D;
-    if (T) a.part = (float *)((char *)workspace + dgu_bytes(T, F, dtype));
+    if (T) {
+        char *rest = (char *)workspace + dgu_bytes(T, F, dtype);
+        a.part = (float *)(rest + range_bytes(dtype));
+        if (dtype == CONV_DTYPE_FP16) a.factor = d.range = (float *)rest;
+    }
     // dx = [dg du] [w_gate; w_up]
     FfnGemmArgs x1 = a;
     x1.b0 = w_gate, x1.b1 = w_up, x1.bs = D, x1.M = T, x1.K = 2 * Fp, x1.ktsplit = Fp / piece, x1.brows = F;

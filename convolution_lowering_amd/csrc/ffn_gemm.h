@@ -192,12 +192,17 @@ __device__ __forceinline__ void ffn_with_act(int act, F &&f) {
     }
 }
 template <typename O>
-__device__ __forceinline__ void ffn_plain_out(const FfnGemmArgs &A, int64_t m, int n, const f32x4_t &acc) {
+__device__ __forceinline__ float ffn_factor(const FfnGemmArgs &A) {
+    if constexpr (__is_same(O, _Float16)) return A.factor ? *A.factor : 1.f;
+    return 1.f;
+}
+template <typename O>
+__device__ __forceinline__ void ffn_plain_out(const FfnGemmArgs &A, int64_t m, int n, const f32x4_t &acc, float by) {
     if (A.splits > 1) {  // this part's sums; their rows are whole 16-byte pieces
         *(float4 *)(A.part + ((int64_t)blockIdx.y * A.M + m) * ffn_part_pitch(A.N) + n) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         return;
     }
-    const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
+    const float v[4] = {acc[0] * by, acc[1] * by, acc[2] * by, acc[3] * by};
     const bool second = m >= A.split;
     const int64_t row = second ? m - A.split : m;
     if (row < A.rows) ffn_put4((O *)(second ? A.out2 : A.out) + row * A.N, n, A.N, v);
@@ -411,6 +416,7 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
         }
     }
 
+    const float by = PLAIN ? ffn_factor<O>(A) : 1.f;
     auto results = [&](auto act) {
 #pragma unroll
         for (int t = 0; t < TM; ++t) {
@@ -420,8 +426,8 @@ __device__ __forceinline__ void ffn_small_body(const FfnGemmArgs &A) {
             for (int f = 0; f < TN; ++f) {
                 const int n = n0 + (wn * TN + f) * 16 + 4 * (lane >> 4);
                 if constexpr (PLAIN) {
-                    if (n < A.N) ffn_plain_out<O>(A, m, n, acc[t][0][f]);
-                    if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[t][1][f]);
+                    if (n < A.N) ffn_plain_out<O>(A, m, n, acc[t][0][f], by);
+                    if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[t][1][f], by);
                 } else if (n < A.N) {
                     ffn_gated_out<O, EPI, decltype(act)::value>(A, m, n, acc[t][0][f], acc[t][1][f]);
                 }
@@ -632,6 +638,7 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
     if (wave < 4) block_barrier();
     CONVLOWER_WAIT_VMCNT(0);  // no load may still write LDS when the block ends
 
+    const float by = PLAIN ? ffn_factor<O>(A) : 1.f;
     auto results = [&](auto act) {
 #pragma unroll
         for (int ha = 0; ha < 2; ++ha)
@@ -643,8 +650,8 @@ __device__ __forceinline__ void ffn_large_body(const FfnGemmArgs &A) {
                 for (int f = 0; f < TB; ++f) {
                     const int n = n0 + (wn * TB + f) * 16 + 4 * (lane >> 4);
                     if constexpr (PLAIN) {
-                        if (n < A.N) ffn_plain_out<O>(A, m, n, acc[ha][0][t][f]);
-                        if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[ha][1][t][f]);
+                        if (n < A.N) ffn_plain_out<O>(A, m, n, acc[ha][0][t][f], by);
+                        if (n + BH < A.N) ffn_plain_out<O>(A, m, n + BH, acc[ha][1][t][f], by);
                     } else if (n < A.N) {
                         ffn_gated_out<O, EPI, decltype(act)::value>(A, m, n, acc[ha][0][t][f], acc[ha][1][t][f]);
                     }
@@ -666,6 +673,7 @@ typedef FfnLarge<2, 2, 1> FfnTile128x64;   // 64 x (16 + 16), two blocks on a CU
 template <typename O>
 __global__ __launch_bounds__(256) void ffn_sum_kernel(FfnGemmArgs A) {
     const int64_t pitch = ffn_part_pitch(A.N), per = pitch / 4, total = A.M * per;
+    const float by = ffn_factor<O>(A);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t m = i / per;
         const int n = (int)(i - m * per) * 4;
@@ -677,6 +685,8 @@ __global__ __launch_bounds__(256) void ffn_sum_kernel(FfnGemmArgs A) {
             const float4 x = *(const float4 *)(A.part + (s * A.M + m) * pitch + n);
             v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= by;
         ffn_put4((O *)(second ? A.out2 : A.out) + row * A.N, n, A.N, v);
     }
 }

@@ -97,6 +97,7 @@ struct FfnGemmArgs {
     bool vec;
     int tile, splits;
     float *part;  // [splits][M][ffn_part_pitch(N)]
+    const float *factor;  // plain, fp16: the results times this; NULL: as they are
 };
 __host__ __device__ inline int64_t ffn_part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
 
@@ -124,7 +125,9 @@ struct FfnGateGrad {
     void *dgu;
     int64_t T;
     int F, Fp, act;
+    float *range;  // fp16: 2^-k, which the products' results meet, and from kFfnRangeAt on the blocks' largest values
 };
+constexpr int kFfnRangeBlocks = 1024, kFfnRangeAt = 4;  // floats
 hipError_t launch_ffn_gate_grad(const FfnGateGrad &a, int dtype, hipStream_t st);
 
 struct W4Args {

@@ -49,8 +49,9 @@ conv_status_t gated_ffn_fwd(const void *x, int64_t x_stride, const void *w_gate,
 
 /* Gradients of gated_ffn_fwd: dh [T][F] (dh_stride); dx [T][D], dw_gate, dw_up
  * [F][D], each overwritten.  The gradients of g and u are rounded to dtype
- * before the products with the weights and with x.  Sums over tokens are
- * added in a fixed order. */
+ * before the products with the weights and with x (fp16: times a power of two
+ * that keeps the largest in range; what is below 2^-38 of it counts as zero).
+ * Sums over tokens are added in a fixed order. */
 conv_status_t gated_ffn_bwd_workspace_size(int64_t T, int D, int F, conv_dtype_t dtype, size_t *bytes_out);
 conv_status_t gated_ffn_bwd(const void *dh, int64_t dh_stride, const void *x, int64_t x_stride, const void *w_gate,
                             const void *w_up, const void *saved, size_t saved_bytes, void *dx, void *dw_gate,

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from convolution_lowering_amd import ffn
+from oracle import ffn as of
 from test_gpu_ffn import DEV, DTYPES, gen, half, inputs, near, say, tiny
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +78,59 @@ def test_slopes_alone(act, t):
     want = turn + rest
     # below the smallest normal numbers (of float32, in which e^-v is taken) nothing has to be kept
     near(dg, want, tol + half(t) * want.abs() * 1.01 + tiny(t) + 1e-34, "dw_gate")
+
+
+# sizes of dh, x, w_gate, w_up (fp16 ends at 65504 and, with few digits, at 6e-8)
+RANGES = {"large": (200, 2.0 ** -6, 2.0 ** -10, 2.0 ** 12),  # dg about 5e4, past it in many places
+          "small": (2e-6, 1.0, 2.0 ** -3, 2.0 ** -6),  # dg and du below the smallest normal number
+          "usual": (1.0, 1.0, 2.0 ** -3, 2.0 ** -3)}
+
+
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("size", [(40, 64, 96), (33, 77, 130), (300, 256, 2048)], ids=str)
+@pytest.mark.parametrize("kind", sorted(RANGES))
+def test_gradients_of_g_and_u_outside_the_range_of_fp16(kind, size, act):
+    """The gradients of g and u may pass what fp16 holds at either end where dx and
+    dW do not.  Each of them and each result is rounded once: half a step, in norm,
+    and half of the smallest step of a result.  Results past the range are infinite."""
+    T, D, F = size
+    say("range", kind, size, act)
+    g = gen(5)
+    sizes = RANGES[kind]
+    dh, x, wg, wu = (((torch.randn(s, generator=g, device=DEV)) * k).half() for s, k in
+                     zip(((T, F), (T, D), (F, D), (F, D)), sizes))
+    _, saved = ffn.gated_ffn_fwd(x, wg, wu, act=act, save=True)
+    got = ffn.gated_ffn_bwd(dh, x, wg, wu, saved, act=act)
+    leaves = [z.double().requires_grad_(True) for z in (x, wg, wu)]
+    h, gd, ud = of.gated_ffn(*leaves, act)
+    inner = torch.autograd.grad(h, (gd, ud), dh.double(), retain_graph=True)
+    most = max(z.abs().max().item() for z in inner)
+    assert {"large": most > 65504, "small": most < 2.0 ** -14, "usual": 1 < most < 1000}[kind]
+    for a, b in zip(got, torch.autograd.grad(h, leaves, dh.double())):
+        past, near_it = b.abs() > 65504 * 1.01, (b.abs() > 65504 * 0.99) & (b.abs() <= 65504 * 1.01)
+        assert (a[past].double() == b[past].sign() * float("inf")).all()
+        a, b = a[~(past | near_it)].double(), b[~(past | near_it)]
+        assert (a - b).norm() <= 2 * half(torch.float16) * b.norm() + tiny(torch.float16) * b.numel() ** 0.5
+
+
+def test_a_token_out_of_range_in_fp16():
+    """Tokens whose values are not finite do not count for the range of the others,
+    and one with large gradients leaves the others their digits."""
+    x, wg, wu = inputs(40, 72, 96, torch.float16)
+    dh = torch.randn(40, 96, generator=gen(2), device=DEV).half()
+    keep = [i for i in range(40) if i != 7]
+    dx = lambda dh, x: ffn.gated_ffn_bwd(dh, x, wg, wu, ffn.gated_ffn_fwd(x, wg, wu, save=True)[1])[0]
+    want = dx(dh, x)
+    for bad in (float("inf"), float("nan")):
+        y = x.clone()
+        y[7, 70] = bad
+        got = dx(dh, y)
+        assert torch.equal(got[keep], want[keep]) and not got[7].isfinite().all()
+        e = dh.clone()
+        e[7, 3] = bad
+        got = dx(e, x)
+        assert torch.equal(got[keep], want[keep]) and not got[7].isfinite().all()
+    e = dh.clone()
+    e[7] = 60000.0
+    assert torch.equal(dx(e, x)[keep], want[keep])
+    assert not dx(torch.zeros_like(dh), x).any()
