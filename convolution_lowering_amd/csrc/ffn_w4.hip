@@ -98,6 +98,14 @@ __device__ __forceinline__ void w4_transpose(uint32_t (&d)[4]) {
     d[0] = c[0], d[1] = c[1], d[2] = e[0], d[3] = e[1];
 }
 
+// Between a wavefront's lanes that write LDS and those of it that read it, either way:
+// its accesses are made in their order, the compiler has to keep it as well.
+__device__ __forceinline__ void w4_between_lanes() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 constexpr int kScaleBytes = 8192;  // scales and zero points in LDS at a time (32 gated tokens, groups of 128: 24 us, with 16 KB 30)
 
 template <typename S>
@@ -213,9 +221,11 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     // Piece `in` of the span; if not `there`, to no effect (a code of 0 is not a weight of 0).
     auto work = [&](const Piece &p, int in, bool there) {
         if constexpr (!DIRECT) {
+            w4_between_lanes();  // the last piece has been read
             turn_x(p);
 #pragma unroll
             for (int m = 0; m < NM; ++m) mine[NT * 16 * UNITS + m * 64 + code_to] = p.w[m];
+            w4_between_lanes();
         }
         uint32_t w[NM][4];
 #pragma unroll
@@ -305,6 +315,7 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
 
     // Result: lane l holds feature l % 16 and tokens 4 (l / 16) .. + 3 of a tile.
     static_assert(NM * 64 <= ROOM, "the sums' room");
+    w4_between_lanes();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         if (n) __syncthreads();
