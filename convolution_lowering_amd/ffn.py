@@ -256,11 +256,25 @@ def gated_ffn_w4_fwd(x, w_gate, gate_scales, w_up, up_scales, gate_zeros=None, u
     return h
 
 
+def _w4_scales(s, dtype):
+    """Scales of at least s, but for their rounding to `dtype`: where that is
+    coarse, below the type's normal numbers, they go up."""
+    info = torch.finfo(dtype)
+    near = s.to(dtype).float()
+    near += torch.where(near < s * (1 - info.eps), info.tiny * info.eps, 0.0)
+    return torch.where(s > 0, near, torch.ones_like(near)).to(dtype)
+
+
 @torch.no_grad()
 def quantize_w4(w, group=128, zeros=False):
     """(codes, scales, zeros) of weights [F, D], as linear_w4_fwd takes them:
     each group's largest value to 7 (zeros None), or its range to 0..15.  For
-    loading: plain torch, in float32."""
+    loading: plain torch, in float32.
+
+    A zero point is rounded to w's dtype as well: the range is taken as much
+    wider as that may move it, so that no value is off by more than half a step
+    (bfloat16: a step of a 15th of the range and a 1920th of its distance from
+    zero)."""
     if group not in GROUPS:
         raise ValueError(f"group {group}: one of {GROUPS} wanted")
     if w.dim() != 2 or w.shape[1] % 8:
@@ -271,11 +285,14 @@ def quantize_w4(w, group=128, zeros=False):
     parts = torch.cat((w, w[:, -1:].expand(F, n * group - D)), 1).float().view(F, n, group)
     if zeros:
         lo, hi = parts.amin(-1), parts.amax(-1)
-        scales = ((hi - lo) / 15).to(w.dtype)
+        half, mid = (hi - lo) / 2, (hi + lo) / 2
+        # a zero point is about mid / scale; its rounding moves the values by eps / 2 of that many steps
+        wide = half + mid.abs() * (torch.finfo(w.dtype).eps / 2)
+        scales = _w4_scales(torch.where(half > 0, wide / 7.5, torch.zeros_like(wide)), w.dtype)
+        # the middle to the middle of the codes; a group of one value is that value, at code 0
+        zero = torch.where(half > 0, 7.5 - mid / scales.float(), -lo).to(w.dtype)
     else:
-        lo, scales = None, (parts.abs().amax(-1) / 7).to(w.dtype)
-    scales = torch.where(scales > 0, scales, torch.ones_like(scales))  # a group of one value
-    zero = None if lo is None else (-lo / scales.float()).to(w.dtype)
+        scales, zero = _w4_scales(parts.abs().amax(-1) / 7, w.dtype), None
     codes = torch.round(parts / scales.float()[..., None] + (8.0 if zero is None else zero.float()[..., None]))
     codes = codes.clamp(0, 15).to(torch.uint8).view(F, -1)[:, :D]
     return (codes[:, 0::2] | codes[:, 1::2] << 4).contiguous(), scales, zero
