@@ -5,8 +5,8 @@
 // Each weight is read once, for up to 64 tokens: HBM bound for few of them.  The codes
 // become operands of the matrix instructions exactly, so that nothing is
 // rounded before the sums of a group (fp32), and a group's scale meets its sum.
-//   * 16-bit x: a code's four bits are set into the low digits of 128 (bf16) or
-//     1024 (fp16), one instruction for two codes; the 128 joins the zero point, whose
+//   * 16-bit x: a code's four bits are set into the low digits of 128 (bf16; of 2^-9, in
+//     units of 2^-16) or 1024 (fp16), one instruction for two codes; the 128 joins the zero point, whose
 //     term needs sum x of the group: one more product, with ones, that leaves it
 //     in the lanes that use it.  The two codes are four places apart, so x's
 //     eight values of a fragment are put in the same order.
@@ -36,11 +36,16 @@ namespace {
 
 constexpr int kPiece = 128;  // values of a row that a wavefront takes at once: 16 bytes of codes a lane
 
+// Codes and the ones beside them count in units of 1 / UNIT: 2^-16 where the exponent
+// has the room, so that no sum of x times 128 or times 15 passes the largest float32
+// number where y does not.  The results meet it at the end.
 template <typename S>
 struct W4Type {  // 16-bit x: one part, codes behind a leading digit
     static constexpr int PARTS = 1;
-    static constexpr uint32_t LEAD = sizeof(S) == 2 && __is_same(S, _Float16) ? 0x64006400u : 0x43004300u;
+    static constexpr uint32_t LEAD = __is_same(S, _Float16) ? 0x64006400u : 0x3b003b00u;
     static constexpr float OFFSET = __is_same(S, _Float16) ? 1024.f : 128.f;
+    static constexpr uint32_t ONES = __is_same(S, _Float16) ? 0x3c003c00u : 0x37803780u;
+    static constexpr float UNIT = __is_same(S, _Float16) ? 1.f : 65536.f;
     typedef S mma_t;
 };
 template <>
@@ -48,6 +53,8 @@ struct W4Type<float> {
     static constexpr int PARTS = 3;
     static constexpr uint32_t LEAD = 0;
     static constexpr float OFFSET = 0.f;
+    static constexpr uint32_t ONES = 0x37803780u;
+    static constexpr float UNIT = 65536.f;
     typedef uint16_t mma_t;
 };
 
@@ -60,8 +67,8 @@ __device__ __forceinline__ uint4 w4_codes(uint32_t d) {
     } else {
         uint32_t f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __float_as_uint((float)((d >> (4 * i)) & 15));
-        // (whole numbers up to 15: the upper half holds them)
+        for (int i = 0; i < 8; ++i) f[i] = __float_as_uint((float)((d >> (4 * i)) & 15) * (1.f / W4Type<S>::UNIT));
+        // (four digits: the upper half holds them)
         return make_uint4(__builtin_amdgcn_perm(f[1], f[0], 0x07060302), __builtin_amdgcn_perm(f[3], f[2], 0x07060302),
                           __builtin_amdgcn_perm(f[5], f[4], 0x07060302), __builtin_amdgcn_perm(f[7], f[6], 0x07060302));
     }
@@ -216,8 +223,7 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
     };
 
     f32x4_t acc[NT][NM] = {};
-    constexpr uint32_t one = __is_same(S, _Float16) ? 0x3c003c00u : 0x3f803f80u;
-    const uint4 ones = make_uint4(one, one, one, one);
+    const uint4 ones = make_uint4(T::ONES, T::ONES, T::ONES, T::ONES);
     // Piece `in` of the span; if not `there`, to no effect (a code of 0 is not a weight of 0).
     auto work = [&](const Piece &p, int in, bool there) {
         if constexpr (!DIRECT) {
@@ -331,6 +337,7 @@ __device__ __forceinline__ void w4_body(const W4Args &A) {
                 y[m] = 0.f;
 #pragma unroll
                 for (int w = 0; w < WAVES; ++w) y[m] += ((const float *)&turned[w][m * 64 + at])[tok & 3];
+                y[m] *= T::UNIT;
             }
             ((S *)A.y)[r * A.F + f0 + f] = mix_out<S>(GATED ? ffn_act<S>(y[0], A.act) * y[NM - 1] : y[0]);
         }
