@@ -79,7 +79,8 @@ def off(y, want):
 @pytest.mark.parametrize("t", DTYPES, ids=str)
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("size", [(1, 4096, 64), (1, 10240, 300), (4, 4104, 33), (7, 1000, 199), (17, 10280, 50), (40, 20000, 24), (70, 33000, 24),
-                                  (1, 4104, 6150), (4, 10280, 6200), (16, 10280, 6150), (33, 4104, 6150), (64, 10280, 6150)], ids=str)
+                                  (1, 4104, 8200), (4, 10280, 6200), (16, 10280, 8200), (16, 4104, 6150),
+                                  (33, 4104, 6150), (64, 10280, 6150), (130, 4104, 4100)], ids=str)
 def test_in_norm(size, group, t):
     """Long rows, whose scales take several turns, in blocks of both sizes: one value
     left out of 33 000 changes a result by 5e-3 of its norm."""
@@ -95,7 +96,8 @@ def test_in_norm(size, group, t):
 @pytest.mark.parametrize("t", DTYPES, ids=str)
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("size", [(1, 4104, 64), (4, 10280, 33), (7, 4104, 70), (30, 10280, 40), (64, 4104, 100), (90, 10280, 20),
-                                  (1, 10280, 6150), (16, 4104, 6150), (32, 10280, 6150), (64, 4104, 6150)], ids=str)
+                                  (1, 10280, 8200), (16, 4104, 8200), (16, 10280, 6150), (32, 10280, 6150),
+                                  (64, 4104, 6150)], ids=str)
 def test_gated_in_norm(size, group, t):
     """g and u are off as above, h by both (the gates' slopes are at most 1.13, near
     1 for what counts in the norm)."""
@@ -111,7 +113,7 @@ def test_gated_in_norm(size, group, t):
 
 @pytest.mark.parametrize("t", DTYPES, ids=str)
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("F", [20, 6150])
+@pytest.mark.parametrize("F", [20, 4120, 8200])
 def test_values_one_by_one(F, group, t):
     """Rows with a single value, at both ends of pieces, of groups and of what the
     scales' room holds, in the last short piece and at random: the result is one
