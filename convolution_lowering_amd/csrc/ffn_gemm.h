@@ -24,8 +24,11 @@
 // from HBM.  Kernel times, MI355X (an 8192 cubed bf16 product of the library 1413
 // TFLOP/s, e4m3 2676): gated forward, 5003 tokens, 4096 to 10240: bf16 591 to 660 us (1270 to
 // 1420 TFLOP/s); 8192 tokens e4m3 509 to 590 (2330 to 2700); training, 8192 tokens, 4096 to
-// 8192: forward with g and u saved 940 us (1170; 768 MB written), dx 730 (1500), dw 790
-// (1390); 200 tokens 59 us, 4 tokens 38 (168 MB of weights, 4.4 TB/s).  The matrix
+// 8192: forward with g and u saved 940 us (1170; 671 MB of
+// results, of which 764 MB leave: h goes in pieces of 32 bytes, and between two of one 64-byte
+// piece lie stores of g and u), dx 730 (1500), dw 790
+// (1390); 200 tokens 59 us, 4 tokens 39 (168 MB of weights,
+// all from HBM, 4.3 TB/s; of one layer again and again, mostly from the Infinity Cache, 25).  The matrix
 // cores are busy 64 to 87 % of the time, no LDS access meets another's bank.
 #pragma once
 

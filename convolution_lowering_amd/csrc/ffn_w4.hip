@@ -2,7 +2,9 @@
 //
 //   y[r,f] = sum over groups G of s[f,G] (sum_{d in G} x[r,d] code[f,d] - z[f,G] sum_{d in G} x[r,d])
 //
-// Each weight is read once, for up to 64 tokens: HBM bound for few of them.  The codes
+// Each weight is read once for up to 64 tokens (32 gated ones of groups of 32; 16 of
+// float32, and of 16-bit rows at odd multiples of 2 bytes), bound by its way here for few
+// of them.  The codes
 // become operands of the matrix instructions exactly, so that nothing is
 // rounded before the sums of a group (fp32), and a group's scale meets its sum.
 //   * 16-bit x: a code's four bits are set into the low digits of 128 (bf16; of 2^-9, in
@@ -24,11 +26,13 @@
 // both are loaded in that order (DIRECT; 1 token 15 us, by LDS 17).  Scales pass
 // through LDS as well.
 //
-// Inside a captured graph, bf16: 10240 to 4096, groups of 128: 1 token 8.4 us, of 21.6
-// MB (2.6 TB/s; the launch and the first pieces' way are 5 of them), 32 tokens 15.6, 64
-// tokens 24.9.  4096 to 10240 gated, groups of 128: 1 token 15.0 us (43 MB, 2.9 TB/s), 32
-// tokens 22.6, 64 tokens 40; groups of 32: 27.8, 52, 74, bound by the arithmetic on
-// scales, which is four times as much.
+// Inside a captured graph, bf16: 10240 to 4096, groups of 128: 1 token 8.5 us, of 21.6
+// MB, 32 tokens 16.4, 64 tokens 26.7; 4096 to 10240 gated: 1 token 14.3 us (45 MB),
+// 32 tokens 21.6, 64 tokens 40.4; groups of 32: 23.1, 43.6, 65.9, bound by the
+// arithmetic on scales, which is four times as much.  (That is of one layer again and
+// again, out of the Infinity Cache.  Of 48 in turn, from HBM: 1 token 10.3 us, 2.1 TB/s,
+// and 15.8, 2.8 TB/s, 32 tokens 18.4 and 24.8; the launch and the first pieces' way
+// are some 5 us of each.)
 #include "ffn_internal.h"
 
 namespace convlower {
@@ -355,15 +359,21 @@ hipError_t w4_run(const W4Args &a, hipStream_t st) {
     hipLaunchKernelGGL((w4_kernel<S, NT, WAVES, GROUP, GATED, VEC, DIRECT>), dim3((unsigned)x, (unsigned)y), dim3(WAVES * 64), 0, st, a);
     return hipGetLastError();
 }
-// Blocks of four wavefronts where there are enough of them for every CU to hold two or
-// more, so that all are there at once (640 blocks of 16 gated features, R = 1: 15.1 us
-// against 25 with eight wavefronts); eight where there are few (256 blocks, R = 1, 4096
-// wide: 5.4 us against 7.1 with sixteen).  Four token tiles at once but for the
-// groups whose sums do not fit the registers (gated, 32, 64 tokens: two by two 74 us;
-// with the scales' rows still on one bank 84, and 114 four at once).
+// Blocks of eight wavefronts where all of them are on the CUs at once: one a CU (256
+// blocks, 4096 wide gated bf16, one token 6.6 us, with four wavefronts 7.6; 32 tokens 10.1
+// and 12.3), two where a second one fits beside it, which several token tiles and
+// float32's LDS leave no room for (512 blocks, one token 10.7 and 11.2, groups of 32 16.0
+// and 20.7; but 32 tokens 19.6 and 17.8, float32, 8 tokens 25.3 and 23.5).  Else four, of which a CU
+// holds more (640 blocks, one token 15.6 and 14.3, 32 tokens 26.2 and 21.3; 128 tokens of 4096
+// features 29.1 and 26.2).  (Eight, not sixteen: one token of 4096 x 4096 5.4 us against 7.1.)
+// Four token tiles at once but for the groups whose sums do not fit the registers (gated,
+// 32, 64 tokens: two by two 74 us; with the scales' rows still on one bank 84, and 114
+// four at once).
 template <typename S, int NT, int GROUP, bool GATED, bool DIRECT>
 hipError_t w4_waves(const W4Args &a, hipStream_t st) {
-    return a.F >= 6144 ? w4_run<S, NT, 4, GROUP, GATED, true, DIRECT>(a, st) : w4_run<S, NT, 8, GROUP, GATED, true, DIRECT>(a, st);
+    const int64_t blocks = ((a.F + 15) / 16) * ((a.R + 16 * NT - 1) / (16 * NT));
+    constexpr int at_once = NT == 1 && (DIRECT || sizeof(S) == 2) ? 512 : 256;
+    return blocks > at_once ? w4_run<S, NT, 4, GROUP, GATED, true, DIRECT>(a, st) : w4_run<S, NT, 8, GROUP, GATED, true, DIRECT>(a, st);
 }
 template <typename S, int GROUP, bool GATED>
 hipError_t w4_tokens(const W4Args &a, hipStream_t st) {

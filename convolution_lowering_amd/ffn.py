@@ -15,8 +15,9 @@ allocated with torch on the stream the library launches on (`stream`, else the
 current one of the tensors' device), and a failing call raises
 ConvLowerError, ValueError or TypeError before anything is launched.
 
-x is ``[T, D]`` or has any number of axes before D, at one stride; everything
-inside a token is dense, and so are weights.
+x is ``[T, D]`` or has any number of axes before D, at one stride of at most
+``MAX_WIDTH`` values (norm_quant_fwd: dense); everything inside a token is dense,
+and so are weights.
 """
 from __future__ import annotations
 

@@ -33,7 +33,9 @@ extern "C" {
  * Gaussian one, z s(2 sqrt(2/pi) (z + 0.044715 z^3)); s(z) = 1 / (1 + e^-z). */
 typedef enum { FFN_ACT_NONE = 0, FFN_ACT_SILU = 1, FFN_ACT_SIGMOID = 2, FFN_ACT_GELU = 3 } ffn_act_t;
 
-/* Limits, above which a call returns CONV_ERR_UNSUPPORTED. */
+/* Limits, above which a call returns CONV_ERR_UNSUPPORTED; so do more rows than
+ * one launch has blocks for (products of 4 bits: some 2^20 to 2^22 rows, by what
+ * is said there of the weights; the norm: 2^22 of the widest). */
 #define FFN_MAX_WIDTH (1 << 20)  /* D, F and strides, in elements */
 #define FFN_MAX_NORM_WIDTH 32768 /* row length of norm_quant_fwd */
 
@@ -79,7 +81,8 @@ conv_status_t gated_ffn8_fwd(const void *x, int64_t x_stride, const float *x_sca
  * scales and zeros [F][ceil(D / group)] in dtype, zeros NULL: 8; group 32, 64 or
  * 128; y [R][F].  Made for a few tokens: each 64 take the weights again (gated
  * groups of 32: each 32; float32, and 16-bit rows at odd multiples of 2 bytes:
- * each 16).  A row of x that holds an infinity or a NaN gives NaN. */
+ * each 16).  A row of x that holds an infinity or a NaN gives NaN; finite ones do not
+ * overflow where y does not, but for bf16 and fp32 zero points past 384. */
 conv_status_t linear_w4_fwd(const void *x, int64_t x_stride, const void *w, const void *scales, const void *zeros,
                             void *y, int64_t R, int D, int F, int group, conv_dtype_t dtype, conv_stream_t stream);
 
