@@ -156,10 +156,10 @@ class MixerBlock(torch.nn.Module):
         """Copies of the feed-forward weights for serving: 8 bits for
         ``prompts`` (bfloat16 and float16 blocks), 4 bits with groups of
         `group` for ``step``.  bits: which of them; without 4, ``step`` stays
-        with the weights themselves, which past some 64 requests are faster
-        than 4-bit ones.  Where the weights have changed since (a training
+        with the weights themselves, which somewhere between 32 and 64 requests
+        become faster than 4-bit ones.  Where the weights have changed since (a training
         step, load_state_dict, another device or type), ``prompts`` and ``step``
-        make the copies again, in place where they fit, so that a captured
+        make the copies again on their stream, in place where they fit, so that a captured
         ``step`` takes the new ones too; what is written past autograd's
         knowledge (``.data``) asks for a call of this."""
         if not self.ffn:
